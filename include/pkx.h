@@ -493,6 +493,89 @@ int pkx_expand_paged_kv_indices(
     int32_t *token_indptr, int32_t *token_indices,
     int64_t token_indices_capacity, void *stream);
 
+/*
+ * 4-bit KV pools.
+ * The pages' pools are bf16 or fp8; a 4-bit pool is this library's own
+ * addition.  A row (one slot, one KV head) of d elements (a multiple of 16) is
+ *   codes        d / 2 bytes of e2m1 codes, element 2i in the low nibble of
+ *                byte i and element 2i + 1 in the high nibble
+ *   block scales d / 16 bytes, one e4m3 scale for every 16 elements
+ * and an element reads code * block_scale * k_scale (v_scale for values;
+ * k_scale, v_scale positive host floats): 0.5625 bytes an element.  K and V
+ * have codes and block scales in tensors of their own:
+ *   k_buffer       codes of (slot, h) at k_buffer + slot*kb_ss + h*kb_sh
+ *   k_block_scale  scales of (slot, h) at k_block_scale + slot*kbs_ss + h*kbs_sh
+ *   v_buffer, v_block_scale  likewise (vb_*, vbs_*)
+ * All strides of a 4-bit pool are in BYTES.  The write and the read back need
+ * code bases and strides that are multiples of 8 bytes; the attention calls
+ * need multiples of 16 bytes, block-scale bases and strides that are multiples
+ * of d / 16 bytes, and slot strides below 2^31 bytes.
+ */
+
+/*
+ * KV write into a 4-bit pool, quantising.  For t < n_tokens, every KV head h
+ * and every block of 16 consecutive elements x of k[t, h] (and of v[t, h]):
+ *   q           = x / k_scale           (IEEE fp32 division)
+ *   block scale = e4m3(max |q| / 6)     (fp32; nearest, ties to even, at most
+ *                                        448)
+ *   code        = the e2m1 value nearest to q / block scale (ties to even,
+ *                 saturating at 6; the choice is exact)
+ * at slot cache_loc[t].  A block whose scale rounds to 0 stores zeros; an
+ * infinity saturates; a block that holds a NaN gets the scale NaN (0x7f) and
+ * reads NaN.  lk and lv are any positive multiples of 16; other arguments and
+ * rules as pkx_set_kv_buffer (v may be NULL: only K is written; slots outside
+ * the pool are skipped).
+ */
+int pkx_set_kv_buffer_fp4(
+    const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+    int64_t v_hs, const int64_t *cache_loc, int64_t n_tokens, int hkv, int lk,
+    int lv, float k_scale, float v_scale, void *k_buffer, int64_t kb_ss,
+    int64_t kb_sh, void *k_block_scale, int64_t kbs_ss, int64_t kbs_sh,
+    void *v_buffer, int64_t vb_ss, int64_t vb_sh, void *v_block_scale,
+    int64_t vbs_ss, int64_t vbs_sh, int64_t num_slots, void *stream);
+
+/*
+ * Rows of a 4-bit pool read back as bf16 (to hand a prefix to a pool of
+ * another format, or to check one).  For r < n_rows and every KV head h:
+ *   k[r, h, :] = bf16(code * block_scale * k_scale) of slot kv_indices[r]
+ * and likewise v (NULL: only K is read; v_buffer and v_block_scale are then
+ * ignored).  code * block_scale is exact, its product with k_scale is rounded
+ * to fp32 and then to bf16.  A row whose slot lies outside the pool reads
+ * zero.
+ *   kv_indices int32 [n_rows]
+ *   k, v       bf16 [n_rows, hkv, lk] / [.., lv], strides (k_ts, k_hs) /
+ *              (v_ts, v_hs) in elements (written)
+ */
+int pkx_get_kv_buffer_fp4(
+    const void *k_buffer, int64_t kb_ss, int64_t kb_sh,
+    const void *k_block_scale, int64_t kbs_ss, int64_t kbs_sh,
+    const void *v_buffer, int64_t vb_ss, int64_t vb_sh,
+    const void *v_block_scale, int64_t vbs_ss, int64_t vbs_sh,
+    int64_t num_slots, const int32_t *kv_indices, int64_t n_rows, int hkv,
+    int lk, int lv, float k_scale, float v_scale, void *k, int64_t k_ts,
+    int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, void *stream);
+
+/*
+ * Decode attention over a 4-bit pool: pkx_decode_attention_fwd with the pool
+ * above, for (lq, lv) = (64, 64) and (128, 128) and hq / hkv <= 128.  With
+ * sliding_window W > 0 the query (at position T_b - 1) sees key j iff
+ * (T_b - 1) - j <= W or j < first_tokens (the first tokens of a sequence stay
+ * visible; first_tokens >= 0, without effect when W <= 0).
+ *   workspace >= pkx_decode_fp4_workspace_size(...) bytes, 256-byte aligned
+ * pkx_workspace_status reports a slot outside the pool (its key and value
+ * read as zero) or an indptr that decreases (PKX_EDEVICE).
+ */
+size_t pkx_decode_fp4_workspace_size(int batch, int hq, int hkv, int lq, int lv);
+int pkx_decode_attention_fwd_fp4(
+    const void *q, void *o, const void *k_buffer, const void *k_block_scale,
+    const void *v_buffer, const void *v_block_scale, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int batch, int hq, int hkv, int lq, int lv,
+    int64_t kb_ss, int64_t kb_sh, int64_t kbs_ss, int64_t kbs_sh,
+    int64_t vb_ss, int64_t vb_sh, int64_t vbs_ss, int64_t vbs_sh,
+    int64_t num_slots, float sm_scale, float logit_cap, int sliding_window,
+    int first_tokens, float k_scale, float v_scale, float *lse_out,
+    void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

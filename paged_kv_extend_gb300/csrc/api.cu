@@ -566,3 +566,169 @@ int pkx_create_kv_indices(const int32_t *req_to_token, int64_t req_to_token_rows
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------- 4-bit pool
+// The rows of one half (K or V) of a 4-bit pool: codes and block scales.
+static int check_fp4_half(const char *name, const void *codes, int64_t ss, int64_t sh,
+                          const void *scales, int64_t s_ss, int64_t s_sh, int code_align,
+                          int scale_align) {
+  if (!codes || !scales) return set_error(PKX_EINVAL, "%s codes or block scales null", name);
+  if (!aligned(codes, code_align) || ss < 0 || sh < 0 || ss % code_align || sh % code_align)
+    return set_error(PKX_EINVAL, "%s codes: base and strides (%lld, %lld) must be multiples of %d "
+                     "bytes", name, (long long)ss, (long long)sh, code_align);
+  if (!aligned(scales, scale_align) || s_ss < 0 || s_sh < 0 || s_ss % scale_align ||
+      s_sh % scale_align)
+    return set_error(PKX_EINVAL, "%s block scales: base and strides (%lld, %lld) must be "
+                     "multiples of %d bytes", name, (long long)s_ss, (long long)s_sh, scale_align);
+  return PKX_OK;
+}
+
+static int check_fp4_scales(float k_scale, float v_scale) {
+  if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return set_error(PKX_EINVAL, "k_scale and v_scale must be positive and finite");
+  return PKX_OK;
+}
+
+// Head dims, pool rows and scales of an attention call over a 4-bit pool.
+static int check_fp4_attention(int hq, int hkv, int lq, int lv, float k_scale,
+                               float v_scale) {
+  int rc;
+  if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
+  if (!((lq == 64 && lv == 64) || (lq == 128 && lv == 128)))
+    return set_error(PKX_EUNSUPPORTED, "a 4-bit pool is built for Lq = Lv = 64 or 128");
+  return check_fp4_scales(k_scale, v_scale);
+}
+
+static int check_fp4_attention_rows(const Fp4Pool &p, int d) {
+  int rc;
+  if ((rc = check_fp4_half("k_buffer", p.k, p.k_ss, p.k_sh, p.ks, p.ks_ss, p.ks_sh, 16, d / 16)))
+    return rc;
+  if ((rc = check_fp4_half("v_buffer", p.v, p.v_ss, p.v_sh, p.vs, p.vs_ss, p.vs_sh, 16, d / 16)))
+    return rc;
+  const int64_t lim = 1ll << 31;
+  if (p.k_ss >= lim || p.v_ss >= lim || p.ks_ss >= lim || p.vs_ss >= lim)
+    return set_error(PKX_EUNSUPPORTED, "a 4-bit pool's slot strides must be below 2^31 bytes");
+  if (p.num_slots <= 0) return set_error(PKX_EINVAL, "num_slots must be positive");
+  if (p.num_slots >= lim) return set_error(PKX_EUNSUPPORTED, "2^31 pool slots or more");
+  return PKX_OK;
+}
+
+static Fp4Pool fp4_pool(const void *k, const void *ks, const void *v, const void *vs,
+                        int64_t k_ss, int64_t k_sh, int64_t ks_ss, int64_t ks_sh, int64_t v_ss,
+                        int64_t v_sh, int64_t vs_ss, int64_t vs_sh, int64_t num_slots) {
+  auto w = [](const void *x) { return static_cast<uint8_t *>(const_cast<void *>(x)); };
+  return Fp4Pool{w(k), w(ks), w(v), w(vs), k_ss, k_sh, ks_ss, ks_sh, v_ss, v_sh, vs_ss, vs_sh,
+                 num_slots};
+}
+
+extern "C" {
+
+int pkx_set_kv_buffer_fp4(const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                          int64_t v_hs, const int64_t *cache_loc, int64_t n_tokens, int hkv,
+                          int lk, int lv, float k_scale, float v_scale, void *k_buffer,
+                          int64_t kb_ss, int64_t kb_sh, void *k_block_scale, int64_t kbs_ss,
+                          int64_t kbs_sh, void *v_buffer, int64_t vb_ss, int64_t vb_sh,
+                          void *v_block_scale, int64_t vbs_ss, int64_t vbs_sh, int64_t num_slots,
+                          void *stream) {
+  int rc;
+  if ((rc = check_fp4_scales(k_scale, v_scale))) return rc;
+  if (n_tokens < 0 || hkv <= 0 || lk <= 0 || lk % 16 || (v && (lv <= 0 || lv % 16)))
+    return set_error(PKX_EINVAL,
+                     "set_kv_buffer_fp4: n_tokens >= 0, hkv > 0, lk (and lv) multiples of 16");
+  if (num_slots < 0) return set_error(PKX_EINVAL, "set_kv_buffer_fp4: negative num_slots");
+  if (n_tokens == 0) return PKX_OK;
+  if (!cache_loc || !aligned(cache_loc, 8))
+    return set_error(PKX_EINVAL, "set_kv_buffer_fp4: cache_loc null or misaligned");
+  if ((rc = check_rows("k", k, k_ts, k_hs))) return rc;
+  if ((rc = check_fp4_half("k_buffer", k_buffer, kb_ss, kb_sh, k_block_scale, kbs_ss, kbs_sh, 8,
+                           1)))
+    return rc;
+  if (v) {
+    if ((rc = check_rows("v", v, v_ts, v_hs))) return rc;
+    if ((rc = check_fp4_half("v_buffer", v_buffer, vb_ss, vb_sh, v_block_scale, vbs_ss, vbs_sh, 8,
+                             1)))
+      return rc;
+  }
+  return launch_set_kv_buffer_fp4(k, k_ts, k_hs, v, v_ts, v_hs, cache_loc, n_tokens, hkv, lk, lv,
+                                  k_scale, v_scale,
+                                  fp4_pool(k_buffer, k_block_scale, v_buffer, v_block_scale, kb_ss,
+                                           kb_sh, kbs_ss, kbs_sh, vb_ss, vb_sh, vbs_ss, vbs_sh,
+                                           num_slots),
+                                  static_cast<cudaStream_t>(stream));
+}
+
+int pkx_get_kv_buffer_fp4(const void *k_buffer, int64_t kb_ss, int64_t kb_sh,
+                          const void *k_block_scale, int64_t kbs_ss, int64_t kbs_sh,
+                          const void *v_buffer, int64_t vb_ss, int64_t vb_sh,
+                          const void *v_block_scale, int64_t vbs_ss, int64_t vbs_sh,
+                          int64_t num_slots, const int32_t *kv_indices, int64_t n_rows, int hkv,
+                          int lk, int lv, float k_scale, float v_scale, void *k, int64_t k_ts,
+                          int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, void *stream) {
+  int rc;
+  if ((rc = check_fp4_scales(k_scale, v_scale))) return rc;
+  if (n_rows < 0 || hkv <= 0 || lk <= 0 || lk % 16 || (v && (lv <= 0 || lv % 16)))
+    return set_error(PKX_EINVAL,
+                     "get_kv_buffer_fp4: n_rows >= 0, hkv > 0, lk (and lv) multiples of 16");
+  if (num_slots < 0) return set_error(PKX_EINVAL, "get_kv_buffer_fp4: negative num_slots");
+  if (n_rows == 0) return PKX_OK;
+  if (!kv_indices || !aligned(kv_indices, 4))
+    return set_error(PKX_EINVAL, "get_kv_buffer_fp4: kv_indices null or misaligned");
+  if ((rc = check_rows("k", k, k_ts, k_hs))) return rc;
+  if ((rc = check_fp4_half("k_buffer", k_buffer, kb_ss, kb_sh, k_block_scale, kbs_ss, kbs_sh, 8,
+                           1)))
+    return rc;
+  if (v) {
+    if ((rc = check_rows("v", v, v_ts, v_hs))) return rc;
+    if ((rc = check_fp4_half("v_buffer", v_buffer, vb_ss, vb_sh, v_block_scale, vbs_ss, vbs_sh, 8,
+                             1)))
+      return rc;
+  }
+  return launch_get_kv_buffer_fp4(
+      fp4_pool(k_buffer, k_block_scale, v_buffer, v_block_scale, kb_ss, kb_sh, kbs_ss, kbs_sh,
+               vb_ss, vb_sh, vbs_ss, vbs_sh, num_slots),
+      kv_indices, n_rows, hkv, lk, lv, k_scale, v_scale, k, k_ts, k_hs, v, v_ts, v_hs,
+      static_cast<cudaStream_t>(stream));
+}
+
+size_t pkx_decode_fp4_workspace_size(int batch, int hq, int hkv, int lq, int lv) {
+  if (batch < 0 || hkv <= 0 || hq <= 0 || hq % hkv || hq / hkv > kBlockM || lq != lv ||
+      (lq != 64 && lq != 128))
+    return 0;
+  return fp4_decode_workspace(hq, hkv, lq);
+}
+
+int pkx_decode_attention_fwd_fp4(
+    const void *q, void *o, const void *k_buffer, const void *k_block_scale, const void *v_buffer,
+    const void *v_block_scale, const int32_t *kv_indptr, const int32_t *kv_indices, int batch,
+    int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh, int64_t kbs_ss, int64_t kbs_sh,
+    int64_t vb_ss, int64_t vb_sh, int64_t vbs_ss, int64_t vbs_sh, int64_t num_slots,
+    float sm_scale, float logit_cap, int sliding_window, int first_tokens, float k_scale,
+    float v_scale, float *lse_out, void *workspace, size_t workspace_bytes, void *stream) {
+  Fp4DecodeArgs a{};
+  int rc;
+  a.pool = fp4_pool(k_buffer, k_block_scale, v_buffer, v_block_scale, kb_ss, kb_sh, kbs_ss,
+                    kbs_sh, vb_ss, vb_sh, vbs_ss, vbs_sh, num_slots);
+  if (batch < 0) return set_error(PKX_EINVAL, "negative batch");
+  if ((rc = check_fp4_attention(hq, hkv, lq, lv, k_scale, v_scale))) return rc;
+  if ((rc = check_scalars(sm_scale, logit_cap))) return rc;
+  if (first_tokens < 0) return set_error(PKX_EINVAL, "negative first_tokens");
+  if (batch == 0) return PKX_OK;
+  if ((rc = check_rows("q", q, 8, 8))) return rc;
+  if ((rc = check_rows("o", o, 8, 8))) return rc;
+  if ((rc = check_fp4_attention_rows(a.pool, lq))) return rc;
+  if (!kv_indptr || !aligned(kv_indptr, 4))
+    return set_error(PKX_EINVAL, "kv_indptr null or misaligned");
+  if (kv_indices && !aligned(kv_indices, 4)) return set_error(PKX_EINVAL, "kv_indices misaligned");
+  if (lse_out && !aligned(lse_out, 4)) return set_error(PKX_EINVAL, "lse_out misaligned");
+  a.q = q; a.o = o; a.lse = lse_out;
+  a.kv_indptr = kv_indptr; a.kv_indices = kv_indices;
+  a.batch = batch; a.hq = hq; a.hkv = hkv; a.d = lq;
+  a.sm_scale = sm_scale; a.logit_cap = logit_cap;
+  a.window = sliding_window; a.first_tokens = first_tokens;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_decode_fp4(a);
+}
+
+}  // extern "C"

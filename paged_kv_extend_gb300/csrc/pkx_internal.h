@@ -24,6 +24,14 @@ enum KeyMode : int {
 // Element format of the KV pool (the values of include/pkx.h's PKX_KV_*).
 enum KvFormat : int { kKvBf16 = 0, kKvFp8E4M3 = 1, kKvFp8E5M2 = 2 };
 
+// A 4-bit pool (fp4.cuh): rows of e2m1 codes and of e4m3 block scales, row
+// (slot, head) of each at base + slot * ss + head * sh bytes.
+struct Fp4Pool {
+  uint8_t *k, *ks, *v, *vs;  // codes and block scales of K and of V
+  int64_t k_ss, k_sh, ks_ss, ks_sh, v_ss, v_sh, vs_ss, vs_sh;
+  int64_t num_slots;
+};
+
 // Which keys a two-stage pass attends to (the ragged + paged split runs the
 // extend keys and the prefix keys as two passes and merges them).
 enum KeySet : int {
@@ -175,6 +183,31 @@ int launch_set_kv_buffer_fp8(const void *k, int64_t k_ts, int64_t k_hs, const vo
                              float v_scale, int fmt, void *k_buffer, int64_t kb_ss,
                              int64_t kb_hs, void *v_buffer, int64_t vb_ss, int64_t vb_hs,
                              int64_t num_slots, cudaStream_t s);
+int launch_set_kv_buffer_fp4(const void *k, int64_t k_ts, int64_t k_hs, const void *v,
+                             int64_t v_ts, int64_t v_hs, const int64_t *cache_loc,
+                             int64_t n_tokens, int hkv, int lk, int lv, float k_scale,
+                             float v_scale, const Fp4Pool &pool, cudaStream_t s);
+int launch_get_kv_buffer_fp4(const Fp4Pool &pool, const int32_t *kv_indices, int64_t n_rows,
+                             int hkv, int lk, int lv, float k_scale, float v_scale, void *k,
+                             int64_t k_ts, int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs,
+                             cudaStream_t s);
+// Arguments of one decode call over a 4-bit pool.
+struct Fp4DecodeArgs {
+  const void *q;
+  void *o;
+  float *lse;
+  Fp4Pool pool;
+  const int32_t *kv_indptr, *kv_indices;
+  int batch, hq, hkv, d;
+  float sm_scale, logit_cap;
+  int window, first_tokens;
+  float k_scale, v_scale;
+  void *workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+size_t fp4_decode_workspace(int hq, int hkv, int d);
+int launch_decode_fp4(const Fp4DecodeArgs &a);
 // Largest batch the index gather takes (its running sum lives in 48 KB of
 // shared memory).
 constexpr int kGatherMaxBatch = 12000;

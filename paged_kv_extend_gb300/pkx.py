@@ -83,6 +83,17 @@ _SIGS = {
     "pkx_expand_paged_kv_indices": (_i, [_p, _p, _p, _i, _i, _p, _p, _i64, _p]),
     "pkx_create_kv_indices": (_i, [
         _p, _i64, _i64, _p, _p, _p, _i, _p, _p, _i64, _p]),
+    "pkx_set_kv_buffer_fp4": (_i, [
+        _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i, _i, _i, _f, _f,
+        _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _p]),
+    "pkx_get_kv_buffer_fp4": (_i, [
+        _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64,
+        _p, _i64, _i, _i, _i, _f, _f, _p, _i64, _i64, _p, _i64, _i64, _p]),
+    "pkx_decode_fp4_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "pkx_decode_attention_fwd_fp4": (_i, [
+        _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _i, _f, _f,
+        _p, _p, _sz, _p]),
 }
 
 
@@ -625,3 +636,157 @@ def expand_paged_kv_indices(kv_indptr, kv_indices, kv_last_page_len, page_size,
         _ptr(kv_last_page_len), int(page_size), int(bs), _ptr(token_indptr),
         _ptr(token_indices) if token_indices.numel() else None, token_indices.numel()))
     return token_indptr, token_indices
+
+
+# ------------------------------------------------------------- 4-bit pools
+def _fp4_half(codes, scales, name):
+    """Strides (bytes) of one half of a 4-bit pool: uint8 codes
+    [slots, hkv, d / 2] and float8_e4m3fn block scales [slots, hkv, d / 16]."""
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.stride(2) != 1 or not codes.is_cuda:
+        raise ValueError(f"{name} must be a CUDA uint8 [slots, heads, dim / 2] tensor with a "
+                         "contiguous last dim")
+    if scales.dim() != 3 or scales.dtype != torch.float8_e4m3fn or scales.stride(2) != 1 or \
+            scales.device != codes.device:
+        raise ValueError(f"{name}'s block scales must be a float8_e4m3fn [slots, heads, dim / 16] "
+                         f"tensor on {codes.device} with a contiguous last dim")
+    if scales.shape[:2] != codes.shape[:2] or scales.shape[2] * 8 != codes.shape[2]:
+        raise ValueError(f"{name} [slots, heads, dim / 2] {tuple(codes.shape)} and its block "
+                         f"scales [slots, heads, dim / 16] {tuple(scales.shape)} disagree")
+    return codes.stride(0), codes.stride(1), scales.stride(0), scales.stride(1)
+
+
+def _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale):
+    """Byte strides of both halves, in the order of the attention calls."""
+    k = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+    v = _fp4_half(v_buffer, v_block_scale, "v_buffer")
+    if v_buffer.shape[:2] != k_buffer.shape[:2] or v_buffer.device != k_buffer.device:
+        raise ValueError("k_buffer and v_buffer must have the same slots, heads and device")
+    return *k, *v
+
+
+def _one_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def set_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, cache_loc, k, v=None,
+                      k_scale=1.0, v_scale=1.0):
+    """Quantising KV write into a 4-bit pool (pkx_set_kv_buffer_fp4): k[t] and
+    v[t] (bf16 [n, hkv, d]) at slot cache_loc[t] (int64 [n]), in place.  The
+    pool is uint8 codes [slots, hkv, d / 2] and float8_e4m3fn block scales
+    [slots, hkv, d / 16] for each of K and V; ``v`` None writes K only."""
+    lib = load_library()
+    _i64_vec(cache_loc, "cache_loc")
+    ks = _rows(k, "k")
+    n, hkv, lk = k.shape
+    _check_len(cache_loc, n, "cache_loc")
+    kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+    if k_buffer.shape[1:] != (hkv, lk // 2) or lk % 16:
+        raise ValueError(f"k {tuple(k.shape)} does not fit k_buffer {tuple(k_buffer.shape)}")
+    lv, vs, vb = 0, (0, 0), (0, 0, 0, 0)
+    if v is not None:
+        vs = _rows(v, "v")
+        lv = v.shape[2]
+        _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+        vb = _fp4_half(v_buffer, v_block_scale, "v_buffer")
+        if v.shape[:2] != (n, hkv) or v_buffer.shape[2] != lv // 2 or lv % 16:
+            raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)} and v_buffer "
+                             f"{tuple(v_buffer.shape)}")
+    _one_device(k.device, k_buffer=k_buffer, cache_loc=cache_loc, v=v)
+    _check(_on(
+        k.device, lib.pkx_set_kv_buffer_fp4,
+        _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _ptr(cache_loc) if n else None, n, hkv,
+        lk, lv, float(k_scale), float(v_scale), _ptr(k_buffer), kb[0], kb[1],
+        _ptr(k_block_scale), kb[2], kb[3], _ptr(v_buffer) if v is not None else None, vb[0], vb[1],
+        _ptr(v_block_scale) if v is not None else None, vb[2], vb[3], k_buffer.shape[0]))
+    return k_buffer, k_block_scale, v_buffer, v_block_scale
+
+
+def get_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, kv_indices, k_scale=1.0,
+                      v_scale=1.0, k_out=None, v_out=None):
+    """Rows kv_indices (int32 [n]) of a 4-bit pool as bf16
+    (pkx_get_kv_buffer_fp4).  Returns (k [n, hkv, dk], v [n, hkv, dv]), written
+    into ``k_out`` / ``v_out`` where given; ``v_buffer`` None reads K only."""
+    lib = load_library()
+    _i32(kv_indices, "kv_indices")
+    kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+    n, dev = kv_indices.numel(), k_buffer.device
+    slots, hkv, lk = k_buffer.shape[0], k_buffer.shape[1], 2 * k_buffer.shape[2]
+    lv, vb, vs = 0, (0, 0, 0, 0), (0, 0)
+    if k_out is None:
+        k_out = torch.empty(n, hkv, lk, dtype=torch.bfloat16, device=dev)
+    ks = _rows(k_out, "k_out")
+    if tuple(k_out.shape) != (n, hkv, lk):
+        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {(n, hkv, lk)}")
+    if v_buffer is not None:
+        _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+        vb = _fp4_half(v_buffer, v_block_scale, "v_buffer")
+        lv = 2 * v_buffer.shape[2]
+        if v_out is None:
+            v_out = torch.empty(n, hkv, lv, dtype=torch.bfloat16, device=dev)
+        vs = _rows(v_out, "v_out")
+        if tuple(v_out.shape) != (n, hkv, lv):
+            raise ValueError(f"v_out has shape {tuple(v_out.shape)}, expected {(n, hkv, lv)}")
+    elif v_out is not None:
+        raise ValueError("v_out needs v_buffer")
+    _one_device(dev, kv_indices=kv_indices, k_out=k_out, v_out=v_out)
+    _check(_on(
+        dev, lib.pkx_get_kv_buffer_fp4,
+        _ptr(k_buffer), kb[0], kb[1], _ptr(k_block_scale), kb[2], kb[3],
+        _ptr(v_buffer), vb[0], vb[1], _ptr(v_block_scale) if v_buffer is not None else None, vb[2],
+        vb[3], slots, _ptr(kv_indices) if n else None, n, hkv, lk, lv, float(k_scale),
+        float(v_scale), _ptr(k_out), ks[0], ks[1], _ptr(v_out), vs[0], vs[1]))
+    return k_out, v_out
+
+
+def decode_fp4_workspace_size(batch, hq, hkv, lq, lv) -> int:
+    return int(load_library().pkx_decode_fp4_workspace_size(batch, hq, hkv, lq, lv))
+
+
+def _check_fp4_attn(q, o, lse, k_buffer, v_buffer):
+    """Shape checks of an attention call over a 4-bit pool; (tokens, hq, hkv, lq, lv)."""
+    if q.dim() != 3 or o.dim() != 3:
+        raise ValueError("q and o must be [tokens, heads, dim]")
+    n, hq, lq = q.shape
+    hkv, lv = k_buffer.shape[1], 2 * v_buffer.shape[2]
+    for t, nm in ((q, "q"), (o, "o")):
+        if not t.is_contiguous() or t.dtype != torch.bfloat16:
+            raise ValueError(f"{nm} must be a contiguous bf16 [tokens, heads, dim] tensor")
+    if tuple(o.shape) != (n, hq, lv):
+        raise ValueError(f"o has shape {tuple(o.shape)}, expected {(n, hq, lv)}")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            tuple(lse.shape) != (n, hq)):
+        raise ValueError(f"lse must be a contiguous float32 [{n}, {hq}] tensor")
+    if 2 * k_buffer.shape[2] != lq:
+        raise ValueError(f"k_buffer holds rows of {2 * k_buffer.shape[2]} elements, q of {lq}")
+    return n, hq, hkv, lq, lv
+
+
+def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_scale, kv_indptr,
+                             kv_indices, sm_scale=None, logit_cap=0.0, sliding_window=-1,
+                             first_tokens=0, lse=None, workspace=None, k_scale=1.0, v_scale=1.0):
+    """Decode attention over a 4-bit pool (pkx_decode_attention_fwd_fp4): q
+    [B, Hq, D] -> o, D = 64 or 128.  With a sliding window the first
+    ``first_tokens`` keys of each sequence stay visible.  Returns the
+    workspace."""
+    lib = load_library()
+    strides = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+    b, hq, hkv, lq, lv = _check_fp4_attn(q, o, lse, k_buffer, v_buffer)
+    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
+    _check_len(kv_indptr, b + 1, "kv_indptr")
+    _one_device(q.device, o=o, k_buffer=k_buffer, kv_indptr=kv_indptr, kv_indices=kv_indices,
+                lse=lse, workspace=workspace)
+    ws = workspace
+    if ws is None:
+        with torch.cuda.device(q.device):
+            size = decode_fp4_workspace_size(b, hq, hkv, lq, lv)
+        ws = _workspace(None, size, q.device)
+    _check(_on(
+        q.device, lib.pkx_decode_attention_fwd_fp4,
+        _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(k_block_scale), _ptr(v_buffer),
+        _ptr(v_block_scale), _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, b,
+        hq, hkv, lq, lv, *strides, k_buffer.shape[0], float(sm_scale or 0.0),
+        float(logit_cap or 0.0), int(sliding_window), int(first_tokens), float(k_scale),
+        float(v_scale), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
+    return ws
