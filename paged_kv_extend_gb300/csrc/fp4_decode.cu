@@ -55,8 +55,8 @@ namespace pkx {
 constexpr int kTile = 32;          // keys of a tile
 constexpr int kMinShareTiles = 2;  // tiles a share holds at least, where there are enough
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-// the codes carry 2^-14 and the scales 2^7: an element is code * scale * 2^-7
-constexpr float kElemUp = 128.0f;
+// elements converted by bits carry 2^-14 (fp4.cuh)
+constexpr float kBitsUp = 16384.0f;
 
 template <int D, int NT>  // head dim; column tiles of eight query heads
 struct DecCfg {
@@ -67,7 +67,10 @@ struct DecCfg {
   static constexpr int OFF_VS = OFF_KS + kTile * SROW;
   static constexpr int STAGE = OFF_VS + kTile * SROW;
   static constexpr int STAGES = (NT == 1 ? 3 : 6) * (D == 64 ? 2 : 1);
-  static constexpr int SMEM = WARPS * STAGES * STAGE;
+  // a warp's ring; the odd 64 bytes put neighbouring heads' rows, which one
+  // copy instruction writes, in different halves of the banks
+  static constexpr int RING = STAGES * STAGE + 64;
+  static constexpr int SMEM = WARPS * RING;
   static_assert(SMEM <= 226 * 1024, "shared memory budget");
 };
 
@@ -78,7 +81,7 @@ struct Fp4DecParams {
   const uint8_t *k, *ks, *v, *vs;
   uint32_t k_ss, ks_ss, v_ss, vs_ss;  // slot strides, bytes
   int64_t k_sh, ks_sh, v_sh, vs_sh;   // head strides, bytes
-  int64_t num_slots;
+  uint32_t num_slots;
   const int32_t *kv_indptr, *kv_indices;
   int batch, hq, hkv, group;
   int window, first;
@@ -87,11 +90,12 @@ struct Fp4DecParams {
   int head_groups;  // CTAs that share one set of shares
   int streams;      // shares a CTA works on
   int max_shares;
-  float scale_log2;  // sm_scale * log2 e * k_scale * 2^7
-  float cap_pre, cap_log2;  // sm_scale * k_scale * 2^7 / cap; cap * log2 e
+  float scale_log2;  // sm_scale * log2 e * k_scale
+  float cap_pre, cap_log2;  // sm_scale * k_scale / cap; cap * log2 e
   int use_cap;
-  float v_scale;     // v_scale * 2^7
-  int32_t *cta_err;  // [grid]
+  float v_scale;
+  uint64_t wait_ns;  // time limit of every bounded wait
+  int32_t *cta_err;  // [grid] status of each CTA
   int2 *entries;     // [max_shares] (sequence, parts) of the sequence split from this share on
   float *plse, *po;  // [2 max_shares][hq], [2 max_shares][hq][D]
 };
@@ -135,6 +139,32 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, ui
                : "memory");
 }
 
+// A word of a key's codes as the four f16 pairs of the QK product: elements
+// (0, 1) and (4, 5) by the converter, (2, 6) and (3, 7) by bits, times 2^-14.
+__device__ __forceinline__ void key_pairs(uint32_t x, uint32_t (&out)[4]) {
+  out[0] = e2m1x2_convert(x);
+  out[1] = e2m1x2_convert(x >> 16);
+  out[2] = e2m1_bits<2>(x);
+  out[3] = e2m1_bits<3>(x);
+}
+
+// The same word of two keys' codes as (key a, key b) pairs of its eight dims:
+// the even dims by the converter, whose bytes take one code of each key, the
+// odd dims by bits, times 2^-14.
+__device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t (&lo)[4],
+                                            uint32_t (&hi)[4]) {
+  const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+  lo[0] = e2m1x2_convert(even);
+  lo[2] = e2m1x2_convert(even >> 8);
+  hi[0] = e2m1x2_convert(even >> 16);
+  hi[2] = e2m1x2_convert(even >> 24);
+  const uint32_t w0 = __byte_perm(a, b, 0x5410), w1 = __byte_perm(a, b, 0x7632);
+  lo[1] = e2m1_bits<1>(w0);
+  lo[3] = e2m1_bits<3>(w0);
+  hi[1] = e2m1_bits<1>(w1);
+  hi[3] = e2m1_bits<3>(w1);
+}
+
 // The share that holds tile t when `shares` equal ones hold `tiles`: share w
 // begins at tile floor(w tiles / shares).
 __device__ __forceinline__ int share_of(int64_t t, int64_t tiles, int64_t shares) {
@@ -151,10 +181,19 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_warp[32];
   __shared__ int s_seq[C::WARPS], s_tile0[C::WARPS];  // per stream: first sequence, its first tile
-  __shared__ int s_err;
+  __shared__ int s_err, s_abort;
+  __shared__ uint64_t s_full[C::WARPS][C::STAGES], s_empty[C::WARPS][C::STAGES];  // [stream]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  if (tid == 0) s_err = 0;
+  const int cta_set = blockIdx.x / p.head_groups, hg = blockIdx.x - cta_set * p.head_groups;
+  // (KV head, column tile) pairs of this CTA: the warps of a stream
+  const int heads = min(p.cta_heads, p.hkv * p.head_tiles - hg * p.cta_heads);
+  if (tid == 0) s_err = s_abort = 0;
+  for (int i = tid; i < p.streams * C::STAGES; i += C::THREADS) {
+    mbar_init(&s_full[i / C::STAGES][i % C::STAGES], heads * 32);
+    mbar_init(&s_empty[i / C::STAGES][i % C::STAGES], heads);
+  }
+  fence_barrier_init();
   grid_dep_wait();
   grid_dep_launch();
 
@@ -184,7 +223,6 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
   }
   const int excl = before + incl - mine;
   const int shares = min(p.max_shares, (tiles + kMinShareTiles - 1) / kMinShareTiles);
-  const int cta_set = blockIdx.x / p.head_groups, hg = blockIdx.x - cta_set * p.head_groups;
   for (int st = 0; st < p.streams; ++st) {
     const int w = cta_set * p.streams + st;
     if (w >= shares) break;
@@ -218,63 +256,83 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
   const int stream = warp / p.cta_heads, head_slot = warp - stream * p.cta_heads;
   const int vh = hg * p.cta_heads + head_slot;
   const int share = cta_set * p.streams + stream;
-  if (stream < p.streams && vh < p.hkv * p.head_tiles && share < p.max_shares) {
+  if (stream < p.streams && head_slot < heads && share < p.max_shares) {
     const int kvh = vh / p.head_tiles;
     const int head0 = (vh - kvh * p.head_tiles) * (8 * NT);  // first head within the group
     int2 entry = make_int2(0, 0);
     if (share < shares) {
       const int tile_end = (int)((int64_t)(share + 1) * tiles / shares);
       const int tile_beg = (int)((int64_t)share * tiles / shares);
-      const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
+      const uint32_t ring = smem_u32(smem) + warp * C::RING;
+      volatile int *abort_flag = &s_abort;
 
-      // -- copy side: the tile `ctile` of sequence cb, whose tiles begin at cbase
+      // -- copy side: the tile `ctile` of sequence cb, whose tiles begin at
+      // cbase.  The stream's warps copy a tile together, consecutive lanes on
+      // consecutive heads of one slot, so that a slot's row is fetched as one
+      // run: with each warp copying its own head's rows, the warps drifted
+      // apart and 64 x 8192 keys at random slots took 229 us against 139 at
+      // sequential ones.
       int cb = s_seq[stream], cbase = s_tile0[stream], ctile = tile_beg;
       int cgap, cn = visible_keys(p, cb, cgap, bad);
-      const uint8_t *kp = p.k + (int64_t)kvh * p.k_sh, *vp = p.v + (int64_t)kvh * p.v_sh;
-      const uint8_t *ksp = p.ks + (int64_t)kvh * p.ks_sh, *vsp = p.vs + (int64_t)kvh * p.vs_sh;
-      // slot of this lane's key of the next tile, -1 past the end
-      auto fetch_index = [&]() -> int {
-        if (ctile >= tile_end) return -1;
+      const int32_t *cidx = p.kv_indices + __ldg(p.kv_indptr + cb);
+      const int flat = head_slot * 32 + lane;  // lane of the stream
+      constexpr int CPR = C::ROW / 16;         // 16-byte chunks of a row
+      constexpr int NCOPY = CPR;               // rows of K (and of V) a lane copies a chunk of
+      const int chunk = flat % CPR, chead = flat / CPR % heads, ckey = flat / (CPR * heads);
+      const int shead = flat % heads, skey = flat / heads;  // its block scales
+      auto kv_head = [&](int slot) { return (hg * p.cta_heads + slot) / p.head_tiles; };
+      const uint8_t *kp = p.k + kv_head(chead) * p.k_sh + chunk * 16;
+      const uint8_t *vp = p.v + kv_head(chead) * p.v_sh + chunk * 16;
+      const uint8_t *ksp = p.ks + kv_head(shead) * p.ks_sh, *vsp = p.vs + kv_head(shead) * p.vs_sh;
+      // V's chunks swap halves every two rows, so that the four rows of a V
+      // load lie in different banks; a lane's rows are a multiple of 4 apart
+      const int vchunk = D == 128 ? chunk ^ (((ckey >> 1) & 1) << 1) : chunk;
+      const uint32_t ring0 = smem_u32(smem) + stream * p.cta_heads * C::RING;
+      const uint32_t kdst = ring0 + chead * C::RING + ckey * C::ROW + chunk * 16;
+      const uint32_t vdst = ring0 + chead * C::RING + C::OFF_V + ckey * C::ROW + vchunk * 16;
+      const uint32_t sdst = ring0 + shead * C::RING + C::OFF_KS + skey * C::SROW;
+      // this lane's key of the next tile: its slot as it stands in the list
+      // (looked at a tile later, so that no lane waits for the load here),
+      // and whether there is one
+      int next_slot = 0;
+      bool next_have = false;
+      auto fetch_index = [&]() {
+        next_have = false;
+        if (ctile >= tile_end) return;
         while ((ctile - cbase) * kTile >= cn) {  // on to the next sequence with keys
           cbase += (cn + kTile - 1) / kTile;
           cn = visible_keys(p, ++cb, cgap, bad);
+          cidx = p.kv_indices + __ldg(p.kv_indptr + cb);
         }
         const int v = (ctile - cbase) * kTile + lane;
         ++ctile;
-        if (v >= cn) return -1;
-        const int real = v < p.first ? v : v + cgap;
-        const int slot = __ldg(p.kv_indices + __ldg(p.kv_indptr + cb) + real);
-        if (slot < 0 || slot >= p.num_slots) {
-          bad = true;
-          return -1;
-        }
-        return slot;
+        next_have = v < cn;
+        if (next_have) next_slot = __ldg(cidx + (v < p.first ? v : v + cgap));
       };
-      auto copy_tile = [&](int stage, int slot) {
-        const uint32_t dst = ring + stage * C::STAGE;
-        constexpr int CPR = C::ROW / 16, KPI = 32 / CPR;  // chunks a row, keys an instruction
+      auto copy_tile = [&](int stage) {
+        const bool in_pool = (uint32_t)next_slot < p.num_slots;
+        bad |= next_have && !in_pool;
+        const int slot = next_have && in_pool ? next_slot : -1;
 #pragma unroll
-        for (int i = 0; i < kTile / KPI; ++i) {
-          const int key = lane / CPR + i * KPI, c = lane % CPR;
-          const int s = __shfl_sync(0xffffffffu, slot, key);
-          const uint32_t n = s >= 0 ? 16u : 0u;
-          const uint32_t su = (uint32_t)max(s, 0);
-          // V's chunks swap halves every two rows, so that the four rows of a
-          // V load lie in different banks
-          const int cv = D == 128 ? c ^ (((key >> 1) & 1) << 1) : c;
-          cp_async_16(dst + key * C::ROW + c * 16, kp + (uint64_t)su * p.k_ss + c * 16, n);
-          cp_async_16(dst + C::OFF_V + key * C::ROW + cv * 16,
-                      vp + (uint64_t)su * p.v_ss + c * 16, n);
+        for (int i = 0; i < NCOPY; ++i) {
+          const int s = __shfl_sync(0xffffffffu, slot, ckey + i * (kTile / NCOPY));
+          const uint32_t n = s >= 0 ? 16u : 0u, su = (uint32_t)max(s, 0);
+          const uint32_t at = stage * C::STAGE + i * (kTile / NCOPY) * C::ROW;
+          cp_async_16(kdst + at, kp + (uint64_t)su * p.k_ss, n);
+          cp_async_16(vdst + at, vp + (uint64_t)su * p.v_ss, n);
         }
-        const uint32_t su = (uint32_t)max(slot, 0), n = slot >= 0 ? (uint32_t)C::SROW : 0u;
-        cp_async_small<C::SROW>(dst + C::OFF_KS + lane * C::SROW, ksp + (uint64_t)su * p.ks_ss, n);
-        cp_async_small<C::SROW>(dst + C::OFF_VS + lane * C::SROW, vsp + (uint64_t)su * p.vs_ss, n);
+        const int s = __shfl_sync(0xffffffffu, slot, skey);
+        const uint32_t su = (uint32_t)max(s, 0), n = s >= 0 ? (uint32_t)C::SROW : 0u;
+        const uint32_t at = sdst + stage * C::STAGE;
+        cp_async_small<C::SROW>(at, ksp + (uint64_t)su * p.ks_ss, n);
+        cp_async_small<C::SROW>(at + (C::OFF_VS - C::OFF_KS), vsp + (uint64_t)su * p.vs_ss, n);
+        cp_async_arrive_noinc(&s_full[stream][stage]);
       };
-      int next_slot = fetch_index();
-      for (int s = 0; s < C::STAGES - 1; ++s) {
-        copy_tile(s, next_slot);
-        cp_async_commit();
-        next_slot = fetch_index();
+      const int n_tiles = tile_end - tile_beg;
+      fetch_index();
+      for (int s = 0; s < C::STAGES - 1 && s < n_tiles; ++s) {
+        copy_tile(s);
+        fetch_index();
       }
 
       // -- compute side
@@ -293,6 +351,13 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
       const int sblk = D == 128 ? g : g >> 1;  // the scale block of this lane's value dims
 
       int b = s_seq[stream], base = s_tile0[stream], tile = tile_beg, stage = 0;
+      uint32_t round = 0;  // times the ring has gone round
+      bool ok = true;          // warp-uniform: no wait ran out
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.wait_ns));
+        if (!ok) *abort_flag = 1;
+        return ok;
+      };
       while (tile < tile_end) {
         int gap;
         int n = visible_keys(p, b, gap, bad);
@@ -304,10 +369,12 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
         const int piece_end = min(tile_end, base + nt);
         const bool starts = tile == base, ends = piece_end == base + nt;
 
-        // Q^T fragments: f16, each head scaled to a largest element in
-        // [2^14, 2^15) by a power of two that its logit factor takes back, so
-        // that a bf16 query keeps all its bits (elements below 2^-31 of the
-        // largest lose some)
+        // Q^T fragments: f16, each head scaled by a power of two (its logit
+        // factor takes it back) to a largest element in [1, 2) where the keys
+        // are converted by hardware, and 2^14 times that where they are
+        // converted by bits and carry 2^-14, so that a bf16 query keeps its
+        // bits (elements below 2^-17 of the head's largest lose some: 2^-25
+        // of the largest at most)
         uint32_t qf[NT][KW][4];
         float mult[NT][2];  // accumulator -> log2 domain, or -> tanh's argument
 #pragma unroll
@@ -327,24 +394,28 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
           }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          top = max(top, 16u);  // biased exponent of the head's largest element
-          const float down = __uint_as_float((268u - top) << 23);
-          const float up = __uint_as_float((top - 14u) << 23);
+          // biased exponent of the head's largest element (16: far stays finite)
+          top = min(max(top, 16u), 254u);
+          const float down = __uint_as_float(top == 254u ? 0x00400000u : (254u - top) << 23);
+          const float up = __uint_as_float(top << 23);
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // elements i and i + 4 of the word's eight
-              const uint32_t lo = qw[w][i >> 1], hi = qw[w][2 + (i >> 1)];
-              const float a = __uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16);
-              const float e = __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16);
-              qf[c][w][i] = f16_pair(a * down, e * down);
-            }
+            // word x[j] holds elements 2 j and 2 j + 1 of the lane's eight; the
+            // pairs are (0, 1), (4, 5), (2, 6), (3, 7): key_pairs()'s order
+            const uint32_t *x = qw[w];
+            auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
+            auto hi = [](uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); };
+            const float far = down * kBitsUp;
+            qf[c][w][0] = f16_pair(lo(x[0]) * down, hi(x[0]) * down);
+            qf[c][w][1] = f16_pair(lo(x[2]) * down, hi(x[2]) * down);
+            qf[c][w][2] = f16_pair(lo(x[1]) * far, lo(x[3]) * far);
+            qf[c][w][3] = f16_pair(hi(x[1]) * far, hi(x[3]) * far);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // heads 2 t and 2 t + 1 of the accumulators
             const float u = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-            mult[c][j] = (p.use_cap ? p.cap_pre : p.scale_log2) * u;
+            // (never 0, so that a masked logit stays -inf)
+            mult[c][j] = fmaxf((p.use_cap ? p.cap_pre : p.scale_log2) * u, 1e-37f);
           }
         }
 
@@ -360,8 +431,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
         }
 
         for (; tile < piece_end; ++tile) {
-          cp_async_wait_group<C::STAGES - 2>();
-          __syncwarp();
+          if (!wait(&s_full[stream][stage], round & 1u)) break;
           const uint32_t st = ring + stage * C::STAGE;
           // S^T of the tile's two key halves of 16
           float s[2][NT][4];
@@ -382,7 +452,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
                 asm volatile("ld.shared.u16 %0,[%1];"
                              : "=h"(two)
                              : "r"(st + C::OFF_KS + row * C::SROW + t * 2));
-                const __half2 f = __hmul2(e4m3x2_to_f16x2(two), __float2half2_rn(kElemUp));
+                const __half2 f = e4m3x2_to_f16x2(two);
                 const uint32_t u = *reinterpret_cast<const uint32_t *>(&f);
                 sc[r][0] = __byte_perm(u, u, 0x1010);
                 sc[r][1] = __byte_perm(u, u, 0x3232);
@@ -394,8 +464,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
                 asm volatile("ld.shared.u8 %0,[%1];"
                              : "=r"(one)
                              : "r"(st + C::OFF_KS + row * C::SROW + t));
-                const __half2 f =
-                    __hmul2(e4m3x2_to_f16x2(one | (one << 8)), __float2half2_rn(kElemUp));
+                const __half2 f = e4m3x2_to_f16x2(one | (one << 8));
                 sc[r][0] = *reinterpret_cast<const uint32_t *>(&f);
               }
             }
@@ -404,7 +473,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
               uint32_t a[2][4];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                e2m1x8_to_f16_pairs(kw[r][w], a[r]);
+                key_pairs(kw[r][w], a[r]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[r][i] = hmul2_u32(a[r][i], sc[r][w / 2]);
               }
@@ -418,22 +487,34 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
 
           // softmax.  s[kt][c][2 r + j]: key row 8 r + g of half kt, head 2 t + j
           const int left = n - (tile - base) * kTile;  // keys of the tile (32 or fewer)
+          if (p.use_cap) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float &x = s[i >> 2][c][i & 3];
+                x = p.cap_log2 * tanhf(x * mult[c][i & 1]);
+              }
+          }
+          if (left < kTile) {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (kt * 16 + r * 8 + krow >= left) {
+#pragma unroll
+                  for (int c = 0; c < NT; ++c) s[kt][c][2 * r] = s[kt][c][2 * r + 1] = -INFINITY;
+                }
+          }
           bool grow = false;
-          float mx[NT][2];
+          float mx[NT][2], mul[NT][2];
 #pragma unroll
           for (int c = 0; c < NT; ++c) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-#pragma unroll
-              for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  float &x = s[kt][c][2 * r + j];
-                  x *= mult[c][j];
-                  if (p.use_cap) x = p.cap_log2 * tanhf(x);
-                  if (left < kTile && kt * 16 + r * 8 + krow >= left) x = -INFINITY;
-                }
-              mx[c][j] = fmaxf(fmaxf(s[0][c][j], s[0][c][2 + j]), fmaxf(s[1][c][j], s[1][c][2 + j]));
+              mul[c][j] = p.use_cap ? 1.0f : mult[c][j];
+              mx[c][j] = mul[c][j] * fmaxf(fmaxf(s[0][c][j], s[0][c][2 + j]),
+                                           fmaxf(s[1][c][j], s[1][c][2 + j]));
               grow |= mx[c][j] > m[c][j] + 8.0f;
             }
           }
@@ -462,13 +543,13 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
           for (int c = 0; c < NT; ++c) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float mr = m[c][j] == -INFINITY ? 0.f : m[c][j];
+              const float nm = m[c][j] == -INFINITY ? 0.f : -m[c][j];
 #pragma unroll
               for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   float &x = s[kt][c][2 * r + j];
-                  x = ex2_approx(x - mr);
+                  x = ex2_approx(fmaf(x, mul[c][j], nm));
                   l[c][j] += x;
                 }
             }
@@ -499,17 +580,17 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
               uint32_t x, y;
               asm volatile("ld.shared.u8 %0,[%1];" : "=r"(x) : "r"(vst + (r * 8 + va) * C::SROW));
               asm volatile("ld.shared.u8 %0,[%1];" : "=r"(y) : "r"(vst + (r * 8 + vb) * C::SROW));
-              const __half2 f = __hmul2(e4m3x2_to_f16x2(x | (y << 8)), __float2half2_rn(kElemUp));
+              const __half2 f = e4m3x2_to_f16x2(x | (y << 8));
               sc[r] = *reinterpret_cast<const uint32_t *>(&f);
             }
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
-              // lo[r]: dims 0..3 of the word, hi[r]: dims 4..7, as (key va, key vb) pairs
+              // lo[r]: dims 0..3 of the word, hi[r]: dims 4..7, as (key va, key vb)
+              // pairs; odd dims carry 2^-14
               uint32_t lo[2][4], hi[2][4];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                e2m1x8_to_f16_pairs(__byte_perm(wa[r][w], wb[r][w], 0x5410), lo[r]);
-                e2m1x8_to_f16_pairs(__byte_perm(wa[r][w], wb[r][w], 0x7632), hi[r]);
+                value_pairs(wa[r][w], wb[r][w], lo[r], hi[r]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   lo[r][i] = hmul2_u32(lo[r][i], sc[r]);
@@ -524,17 +605,24 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
                           pb[kt][c][1]);
             }
           }
-          // the stage is free: refill it with the tile STAGES - 1 ahead
+          // this warp is done with the stage; refill the one before it with the
+          // tile STAGES - 1 ahead once the stream's other warps are done too
           __syncwarp();
-          {
-            int fill = stage + C::STAGES - 1;
-            if (fill >= C::STAGES) fill -= C::STAGES;
-            copy_tile(fill, next_slot);
-            cp_async_commit();
-            next_slot = fetch_index();
+          if (lane == 0) mbar_arrive(&s_empty[stream][stage]);
+          if (tile + C::STAGES - 1 < tile_end) {
+            const int fill = stage == 0 ? C::STAGES - 1 : stage - 1;
+            if (tile > tile_beg &&
+                !wait(&s_empty[stream][fill], (stage == 0 ? round - 1 : round) & 1u))
+              break;
+            copy_tile(fill);
+            fetch_index();
           }
-          if (++stage == C::STAGES) stage = 0;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            ++round;
+          }
         }
+        if (!ok) break;
 
         // ---- the piece's result.  Lane (g, t) holds dims (D / 8) g + ... of
         // heads 2 t and 2 t + 1
@@ -553,14 +641,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
             if (head >= p.group) continue;
             const int hqi = kvh * p.group + head;
             const float inv = ls == 0.f ? 0.f : p.v_scale / ls;  // a NaN sum stays NaN
+            const float inv_bits = inv * kBitsUp;
             const float lse = ls == 0.f ? -INFINITY : (m[c][j] + __log2f(ls)) * kLn2;
             float x[D / 8];
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                x[8 * w + i] = acc[c][4 * w + i][j] * inv;
-                x[8 * w + 4 + i] = acc[c][4 * w + i][2 + j] * inv;
+                const float f = (i & 1) ? inv_bits : inv;
+                x[8 * w + i] = acc[c][4 * w + i][j] * f;
+                x[8 * w + 4 + i] = acc[c][4 * w + i][2 + j] * f;
               }
             if (whole) {
               uint4 *row = reinterpret_cast<uint4 *>(p.o + ((int64_t)b * p.hq + hqi) * D + g * (D / 8));
@@ -586,7 +676,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) s_err = PKX_EDEVICE;
   __syncthreads();
-  if (tid == 0) p.cta_err[blockIdx.x] = s_err;
+  if (tid == 0) p.cta_err[blockIdx.x] = s_abort ? PKX_ETIMEOUT : s_err;
 }
 
 // Merge of the sequences that several shares hold: part i of entry `share`
@@ -613,10 +703,14 @@ __global__ void __launch_bounds__(kMergeThreads)
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0) {
-    int err = 0;
-    for (int i = threadIdx.x; i < n_err; i += kMergeThreads) err |= cta_err[i];
-    err = __syncthreads_or(err);
-    if (threadIdx.x == 0) hdr->status = err ? PKX_EDEVICE : PKX_OK;
+    bool late = false, bad = false;
+    for (int i = threadIdx.x; i < n_err; i += kMergeThreads) {
+      late |= cta_err[i] == PKX_ETIMEOUT;
+      bad |= cta_err[i] == PKX_EDEVICE;
+    }
+    late = __syncthreads_or(late);
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) hdr->status = late ? PKX_ETIMEOUT : bad ? PKX_EDEVICE : PKX_OK;
   }
   // parts [i0, n) by step: running maximum, sum and weighted sum of one row
   auto gather = [&](int share, int h, int i0, int n, int step, float &m, float &l, float (&a)[E]) {
@@ -776,7 +870,7 @@ int launch_decode_fp4(const Fp4DecodeArgs &a) {
   p.k_ss = (uint32_t)a.pool.k_ss; p.ks_ss = (uint32_t)a.pool.ks_ss;
   p.v_ss = (uint32_t)a.pool.v_ss; p.vs_ss = (uint32_t)a.pool.vs_ss;
   p.k_sh = a.pool.k_sh; p.ks_sh = a.pool.ks_sh; p.v_sh = a.pool.v_sh; p.vs_sh = a.pool.vs_sh;
-  p.num_slots = a.pool.num_slots;
+  p.num_slots = (uint32_t)a.pool.num_slots;
   p.kv_indptr = a.kv_indptr;
   p.kv_indices = a.kv_indices;
   p.batch = a.batch; p.hq = a.hq; p.hkv = a.hkv; p.group = a.hq / a.hkv;
@@ -788,11 +882,13 @@ int launch_decode_fp4(const Fp4DecodeArgs &a) {
   p.streams = P.streams;
   p.max_shares = P.max_shares;
   const float sm_scale = (a.sm_scale > 0.f ? a.sm_scale : 1.0f / sqrtf((float)a.d)) * a.k_scale;
-  p.scale_log2 = sm_scale * kLog2e * kElemUp;
+  p.scale_log2 = sm_scale * kLog2e;
   p.use_cap = a.logit_cap > 0.f;
-  p.cap_pre = p.use_cap ? sm_scale * kElemUp / a.logit_cap : 0.f;
+  p.cap_pre = p.use_cap ? sm_scale / a.logit_cap : 0.f;
   p.cap_log2 = p.use_cap ? a.logit_cap * kLog2e : 0.f;
-  p.v_scale = a.v_scale * kElemUp;
+  p.v_scale = a.v_scale;
+  int stall;
+  wait_settings(&p.wait_ns, &stall);
   p.cta_err = reinterpret_cast<int32_t *>(ws + L.err);
   p.entries = reinterpret_cast<int2 *>(ws + L.entries);
   p.plse = reinterpret_cast<float *>(ws + L.plse);

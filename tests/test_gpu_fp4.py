@@ -211,6 +211,14 @@ def test_decode_query_range(qamp):
     R.check(o, lse, c.reference(), 128, c.scale, F16_STEP)
 
 
+def test_decode_query_of_the_largest_exponent():
+    c = Decode(128, 8, 2, [70, 9], seed=12)
+    c.q[0, 3, 5], c.q[1, 7, 64], c.q[1, 7, 66] = 3.2e38, -2.5e38, 1e36
+    c.scale = 2e-38
+    o, lse, _ = c.run()
+    R.check(o, lse, c.reference(), 128, c.scale, F16_STEP)
+
+
 def test_decode_zero_query_and_zero_pool():
     """All logits 0: the mean of the values; a pool of zeros gives zeros."""
     c = Decode(128, 8, 2, [100, 33], seed=6)
