@@ -12,7 +12,6 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 namespace pkx {
@@ -25,39 +24,21 @@ __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t two) {
   return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
 }
 
-// An e2m1 code becomes f16 in one of two ways.
-//  * By bits: the sign to bit 15 and the three magnitude bits to bits 11..9
-//    (the low exponent bits and the top mantissa bit), which is the value
-//    times 2^-14, the subnormal 0.5 included: three or four integer
-//    operations for a pair, one code in each half of the word.
-//  * By the hardware's converter, which takes the two codes of a byte: one
-//    instruction, but it issues once in about nine clocks a quarter SM.
-// Measured on its own with the block scale and the product behind it
-// (elements a clock and SM; the copy bandwidth delivers 41): 38.5 all by bits,
-// 44.1 with two of a word's four pairs by the converter, 39.6 all by it.
-
-// Code i of each 16-bit half of x (i = 0..3) as a pair of f16 times 2^-14.
-template <int I>
-__device__ __forceinline__ uint32_t e2m1_bits(uint32_t x) {
-  constexpr uint32_t S = 0x80008000u, M = 0x0E000E00u;
-  if constexpr (I == 3) return (x & S) | ((x >> 3) & M);
-  else return ((x << (12 - 4 * I)) & S) | ((x << (9 - 4 * I)) & M);
-}
-
-// Eight e2m1 codes of a word as four f16 pairs times 2^-14: out[i] holds
-// element i in its low half and element i + 4 in its high half.
-__device__ __forceinline__ void e2m1x8_to_f16_pairs(uint32_t x, uint32_t (&out)[4]) {
-  out[0] = e2m1_bits<0>(x);
-  out[1] = e2m1_bits<1>(x);
-  out[2] = e2m1_bits<2>(x);
-  out[3] = e2m1_bits<3>(x);
-}
-
-// The two e2m1 codes of x's low byte as a pair of f16 (low nibble in the low half).
-__device__ __forceinline__ uint32_t e2m1x2_convert(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(x));
-  return r;
+// The eight e2m1 codes of a word as four f16 pairs (out[i]: the codes of byte
+// i, low nibble in the low half), by the hardware's converter.  Spreading the
+// codes' bits by hand (sign to bit 15, magnitude to bits 11..9: the value
+// times 2^-14) takes four integer operations a pair; decode over 64 x 8192
+// keys ran in 162 us with that, 149 us with half of each and 138 us with the
+// converter alone.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t x, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(x));
 }
 
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {

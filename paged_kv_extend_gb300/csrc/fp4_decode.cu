@@ -53,10 +53,7 @@
 namespace pkx {
 
 constexpr int kTile = 32;          // keys of a tile
-constexpr int kMinShareTiles = 2;  // tiles a share holds at least, where there are enough
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-// elements converted by bits carry 2^-14 (fp4.cuh)
-constexpr float kBitsUp = 16384.0f;
 
 template <int D, int NT>  // head dim; column tiles of eight query heads
 struct DecCfg {
@@ -139,30 +136,12 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, ui
                : "memory");
 }
 
-// A word of a key's codes as the four f16 pairs of the QK product: elements
-// (0, 1) and (4, 5) by the converter, (2, 6) and (3, 7) by bits, times 2^-14.
-__device__ __forceinline__ void key_pairs(uint32_t x, uint32_t (&out)[4]) {
-  out[0] = e2m1x2_convert(x);
-  out[1] = e2m1x2_convert(x >> 16);
-  out[2] = e2m1_bits<2>(x);
-  out[3] = e2m1_bits<3>(x);
-}
-
-// The same word of two keys' codes as (key a, key b) pairs of its eight dims:
-// the even dims by the converter, whose bytes take one code of each key, the
-// odd dims by bits, times 2^-14.
-__device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t (&lo)[4],
-                                            uint32_t (&hi)[4]) {
-  const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-  lo[0] = e2m1x2_convert(even);
-  lo[2] = e2m1x2_convert(even >> 8);
-  hi[0] = e2m1x2_convert(even >> 16);
-  hi[2] = e2m1x2_convert(even >> 24);
-  const uint32_t w0 = __byte_perm(a, b, 0x5410), w1 = __byte_perm(a, b, 0x7632);
-  lo[1] = e2m1_bits<1>(w0);
-  lo[3] = e2m1_bits<3>(w0);
-  hi[1] = e2m1_bits<1>(w1);
-  hi[3] = e2m1_bits<3>(w1);
+// A word of eight dims' codes of two keys as (key a, key b) f16 pairs of each
+// dim: each byte that goes to the converter holds one code of each key.
+__device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t (&even)[4],
+                                            uint32_t (&odd)[4]) {
+  e2m1x8_to_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even);
+  e2m1x8_to_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd);
 }
 
 // The share that holds tile t when `shares` equal ones hold `tiles`: share w
@@ -222,7 +201,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
     tiles += x;
   }
   const int excl = before + incl - mine;
-  const int shares = min(p.max_shares, (tiles + kMinShareTiles - 1) / kMinShareTiles);
+  const int shares = min(p.max_shares, tiles);
   for (int st = 0; st < p.streams; ++st) {
     const int w = cta_set * p.streams + st;
     if (w >= shares) break;
@@ -370,11 +349,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
         const bool starts = tile == base, ends = piece_end == base + nt;
 
         // Q^T fragments: f16, each head scaled by a power of two (its logit
-        // factor takes it back) to a largest element in [1, 2) where the keys
-        // are converted by hardware, and 2^14 times that where they are
-        // converted by bits and carry 2^-14, so that a bf16 query keeps its
-        // bits (elements below 2^-17 of the head's largest lose some: 2^-25
-        // of the largest at most)
+        // factor takes it back) to a largest element in [2^14, 2^15), so that
+        // a bf16 query keeps its bits (elements below 2^-31 of the head's
+        // largest lose some)
         uint32_t qf[NT][KW][4];
         float mult[NT][2];  // accumulator -> log2 domain, or -> tanh's argument
 #pragma unroll
@@ -394,22 +371,15 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
           }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // biased exponent of the head's largest element (16: far stays finite)
-          top = min(max(top, 16u), 254u);
-          const float down = __uint_as_float(top == 254u ? 0x00400000u : (254u - top) << 23);
-          const float up = __uint_as_float(top << 23);
+          top = min(max(top, 15u), 254u);  // biased exponent of the head's largest element
+          const float down = __uint_as_float((268u - top) << 23);
+          const float up = __uint_as_float((top - 14u) << 23);
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
-            // word x[j] holds elements 2 j and 2 j + 1 of the lane's eight; the
-            // pairs are (0, 1), (4, 5), (2, 6), (3, 7): key_pairs()'s order
-            const uint32_t *x = qw[w];
-            auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
-            auto hi = [](uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); };
-            const float far = down * kBitsUp;
-            qf[c][w][0] = f16_pair(lo(x[0]) * down, hi(x[0]) * down);
-            qf[c][w][1] = f16_pair(lo(x[2]) * down, hi(x[2]) * down);
-            qf[c][w][2] = f16_pair(lo(x[1]) * far, lo(x[3]) * far);
-            qf[c][w][3] = f16_pair(hi(x[1]) * far, hi(x[3]) * far);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // elements 2 i and 2 i + 1 of the word's eight
+              qf[c][w][i] = f16_pair(__uint_as_float(qw[w][i] << 16) * down,
+                                     __uint_as_float(qw[w][i] & 0xFFFF0000u) * down);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // heads 2 t and 2 t + 1 of the accumulators
@@ -473,7 +443,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
               uint32_t a[2][4];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                key_pairs(kw[r][w], a[r]);
+                e2m1x8_to_f16(kw[r][w], a[r]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[r][i] = hmul2_u32(a[r][i], sc[r][w / 2]);
               }
@@ -585,24 +555,23 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
             }
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
-              // lo[r]: dims 0..3 of the word, hi[r]: dims 4..7, as (key va, key vb)
-              // pairs; odd dims carry 2^-14
-              uint32_t lo[2][4], hi[2][4];
+              // row g of tile 4 w + i is dim 2 i of the word, row g + 8 dim 2 i + 1
+              uint32_t even[2][4], odd[2][4];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                value_pairs(wa[r][w], wb[r][w], lo[r], hi[r]);
+                value_pairs(wa[r][w], wb[r][w], even[r], odd[r]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  lo[r][i] = hmul2_u32(lo[r][i], sc[r]);
-                  hi[r][i] = hmul2_u32(hi[r][i], sc[r]);
+                  even[r][i] = hmul2_u32(even[r][i], sc[r]);
+                  odd[r][i] = hmul2_u32(odd[r][i], sc[r]);
                 }
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
-                  mma_f16(acc[c][4 * w + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pb[kt][c][0],
-                          pb[kt][c][1]);
+                  mma_f16(acc[c][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i],
+                          pb[kt][c][0], pb[kt][c][1]);
             }
           }
           // this warp is done with the stage; refill the one before it with the
@@ -641,16 +610,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
             if (head >= p.group) continue;
             const int hqi = kvh * p.group + head;
             const float inv = ls == 0.f ? 0.f : p.v_scale / ls;  // a NaN sum stays NaN
-            const float inv_bits = inv * kBitsUp;
             const float lse = ls == 0.f ? -INFINITY : (m[c][j] + __log2f(ls)) * kLn2;
             float x[D / 8];
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float f = (i & 1) ? inv_bits : inv;
-                x[8 * w + i] = acc[c][4 * w + i][j] * f;
-                x[8 * w + 4 + i] = acc[c][4 * w + i][2 + j] * f;
+                x[8 * w + 2 * i] = acc[c][4 * w + i][j] * inv;
+                x[8 * w + 2 * i + 1] = acc[c][4 * w + i][2 + j] * inv;
               }
             if (whole) {
               uint4 *row = reinterpret_cast<uint4 *>(p.o + ((int64_t)b * p.hq + hqi) * D + g * (D / 8));
@@ -683,7 +650,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
 // lies in slot 2 share + 1 (i = 0) or 2 (share + i).  lse = log sum exp lse_i,
 // o = sum exp(lse_i - lse) o_i.  Few parts: a warp a row; many (a long
 // sequence over the whole device): a CTA a row, its warps taking every eighth
-// part, because one warp's chain of loads over 300 parts took 28 us.
+// part.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeWarpParts = 32;
 // Sequences of more than kMergeWarpParts parts: n parts take n - 1 share
@@ -718,19 +685,45 @@ __global__ void __launch_bounds__(kMergeThreads)
     l = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
-    for (int i = i0; i < n; i += step) {
-      const int64_t row = (i == 0 ? 2 * (int64_t)share + 1 : 2 * ((int64_t)share + i)) * hq + h;
-      const float pl = plse[row];
-      float x[E];
+    // eight parts' loads go out together: one at a time, a row of 300 parts
+    // was a chain of 38 loads a warp (16 us)
+    constexpr int U = 8;
+    for (int i = i0; i < n; i += step * U) {
+      float pl[U], x[U][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = po[row * D + lane * E + e];
-      const float mn = fmaxf(m, pl);
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u * step;
+        pl[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+        if (k < n) {
+          const int64_t row = (k == 0 ? 2 * (int64_t)share + 1 : 2 * ((int64_t)share + k)) * hq + h;
+          pl[u] = __ldcg(plse + row);
+          if constexpr (E == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(po + row * D) + lane);
+            x[u][0] = f.x; x[u][1] = f.y; x[u][2] = f.z; x[u][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2 *>(po + row * D) + lane);
+            x[u][0] = f.x; x[u][1] = f.y;
+          }
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, pl[u]);
       const float mr = mn == -INFINITY ? 0.f : mn;
-      const float wo = ex2_approx((m - mr) * kLog2e), wn = ex2_approx((pl - mr) * kLog2e);
+      const float wo = ex2_approx((m - mr) * kLog2e);
       m = mn;
-      l = l * wo + wn;
+      l *= wo;
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = a[e] * wo + wn * x[e];
+      for (int e = 0; e < E; ++e) a[e] *= wo;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2_approx((pl[u] - mr) * kLog2e);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] += w * x[u][e];
+      }
     }
   };
   auto store = [&](int b, int h, float m, float l, const float (&a)[E]) {

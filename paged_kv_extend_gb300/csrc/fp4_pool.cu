@@ -217,17 +217,15 @@ __global__ void __launch_bounds__(kFp4Threads) get_kv_buffer_fp4_kernel(const Fp
 #pragma unroll
     for (int u = 0; u < kReadUnroll; ++u) {
       if (!dst[u]) continue;
+      const float s = __low2float(e4m3x2_to_f16x2(sc[u]));
       uint32_t h[4];
-      e2m1x8_to_f16_pairs(code[u], h);
-      // code * 2^-14 times block_scale * 2^14: both factors and the product
-      // are exact in fp32
-      const float s = __low2float(e4m3x2_to_f16x2(sc[u])) * 16384.0f;
+      e2m1x8_to_f16(code[u], h);
       float x[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-        x[i] = f.x * s * ts[u];
-        x[i + 4] = f.y * s * ts[u];
+        x[2 * i] = f.x * s * ts[u];  // the first product is exact
+        x[2 * i + 1] = f.y * s * ts[u];
       }
       *dst[u] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                            pack_bf16(x[6], x[7]));
