@@ -576,6 +576,59 @@ int pkx_decode_attention_fwd_fp4(
     int first_tokens, float k_scale, float v_scale, float *lse_out,
     void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Extend attention, two-stage form, with the prefix in a 4-bit pool:
+ * pkx_extend_attention_fwd for (lq, lv) = (64, 64) and (128, 128), the prefix
+ * keys and values read from the pool above (k_scale and v_scale apply to them
+ * alone; k_extend / v_extend stay bf16).  With sliding_window W > 0, key j is
+ * visible to the query at position P iff j <= P and (P - j <= W or
+ * j < first_tokens).  first_tokens with a window and a custom mask together
+ * return PKX_EUNSUPPORTED.
+ *   workspace >= pkx_extend_workspace_size(...) bytes
+ */
+int pkx_extend_attention_fwd_fp4(
+    const void *q_extend, const void *k_extend, const void *v_extend,
+    void *o_extend, const void *k_buffer, const void *k_block_scale,
+    const void *v_buffer, const void *v_block_scale, const int32_t *qo_indptr,
+    const int32_t *kv_indptr, const int32_t *kv_indices, int batch,
+    int num_q_tokens, int hq, int hkv, int lq, int lv, int64_t ke_st,
+    int64_t ke_sh, int64_t ve_st, int64_t ve_sh, int64_t kb_ss, int64_t kb_sh,
+    int64_t kbs_ss, int64_t kbs_sh, int64_t vb_ss, int64_t vb_sh,
+    int64_t vbs_ss, int64_t vbs_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int sliding_window, int first_tokens,
+    const uint8_t *custom_mask, const int32_t *mask_indptr, const float *sinks,
+    float k_scale, float v_scale, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/*
+ * The streaming window over a bf16 pool: pkx_extend_attention_fwd and
+ * pkx_decode_attention_fwd with a sliding window before which the first
+ * tokens of every sequence stay visible.  Key j is visible to the query at
+ * position P (P_b + i in extend, T_b - 1 in decode) iff j <= P and
+ * (P - j <= sliding_window or j < first_tokens).  The keys between the first
+ * tokens and a query block's window are not read.  first_tokens >= 0, without
+ * effect when sliding_window <= 0.  For (lq, lv) = (64, 64) and (128, 128);
+ * other arguments and the workspaces as in those calls (no custom mask, no
+ * fp8 pool; the extend form takes sinks).
+ */
+int pkx_extend_attention_fwd_streaming(
+    const void *q_extend, const void *k_extend, const void *v_extend,
+    void *o_extend, const void *k_buffer, const void *v_buffer,
+    const int32_t *qo_indptr, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int batch, int num_q_tokens, int hq, int hkv,
+    int lq, int lv, int64_t ke_st, int64_t ke_sh, int64_t ve_st,
+    int64_t ve_sh, int64_t kb_ss, int64_t kb_sh, int64_t vb_ss, int64_t vb_sh,
+    int64_t num_slots, float sm_scale, float logit_cap, int sliding_window,
+    int first_tokens, const float *sinks, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream);
+int pkx_decode_attention_fwd_streaming(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer,
+    const int32_t *kv_indptr, const int32_t *kv_indices, int batch, int hq,
+    int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh, int64_t vb_ss,
+    int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap,
+    int sliding_window, int first_tokens, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

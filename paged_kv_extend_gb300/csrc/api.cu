@@ -198,6 +198,50 @@ static int two_stage_args(AttnArgs &a, const void *q_extend, const void *k_exten
   return PKX_OK;
 }
 
+// Validation and argument packing shared by the decode entry points.
+static int decode_args(AttnArgs &a, const void *q, void *o, const void *k_buffer,
+                       const void *v_buffer, const int32_t *kv_indptr, const int32_t *kv_indices,
+                       int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
+                       int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+                       float logit_cap, int sliding_window, int kv_dtype, float k_scale,
+                       float v_scale, float *lse_out, bool *nothing_to_do) {
+  int rc;
+  *nothing_to_do = false;
+  if (batch < 0) return set_error(PKX_EINVAL, "negative batch");
+  if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
+  if ((rc = check_scalars(sm_scale, logit_cap))) return rc;
+  if ((rc = check_kv_format(kv_dtype, k_scale, v_scale, lq, lv, true))) return rc;
+  if (batch == 0) {
+    *nothing_to_do = true;
+    return PKX_OK;
+  }
+  if ((rc = check_rows("q", q, 8, 8))) return rc;
+  if ((rc = check_rows("o", o, 8, 8))) return rc;
+  if ((rc = check_rows("k_buffer", k_buffer, kb_ss, kb_sh))) return rc;
+  if ((rc = check_rows("v_buffer", v_buffer, vb_ss, vb_sh))) return rc;
+  if (!kv_indptr || !aligned(kv_indptr, 4))
+    return set_error(PKX_EINVAL, "kv_indptr null or misaligned");
+  if (kv_indices && !aligned(kv_indices, 4)) return set_error(PKX_EINVAL, "kv_indices misaligned");
+  if (lse_out && !aligned(lse_out, 4)) return set_error(PKX_EINVAL, "lse_out misaligned");
+  if (num_slots <= 0) return set_error(PKX_EINVAL, "num_slots must be positive");
+  a.mode = kDecode;
+  a.q = q;
+  a.o = o;
+  a.lse = lse_out;
+  a.k_buf = k_buffer;
+  a.v_buf = v_buffer;
+  a.kb_ss = kb_ss; a.kb_sh = kb_sh; a.vb_ss = vb_ss; a.vb_sh = vb_sh;
+  a.num_slots = num_slots;
+  a.qo_indptr = nullptr;
+  a.kv_indptr = kv_indptr;
+  a.prefix_lens = nullptr;
+  a.kv_indices = kv_indices;
+  a.batch = batch; a.num_q_tokens = batch; a.hq = hq; a.hkv = hkv; a.lq = lq; a.lv = lv;
+  a.sm_scale = sm_scale; a.logit_cap = logit_cap; a.window = sliding_window;
+  a.kv_fmt = kv_dtype; a.k_scale = k_scale; a.v_scale = v_scale;
+  return PKX_OK;
+}
+
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of the ragged + paged split: one attention pass's scratch (the
@@ -395,37 +439,12 @@ int pkx_decode_attention_fwd(const void *q, void *o, const void *k_buffer, const
                              float logit_cap, int sliding_window, int kv_dtype, float k_scale,
                              float v_scale, float *lse_out, void *workspace,
                              size_t workspace_bytes, void *stream) {
-  int rc;
-  if (batch < 0) return set_error(PKX_EINVAL, "negative batch");
-  if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
-  if ((rc = check_scalars(sm_scale, logit_cap))) return rc;
-  if ((rc = check_kv_format(kv_dtype, k_scale, v_scale, lq, lv, true))) return rc;
-  if (batch == 0) return PKX_OK;
-  if ((rc = check_rows("q", q, 8, 8))) return rc;
-  if ((rc = check_rows("o", o, 8, 8))) return rc;
-  if ((rc = check_rows("k_buffer", k_buffer, kb_ss, kb_sh))) return rc;
-  if ((rc = check_rows("v_buffer", v_buffer, vb_ss, vb_sh))) return rc;
-  if (!kv_indptr || !aligned(kv_indptr, 4))
-    return set_error(PKX_EINVAL, "kv_indptr null or misaligned");
-  if (kv_indices && !aligned(kv_indices, 4)) return set_error(PKX_EINVAL, "kv_indices misaligned");
-  if (lse_out && !aligned(lse_out, 4)) return set_error(PKX_EINVAL, "lse_out misaligned");
-  if (num_slots <= 0) return set_error(PKX_EINVAL, "num_slots must be positive");
   AttnArgs a{};
-  a.mode = kDecode;
-  a.q = q;
-  a.o = o;
-  a.lse = lse_out;
-  a.k_buf = k_buffer;
-  a.v_buf = v_buffer;
-  a.kb_ss = kb_ss; a.kb_sh = kb_sh; a.vb_ss = vb_ss; a.vb_sh = vb_sh;
-  a.num_slots = num_slots;
-  a.qo_indptr = nullptr;
-  a.kv_indptr = kv_indptr;
-  a.prefix_lens = nullptr;
-  a.kv_indices = kv_indices;
-  a.batch = batch; a.num_q_tokens = batch; a.hq = hq; a.hkv = hkv; a.lq = lq; a.lv = lv;
-  a.sm_scale = sm_scale; a.logit_cap = logit_cap; a.window = sliding_window;
-  a.kv_fmt = kv_dtype; a.k_scale = k_scale; a.v_scale = v_scale;
+  bool done;
+  int rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,
+                       kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, sliding_window,
+                       kv_dtype, k_scale, v_scale, lse_out, &done);
+  if (rc != PKX_OK || done) return rc;
   a.workspace = workspace; a.workspace_bytes = workspace_bytes;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_attention(a);
@@ -613,6 +632,23 @@ static int check_fp4_attention_rows(const Fp4Pool &p, int d) {
   return PKX_OK;
 }
 
+// First tokens that stay visible need no window to be valid, but no custom
+// mask replaces their causal term.
+static int check_first_tokens(int first_tokens, int window, bool masked) {
+  if (first_tokens < 0) return set_error(PKX_EINVAL, "negative first_tokens");
+  if (first_tokens > 0 && window > 0 && masked)
+    return set_error(PKX_EUNSUPPORTED, "first_tokens with a custom mask is not built");
+  return PKX_OK;
+}
+
+static int check_streaming(int hq, int hkv, int lq, int lv, int window, int first_tokens) {
+  int rc;
+  if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
+  if (!((lq == 64 && lv == 64) || (lq == 128 && lv == 128)))
+    return set_error(PKX_EUNSUPPORTED, "the streaming window is built for Lq = Lv = 64 or 128");
+  return check_first_tokens(first_tokens, window, false);
+}
+
 static Fp4Pool fp4_pool(const void *k, const void *ks, const void *v, const void *vs,
                         int64_t k_ss, int64_t k_sh, int64_t ks_ss, int64_t ks_sh, int64_t v_ss,
                         int64_t v_sh, int64_t vs_ss, int64_t vs_sh, int64_t num_slots) {
@@ -729,6 +765,83 @@ int pkx_decode_attention_fwd_fp4(
   a.workspace = workspace; a.workspace_bytes = workspace_bytes;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_decode_fp4(a);
+}
+
+int pkx_extend_attention_fwd_fp4(
+    const void *q_extend, const void *k_extend, const void *v_extend, void *o_extend,
+    const void *k_buffer, const void *k_block_scale, const void *v_buffer,
+    const void *v_block_scale, const int32_t *qo_indptr, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int batch, int num_q_tokens, int hq, int hkv, int lq, int lv,
+    int64_t ke_st, int64_t ke_sh, int64_t ve_st, int64_t ve_sh, int64_t kb_ss, int64_t kb_sh,
+    int64_t kbs_ss, int64_t kbs_sh, int64_t vb_ss, int64_t vb_sh, int64_t vbs_ss, int64_t vbs_sh,
+    int64_t num_slots, float sm_scale, float logit_cap, int sliding_window, int first_tokens,
+    const uint8_t *custom_mask, const int32_t *mask_indptr, const float *sinks, float k_scale,
+    float v_scale, float *lse_out, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc;
+  if ((rc = check_fp4_attention(hq, hkv, lq, lv, k_scale, v_scale))) return rc;
+  if ((rc = check_first_tokens(first_tokens, sliding_window, custom_mask != nullptr))) return rc;
+  AttnArgs a{};
+  bool done;
+  rc = two_stage_args(a, q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffer, qo_indptr,
+                      kv_indptr, kv_indices, batch, num_q_tokens, hq, hkv, lq, lv, ke_st, ke_sh,
+                      ve_st, ve_sh, kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap,
+                      sliding_window, custom_mask, mask_indptr, sinks, kKvBf16, 1.f, 1.f, lse_out,
+                      &done);
+  if (rc != PKX_OK || done) return rc;
+  const Fp4Pool pool = fp4_pool(k_buffer, k_block_scale, v_buffer, v_block_scale, kb_ss, kb_sh,
+                                kbs_ss, kbs_sh, vb_ss, vb_sh, vbs_ss, vbs_sh, num_slots);
+  if ((rc = check_fp4_attention_rows(pool, lq))) return rc;
+  a.kv_fmt = kKvFp4;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.k_bscale = k_block_scale; a.v_bscale = v_block_scale;
+  a.kbs_ss = kbs_ss; a.kbs_sh = kbs_sh; a.vbs_ss = vbs_ss; a.vbs_sh = vbs_sh;
+  a.first_tokens = first_tokens;
+  a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_attention(a);
+}
+
+int pkx_extend_attention_fwd_streaming(
+    const void *q_extend, const void *k_extend, const void *v_extend, void *o_extend,
+    const void *k_buffer, const void *v_buffer, const int32_t *qo_indptr,
+    const int32_t *kv_indptr, const int32_t *kv_indices, int batch, int num_q_tokens, int hq,
+    int hkv, int lq, int lv, int64_t ke_st, int64_t ke_sh, int64_t ve_st, int64_t ve_sh,
+    int64_t kb_ss, int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int sliding_window, int first_tokens, const float *sinks, float *lse_out,
+    void *workspace, size_t workspace_bytes, void *stream) {
+  int rc;
+  if ((rc = check_streaming(hq, hkv, lq, lv, sliding_window, first_tokens))) return rc;
+  AttnArgs a{};
+  bool done;
+  rc = two_stage_args(a, q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffer, qo_indptr,
+                      kv_indptr, kv_indices, batch, num_q_tokens, hq, hkv, lq, lv, ke_st, ke_sh,
+                      ve_st, ve_sh, kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap,
+                      sliding_window, nullptr, nullptr, sinks, kKvBf16, 1.f, 1.f, lse_out, &done);
+  if (rc != PKX_OK || done) return rc;
+  a.first_tokens = first_tokens;
+  a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_attention(a);
+}
+
+int pkx_decode_attention_fwd_streaming(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss,
+    int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int sliding_window, int first_tokens, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream) {
+  int rc;
+  if ((rc = check_streaming(hq, hkv, lq, lv, sliding_window, first_tokens))) return rc;
+  AttnArgs a{};
+  bool done;
+  rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,
+                   kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, sliding_window,
+                   kKvBf16, 1.f, 1.f, lse_out, &done);
+  if (rc != PKX_OK || done) return rc;
+  a.first_tokens = first_tokens;
+  a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_attention(a);
 }
 
 }  // extern "C"

@@ -39,8 +39,13 @@
 //  * an fp8 pool (e4m3 / e5m2 codes with k_scale, v_scale) is staged as
 //    codes and converted in place to exact bf16 (f16 for decode) by the
 //    copy warps; the scales go into the logit scale and P (or the output);
+//  * a 4-bit pool (extend only) is staged as codes with their block scales
+//    and converted in place the same way;
 //  * the KV loop stops at the causal diagonal and starts at the window edge
-//    (the Triton kernel walks every tile and masks);
+//    (the Triton kernel walks every tile and masks).  First tokens that stay
+//    visible before a window come in front: a block's visible keys are then
+//    numbered without the gap between them and the window, so that no tile is
+//    spent on it (FIRST instantiations);
 //  * a device-built work list (no host sync, graph-safe) splits long key
 //    ranges across CTAs (split-KV); a combine kernel merges the partial
 //    (o, lse) pairs with the merge_state formula;
@@ -57,6 +62,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "fp4.cuh"
 #include "pkx_internal.h"
 #include "ptx.cuh"
 
@@ -69,6 +75,7 @@ struct SchedParams {
   int mode;
   const int32_t *qo_indptr, *kv_indptr, *prefix_lens;
   int batch, hkv, tok, window, num_q_tokens;
+  int first;       // with a window: first tokens that stay visible (0: none)
   int bn;        // keys per K/V tile
   int q_tile_tok;  // query tokens of one Q tile
   int no_causal;   // a custom mask replaces the causal mask: blocks see every key
@@ -146,7 +153,22 @@ __device__ SeqDims seq_dims(const SchedParams &p, int b) {
   return d;
 }
 
-// Key range [lo, hi) of query block qb of a sequence.
+// First tokens that stay visible.  A query block whose first query sits at
+// qpos0 sees the keys [0, first) and those from qpos0 - window on; the keys
+// between them, block_gap() of them, are left out, and the block's keys are
+// numbered without them: number v is key v below `first`, key v + gap from
+// there on.
+__device__ __forceinline__ int block_gap(int qpos0, int window, int first) {
+  if (first <= 0 || window <= 0) return 0;
+  return (int)max((long long)qpos0 - window - first, 0ll);
+}
+// The number of key j (for a key in the gap: of the next one that is not).
+__device__ __forceinline__ int key_number(int j, int first, int gap) {
+  return j <= first ? j : max(first, j - gap);
+}
+
+// Key range [lo, hi) of query block qb of a sequence (key numbers where first
+// tokens stay visible).
 __device__ __forceinline__ void qblock_range(const SchedParams &p, const SeqDims &d, int qb,
                                              int &lo, int &hi, int &i0, int &i1) {
   i0 = qb * p.tok;
@@ -155,6 +177,10 @@ __device__ __forceinline__ void qblock_range(const SchedParams &p, const SeqDims
   hi = p.no_causal ? d.T : min(qmax + 1, d.T);
   lo = p.window > 0 ? max(0, qmin - p.window) : 0;
   if (hi < lo) hi = lo;
+  if (p.first > 0 && p.window > 0) {
+    hi = key_number(hi, p.first, block_gap(qmin, p.window, p.first));
+    lo = 0;
+  }
 }
 
 // Number of K/V tiles of the key range [kb, ke) when tiles may not straddle
@@ -458,9 +484,11 @@ __global__ void __launch_bounds__(1024, 1) sched_kernel(SchedParams p) {
     const int sp = k / nd, dq = k - sp * nd;
     const int b = bSeq[qb];
     const SeqDims d = dims(b);
-    const int split_at = p.mode == kTwoStage ? d.P : INT_MAX;
     int lo, hi, i0, i1;
     qblock_range(p, d, qb - sOff[b], lo, hi, i0, i1);
+    const int split_at = p.mode != kTwoStage ? INT_MAX
+                         : p.first > 0 ? key_number(d.P, p.first, block_gap(d.P + i0, p.window, p.first))
+                                       : d.P;
     const int nt = bNt[qb], S = splits(qb);
     // split sp covers tiles [sp nt / S, (sp + 1) nt / S) (sizes differ by
     // one at most), or (stream partition) the block's tiles inside share
@@ -553,6 +581,10 @@ struct KParams {
   const int32_t *qo_indptr, *kv_indptr;
   const void *kv_indices;
   int hq, group, tok, q_box_tok, window, use_cap, rows_per_slot;
+  int first;  // FIRST instantiations: first tokens that stay visible before the window
+  // 4-bit pool: block scales of K and V rows (byte strides)
+  const uint8_t *k_bs, *v_bs;
+  int64_t kbs_ss, kbs_sh, vbs_ss, vbs_sh;
   float scale_log2;  // sm_scale * log2(e)           (no cap)
   float cap_pre;     // sm_scale / cap                (cap)
   float cap_log2;    // cap * log2(e)                 (cap)
@@ -770,12 +802,31 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8_scaled(uint4 v) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// Eight e2m1 codes times their e4m3 block scale (byte `at` of sw) as eight
+// bf16: exact, since the product has six significant bits.
+__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, uint32_t sw, int at) {
+  const uint32_t sc = (sw >> (8 * at)) & 0xFFu;
+  const __half2 s2 = e4m3x2_to_f16x2(sc | (sc << 8));
+  uint32_t h[4], out[4];
+  e2m1x8_to_f16(codes, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s2));
+    out[i] = pack_bf16(f.x, f.y);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // FMT: the pool's element format (0 bf16; 1 fp8 e4m3, 2 fp8 e5m2 with
-// k_scale / v_scale).  Extend rows of the two-stage form are always bf16.
-template <int HD, int MODE, bool MASK, int FMT = 0>
+// k_scale / v_scale; 3 the 4-bit pool, extend only).  Extend rows of the
+// two-stage form are always bf16.  FIRST: first tokens stay visible before the
+// window, and key ranges are key numbers (block_gap); its own instantiation,
+// so that the others carry none of it.
+template <int HD, int MODE, bool MASK, int FMT = 0, bool FIRST = false>
 __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     attn_kernel(const __grid_constant__ TMaps tm, const KParams p) {
   using C = Cfg<HD>;
+  static_assert(!(FIRST && MASK) && !(FMT == 3 && MODE == kDecode), "not built");
   // Decode over an fp8 pool runs its products in f16: a code becomes f16 in
   // one step (exact), the unit's query rows are converted once (times 2^-8),
   // P is written as f16 and v_scale is applied to the output.
@@ -905,6 +956,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       const int t = tok0 + r / G, g = r - (r / G) * G;
       const int qpos = w.qpos0 + t;
       const int qmin = w.qpos0 + tok0, qmax = w.qpos0 + tok0 + n_tok_i - 1;
+      const int gap = FIRST ? block_gap(w.qpos0, p.window, p.first) : 0;
       const int64_t orow_idx = (int64_t)(w.q_tok0 + t) * p.hq + w.kvh * G + g;
       const int64_t prow_idx =
           MODE == kDecode ? (int64_t)(w.slot + wg) * p.rows_per_slot + r
@@ -1009,8 +1061,15 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
             for (int i = 0; i < C::BN; ++i) x[i] = p.cap_log2 * tanh_approx(x[i] * pre);
             sc = 1.0f;
           }
-          const bool need_mask = MASK || (ke - 1 > qmin) || (ke - kb < C::BN) ||
-                                 (p.window > 0 && kb < qmax - p.window);
+          bool need_mask = MASK || (ke - 1 > qmin) || (ke - kb < C::BN) ||
+                           (p.window > 0 && kb < qmax - p.window);
+          if constexpr (FIRST) {
+            // the last key is past the first query, or a key behind the first
+            // tokens is before the last query's window
+            const int last = ke - 1 >= p.first ? ke - 1 + gap : ke - 1;
+            need_mask = last > qmin || ke - kb < C::BN ||
+                        (ke > p.first && max(kb, p.first) + gap < qmax - p.window);
+          }
           if constexpr (MASK) {
             // the custom mask replaces the causal term; the window stays.
             // A row that sees every key of the tile (all bits set, the
@@ -1027,6 +1086,18 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
               }
               sc = 1.0f;
             }
+          } else if (FIRST && need_mask) {
+            // numbers of the row's last key (causal, end of the tile) and of
+            // the first one in its window
+            const int vhi =
+                min(ke - 1, qpos - gap >= p.first ? qpos - gap : min(qpos, p.first - 1));
+            const int vlo = qpos - p.window - gap;
+#pragma unroll
+            for (int i = 0; i < C::BN; ++i) {
+              const int v = kb + i;
+              x[i] = v <= vhi && (v < p.first || v >= vlo) ? x[i] * sc : -INFINITY;
+            }
+            sc = 1.0f;
           } else if (need_mask) {
 #pragma unroll
             for (int i = 0; i < C::BN; ++i) {
@@ -1426,6 +1497,10 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       ++q_cnt;
       const int64_t kv_base = p.kv_indptr[w.b];
       const int64_t ext_base = MODE == kTwoStage ? p.qo_indptr[w.b] : 0;
+      const int gap = FIRST ? block_gap(w.qpos0, p.window, p.first) : 0;
+      // position of the first extend key
+      const int ext_pos = FIRST && MODE == kTwoStage ? (int)(p.kv_indptr[w.b + 1] - kv_base)
+                                                     : w.k_split;
       for (int j = 0; j < nt; ++j) {
         int kb, ke;
         tile_keys(w, j, kb, ke);
@@ -1434,11 +1509,12 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int jpos = kb + 4 * lane + i;
+          int jpos = kb + 4 * lane + i;
           int64_t row = -1;
           if (jpos < ke) {
+            if (FIRST && jpos >= p.first) jpos += gap;
             if (from_ext) {
-              row = ext_base + (jpos - w.k_split);
+              row = ext_base + (jpos - ext_pos);
             } else {
               row = MODE == kUnified
                         ? __ldg(static_cast<const int64_t *>(p.kv_indices) + kv_base + jpos)
@@ -1763,14 +1839,21 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     // tiles (bf16 rows of the two-stage form) take the plain copy.  One
     // cp.async group is committed per issued tile.
     // (split head dims: by 64-dim atom, as copy_rows does; a row of L codes)
-    auto issue_raw = [&](uint32_t stage, const uint8_t *base, int64_t stride, const int *rows,
-                         auto l_c) {
+    // (a 4-bit pool: the chunk's four code bytes, and behind them the word of
+    // block scales that holds the chunk's; sbase4 / sstride: the scale rows)
+    auto issue_raw = [&](uint32_t stage, const uint8_t *base, int64_t stride, const uint8_t *sbase4,
+                         int64_t sstride, const int *rows, auto l_c) {
       constexpr int L = decltype(l_c)::value;
       static_for<0, NKEYS>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
         const int r = rows[i];
         const uint8_t *src = base + (int64_t)max(r, 0) * stride;
-        if constexpr (!C::SPLIT) {
+        if constexpr (FMT == 3) {
+          static_assert(!C::SPLIT, "4-bit pools are built for Lq = Lv");
+          cp_async_4_at<i * KPP * 128>(stage + dthr, src, r >= 0 ? 4u : 0u);
+          cp_async_4_at<i * KPP * 128 + 4>(stage + dthr, sbase4 + (int64_t)max(r, 0) * sstride,
+                                           r >= 0 ? 4u : 0u);
+        } else if constexpr (!C::SPLIT) {
           static_assert(L == C::LQ || L == C::HDV, "row length");
           cp_async_8_at<i * KPP * 128>(stage + dthr, src, r >= 0 ? 8u : 0u);
         } else {
@@ -1787,7 +1870,11 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       constexpr int L = decltype(l_c)::value;
       static_for<0, NKEYS>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
-        if constexpr (!C::SPLIT) {
+        if constexpr (FMT == 3) {
+          const uint32_t a = stage + dthr + i * KPP * 128;
+          const uint2 u = ld_shared_u2(a);
+          st_shared_u4(a, fp4x8_to_bf16x8(u.x, u.y, (ch >> 1) & 3));
+        } else if constexpr (!C::SPLIT) {
           const uint32_t a = stage + dthr + i * KPP * 128;
           st_shared_u4(a, fp8x8_to_bf16x8<FMT>(ld_shared_u2(a)));
         } else {
@@ -1808,10 +1895,13 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       const WorkUnit w = p.units[p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
+      constexpr int CB = FMT == 3 ? 4 : 8;  // code bytes of a chunk
       const uint8_t *kp8 =
-          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + ch * 8;
+          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + ch * CB;
       const uint8_t *vp8 =
-          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + ch * 8;
+          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + ch * CB;
+      const uint8_t *ks8 = FMT == 3 ? p.k_bs + (int64_t)w.kvh * p.kbs_sh + (ch >> 3) * 4 : nullptr;
+      const uint8_t *vs8 = FMT == 3 ? p.v_bs + (int64_t)w.kvh * p.vbs_sh + (ch >> 3) * 4 : nullptr;
       const bf16 *kx = p.k_ext + (int64_t)w.kvh * p.ke_sh + ch * 8;
       const bf16 *vx = p.v_ext + (int64_t)w.kvh * p.ve_sh + ch * 8;
       int rows[NKEYS];
@@ -1848,7 +1938,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, kx, p.ke_st, rows, K_LEN);
           cp_async_arrive_noinc(&k_full[ks]);
         } else {
-          issue_raw(stage, kp8, p.kb_ss, rows, K_LEN);
+          issue_raw(stage, kp8, p.kb_ss, ks8, p.kbs_ss, rows, K_LEN);
         }
         cp_async_commit();
         ++kc;
@@ -1864,7 +1954,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, vx, p.ve_st, rows, V_LEN);
           cp_async_arrive_noinc(&v_full[vs]);
         } else {
-          issue_raw(stage, vp8, p.vb_ss, rows, V_LEN);
+          issue_raw(stage, vp8, p.vb_ss, vs8, p.vbs_ss, rows, V_LEN);
         }
         cp_async_commit();
         ++vc;
@@ -2183,18 +2273,18 @@ static int make_q_map(CUtensorMap *m, const void *q, int64_t n, int hq, int lq, 
   return PKX_OK;
 }
 
-template <int HD, int MODE, bool MASK = false, int FMT = 0>
+template <int HD, int MODE, bool MASK = false, int FMT = 0, bool FIRST = false>
 static int launch_attn_kernel(const TMaps &tmaps, const KParams &kp, int grid, cudaStream_t s) {
   using C = Cfg<HD>;
   static bool configured[kMaxDevicesCfg] = {};  // per instantiation and device
   if (needs_config(configured)) {
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<HD, MODE, MASK, FMT>,
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<HD, MODE, MASK, FMT, FIRST>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
       return set_error(PKX_ECUDA, "cudaFuncSetAttribute(attn_kernel): %s", cudaGetErrorString(e));
     mark_configured(configured);
   }
-  cudaError_t e = launch_pdl(attn_kernel<HD, MODE, MASK, FMT>, dim3(grid), dim3(C::THREADS),
+  cudaError_t e = launch_pdl(attn_kernel<HD, MODE, MASK, FMT, FIRST>, dim3(grid), dim3(C::THREADS),
                              C::SMEM, s, tmaps, kp);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "attn_kernel launch: %s", cudaGetErrorString(e));
@@ -2213,6 +2303,22 @@ static int launch_attn_fp8(int mode, bool masked, const TMaps &tmaps, const KPar
     return masked ? launch_attn_kernel<HD, kUnified, true, FMT>(tmaps, kp, grid, s)
                   : launch_attn_kernel<HD, kUnified, false, FMT>(tmaps, kp, grid, s);
   return launch_attn_kernel<HD, kDecode, false, FMT>(tmaps, kp, grid, s);
+}
+
+// Two-stage extend over a 4-bit pool, and the two forms with first tokens that
+// stay visible over a bf16 pool (Lq = Lv, one head size).
+template <int HD>
+static int launch_attn_fp4(bool masked, bool first, const TMaps &tmaps, const KParams &kp, int grid,
+                           cudaStream_t s) {
+  if (masked) return launch_attn_kernel<HD, kTwoStage, true, kKvFp4>(tmaps, kp, grid, s);
+  return first ? launch_attn_kernel<HD, kTwoStage, false, kKvFp4, true>(tmaps, kp, grid, s)
+               : launch_attn_kernel<HD, kTwoStage, false, kKvFp4>(tmaps, kp, grid, s);
+}
+template <int HD>
+static int launch_attn_first(int mode, const TMaps &tmaps, const KParams &kp, int grid,
+                             cudaStream_t s) {
+  return mode == kDecode ? launch_attn_kernel<HD, kDecode, false, 0, true>(tmaps, kp, grid, s)
+                         : launch_attn_kernel<HD, kTwoStage, false, 0, true>(tmaps, kp, grid, s);
 }
 
 // Pair kernel launch: clusters of two CTAs, programmatic dependent launch.
@@ -2349,6 +2455,7 @@ int launch_attention(const AttnArgs &a) {
   sp.two_streams = !mla && !split && (!decode || dec_two);
   sp.n_dsplit = 1;
   sp.window = a.window;
+  sp.first = a.window > 0 ? a.first_tokens : 0;
   sp.num_q_tokens = nq;
   sp.unit_target = mla ? 4 * pairs : L.unit_target;
   // MLA decode with one KV head: a stream partition, one share of the key
@@ -2421,6 +2528,10 @@ int launch_attention(const AttnArgs &a) {
   kp.tok = tok;
   kp.q_box_tok = decode ? 1 : tok;
   kp.window = a.window;
+  kp.first = sp.first;
+  kp.k_bs = static_cast<const uint8_t *>(a.k_bscale);
+  kp.v_bs = static_cast<const uint8_t *>(a.v_bscale);
+  kp.kbs_ss = a.kbs_ss; kp.kbs_sh = a.kbs_sh; kp.vbs_ss = a.vbs_ss; kp.vbs_sh = a.vbs_sh;
   kp.rows_per_slot = L.rows_per_slot;
   const float log2e = 1.4426950408889634f;
   const float sm_scale = a.sm_scale > 0.f ? a.sm_scale : 1.0f / sqrtf((float)a.lq);
@@ -2456,7 +2567,13 @@ int launch_attention(const AttnArgs &a) {
   attention_events(&ev_before, &ev_after);
   if (ev_before) cudaEventRecord(ev_before, a.stream);
   const bool masked = a.custom_mask != nullptr;
-  if (a.kv_fmt != kKvBf16 && mla) {
+  if (a.kv_fmt == kKvFp4) {  // Lq = Lv = 64 or 128, two-stage (the entry point checks)
+    rc = a.lq == 128 ? launch_attn_fp4<128>(masked, sp.first > 0, tm, kp, grid, a.stream)
+                     : launch_attn_fp4<64>(masked, sp.first > 0, tm, kp, grid, a.stream);
+  } else if (sp.first > 0) {  // bf16 pool, Lq = Lv = 64 or 128, two-stage or decode, no mask
+    rc = a.lq == 128 ? launch_attn_first<128>(a.mode, tm, kp, grid, a.stream)
+                     : launch_attn_first<64>(a.mode, tm, kp, grid, a.stream);
+  } else if (a.kv_fmt != kKvBf16 && mla) {
     // the MLA pair kernel over an fp8 pool
     const bool e4 = a.kv_fmt == kKvFp8E4M3;
     if (a.mode == kTwoStage)

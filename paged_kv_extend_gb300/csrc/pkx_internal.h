@@ -22,7 +22,8 @@ enum KeyMode : int {
 };
 
 // Element format of the KV pool (the values of include/pkx.h's PKX_KV_*).
-enum KvFormat : int { kKvBf16 = 0, kKvFp8E4M3 = 1, kKvFp8E5M2 = 2 };
+// kKvFp4 is the 4-bit pool of the *_fp4 entry points.
+enum KvFormat : int { kKvBf16 = 0, kKvFp8E4M3 = 1, kKvFp8E5M2 = 2, kKvFp4 = 3 };
 
 // A 4-bit pool (fp4.cuh): rows of e2m1 codes and of e4m3 block scales, row
 // (slot, head) of each at base + slot * ss + head * sh bytes.
@@ -56,7 +57,8 @@ struct __align__(16) WorkUnit {
   int32_t n_tok;    // tokens in the block
   int32_t qpos0;    // position of the first query token in its sequence
   int32_t kvh;      // KV head
-  int32_t k_begin;  // key positions [k_begin, k_end)
+  int32_t k_begin;  // key positions [k_begin, k_end); with first tokens that stay visible
+                    // before a window, numbers in the list of visible keys (block_gap)
   int32_t k_end;
   int32_t k_split;  // keys >= k_split come from the extend rows (two-stage)
   int32_t n_tiles;  // K/V tiles (no tile straddles k_split)
@@ -153,11 +155,14 @@ struct AttnArgs {
   int batch, num_q_tokens, hq, hkv, lq, lv;
   float sm_scale, logit_cap;
   int window;
+  int first_tokens = 0;         // with a window: the first tokens that stay visible
   const uint8_t *custom_mask;   // nullable: replaces the causal mask
   const int32_t *mask_indptr;   // [batch+1] offsets into custom_mask
   const float *sinks;           // nullable [hq] sink logits
   int kv_fmt = 0;               // pool format: kKvBf16, kKvFp8E4M3, kKvFp8E5M2
   float k_scale = 1.f, v_scale = 1.f;  // fp8 pool: key = code * k_scale, value = code * v_scale
+  const void *k_bscale = nullptr, *v_bscale = nullptr;  // 4-bit pool: block scales, byte strides
+  int64_t kbs_ss = 0, kbs_sh = 0, vbs_ss = 0, vbs_sh = 0;
   int key_set = kAllKeys;       // two-stage form: which keys this pass sees
   int keep_status = 0;          // a later pass of one call keeps the status word
   const int64_t *cache_loc = nullptr;  // two-stage: fused KV write of the extend rows

@@ -223,6 +223,13 @@ __device__ __forceinline__ void cp_async_8_at(uint32_t dst, const void *src, uin
                "r"(src_bytes), "n"(DOFF)
                : "memory");
 }
+// The same for 4 bytes.
+template <uint32_t DOFF>
+__device__ __forceinline__ void cp_async_4_at(uint32_t dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0+%3], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(src_bytes), "n"(DOFF)
+               : "memory");
+}
 __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");

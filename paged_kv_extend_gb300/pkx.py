@@ -94,6 +94,17 @@ _SIGS = {
         _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i,
         _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _i, _f, _f,
         _p, _p, _sz, _p]),
+    "pkx_extend_attention_fwd_fp4": (_i, [
+        _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
+        _f, _f, _i, _i, _p, _p, _p, _f, _f, _p, _p, _sz, _p]),
+    "pkx_extend_attention_fwd_streaming": (_i, [
+        _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _i, _p,
+        _p, _p, _sz, _p]),
+    "pkx_decode_attention_fwd_streaming": (_i, [
+        _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _i, _p, _p, _sz, _p]),
 }
 
 
@@ -777,11 +788,7 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
     _check_len(kv_indptr, b + 1, "kv_indptr")
     _one_device(q.device, o=o, k_buffer=k_buffer, kv_indptr=kv_indptr, kv_indices=kv_indices,
                 lse=lse, workspace=workspace)
-    ws = workspace
-    if ws is None:
-        with torch.cuda.device(q.device):
-            size = decode_fp4_workspace_size(b, hq, hkv, lq, lv)
-        ws = _workspace(None, size, q.device)
+    ws = _own_workspace(workspace, decode_fp4_workspace_size, q.device, b, hq, hkv, lq, lv)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd_fp4,
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(k_block_scale), _ptr(v_buffer),
@@ -789,4 +796,128 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
         hq, hkv, lq, lv, *strides, k_buffer.shape[0], float(sm_scale or 0.0),
         float(logit_cap or 0.0), int(sliding_window), int(first_tokens), float(k_scale),
         float(v_scale), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
+    return ws
+
+
+def _two_stage_checks(q, k_extend, v_extend, hkv, lq, lv, qo_indptr, kv_indptr, kv_indices):
+    """Shared checks of the two-stage calls below; (batch, k strides, v strides)."""
+    n, batch = q.shape[0], qo_indptr.numel() - 1
+    _i32(qo_indptr, "qo_indptr"), _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
+    if batch < 0:
+        raise ValueError("qo_indptr must hold at least one entry")
+    _check_len(kv_indptr, batch + 1, "kv_indptr")
+    if tuple(k_extend.shape) != (n, hkv, lq) or tuple(v_extend.shape) != (n, hkv, lv):
+        raise ValueError("k_extend / v_extend must be [tokens, Hkv, Lq] / [tokens, Hkv, Lv] "
+                         "with q's token count")
+    return batch, _rows(k_extend, "k_extend"), _rows(v_extend, "v_extend")
+
+
+def _one_sink_per_head(sinks, hq):
+    if sinks is not None:
+        _check_len(sinks, hq, "sinks")
+
+
+def _own_workspace(workspace, size_fn, dev, *shape):
+    """The caller's workspace, or a new one of size_fn(*shape) bytes on ``dev``."""
+    if workspace is not None:
+        return workspace
+    with torch.cuda.device(dev):
+        return _workspace(None, size_fn(*shape), dev)
+
+
+def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k_block_scale,
+                             v_buffer, v_block_scale, qo_indptr, kv_indptr, kv_indices,
+                             sm_scale=None, logit_cap=0.0, sliding_window=-1, first_tokens=0,
+                             lse=None, workspace=None, custom_mask=None, mask_indptr=None,
+                             sinks=None, k_scale=1.0, v_scale=1.0):
+    """Two-stage extend attention with the prefix in a 4-bit pool
+    (pkx_extend_attention_fwd_fp4); the new rows stay bf16.  Writes o_extend
+    (and lse) in place; other arguments as extend_attention_fwd and
+    decode_attention_fwd_fp4.  Returns the workspace."""
+    lib = load_library()
+    strides = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+    n, hq, hkv, lq, lv = _check_fp4_attn(q_extend, o_extend, lse, k_buffer, v_buffer)
+    batch, ke, ve = _two_stage_checks(q_extend, k_extend, v_extend, hkv, lq, lv, qo_indptr,
+                                      kv_indptr, kv_indices)
+    dev = q_extend.device
+    _one_device(dev, o_extend=o_extend, k_extend=k_extend, v_extend=v_extend, k_buffer=k_buffer,
+                qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, lse=lse,
+                workspace=workspace, custom_mask=custom_mask, mask_indptr=mask_indptr, sinks=sinks)
+    _one_sink_per_head(sinks, hq)
+    ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
+    _check(_on(
+        dev, lib.pkx_extend_attention_fwd_fp4,
+        _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
+        _ptr(k_block_scale), _ptr(v_buffer), _ptr(v_block_scale), _ptr(qo_indptr),
+        _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq,
+        lv, *ke, *ve, *strides, k_buffer.shape[0], float(sm_scale or 0.0),
+        float(logit_cap or 0.0), int(sliding_window), int(first_tokens),
+        *_mask_sinks(custom_mask, mask_indptr, sinks), float(k_scale), float(v_scale), _ptr(lse),
+        _ptr(ws), ws.numel() * ws.element_size()))
+    return ws
+
+
+# ------------------------------------------------- streaming window, bf16 pools
+def _bf16_pools(k_buffer, v_buffer):
+    kb, vb, kv_dtype = _pool_rows(k_buffer, v_buffer)
+    if kv_dtype != PKX_KV_BF16:
+        raise ValueError("the streaming window reads a bf16 pool")
+    return *kb, *vb
+
+
+def extend_attention_fwd_streaming(q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffer,
+                                   qo_indptr, kv_indptr, kv_indices, sliding_window, first_tokens,
+                                   sm_scale=None, logit_cap=0.0, lse=None, workspace=None,
+                                   sinks=None):
+    """Two-stage extend attention with a sliding window before which the first
+    ``first_tokens`` keys of each sequence stay visible
+    (pkx_extend_attention_fwd_streaming), over a bf16 pool with head dims 64
+    or 128.  Other arguments as extend_attention_fwd.  Returns the workspace."""
+    lib = load_library()
+    n, hq, lq = q_extend.shape
+    hkv, lv = k_buffer.shape[1], v_buffer.shape[2]
+    _check_attn(q_extend, o_extend, lse, k_buffer, v_buffer, n, hq, lq, lv)
+    strides = _bf16_pools(k_buffer, v_buffer)
+    batch, ke, ve = _two_stage_checks(q_extend, k_extend, v_extend, hkv, lq, lv, qo_indptr,
+                                      kv_indptr, kv_indices)
+    dev = q_extend.device
+    _one_device(dev, o_extend=o_extend, k_extend=k_extend, v_extend=v_extend, k_buffer=k_buffer,
+                v_buffer=v_buffer, qo_indptr=qo_indptr, kv_indptr=kv_indptr,
+                kv_indices=kv_indices, lse=lse, workspace=workspace, sinks=sinks)
+    _one_sink_per_head(sinks, hq)
+    ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
+    _check(_on(
+        dev, lib.pkx_extend_attention_fwd_streaming,
+        _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
+        _ptr(v_buffer), _ptr(qo_indptr), _ptr(kv_indptr),
+        _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq, lv, *ke, *ve,
+        *strides, k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
+        int(sliding_window), int(first_tokens), _mask_sinks(None, None, sinks)[2], _ptr(lse),
+        _ptr(ws), ws.numel() * ws.element_size()))
+    return ws
+
+
+def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indices,
+                                   sliding_window, first_tokens, sm_scale=None, logit_cap=0.0,
+                                   lse=None, workspace=None):
+    """Decode attention with a sliding window before which the first
+    ``first_tokens`` keys of each sequence stay visible
+    (pkx_decode_attention_fwd_streaming), over a bf16 pool with head dims 64 or
+    128.  Other arguments as decode_attention_fwd.  Returns the workspace."""
+    lib = load_library()
+    b, hq, lq = q.shape
+    hkv, lv = k_buffer.shape[1], v_buffer.shape[2]
+    _check_attn(q, o, lse, k_buffer, v_buffer, b, hq, lq, lv)
+    strides = _bf16_pools(k_buffer, v_buffer)
+    _check_len(kv_indptr, b + 1, "kv_indptr")
+    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
+    _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
+                kv_indices=kv_indices, lse=lse, workspace=workspace)
+    ws = _own_workspace(workspace, decode_workspace_size, q.device, b, hq, hkv, lq, lv)
+    _check(_on(
+        q.device, lib.pkx_decode_attention_fwd_streaming,
+        _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(v_buffer), _ptr(kv_indptr),
+        _ptr(kv_indices) if kv_indices.numel() else None, b, hq, hkv, lq, lv, *strides,
+        k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), int(sliding_window),
+        int(first_tokens), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
     return ws

@@ -88,17 +88,19 @@ def attend(q, k, v, ok, scale, cap=0.0, sinks=None):
     return o, lse, av, aq
 
 
-def check(o, lse, ref, d, scale, p_step, what=""):
+def check(o, lse, ref, d, scale, p_step, what="", tanh_step=0.0):
     """o (bf16) and lse (fp32) against attend()'s result.
 
     Logits: d fp32 products summed with at most one rounding (or truncation,
     2^-23) a step, so |ds| <= d 2^-23 sum|q k| scale, and a few more ulp of the
     logit and of the exponent (2^-20 of sum|q k| scale, 2^-18 absolute).  P is
     rounded to a type of half step p_step and o to bf16 (2^-8): |do| <= 2^-8
-    |o| + (p_step + 2 |ds|) sum p |v|.  lse errs by |ds| (and 2^-22 |lse|)."""
+    |o| + (p_step + 2 |ds|) sum p |v|.  lse errs by |ds| (and 2^-22 |lse|).
+    tanh_step: relative error of the tanh behind a logit cap (2^-11 for
+    tanh.approx), of a logit of at most sum |q k| scale."""
     ro, rl, av, aq = ref
     o, lse = o.detach().cpu().double(), lse.detach().cpu().double()
-    ds = (d * 2.0 ** -23 + 2.0 ** -20) * aq * scale + 2.0 ** -18
+    ds = (d * 2.0 ** -23 + 2.0 ** -20 + tanh_step) * aq * scale + 2.0 ** -18
     assert torch.equal(torch.isinf(lse), torch.isinf(rl)), f"{what}: lse finiteness"
     fin = torch.isfinite(rl)
     err = (lse - rl)[fin].abs() - (ds + 2.0 ** -22 * rl.abs())[fin]
@@ -107,3 +109,21 @@ def check(o, lse, ref, d, scale, p_step, what=""):
     assert torch.isfinite(o).all(), f"{what}: non-finite output"
     over = (o - ro).abs() - tol
     assert over.max() <= 0, f"{what}: o off by {over.max().item():.2e} too much"
+
+
+def extend(wl, k_prefix, v_prefix, k_ext, v_ext, window=-1, first=0, cap=0.0, sinks=None, masks=None):
+    """attend() over every sequence of a drawn workload: its prefix rows
+    (float64 [P, hkv, d] each) and its extend rows."""
+    out, q0, p0 = [], 0, 0
+    for b, (p, e) in enumerate(zip(wl.prefix_lens, wl.extend_lens)):
+        k = torch.cat([k_prefix[p0:p0 + p], k_ext[q0:q0 + e].double()])
+        v = torch.cat([v_prefix[p0:p0 + p], v_ext[q0:q0 + e].double()])
+        pos = torch.arange(e) + p
+        ok = visible(pos, p + e, window, first)
+        if masks is not None:
+            ok = masks[b].bool()
+            if window > 0:
+                ok = ok & (pos[:, None] - torch.arange(p + e)[None] <= window)
+        out.append(attend(wl.q[q0:q0 + e].double(), k, v, ok, wl.sm_scale, cap, sinks))
+        q0, p0 = q0 + e, p0 + p
+    return [torch.cat(x) for x in zip(*out)]
