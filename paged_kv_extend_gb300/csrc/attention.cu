@@ -76,6 +76,7 @@ struct SchedParams {
   const int32_t *qo_indptr, *kv_indptr, *prefix_lens;
   int batch, hkv, tok, window, num_q_tokens;
   int first;       // with a window: first tokens that stay visible (0: none)
+  int head_minor;  // number a block's units of all KV heads one after another
   int bn;        // keys per K/V tile
   int q_tile_tok;  // query tokens of one Q tile
   int no_causal;   // a custom mask replaces the causal mask: blocks see every key
@@ -473,7 +474,10 @@ __global__ void __launch_bounds__(1024, 1) sched_kernel(SchedParams p) {
   // block with bUo[qb] <= rest, and the unit is its (split, value slice)
   // number rest - bUo[qb].
   auto unit_at = [&](int u) {
-    const int kvh = u / tu, rest = u - kvh * tu;
+    // (head_minor: unit u is of KV head u % hkv, so that the heads' units of a
+    // block are claimed close together)
+    const int kvh = p.head_minor ? u % p.hkv : u / tu;
+    const int rest = p.head_minor ? u / p.hkv : u - kvh * tu;
     int lo_b = 0, hi_b = total_qb - 1;
     while (lo_b < hi_b) {
       const int mid = (lo_b + hi_b + 1) >> 1;
@@ -668,6 +672,8 @@ struct Cfg {
   // swizzle atom (chunk t % 8 of every atom, keys t / 8 + 16 i) for the
   // split dims, whose 24 or 36 chunks per row do not divide 128 threads
   static constexpr int KPP = SPLIT ? 16 : COPY_THREADS / (HD / 8);
+  // a 4-bit pool: 16-byte code chunks of a row (32 elements each), keys per pass
+  static constexpr int Q4 = SPLIT ? 4 : HD / 32, KP4 = COPY_THREADS / Q4;
   // Registers: the kernel launches with REGS_LAUNCH per thread (checked at
   // build time); the softmax warpgroups take REGS_SOFTMAX, the other two
   // give back down to REGS_OTHER.  The split must add up exactly.
@@ -802,17 +808,20 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8_scaled(uint4 v) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Eight e2m1 codes times their e4m3 block scale (byte `at` of sw) as eight
-// bf16: exact, since the product has six significant bits.
-__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, uint32_t sw, int at) {
-  const uint32_t sc = (sw >> (8 * at)) & 0xFFu;
-  const __half2 s2 = e4m3x2_to_f16x2(sc | (sc << 8));
+// Eight e2m1 codes times their e4m3 block scale (sw's low byte) as eight
+// bf16: exact, since the product has six significant bits.  The f16 of a code
+// shifted by the three bits that bf16's exponent is longer is its bf16 times
+// 2^-112; the scale brings the 2^112 (448 * 2^112 is in range).
+__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, uint32_t sw) {
+  const float sc = __low2float(e4m3x2_to_f16x2(sw & 0xFFu)) * 0x1p112f;
+  const __nv_bfloat162 s2 = __float2bfloat162_rn(sc);
   uint32_t h[4], out[4];
   e2m1x8_to_f16(codes, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s2));
-    out[i] = pack_bf16(f.x, f.y);
+    const uint32_t b = (h[i] & 0x80008000u) | ((h[i] >> 3) & 0x0FC00FC0u);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), s2);
+    out[i] = *reinterpret_cast<const uint32_t *>(&x);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
@@ -1536,7 +1545,8 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         }
         {
           // ring[key % KPP][key / KPP]: each copy thread's rows contiguous
-          constexpr int KPP = C::KPP, NK_T = C::BN / KPP;
+          // (a tile of a 4-bit pool: KP4 for KPP)
+          const int KPP = FMT == 3 && !from_ext ? C::KP4 : C::KPP, NK_T = C::BN / KPP;
           int *ring = reinterpret_cast<int *>(smem + C::OFF_I + is * C::I_BYTES);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1839,21 +1849,14 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     // tiles (bf16 rows of the two-stage form) take the plain copy.  One
     // cp.async group is committed per issued tile.
     // (split head dims: by 64-dim atom, as copy_rows does; a row of L codes)
-    // (a 4-bit pool: the chunk's four code bytes, and behind them the word of
-    // block scales that holds the chunk's; sbase4 / sstride: the scale rows)
-    auto issue_raw = [&](uint32_t stage, const uint8_t *base, int64_t stride, const uint8_t *sbase4,
-                         int64_t sstride, const int *rows, auto l_c) {
+    auto issue_raw = [&](uint32_t stage, const uint8_t *base, int64_t stride, const int *rows,
+                         auto l_c) {
       constexpr int L = decltype(l_c)::value;
       static_for<0, NKEYS>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
         const int r = rows[i];
         const uint8_t *src = base + (int64_t)max(r, 0) * stride;
-        if constexpr (FMT == 3) {
-          static_assert(!C::SPLIT, "4-bit pools are built for Lq = Lv");
-          cp_async_4_at<i * KPP * 128>(stage + dthr, src, r >= 0 ? 4u : 0u);
-          cp_async_4_at<i * KPP * 128 + 4>(stage + dthr, sbase4 + (int64_t)max(r, 0) * sstride,
-                                           r >= 0 ? 4u : 0u);
-        } else if constexpr (!C::SPLIT) {
+        if constexpr (!C::SPLIT) {
           static_assert(L == C::LQ || L == C::HDV, "row length");
           cp_async_8_at<i * KPP * 128>(stage + dthr, src, r >= 0 ? 8u : 0u);
         } else {
@@ -1870,11 +1873,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       constexpr int L = decltype(l_c)::value;
       static_for<0, NKEYS>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
-        if constexpr (FMT == 3) {
-          const uint32_t a = stage + dthr + i * KPP * 128;
-          const uint2 u = ld_shared_u2(a);
-          st_shared_u4(a, fp4x8_to_bf16x8(u.x, u.y, (ch >> 1) & 3));
-        } else if constexpr (!C::SPLIT) {
+        if constexpr (!C::SPLIT) {
           const uint32_t a = stage + dthr + i * KPP * 128;
           st_shared_u4(a, fp8x8_to_bf16x8<FMT>(ld_shared_u2(a)));
         } else {
@@ -1889,19 +1888,64 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       });
       fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
     };
+    // A 4-bit pool's tile: a thread takes chunk q4 (16 code bytes, 32 elements)
+    // of keys key4 + KP4 i, and writes their bf16, four 16-byte chunks a key.
+    // The codes land in the first of the four and the word that holds their
+    // two block scales in the second, so again no thread overwrites another's
+    // codes.  Eight neighbouring lanes hold eight keys of one chunk: their
+    // stores lie in different banks.  (Four code bytes a thread and key, laid
+    // out as the fp8 codes are, took 128 copy instructions of ten passes each
+    // a tile: 1039 us on 64 x (8192 + 16).)
+    constexpr int Q4 = C::Q4, KP4 = C::KP4, N4 = C::BN / KP4;
+    const int q4 = lane / (32 / Q4);
+    const int key4 = (warp - C::COPY_WARP0) * (32 / Q4) + lane % (32 / Q4);
+    const uint32_t d4 = (uint32_t)(q4 >> 1) * (C::BN * 128) + (uint32_t)key4 * 128u;
+    const uint32_t c4 = (uint32_t)((4 * (q4 & 1)) ^ (key4 & 7));  // sub-chunk s: chunk c4 ^ s
+    auto issue_4 = [&](uint32_t stage, const uint8_t *base, int64_t stride, const uint8_t *sbase4,
+                       int64_t sstride, const int *rows) {
+#pragma unroll
+      for (int i = 0; i < N4; ++i) {
+        const int64_t r = max(rows[i], 0);
+        const uint32_t at = stage + d4 + i * (KP4 * 128);
+        cp_async_16(at + (c4 << 4), base + r * stride, rows[i] >= 0 ? 16u : 0u);
+        cp_async_4_at<0>(at + ((c4 ^ 1) << 4), sbase4 + r * sstride, rows[i] >= 0 ? 4u : 0u);
+      }
+    };
+    auto convert_4 = [&](uint32_t stage) {
+      uint4 codes[N4];
+      uint32_t sw[N4];
+      // every load goes out before the first store (they keep their order)
+#pragma unroll
+      for (int i = 0; i < N4; ++i) {
+        const uint32_t at = stage + d4 + i * (KP4 * 128);
+        codes[i] = ld_shared_u4(at + (c4 << 4));
+        sw[i] = ld_shared_u2(at + ((c4 ^ 1) << 4)).x;
+      }
+#pragma unroll
+      for (int i = 0; i < N4; ++i) {
+        const uint32_t at = stage + d4 + i * (KP4 * 128);
+        const uint32_t two = sw[i] >> (16 * (q4 & 1));
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub)
+          st_shared_u4(at + ((c4 ^ sub) << 4), fp4x8_to_bf16x8(w[sub], two >> (8 * (sub >> 1))));
+      }
+      fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
+    };
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
       const WorkUnit w = p.units[p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
-      constexpr int CB = FMT == 3 ? 4 : 8;  // code bytes of a chunk
+      // the thread's chunk of a row's codes (and, 4-bit, its word of block scales)
+      const int cb = FMT == 3 ? q4 * 16 : ch * 8;
       const uint8_t *kp8 =
-          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + ch * CB;
+          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + cb;
       const uint8_t *vp8 =
-          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + ch * CB;
-      const uint8_t *ks8 = FMT == 3 ? p.k_bs + (int64_t)w.kvh * p.kbs_sh + (ch >> 3) * 4 : nullptr;
-      const uint8_t *vs8 = FMT == 3 ? p.v_bs + (int64_t)w.kvh * p.vbs_sh + (ch >> 3) * 4 : nullptr;
+          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + cb;
+      const uint8_t *ks4 = FMT == 3 ? p.k_bs + (int64_t)w.kvh * p.kbs_sh + (q4 >> 1) * 4 : nullptr;
+      const uint8_t *vs4 = FMT == 3 ? p.v_bs + (int64_t)w.kvh * p.vbs_sh + (q4 >> 1) * 4 : nullptr;
       const bf16 *kx = p.k_ext + (int64_t)w.kvh * p.ke_sh + ch * 8;
       const bf16 *vx = p.v_ext + (int64_t)w.kvh * p.ve_sh + ch * 8;
       int rows[NKEYS];
@@ -1910,9 +1954,18 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         tile_keys(w, j, kb, ke);
         return MODE == kTwoStage && kb >= w.k_split;
       };
-      auto fetch = [&]() -> bool {
+      auto fetch = [&]([[maybe_unused]] bool from_ext) -> bool {
         const int is = ic % C::NI;
         if (!mbar_wait(&i_full[is], (ic / C::NI) & 1u, abort_flag, p.wait_ns)) return false;
+        if (FMT == 3 && !from_ext) {  // the 4-bit layout of the ring
+          const int *ring = reinterpret_cast<const int *>(smem + C::OFF_I + is * C::I_BYTES) + key4 * N4;
+#pragma unroll
+          for (int q = 0; q < N4; ++q) rows[q] = ring[q];
+          __syncwarp();  // the warp is done with the ring slot
+          if (lane == 0) mbar_arrive(&i_empty[is]);
+          ++ic;
+          return true;
+        }
         const int4 *ring =
             reinterpret_cast<const int4 *>(smem + C::OFF_I + is * C::I_BYTES) + key0 * (NKEYS / 4);
 #pragma unroll
@@ -1938,7 +1991,8 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, kx, p.ke_st, rows, K_LEN);
           cp_async_arrive_noinc(&k_full[ks]);
         } else {
-          issue_raw(stage, kp8, p.kb_ss, ks8, p.kbs_ss, rows, K_LEN);
+          if constexpr (FMT == 3) issue_4(stage, kp8, p.kb_ss, ks4, p.kbs_ss, rows);
+          else issue_raw(stage, kp8, p.kb_ss, rows, K_LEN);
         }
         cp_async_commit();
         ++kc;
@@ -1954,7 +2008,8 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, vx, p.ve_st, rows, V_LEN);
           cp_async_arrive_noinc(&v_full[vs]);
         } else {
-          issue_raw(stage, vp8, p.vb_ss, vs8, p.vbs_ss, rows, V_LEN);
+          if constexpr (FMT == 3) issue_4(stage, vp8, p.vb_ss, vs4, p.vbs_ss, rows);
+          else issue_raw(stage, vp8, p.vb_ss, rows, V_LEN);
         }
         cp_async_commit();
         ++vc;
@@ -1966,7 +2021,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         // are converted as soon as they land
         for (int j = 0; j < nt; ++j) {
           const bool ext = tile_from_ext(j);
-          if (!fetch() || !issue_k(ext)) {
+          if (!fetch(ext) || !issue_k(ext)) {
             ok = false;
             break;
           }
@@ -1990,7 +2045,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         continue;
       }
       bool ext_j = tile_from_ext(0);
-      if (!fetch() || !issue_k(ext_j) || !issue_v(ext_j)) {
+      if (!fetch(ext_j) || !issue_k(ext_j) || !issue_v(ext_j)) {
         ok = false;
         break;
       }
@@ -1998,7 +2053,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         const int ks_j = (kc - 1) % NK_, vs_j = (vc - 1) % C::NV;
         const bool more = j + 1 < nt;
         const bool ext_n = more && tile_from_ext(j + 1);
-        if (more && (!fetch() || !issue_k(ext_n))) {
+        if (more && (!fetch(ext_n) || !issue_k(ext_n))) {
           ok = false;
           break;
         }
@@ -2006,19 +2061,32 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           // groups issued after K(j): V(j), and K(j+1) if there is one
           if (more) cp_async_wait_group<2>();
           else cp_async_wait_group<1>();
-          convert(sbase + K0 + ks_j * C::K_BYTES, K_LEN);
+          if constexpr (FMT == 3) convert_4(sbase + K0 + ks_j * C::K_BYTES);
+          else convert(sbase + K0 + ks_j * C::K_BYTES, K_LEN);
           mbar_arrive(&k_full[ks_j]);
         }
-        if (more && !issue_v(ext_n)) {
+        // A 4-bit pool converts V(j) before V(j+1) goes out: by then the
+        // product that reads V(j+1)'s stage is done, where the other order
+        // waits for it between the two conversions (768 against %%EXT us on
+        // 64 x (8192 + 16)).
+        constexpr bool V_FIRST = FMT == 3;
+        if (!V_FIRST && more && !issue_v(ext_n)) {
           ok = false;
           break;
         }
         if (!ext_j) {
-          // groups issued after V(j): K(j+1) and V(j+1) if there are
-          if (more) cp_async_wait_group<2>();
-          else cp_async_wait_group<0>();
-          convert(sbase + C::OFF_V + vs_j * C::V_BYTES, V_LEN);
+          // groups issued after V(j): K(j+1) and V(j+1) (V_FIRST: K(j+1)) if
+          // there are
+          if (!more) cp_async_wait_group<0>();
+          else if (V_FIRST) cp_async_wait_group<1>();
+          else cp_async_wait_group<2>();
+          if constexpr (FMT == 3) convert_4(sbase + C::OFF_V + vs_j * C::V_BYTES);
+          else convert(sbase + C::OFF_V + vs_j * C::V_BYTES, V_LEN);
           mbar_arrive(&v_full[vs_j]);
+        }
+        if (V_FIRST && more && !issue_v(ext_n)) {
+          ok = false;
+          break;
         }
         ext_j = ext_n;
       }
@@ -2456,6 +2524,8 @@ int launch_attention(const AttnArgs &a) {
   sp.n_dsplit = 1;
   sp.window = a.window;
   sp.first = a.window > 0 ? a.first_tokens : 0;
+  // a 4-bit row is 64 bytes, and four heads' block scales share a DRAM sector
+  sp.head_minor = a.kv_fmt == kKvFp4;
   sp.num_q_tokens = nq;
   sp.unit_target = mla ? 4 * pairs : L.unit_target;
   // MLA decode with one KV head: a stream partition, one share of the key
