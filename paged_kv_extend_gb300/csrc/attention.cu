@@ -656,7 +656,9 @@ struct Cfg {
   static constexpr int NRAW = 4;
   static constexpr int RAW_BYTES = BN * LQ;  // the fp8 codes of one K or V tile
   static constexpr int OFF_RAW = OFF_Q + Q_BYTES;
-  static constexpr int N_BARS = 17 + 2 * NK + 2 * NV + 2 * NI + 2 * NRAW;
+  // (extend over a 4-bit pool: the raw barriers are one per K and V stage)
+  static constexpr int N_RAW_BARS = 2 * NRAW > NK + NV ? 2 * NRAW : NK + NV;
+  static constexpr int N_BARS = 17 + 2 * NK + 2 * NV + 2 * NI + N_RAW_BARS;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 1024;  // + alignment slack
   // S0 | S1 | O0 | O1, 128 columns each (split dims: S0 | unused | O0 of Lv)
   static constexpr int TMEM_COLS = 512;
@@ -672,8 +674,6 @@ struct Cfg {
   // swizzle atom (chunk t % 8 of every atom, keys t / 8 + 16 i) for the
   // split dims, whose 24 or 36 chunks per row do not divide 128 threads
   static constexpr int KPP = SPLIT ? 16 : COPY_THREADS / (HD / 8);
-  // a 4-bit pool: 16-byte code chunks of a row (32 elements each), keys per pass
-  static constexpr int Q4 = SPLIT ? 4 : HD / 32, KP4 = COPY_THREADS / Q4;
   // Registers: the kernel launches with REGS_LAUNCH per thread (checked at
   // build time); the softmax warpgroups take REGS_SOFTMAX, the other two
   // give back down to REGS_OTHER.  The split must add up exactly.
@@ -808,20 +808,16 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8_scaled(uint4 v) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Eight e2m1 codes times their e4m3 block scale (sw's low byte) as eight
-// bf16: exact, since the product has six significant bits.  The f16 of a code
-// shifted by the three bits that bf16's exponent is longer is its bf16 times
-// 2^-112; the scale brings the 2^112 (448 * 2^112 is in range).
-__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, uint32_t sw) {
-  const float sc = __low2float(e4m3x2_to_f16x2(sw & 0xFFu)) * 0x1p112f;
-  const __nv_bfloat162 s2 = __float2bfloat162_rn(sc);
+// Eight e2m1 codes times their block scale (a pair of f16) as eight bf16:
+// exact, since the product has six significant bits.  (27 clocks a word on a
+// quarter SM; shifting the f16 bits to bf16's exponent, 37.)
+__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, __half2 s2) {
   uint32_t h[4], out[4];
   e2m1x8_to_f16(codes, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t b = (h[i] & 0x80008000u) | ((h[i] >> 3) & 0x0FC00FC0u);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), s2);
-    out[i] = *reinterpret_cast<const uint32_t *>(&x);
+    const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s2));
+    out[i] = pack_bf16(f.x, f.y);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
@@ -846,7 +842,9 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   constexpr int NK_ = F16 ? C::NK - 1 : C::NK;
   constexpr uint32_t K0 = C::OFF_K + (F16 ? C::K_BYTES : 0);
   // decode over fp8: warps 10-11 copy the codes, warps 12-13 convert the K
-  // tiles and 14-15 the V tiles
+  // tiles and 14-15 the V tiles; extend over a 4-bit pool likewise (warp 10
+  // copies K, warp 11 V)
+  constexpr bool F4 = FMT == 3;
   constexpr int RAW_THREADS = 64, CONV_THREADS = 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -887,25 +885,29 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       // softmax, MMA and copy warps (+ the two writer warps with the fused
       // KV write)
       mbar_init(&bars[B_U_EMPTY + i],
-                8 + 1 + C::COPY_THREADS / 32 + (kv_write || F16 ? 2 : 0));
+                8 + 1 + C::COPY_THREADS / 32 + (kv_write || F16 || F4 ? 2 : 0));
     }
     // stages are filled by the copy warps, or by the converting warps in
     // decode over fp8
     for (int s = 0; s < C::NK; ++s) {
-      mbar_init(&k_full[s], F16 ? CONV_THREADS : C::COPY_THREADS);
+      mbar_init(&k_full[s], F16 || F4 ? CONV_THREADS : C::COPY_THREADS);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < C::NV; ++s) {
-      mbar_init(&v_full[s], F16 ? CONV_THREADS : C::COPY_THREADS);
+      mbar_init(&v_full[s], F16 || F4 ? CONV_THREADS : C::COPY_THREADS);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < C::NRAW; ++s) {
-      mbar_init(&raw_full[s], RAW_THREADS);
-      mbar_init(&raw_empty[s], CONV_THREADS);
+    if constexpr (F4) {  // codes of a K or V stage landed: the copying warp's lanes
+      for (int s = 0; s < C::NK + C::NV; ++s) mbar_init(&raw_full[s], 32);
+    } else {
+      for (int s = 0; s < C::NRAW; ++s) {
+        mbar_init(&raw_full[s], RAW_THREADS);
+        mbar_init(&raw_empty[s], CONV_THREADS);
+      }
     }
     for (int s = 0; s < C::NI; ++s) {
       mbar_init(&i_full[s], 32);
-      mbar_init(&i_empty[s], (F16 ? RAW_THREADS : C::COPY_THREADS) / 32);
+      mbar_init(&i_empty[s], (F16 || F4 ? RAW_THREADS : C::COPY_THREADS) / 32);
     }
     s_abort = 0;
     fence_barrier_init();
@@ -1545,8 +1547,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         }
         {
           // ring[key % KPP][key / KPP]: each copy thread's rows contiguous
-          // (a tile of a 4-bit pool: KP4 for KPP)
-          const int KPP = FMT == 3 && !from_ext ? C::KP4 : C::KPP, NK_T = C::BN / KPP;
+          constexpr int KPP = C::KPP, NK_T = C::BN / KPP;
           int *ring = reinterpret_cast<int *>(smem + C::OFF_I + is * C::I_BYTES);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1731,6 +1732,164 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     if (!ok) abort_cta(abort_flag, p.status, PKX_ETIMEOUT);
     cp_async_wait_all();
     }
+  } else if (F4) {
+    // ---------------------- extend over a 4-bit pool (warps 10-15)
+    // Warp 10 copies the K tiles into their stages and warp 11 the V tiles;
+    // warps 12-13 convert K and 14-15 V, in place.  Copies and conversions of
+    // K and of V thus wait for nothing of each other: with four warps that
+    // copied and converted both in turn, a tile was a chain of two conversions,
+    // two landings and the product that frees V's stage (678 us on
+    // 64 x (8192 + 16)).
+    // A lane takes chunk q4 (16 code bytes, 32 elements) of its keys: the codes
+    // land in the first of the four 16-byte chunks that their bf16 fill, and a
+    // key's block scales in the second chunk of its row, so that only lanes of
+    // the converting warp that holds all of a key overwrite what it still
+    // reads (they load first).  Neighbouring lanes hold consecutive keys of one
+    // chunk: their stores lie in different banks.  Every tile's landing is one
+    // phase of its stage's raw barrier; a tile of extend rows (bf16) passes
+    // through the converting warps untouched.
+    if constexpr (F4) {
+    static_assert(!C::SPLIT, "4-bit pools are built for Lq = Lv");
+    constexpr int Q4 = HD / 32, KPW = 32 / Q4;  // chunks of a row; keys of a warp's pass
+    static_assert(KPW == C::KPP, "the index ring's layout");
+    const int q4 = lane / KPW, kl = lane % KPW;
+    // sub-chunk s of the lane's four: chunk c4 ^ s of its row's swizzled atom
+    const uint32_t c4 = (uint32_t)((4 * (q4 & 1)) ^ (kl & 7));
+    const uint32_t d4 = (uint32_t)(q4 >> 1) * (C::BN * 128) + (uint32_t)kl * 128u;
+    const uint32_t sc4 = (uint32_t)kl * 128u + (((uint32_t)(kl & 7) ^ 1u) << 4);  // block scales
+    const bool is_v = warp == 11 || warp >= 14;
+    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+    uint64_t *landed = is_v ? raw_full + C::NK : raw_full;
+    const uint32_t n_stages = is_v ? C::NV : C::NK;
+    const uint32_t stages = sbase + (is_v ? C::OFF_V : K0);
+    constexpr uint32_t STAGE_BYTES = C::K_BYTES;
+    static_assert(C::K_BYTES == C::V_BYTES, "one stage size");
+    uint32_t c = 0, ic = 0;  // tiles of this warp's kind, so far
+    bool ok = true;
+    for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
+      const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
+      if (u < 0) break;
+      const WorkUnit w = p.units[p.uorder[u]];
+      const int nt = w.n_tiles;
+      auto from_ext = [&](int j) {
+        int kb, ke;
+        tile_keys(w, j, kb, ke);
+        return MODE == kTwoStage && kb >= w.k_split;
+      };
+      if (warp < 12) {
+        const uint8_t *pool = reinterpret_cast<const uint8_t *>(is_v ? p.v_pool : p.k_pool) +
+                              (int64_t)w.kvh * (is_v ? p.vb_sh : p.kb_sh) + q4 * 16;
+        const uint8_t *scales = (is_v ? p.v_bs : p.k_bs) +
+                                (int64_t)w.kvh * (is_v ? p.vbs_sh : p.kbs_sh);
+        const bf16 *ext = (is_v ? p.v_ext : p.k_ext) + (int64_t)w.kvh * (is_v ? p.ve_sh : p.ke_sh) +
+                          q4 * 32;
+        const int64_t ss = is_v ? p.vb_ss : p.kb_ss, sss = is_v ? p.vbs_ss : p.kbs_ss;
+        const int64_t es = is_v ? p.ve_st : p.ke_st;
+        constexpr int N = C::BN / KPW;  // keys of a lane
+        for (int j = 0; j < nt; ++j) {
+          const int is = ic % C::NI;
+          if (!mbar_wait(&i_full[is], (ic / C::NI) & 1u, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          int rows[N];
+          const int4 *ring = reinterpret_cast<const int4 *>(smem + C::OFF_I + is * C::I_BYTES) + kl * (N / 4);
+#pragma unroll
+          for (int q = 0; q < N / 4; ++q) {
+            const int4 v = ring[q];
+            rows[4 * q] = v.x;
+            rows[4 * q + 1] = v.y;
+            rows[4 * q + 2] = v.z;
+            rows[4 * q + 3] = v.w;
+          }
+          __syncwarp();  // the warp is done with the ring slot
+          if (lane == 0) mbar_arrive(&i_empty[is]);
+          ++ic;
+          const uint32_t st = c % n_stages;
+          if (c >= n_stages && !mbar_wait(&empty[st], ((c / n_stages) - 1) & 1u, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = stages + st * STAGE_BYTES + d4;
+          if (from_ext(j)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const bf16 *src = ext + (int64_t)max(rows[i], 0) * es;
+              const uint32_t n = rows[i] >= 0 ? 16u : 0u, dst = at + i * (KPW * 128);
+#pragma unroll
+              for (int sub = 0; sub < 4; ++sub)
+                cp_async_16(dst + ((c4 ^ sub) << 4), src + sub * 8, n);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const int64_t r = max(rows[i], 0);
+              const uint32_t dst = at + i * (KPW * 128);
+              cp_async_16(dst + (c4 << 4), pool + r * ss, rows[i] >= 0 ? 16u : 0u);
+            }
+            // block scales, one copy a key: chunk q4's lanes take every Q4-th pass
+#pragma unroll
+            for (int i = 0; i < N; i += Q4) {
+              int row = rows[i];
+#pragma unroll
+              for (int k = 1; k < Q4; ++k)
+                if (q4 == k) row = rows[i + k];
+              const uint32_t dst = stages + st * STAGE_BYTES + sc4 + (i + q4) * (KPW * 128);
+              const uint8_t *src = scales + (int64_t)max(row, 0) * sss;
+              if constexpr (HD == 128) cp_async_8_at<0>(dst, src, row >= 0 ? 8u : 0u);
+              else cp_async_4_at<0>(dst, src, row >= 0 ? 4u : 0u);
+            }
+          }
+          cp_async_arrive_noinc(&landed[st]);
+          ++c;
+        }
+      } else {
+        constexpr int N = C::BN / (2 * KPW);  // keys of a lane (two warps a tile)
+        for (int j = 0; j < nt; ++j) {
+          const uint32_t st = c % n_stages;
+          if (!mbar_wait(&landed[st], (c / n_stages) & 1u, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          if (!from_ext(j)) {
+            const uint32_t tile = stages + st * STAGE_BYTES + (warp & 1) * (KPW * 128);
+#pragma unroll
+            for (int i0 = 0; i0 < N; i0 += 4) {
+              uint4 codes[4];
+              __half2 sc[4][2];  // the chunk's two block scales, each twice
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t key = tile + (i0 + i) * (2 * KPW * 128);
+                codes[i] = ld_shared_u4(key + d4 + (c4 << 4));
+                const uint2 sw = ld_shared_u2(key + sc4);
+                const uint32_t two = (q4 & 2 ? sw.y : sw.x) >> (16 * (q4 & 1));
+                const __half2 s = e4m3x2_to_f16x2(two & 0xFFFFu);
+                sc[i][0] = __low2half2(s);
+                sc[i][1] = __high2half2(s);
+              }
+              __syncwarp();  // every lane has read before any writes
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t dst = tile + d4 + (i0 + i) * (2 * KPW * 128);
+                const uint32_t x[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                uint4 out[4];  // all four before a store, for the chains to overlap
+#pragma unroll
+                for (int sub = 0; sub < 4; ++sub)
+                  out[sub] = fp4x8_to_bf16x8(x[sub], sc[i][sub >> 1]);
+#pragma unroll
+                for (int sub = 0; sub < 4; ++sub) st_shared_u4(dst + ((c4 ^ sub) << 4), out[sub]);
+              }
+            }
+          }
+          fence_proxy_async_smem();  // copies' and this warp's writes -> tensor-core reads
+          mbar_arrive(&full[st]);
+          ++c;
+        }
+      }
+    }
+    if (!ok) abort_cta(abort_flag, p.status, PKX_ETIMEOUT);
+    cp_async_wait_all();
+    }
   } else if (warp < C::COPY_WARP0 + C::COPY_THREADS / 32) {
     // ------------------------------------------------ K/V copies (4 warps)
     // Thread ct copies 16-byte chunk ch = ct % CPR of keys key0 + KPP * i
@@ -1778,7 +1937,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     uint32_t kc = 0, vc = 0, ic = 0;
     [[maybe_unused]] uint32_t qc = 0;
     bool ok = true;
-    if constexpr (FMT == 0) {
+    if constexpr (FMT == 0 || F4) {  // (F4 has its own warps, above)
       for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
         const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
         if (u < 0) break;
@@ -1888,64 +2047,16 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       });
       fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
     };
-    // A 4-bit pool's tile: a thread takes chunk q4 (16 code bytes, 32 elements)
-    // of keys key4 + KP4 i, and writes their bf16, four 16-byte chunks a key.
-    // The codes land in the first of the four and the word that holds their
-    // two block scales in the second, so again no thread overwrites another's
-    // codes.  Eight neighbouring lanes hold eight keys of one chunk: their
-    // stores lie in different banks.  (Four code bytes a thread and key, laid
-    // out as the fp8 codes are, took 128 copy instructions of ten passes each
-    // a tile: 1039 us on 64 x (8192 + 16).)
-    constexpr int Q4 = C::Q4, KP4 = C::KP4, N4 = C::BN / KP4;
-    const int q4 = lane / (32 / Q4);
-    const int key4 = (warp - C::COPY_WARP0) * (32 / Q4) + lane % (32 / Q4);
-    const uint32_t d4 = (uint32_t)(q4 >> 1) * (C::BN * 128) + (uint32_t)key4 * 128u;
-    const uint32_t c4 = (uint32_t)((4 * (q4 & 1)) ^ (key4 & 7));  // sub-chunk s: chunk c4 ^ s
-    auto issue_4 = [&](uint32_t stage, const uint8_t *base, int64_t stride, const uint8_t *sbase4,
-                       int64_t sstride, const int *rows) {
-#pragma unroll
-      for (int i = 0; i < N4; ++i) {
-        const int64_t r = max(rows[i], 0);
-        const uint32_t at = stage + d4 + i * (KP4 * 128);
-        cp_async_16(at + (c4 << 4), base + r * stride, rows[i] >= 0 ? 16u : 0u);
-        cp_async_4_at<0>(at + ((c4 ^ 1) << 4), sbase4 + r * sstride, rows[i] >= 0 ? 4u : 0u);
-      }
-    };
-    auto convert_4 = [&](uint32_t stage) {
-      uint4 codes[N4];
-      uint32_t sw[N4];
-      // every load goes out before the first store (they keep their order)
-#pragma unroll
-      for (int i = 0; i < N4; ++i) {
-        const uint32_t at = stage + d4 + i * (KP4 * 128);
-        codes[i] = ld_shared_u4(at + (c4 << 4));
-        sw[i] = ld_shared_u2(at + ((c4 ^ 1) << 4)).x;
-      }
-#pragma unroll
-      for (int i = 0; i < N4; ++i) {
-        const uint32_t at = stage + d4 + i * (KP4 * 128);
-        const uint32_t two = sw[i] >> (16 * (q4 & 1));
-        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub)
-          st_shared_u4(at + ((c4 ^ sub) << 4), fp4x8_to_bf16x8(w[sub], two >> (8 * (sub >> 1))));
-      }
-      fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
-    };
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
       const WorkUnit w = p.units[p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
-      // the thread's chunk of a row's codes (and, 4-bit, its word of block scales)
-      const int cb = FMT == 3 ? q4 * 16 : ch * 8;
       const uint8_t *kp8 =
-          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + cb;
+          reinterpret_cast<const uint8_t *>(p.k_pool) + (int64_t)w.kvh * p.kb_sh + ch * 8;
       const uint8_t *vp8 =
-          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + cb;
-      const uint8_t *ks4 = FMT == 3 ? p.k_bs + (int64_t)w.kvh * p.kbs_sh + (q4 >> 1) * 4 : nullptr;
-      const uint8_t *vs4 = FMT == 3 ? p.v_bs + (int64_t)w.kvh * p.vbs_sh + (q4 >> 1) * 4 : nullptr;
+          reinterpret_cast<const uint8_t *>(p.v_pool) + (int64_t)w.kvh * p.vb_sh + ch * 8;
       const bf16 *kx = p.k_ext + (int64_t)w.kvh * p.ke_sh + ch * 8;
       const bf16 *vx = p.v_ext + (int64_t)w.kvh * p.ve_sh + ch * 8;
       int rows[NKEYS];
@@ -1954,18 +2065,9 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         tile_keys(w, j, kb, ke);
         return MODE == kTwoStage && kb >= w.k_split;
       };
-      auto fetch = [&]([[maybe_unused]] bool from_ext) -> bool {
+      auto fetch = [&]() -> bool {
         const int is = ic % C::NI;
         if (!mbar_wait(&i_full[is], (ic / C::NI) & 1u, abort_flag, p.wait_ns)) return false;
-        if (FMT == 3 && !from_ext) {  // the 4-bit layout of the ring
-          const int *ring = reinterpret_cast<const int *>(smem + C::OFF_I + is * C::I_BYTES) + key4 * N4;
-#pragma unroll
-          for (int q = 0; q < N4; ++q) rows[q] = ring[q];
-          __syncwarp();  // the warp is done with the ring slot
-          if (lane == 0) mbar_arrive(&i_empty[is]);
-          ++ic;
-          return true;
-        }
         const int4 *ring =
             reinterpret_cast<const int4 *>(smem + C::OFF_I + is * C::I_BYTES) + key0 * (NKEYS / 4);
 #pragma unroll
@@ -1991,8 +2093,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, kx, p.ke_st, rows, K_LEN);
           cp_async_arrive_noinc(&k_full[ks]);
         } else {
-          if constexpr (FMT == 3) issue_4(stage, kp8, p.kb_ss, ks4, p.kbs_ss, rows);
-          else issue_raw(stage, kp8, p.kb_ss, rows, K_LEN);
+          issue_raw(stage, kp8, p.kb_ss, rows, K_LEN);
         }
         cp_async_commit();
         ++kc;
@@ -2008,8 +2109,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           copy_rows(stage, vx, p.ve_st, rows, V_LEN);
           cp_async_arrive_noinc(&v_full[vs]);
         } else {
-          if constexpr (FMT == 3) issue_4(stage, vp8, p.vb_ss, vs4, p.vbs_ss, rows);
-          else issue_raw(stage, vp8, p.vb_ss, rows, V_LEN);
+          issue_raw(stage, vp8, p.vb_ss, rows, V_LEN);
         }
         cp_async_commit();
         ++vc;
@@ -2021,7 +2121,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         // are converted as soon as they land
         for (int j = 0; j < nt; ++j) {
           const bool ext = tile_from_ext(j);
-          if (!fetch(ext) || !issue_k(ext)) {
+          if (!fetch() || !issue_k(ext)) {
             ok = false;
             break;
           }
@@ -2045,7 +2145,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         continue;
       }
       bool ext_j = tile_from_ext(0);
-      if (!fetch(ext_j) || !issue_k(ext_j) || !issue_v(ext_j)) {
+      if (!fetch() || !issue_k(ext_j) || !issue_v(ext_j)) {
         ok = false;
         break;
       }
@@ -2053,7 +2153,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         const int ks_j = (kc - 1) % NK_, vs_j = (vc - 1) % C::NV;
         const bool more = j + 1 < nt;
         const bool ext_n = more && tile_from_ext(j + 1);
-        if (more && (!fetch(ext_n) || !issue_k(ext_n))) {
+        if (more && (!fetch() || !issue_k(ext_n))) {
           ok = false;
           break;
         }
@@ -2061,32 +2161,19 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           // groups issued after K(j): V(j), and K(j+1) if there is one
           if (more) cp_async_wait_group<2>();
           else cp_async_wait_group<1>();
-          if constexpr (FMT == 3) convert_4(sbase + K0 + ks_j * C::K_BYTES);
-          else convert(sbase + K0 + ks_j * C::K_BYTES, K_LEN);
+          convert(sbase + K0 + ks_j * C::K_BYTES, K_LEN);
           mbar_arrive(&k_full[ks_j]);
         }
-        // A 4-bit pool converts V(j) before V(j+1) goes out: by then the
-        // product that reads V(j+1)'s stage is done, where the other order
-        // waits for it between the two conversions (768 against %%EXT us on
-        // 64 x (8192 + 16)).
-        constexpr bool V_FIRST = FMT == 3;
-        if (!V_FIRST && more && !issue_v(ext_n)) {
+        if (more && !issue_v(ext_n)) {
           ok = false;
           break;
         }
         if (!ext_j) {
-          // groups issued after V(j): K(j+1) and V(j+1) (V_FIRST: K(j+1)) if
-          // there are
-          if (!more) cp_async_wait_group<0>();
-          else if (V_FIRST) cp_async_wait_group<1>();
-          else cp_async_wait_group<2>();
-          if constexpr (FMT == 3) convert_4(sbase + C::OFF_V + vs_j * C::V_BYTES);
-          else convert(sbase + C::OFF_V + vs_j * C::V_BYTES, V_LEN);
+          // groups issued after V(j): K(j+1) and V(j+1) if there are
+          if (more) cp_async_wait_group<2>();
+          else cp_async_wait_group<0>();
+          convert(sbase + C::OFF_V + vs_j * C::V_BYTES, V_LEN);
           mbar_arrive(&v_full[vs_j]);
-        }
-        if (V_FIRST && more && !issue_v(ext_n)) {
-          ok = false;
-          break;
         }
         ext_j = ext_n;
       }
