@@ -44,6 +44,8 @@ def _to_dev(codes, bscale):
 @pytest.mark.parametrize("n,hkv,lk,lv,ks,vs,amp", [
     (1, 1, 64, 64, 1.0, 1.0, 1.0), (77, 8, 128, 128, 0.373, 2.5, 3.0), (130, 3, 64, 64, 1.0, 1.0, 1e-3),
     (63, 2, 16, 48, 1.0, 0.7, 2e4), (19, 1, 576, 512, 0.051, 1.0, 1.0), (700, 5, 128, 64, 3.1, 1.0, 40.0),
+    (5000, 3, 64, 128, 0.125, 2.0 ** 20, 5.0), (33, 40, 128, 128, 2.0 ** -64, 2.0 ** 64, 1.0),
+    (33, 2, 128, 128, 2.0 ** -65, 2.0 ** 65, 1e-19), (9, 64, 256, 48, 1.0, 1.0, 1.0),
 ])
 def test_write_bit_exact(n, hkv, lk, lv, ks, vs, amp):
     """Codes and block scales of every row; strided inputs; slots that are
@@ -87,7 +89,7 @@ def test_write_borders():
              [3e38] * 8 + [-3e38] * 8, [6.375 * 2.0 ** i for i in range(-8, 8)]]
     x = torch.tensor(rows).bfloat16()[:, None]  # [n, 1, 16]
     n = x.shape[0]
-    for scale in (1.0, 0.37):
+    for scale in (1.0, 0.37, 2.0 ** -7, 64.0):
         c, b = R.pack(x, scale)
         kc = torch.zeros(n, 1, 8, dtype=torch.uint8, device=DEV)
         kb = torch.zeros(n, 1, 1, dtype=torch.float8_e4m3fn, device=DEV)
@@ -96,6 +98,27 @@ def test_write_borders():
         assert torch.equal(kb.view(torch.uint8).cpu(), b)
         assert torch.equal(kc.cpu(), c)
     assert int(b[-4]) == 0x7F and int(b[-3]) == 0x7F  # the rows with a NaN
+
+
+@pytest.mark.parametrize("scale", [1.0, 4.0, 0.3])
+def test_write_every_bf16(scale):
+    """Every finite bf16 next to block maxima of all mantissas, so that every
+    quotient of a value and a block scale is met at all its roundings."""
+    g = _gen(17)
+    bits = torch.arange(0x0080, 0x7F80, dtype=torch.int32)
+    vals = bits.to(torch.int16).view(torch.bfloat16)
+    near = vals[(vals > 2.0 ** -12) & (vals < 2.0 ** 12)]
+    n = 60000
+    top = near[torch.randint(0, near.numel(), (n,), generator=g)].float()
+    x = (top[:, None] * torch.rand(n, 16, generator=g)).bfloat16()
+    x[:, 0] = top.bfloat16()
+    x[:, 1] = vals[torch.randint(0, vals.numel(), (n,), generator=g)]
+    x = (x.float() * (torch.randint(0, 2, x.shape, generator=g) * 2 - 1)).bfloat16()[:, None]
+    c, b = R.pack(x, scale)
+    kc = torch.zeros(n, 1, 8, dtype=torch.uint8, device=DEV)
+    kb = torch.zeros(n, 1, 1, dtype=torch.float8_e4m3fn, device=DEV)
+    pkx.set_kv_buffer_fp4(kc, kb, None, None, torch.arange(n, device=DEV), x.to(DEV), k_scale=scale)
+    assert torch.equal(kb.view(torch.uint8).cpu(), b) and torch.equal(kc.cpu(), c)
 
 
 def test_write_nothing():
