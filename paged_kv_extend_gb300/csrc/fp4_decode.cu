@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kMergeThreads)
                             const float *__restrict__ po, __nv_bfloat16 *o, float *lse_out, int hq) {
   constexpr int E = D / 32;  // elements a lane holds
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps], s_o[kMergeWarps][D];
-  __shared__ int s_long[kMergeLong], s_n_long;
+  __shared__ int s_few[kMaxShares], s_long[kMergeLong];
+  __shared__ int2 s_count[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
@@ -685,9 +686,9 @@ __global__ void __launch_bounds__(kMergeThreads)
     l = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
-    // eight parts' loads go out together: one at a time, a row of 300 parts
+    // sixteen parts' loads go out together: one at a time, a row of 300 parts
     // was a chain of 38 loads a warp (16 us)
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int i = i0; i < n; i += step * U) {
       float pl[U], x[U][E];
 #pragma unroll
@@ -734,24 +735,44 @@ __global__ void __launch_bounds__(kMergeThreads)
       *reinterpret_cast<uint32_t *>(o + row * D + lane * E + e) = pack_bf16(a[e] * inv, a[e + 1] * inv);
     if (lse_out && lane == 0) lse_out[row] = l == 0.f ? -INFINITY : m + __logf(l);
   };
-  for (int64_t i = (int64_t)blockIdx.x * kMergeWarps + warp; i < (int64_t)max_shares * hq;
-       i += (int64_t)gridDim.x * kMergeWarps) {
-    const int share = (int)(i / hq), h = (int)(i - (int64_t)share * hq);
+  // the split sequences' shares, in order (every CTA takes its rows by their
+  // place in this list, so it has to be the same list in all of them): of few
+  // parts in s_few, of many in s_long
+  int n_few = 0, n_long = 0;
+  for (int base = 0; base < max_shares; base += kMergeThreads) {
+    const int i = base + (int)threadIdx.x;
+    const int n = i < max_shares ? entries[i].y : 0;
+    const unsigned few = __ballot_sync(0xffffffffu, n > 0 && n <= kMergeWarpParts);
+    const unsigned many = __ballot_sync(0xffffffffu, n > kMergeWarpParts);
+    if (lane == 0) s_count[warp] = make_int2(__popc(few), __popc(many));
+    __syncthreads();
+    int at_few = n_few, at_long = n_long;
+    for (int w = 0; w < kMergeWarps; ++w) {
+      const int2 c = s_count[w];
+      if (w < warp) {
+        at_few += c.x;
+        at_long += c.y;
+      }
+      n_few += c.x;
+      n_long += c.y;
+    }
+    const unsigned below = (1u << lane) - 1u;
+    if (n > kMergeWarpParts) {
+      const int at = at_long + __popc(many & below);
+      if (at < kMergeLong) s_long[at] = i;
+    } else if (n > 0) {
+      s_few[at_few + __popc(few & below)] = i;
+    }
+    __syncthreads();
+  }
+  n_long = min(n_long, kMergeLong);
+  for (int i = blockIdx.x * kMergeWarps + warp; i < n_few * hq; i += gridDim.x * kMergeWarps) {
+    const int k = i / hq, h = i - k * hq, share = s_few[k];
     const int2 e = entries[share];
-    if (e.y == 0 || e.y > kMergeWarpParts) continue;
     float m, l, a[E];
     gather(share, h, 0, e.y, 1, m, l, a);
     store(e.x, h, m, l, a);
   }
-  if (threadIdx.x == 0) s_n_long = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < max_shares; i += kMergeThreads)
-    if (entries[i].y > kMergeWarpParts) {
-      const int at = atomicAdd(&s_n_long, 1);  // their order changes no result
-      if (at < kMergeLong) s_long[at] = i;
-    }
-  __syncthreads();
-  const int n_long = min(s_n_long, kMergeLong);
   for (int k = 0; k < n_long; ++k) {
     const int share = s_long[k];
     const int2 e = entries[share];

@@ -150,8 +150,11 @@ def _on(dev: torch.device, fn, *args):
     CUDA device and that device's current stream as the last argument: the
     library launches on the current device, so a tensor on another GPU than
     the current one still gets its kernels on its own device."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, stream)
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return fn(*args, stream)
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -651,33 +654,36 @@ def expand_paged_kv_indices(kv_indptr, kv_indices, kv_last_page_len, page_size,
 
 # ------------------------------------------------------------- 4-bit pools
 def _fp4_half(codes, scales, name):
-    """Strides (bytes) of one half of a 4-bit pool: uint8 codes
+    """Slots, heads, elements of a row and byte strides (codes slot, head, block
+    scales slot, head) of one half of a 4-bit pool: uint8 codes
     [slots, hkv, d / 2] and float8_e4m3fn block scales [slots, hkv, d / 16]."""
-    if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.stride(2) != 1 or not codes.is_cuda:
+    shape, sshape = tuple(codes.shape), tuple(scales.shape)
+    st, sst = codes.stride(), scales.stride()
+    if len(shape) != 3 or codes.dtype != torch.uint8 or st[2] != 1 or not codes.is_cuda:
         raise ValueError(f"{name} must be a CUDA uint8 [slots, heads, dim / 2] tensor with a "
                          "contiguous last dim")
-    if scales.dim() != 3 or scales.dtype != torch.float8_e4m3fn or scales.stride(2) != 1 or \
-            scales.device != codes.device:
+    if len(sshape) != 3 or scales.dtype != torch.float8_e4m3fn or \
+            (sst[2] != 1 and sshape[2] > 1) or scales.device != codes.device:
         raise ValueError(f"{name}'s block scales must be a float8_e4m3fn [slots, heads, dim / 16] "
                          f"tensor on {codes.device} with a contiguous last dim")
-    if scales.shape[:2] != codes.shape[:2] or scales.shape[2] * 8 != codes.shape[2]:
-        raise ValueError(f"{name} [slots, heads, dim / 2] {tuple(codes.shape)} and its block "
-                         f"scales [slots, heads, dim / 16] {tuple(scales.shape)} disagree")
-    return codes.stride(0), codes.stride(1), scales.stride(0), scales.stride(1)
+    if sshape[:2] != shape[:2] or sshape[2] * 8 != shape[2]:
+        raise ValueError(f"{name} [slots, heads, dim / 2] {shape} and its block scales [slots, "
+                         f"heads, dim / 16] {sshape} disagree")
+    return (shape[0], shape[1], 2 * shape[2]), (st[0], st[1], sst[0], sst[1])
 
 
 def _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale):
-    """Byte strides of both halves, in the order of the attention calls."""
-    k = _fp4_half(k_buffer, k_block_scale, "k_buffer")
-    v = _fp4_half(v_buffer, v_block_scale, "v_buffer")
-    if v_buffer.shape[:2] != k_buffer.shape[:2] or v_buffer.device != k_buffer.device:
+    """(slots, heads, Lk, Lv), K byte strides, V byte strides."""
+    kd, ks = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+    vd, vs = _fp4_half(v_buffer, v_block_scale, "v_buffer")
+    if vd[:2] != kd[:2] or v_buffer.device != k_buffer.device:
         raise ValueError("k_buffer and v_buffer must have the same slots, heads and device")
-    return *k, *v
+    return (*kd, vd[2]), ks, vs
 
 
 def _one_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
+    for name, t in tensors.items():  # (indices first: cheap, and enough between GPUs)
+        if t is not None and t.get_device() != dev.index:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
@@ -692,25 +698,27 @@ def set_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, cache_lo
     ks = _rows(k, "k")
     n, hkv, lk = k.shape
     _check_len(cache_loc, n, "cache_loc")
-    kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
-    if k_buffer.shape[1:] != (hkv, lk // 2) or lk % 16:
-        raise ValueError(f"k {tuple(k.shape)} does not fit k_buffer {tuple(k_buffer.shape)}")
     lv, vs, vb = 0, (0, 0), (0, 0, 0, 0)
-    if v is not None:
+    if v is None:
+        (slots, *row), kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+        v_buffer_ptr = v_scale_ptr = None
+    else:
+        (slots, *row, row_v), kb, vb = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
         vs = _rows(v, "v")
         lv = v.shape[2]
-        _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
-        vb = _fp4_half(v_buffer, v_block_scale, "v_buffer")
-        if v.shape[:2] != (n, hkv) or v_buffer.shape[2] != lv // 2 or lv % 16:
-            raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)} and v_buffer "
-                             f"{tuple(v_buffer.shape)}")
+        if tuple(v.shape) != (n, hkv, row_v):
+            raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)} and v_buffer's "
+                             f"rows of {row_v} elements")
+        v_buffer_ptr, v_scale_ptr = _ptr(v_buffer), _ptr(v_block_scale)
+    if row != [hkv, lk]:
+        raise ValueError(f"k {tuple(k.shape)} does not fit k_buffer's rows of {row} heads and elements")
     _one_device(k.device, k_buffer=k_buffer, cache_loc=cache_loc, v=v)
     _check(_on(
         k.device, lib.pkx_set_kv_buffer_fp4,
         _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _ptr(cache_loc) if n else None, n, hkv,
         lk, lv, float(k_scale), float(v_scale), _ptr(k_buffer), kb[0], kb[1],
-        _ptr(k_block_scale), kb[2], kb[3], _ptr(v_buffer) if v is not None else None, vb[0], vb[1],
-        _ptr(v_block_scale) if v is not None else None, vb[2], vb[3], k_buffer.shape[0]))
+        _ptr(k_block_scale), kb[2], kb[3], v_buffer_ptr, vb[0], vb[1], v_scale_ptr, vb[2], vb[3],
+        slots))
     return k_buffer, k_block_scale, v_buffer, v_block_scale
 
 
@@ -721,33 +729,35 @@ def get_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, kv_indic
     into ``k_out`` / ``v_out`` where given; ``v_buffer`` None reads K only."""
     lib = load_library()
     _i32(kv_indices, "kv_indices")
-    kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
     n, dev = kv_indices.numel(), k_buffer.device
-    slots, hkv, lk = k_buffer.shape[0], k_buffer.shape[1], 2 * k_buffer.shape[2]
     lv, vb, vs = 0, (0, 0, 0, 0), (0, 0)
-    if k_out is None:
-        k_out = torch.empty(n, hkv, lk, dtype=torch.bfloat16, device=dev)
-    ks = _rows(k_out, "k_out")
-    if tuple(k_out.shape) != (n, hkv, lk):
-        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {(n, hkv, lk)}")
-    if v_buffer is not None:
-        _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
-        vb = _fp4_half(v_buffer, v_block_scale, "v_buffer")
-        lv = 2 * v_buffer.shape[2]
-        if v_out is None:
-            v_out = torch.empty(n, hkv, lv, dtype=torch.bfloat16, device=dev)
-        vs = _rows(v_out, "v_out")
-        if tuple(v_out.shape) != (n, hkv, lv):
-            raise ValueError(f"v_out has shape {tuple(v_out.shape)}, expected {(n, hkv, lv)}")
-    elif v_out is not None:
-        raise ValueError("v_out needs v_buffer")
-    _one_device(dev, kv_indices=kv_indices, k_out=k_out, v_out=v_out)
+    if v_buffer is None:
+        if v_out is not None:
+            raise ValueError("v_out needs v_buffer")
+        (slots, hkv, lk), kb = _fp4_half(k_buffer, k_block_scale, "k_buffer")
+        v_scale_ptr = None
+    else:
+        (slots, hkv, lk, lv), kb, vb = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+        v_scale_ptr = _ptr(v_block_scale)
+
+    def output(t, d, name):
+        if t is None:
+            return torch.empty(n, hkv, d, dtype=torch.bfloat16, device=dev), (hkv * d, d)
+        strides = _rows(t, name)
+        if tuple(t.shape) != (n, hkv, d) or t.device != dev:
+            raise ValueError(f"{name} is {tuple(t.shape)} on {t.device}, expected {(n, hkv, d)} on {dev}")
+        return t, strides
+
+    k_out, ks = output(k_out, lk, "k_out")
+    if lv:
+        v_out, vs = output(v_out, lv, "v_out")
+    _one_device(dev, kv_indices=kv_indices)
     _check(_on(
         dev, lib.pkx_get_kv_buffer_fp4,
         _ptr(k_buffer), kb[0], kb[1], _ptr(k_block_scale), kb[2], kb[3],
-        _ptr(v_buffer), vb[0], vb[1], _ptr(v_block_scale) if v_buffer is not None else None, vb[2],
-        vb[3], slots, _ptr(kv_indices) if n else None, n, hkv, lk, lv, float(k_scale),
-        float(v_scale), _ptr(k_out), ks[0], ks[1], _ptr(v_out), vs[0], vs[1]))
+        _ptr(v_buffer), vb[0], vb[1], v_scale_ptr, vb[2], vb[3], slots,
+        _ptr(kv_indices) if n else None, n, hkv, lk, lv, float(k_scale), float(v_scale),
+        _ptr(k_out) if n else None, ks[0], ks[1], _ptr(v_out), vs[0], vs[1]))
     return k_out, v_out
 
 
@@ -755,22 +765,21 @@ def decode_fp4_workspace_size(batch, hq, hkv, lq, lv) -> int:
     return int(load_library().pkx_decode_fp4_workspace_size(batch, hq, hkv, lq, lv))
 
 
-def _check_fp4_attn(q, o, lse, k_buffer, v_buffer):
-    """Shape checks of an attention call over a 4-bit pool; (tokens, hq, hkv, lq, lv)."""
-    if q.dim() != 3 or o.dim() != 3:
-        raise ValueError("q and o must be [tokens, heads, dim]")
-    n, hq, lq = q.shape
-    hkv, lv = k_buffer.shape[1], 2 * v_buffer.shape[2]
-    for t, nm in ((q, "q"), (o, "o")):
-        if not t.is_contiguous() or t.dtype != torch.bfloat16:
-            raise ValueError(f"{nm} must be a contiguous bf16 [tokens, heads, dim] tensor")
-    if tuple(o.shape) != (n, hq, lv):
-        raise ValueError(f"o has shape {tuple(o.shape)}, expected {(n, hq, lv)}")
+def _check_fp4_attn(q, o, lse, dims):
+    """Shape checks of an attention call over a 4-bit pool of (slots, heads,
+    Lk, Lv); returns (tokens, hq, hkv, lq, lv)."""
+    _, hkv, lk, lv = dims
+    qs = tuple(q.shape)
+    if len(qs) != 3 or not q.is_contiguous() or q.dtype != torch.bfloat16:
+        raise ValueError("q must be a contiguous bf16 [tokens, heads, dim] tensor")
+    n, hq, lq = qs
+    if tuple(o.shape) != (n, hq, lv) or not o.is_contiguous() or o.dtype != torch.bfloat16:
+        raise ValueError(f"o must be a contiguous bf16 {(n, hq, lv)} tensor, got {o.dtype} {tuple(o.shape)}")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
                             tuple(lse.shape) != (n, hq)):
         raise ValueError(f"lse must be a contiguous float32 [{n}, {hq}] tensor")
-    if 2 * k_buffer.shape[2] != lq:
-        raise ValueError(f"k_buffer holds rows of {2 * k_buffer.shape[2]} elements, q of {lq}")
+    if lk != lq:
+        raise ValueError(f"k_buffer holds rows of {lk} elements, q of {lq}")
     return n, hq, hkv, lq, lv
 
 
@@ -782,8 +791,8 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
     ``first_tokens`` keys of each sequence stay visible.  Returns the
     workspace."""
     lib = load_library()
-    strides = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
-    b, hq, hkv, lq, lv = _check_fp4_attn(q, o, lse, k_buffer, v_buffer)
+    dims, ks, vs = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+    b, hq, hkv, lq, lv = _check_fp4_attn(q, o, lse, dims)
     _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
     _check_len(kv_indptr, b + 1, "kv_indptr")
     _one_device(q.device, o=o, k_buffer=k_buffer, kv_indptr=kv_indptr, kv_indices=kv_indices,
@@ -793,7 +802,7 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
         q.device, lib.pkx_decode_attention_fwd_fp4,
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(k_block_scale), _ptr(v_buffer),
         _ptr(v_block_scale), _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, b,
-        hq, hkv, lq, lv, *strides, k_buffer.shape[0], float(sm_scale or 0.0),
+        hq, hkv, lq, lv, *ks, *vs, dims[0], float(sm_scale or 0.0),
         float(logit_cap or 0.0), int(sliding_window), int(first_tokens), float(k_scale),
         float(v_scale), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
     return ws
@@ -835,8 +844,8 @@ def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k
     (and lse) in place; other arguments as extend_attention_fwd and
     decode_attention_fwd_fp4.  Returns the workspace."""
     lib = load_library()
-    strides = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
-    n, hq, hkv, lq, lv = _check_fp4_attn(q_extend, o_extend, lse, k_buffer, v_buffer)
+    dims, ks, vs = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
+    n, hq, hkv, lq, lv = _check_fp4_attn(q_extend, o_extend, lse, dims)
     batch, ke, ve = _two_stage_checks(q_extend, k_extend, v_extend, hkv, lq, lv, qo_indptr,
                                       kv_indptr, kv_indices)
     dev = q_extend.device
@@ -850,8 +859,8 @@ def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k
         _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
         _ptr(k_block_scale), _ptr(v_buffer), _ptr(v_block_scale), _ptr(qo_indptr),
         _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq,
-        lv, *ke, *ve, *strides, k_buffer.shape[0], float(sm_scale or 0.0),
-        float(logit_cap or 0.0), int(sliding_window), int(first_tokens),
+        lv, *ke, *ve, *ks, *vs, dims[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
+        int(sliding_window), int(first_tokens),
         *_mask_sinks(custom_mask, mask_indptr, sinks), float(k_scale), float(v_scale), _ptr(lse),
         _ptr(ws), ws.numel() * ws.element_size()))
     return ws

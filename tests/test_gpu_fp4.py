@@ -324,6 +324,16 @@ def test_decode_repeats_and_streams_and_graph():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], full)
 
 
+def test_decode_many_split_sequences():
+    """More sequences that several shares hold than a CTA of the merge takes
+    rows: every one is merged, in repeated calls on one workspace."""
+    c = Decode(64, 32, 4, [700 + 13 * i for i in range(90)], seed=15)
+    ref, ws = c.reference(), None
+    for _ in range(20):
+        o, lse, ws = c.run(ws=ws)
+        R.check(o, lse, ref, 64, c.scale, F16_STEP)
+
+
 def test_write_then_decode():
     """A decode step as a serving loop runs it: the new token is written, then
     read by the attention, over several steps."""
