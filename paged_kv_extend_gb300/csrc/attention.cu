@@ -808,18 +808,21 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8_scaled(uint4 v) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Eight e2m1 codes times their block scale (a pair of f16) as eight bf16:
-// exact, since the product has six significant bits.  (27 clocks a word on a
-// quarter SM; shifting the f16 bits to bf16's exponent, 37.)
-__device__ __forceinline__ uint4 fp4x8_to_bf16x8(uint32_t codes, __half2 s2) {
-  uint32_t h[4], out[4];
+// Eight e2m1 codes times their block scale (a pair of f16) as eight f16 or
+// bf16: exact in both, since the product has six significant bits and lies in
+// [2^-10, 2688].  On a quarter SM a word takes 13.5 clocks to f16 and 27 to
+// bf16 (37 by shifting the f16 bits to bf16's exponent).
+template <bool BF16>
+__device__ __forceinline__ uint4 fp4x8_to_16bit(uint32_t codes, __half2 s2) {
+  uint32_t h[4];
   e2m1x8_to_f16(codes, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s2));
-    out[i] = pack_bf16(f.x, f.y);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), s2);
+    const float2 f = __half22float2(x);
+    h[i] = BF16 ? pack_bf16(f.x, f.y) : *reinterpret_cast<const uint32_t *>(&x);
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // FMT: the pool's element format (0 bf16; 1 fp8 e4m3, 2 fp8 e5m2 with
@@ -842,8 +845,8 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   constexpr int NK_ = F16 ? C::NK - 1 : C::NK;
   constexpr uint32_t K0 = C::OFF_K + (F16 ? C::K_BYTES : 0);
   // decode over fp8: warps 10-11 copy the codes, warps 12-13 convert the K
-  // tiles and 14-15 the V tiles; extend over a 4-bit pool likewise (warp 10
-  // copies K, warp 11 V)
+  // tiles and 14-15 the V tiles; extend over a 4-bit pool: warp 10 copies K,
+  // warp 11 V, warps 12-14 convert K and 14-15 V
   constexpr bool F4 = FMT == 3;
   constexpr int RAW_THREADS = 64, CONV_THREADS = 64;
   extern __shared__ uint8_t smem_raw[];
@@ -890,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     // stages are filled by the copy warps, or by the converting warps in
     // decode over fp8
     for (int s = 0; s < C::NK; ++s) {
-      mbar_init(&k_full[s], F16 || F4 ? CONV_THREADS : C::COPY_THREADS);
+      mbar_init(&k_full[s], F4 ? 96 : F16 ? CONV_THREADS : C::COPY_THREADS);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < C::NV; ++s) {
@@ -1159,7 +1162,15 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           float nm = -mref;
           float lscale = 1.0f;
           if constexpr (FMT != 0 && !F16) {
-            if (pool8) {
+            if constexpr (F4) {
+              // the output takes v_scale; P of a tile of extend rows is
+              // divided by it (bf16 has the range, the f16 P of a pool tile
+              // has not)
+              if (!pool8) {
+                nm -= p.log2_v_scale;
+                lscale = p.v_scale;
+              }
+            } else if (pool8) {
               nm += p.log2_v_scale;
               lscale = p.inv_v_scale;
             }
@@ -1172,12 +1183,11 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
             const float e1 = ex2_approx(fmaf(x[i + 1], sc, nm));
             l0 += e0;
             l1 += e1;
-            if constexpr (F16) {
-              const __half2 h = __floats2half2_rn(e0, e1);
-              pk[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
-            } else {
-              pk[i / 2] = pack_bf16(e0, e1);
-            }
+            const __half2 h = __floats2half2_rn(e0, e1);
+            const uint32_t h2 = *reinterpret_cast<const uint32_t *>(&h);
+            if constexpr (F16) pk[i / 2] = h2;
+            else if constexpr (F4) pk[i / 2] = pool8 ? h2 : pack_bf16(e0, e1);
+            else pk[i / 2] = pack_bf16(e0, e1);
           }
           if constexpr (FMT != 0) l += (l0 + l1) * lscale;
           else l += l0 + l1;
@@ -1232,7 +1242,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           inv = a_m / lt;
           lse_v = (M + __log2f(lt)) * 0.69314718055994531f;
         }
-        if constexpr (F16) inv *= p.v_scale;  // V was read as its codes
+        if constexpr (F16 || F4) inv *= p.v_scale;  // V was read as its codes
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < C::HDV / 32; ++c) {
@@ -1311,13 +1321,18 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         });
         if (leader) tc_commit(&bars[B_S_FULL + buf]);
       };
-      auto issue_pv = [&](int qt, uint32_t sV, bool acc_first) {
+      // (4-bit pool: the first n_pool tiles of a unit have f16 V and P, the
+      // tiles of extend rows bf16)
+      [[maybe_unused]] int n_pool = 0;
+      auto issue_pv = [&](int qt, uint32_t sV, bool acc_first, [[maybe_unused]] int tile) {
+        uint32_t idpv = IDPV;
+        if constexpr (F4) idpv = tile < n_pool ? idesc_f16_f32(C::BM, C::HDV, 1) : IDPV;
         const uint32_t b_lo = V_LO | desc_addr(sV);
         const uint32_t d = tmem + 2 * C::BN + qt * C::HDV, a = tmem + qt * C::BN;
         const uint32_t acc0 = acc_first ? 1u : 0u;
         static_for<0, C::BN / 16>([&](auto kk_c) {
           constexpr int kk = decltype(kk_c)::value;
-          if (leader) tc_mma_ts_step<kk * 8, kk * 128>(d, a, b_lo, V_HI, IDPV, kk > 0 ? 1u : acc0);
+          if (leader) tc_mma_ts_step<kk * 8, kk * 128>(d, a, b_lo, V_HI, idpv, kk > 0 ? 1u : acc0);
         });
       };
       for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
@@ -1326,6 +1341,10 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         const WorkUnit w = p.units[p.uorder[u]];
         const int nt = w.n_tiles;
         if (nt == 0) continue;
+        if constexpr (F4) {  // tile_keys()'s count of tiles before k_split
+          const int pe = min(w.k_end, w.k_split);
+          n_pool = pe > w.k_begin ? (pe - w.k_begin + C::BN - 1) / C::BN : 0;
+        }
         const bool q1 = w.n_tok > TOK;
         if (!mbar_wait(&bars[F16 ? B_Q_CONV : B_Q_FULL], q_cnt & 1u, abort_flag, p.wait_ns)) {
           ok = false;
@@ -1352,7 +1371,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
               ++pc;
               fence_proxy_async_smem();
               tc_fence_after();
-              issue_pv(b, sbase + C::OFF_V + vs * C::V_BYTES, j >= 4);
+              issue_pv(b, sbase + C::OFF_V + vs * C::V_BYTES, j >= 4, j - 2);
               if (leader) tc_commit(&v_empty[vs]);
               ++vc;
             }
@@ -1378,7 +1397,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
             ++pc;
             fence_proxy_async_smem();
             tc_fence_after();
-            issue_pv(b, sbase + C::OFF_V + vs * C::V_BYTES, j >= 2);
+            issue_pv(b, sbase + C::OFF_V + vs * C::V_BYTES, j >= 2, j);
             if (leader) tc_commit(&bars[B_O_DONE + b]);
             if (leader) tc_commit(&v_empty[vs]);
             ++vc;
@@ -1408,13 +1427,13 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           tc_fence_after();
           const uint32_t sK = sbase + K0 + ks * C::K_BYTES;
           const uint32_t sV = sbase + C::OFF_V + vs * C::V_BYTES;
-          issue_pv(0, sV, j > 1);
+          issue_pv(0, sV, j > 1, j - 1);
           issue_s(0, sK);
           if (q1) {
             if (!mbar_wait(&bars[B_P_FULL + 1], p_cnt1 & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
             ++p_cnt1;
             tc_fence_after();
-            issue_pv(1, sV, j > 1);
+            issue_pv(1, sV, j > 1, j - 1);
             issue_s(1, sK);
           }
           if (leader) tc_commit(&v_empty[vs]);
@@ -1433,13 +1452,13 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           fence_proxy_async_smem();
           tc_fence_after();
           const uint32_t sV = sbase + C::OFF_V + vs * C::V_BYTES;
-          issue_pv(0, sV, nt > 1);
+          issue_pv(0, sV, nt > 1, nt - 1);
           if (leader) tc_commit(&bars[B_O_DONE + 0]);
           if (q1) {
             if (!mbar_wait(&bars[B_P_FULL + 1], p_cnt1 & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
             ++p_cnt1;
             tc_fence_after();
-            issue_pv(1, sV, nt > 1);
+            issue_pv(1, sV, nt > 1, nt - 1);
             if (leader) tc_commit(&bars[B_O_DONE + 1]);
           }
           if (leader) tc_commit(&v_empty[vs]);
@@ -1735,7 +1754,10 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   } else if (F4) {
     // ---------------------- extend over a 4-bit pool (warps 10-15)
     // Warp 10 copies the K tiles into their stages and warp 11 the V tiles;
-    // warps 12-13 convert K and 14-15 V, in place.  Copies and conversions of
+    // warps 12-15 convert in place, K to bf16 (Q's type) and V to f16, which
+    // takes half the time: P of a pool tile is f16 too, and the output takes
+    // v_scale.  Warps 12 and 13 convert 3/8 of K each, warp 14 the rest of K
+    // and a quarter of V, warp 15 the rest of V: equal shares of the work.  Copies and conversions of
     // K and of V thus wait for nothing of each other: with four warps that
     // copied and converted both in turn, a tile was a chain of two conversions,
     // two landings and the product that frees V's stage (678 us on
@@ -1757,13 +1779,48 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     const uint32_t c4 = (uint32_t)((4 * (q4 & 1)) ^ (kl & 7));
     const uint32_t d4 = (uint32_t)(q4 >> 1) * (C::BN * 128) + (uint32_t)kl * 128u;
     const uint32_t sc4 = (uint32_t)kl * 128u + (((uint32_t)(kl & 7) ^ 1u) << 4);  // block scales
-    const bool is_v = warp == 11 || warp >= 14;
-    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+    static_assert(C::K_BYTES == C::V_BYTES, "one stage size");
+    const bool is_v = warp == 11;  // of the copying warps
+    uint64_t *empty = is_v ? v_empty : k_empty;
     uint64_t *landed = is_v ? raw_full + C::NK : raw_full;
     const uint32_t n_stages = is_v ? C::NV : C::NK;
     const uint32_t stages = sbase + (is_v ? C::OFF_V : K0);
     constexpr uint32_t STAGE_BYTES = C::K_BYTES;
-    static_assert(C::K_BYTES == C::V_BYTES, "one stage size");
+    // key groups [g0, g1) (KPW keys each) of the tile in `stage`, two at a time
+    // (one where a warp's count of groups is odd).
+    // A loop, not unrolled: unrolled over a tile the code of the warps' roles
+    // outgrew the instruction cache, and a word took 140 clocks.
+    auto convert = [&](uint32_t stage, int g0, int g1, auto bf16_c) {
+      constexpr bool BF16 = decltype(bf16_c)::value;
+      constexpr int U = HD == 128 ? 2 : 1;
+#pragma unroll 1
+      for (uint32_t at = stage + g0 * (KPW * 128); at < stage + g1 * (KPW * 128);
+           at += U * KPW * 128) {
+        uint4 codes[U];
+        __half2 sc[U][2];  // the chunk's two block scales, each twice
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint32_t key = at + i * (KPW * 128);
+          codes[i] = ld_shared_u4(key + d4 + (c4 << 4));
+          const uint2 sw = ld_shared_u2(key + sc4);
+          const uint32_t two = (q4 & 2 ? sw.y : sw.x) >> (16 * (q4 & 1));
+          const __half2 s = e4m3x2_to_f16x2(two & 0xFFFFu);
+          sc[i][0] = __low2half2(s);
+          sc[i][1] = __high2half2(s);
+        }
+        __syncwarp();  // every lane has read before any writes
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint32_t dst = at + d4 + i * (KPW * 128);
+          const uint32_t x[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          uint4 out[4];  // all four before a store, for the chains to overlap
+#pragma unroll
+          for (int sub = 0; sub < 4; ++sub) out[sub] = fp4x8_to_16bit<BF16>(x[sub], sc[i][sub >> 1]);
+#pragma unroll
+          for (int sub = 0; sub < 4; ++sub) st_shared_u4(dst + ((c4 ^ sub) << 4), out[sub]);
+        }
+      }
+    };
     uint32_t c = 0, ic = 0;  // tiles of this warp's kind, so far
     bool ok = true;
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
@@ -1844,45 +1901,33 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           ++c;
         }
       } else {
-        constexpr int N = C::BN / (2 * KPW);  // keys of a lane (two warps a tile)
+        // K groups of warps 12, 13, 14 and V groups of warps 14, 15
+        constexpr int NG = C::BN / KPW;
+        const int k0 = warp == 12 ? 0 : warp == 13 ? NG * 3 / 8 : NG * 6 / 8;
+        const int k1 = warp == 12 ? NG * 3 / 8 : warp == 13 ? NG * 6 / 8 : NG;
+        const int v0 = warp == 14 ? 0 : NG * 2 / 8, v1 = warp == 14 ? NG * 2 / 8 : NG;
         for (int j = 0; j < nt; ++j) {
-          const uint32_t st = c % n_stages;
-          if (!mbar_wait(&landed[st], (c / n_stages) & 1u, abort_flag, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          if (!from_ext(j)) {
-            const uint32_t tile = stages + st * STAGE_BYTES + (warp & 1) * (KPW * 128);
-#pragma unroll
-            for (int i0 = 0; i0 < N; i0 += 4) {
-              uint4 codes[4];
-              __half2 sc[4][2];  // the chunk's two block scales, each twice
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t key = tile + (i0 + i) * (2 * KPW * 128);
-                codes[i] = ld_shared_u4(key + d4 + (c4 << 4));
-                const uint2 sw = ld_shared_u2(key + sc4);
-                const uint32_t two = (q4 & 2 ? sw.y : sw.x) >> (16 * (q4 & 1));
-                const __half2 s = e4m3x2_to_f16x2(two & 0xFFFFu);
-                sc[i][0] = __low2half2(s);
-                sc[i][1] = __high2half2(s);
-              }
-              __syncwarp();  // every lane has read before any writes
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t dst = tile + d4 + (i0 + i) * (2 * KPW * 128);
-                const uint32_t x[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-                uint4 out[4];  // all four before a store, for the chains to overlap
-#pragma unroll
-                for (int sub = 0; sub < 4; ++sub)
-                  out[sub] = fp4x8_to_bf16x8(x[sub], sc[i][sub >> 1]);
-#pragma unroll
-                for (int sub = 0; sub < 4; ++sub) st_shared_u4(dst + ((c4 ^ sub) << 4), out[sub]);
-              }
+          const bool ext = from_ext(j);  // bf16 already: passed on
+          if (warp < 15) {
+            const uint32_t st = c % C::NK, stage = sbase + K0 + st * STAGE_BYTES;
+            if (!mbar_wait(&raw_full[st], (c / C::NK) & 1u, abort_flag, p.wait_ns)) {
+              ok = false;
+              break;
             }
+            if (!ext) convert(stage, k0, k1, std::true_type{});
+            fence_proxy_async_smem();  // copies' and this warp's writes -> tensor-core reads
+            mbar_arrive(&k_full[st]);
           }
-          fence_proxy_async_smem();  // copies' and this warp's writes -> tensor-core reads
-          mbar_arrive(&full[st]);
+          if (warp >= 14) {
+            const uint32_t st = c % C::NV, stage = sbase + C::OFF_V + st * STAGE_BYTES;
+            if (!mbar_wait(&raw_full[C::NK + st], (c / C::NV) & 1u, abort_flag, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            if (!ext) convert(stage, v0, v1, std::false_type{});
+            fence_proxy_async_smem();
+            mbar_arrive(&v_full[st]);
+          }
           ++c;
         }
       }

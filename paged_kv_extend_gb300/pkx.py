@@ -145,16 +145,21 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# the current stream's handle of a device by its index; torch builds a Stream
+# object around it (3 us a call) where it does not offer the handle itself
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(dev: torch.device, fn, *args):
     """Call C entry point ``fn`` with ``dev`` as the calling thread's current
     CUDA device and that device's current stream as the last argument: the
     library launches on the current device, so a tensor on another GPU than
     the current one still gets its kernels on its own device."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
     if dev.index == torch.cuda.current_device():
-        return fn(*args, stream)
+        return fn(*args, _raw_stream(dev.index))
     with torch.cuda.device(dev):
-        return fn(*args, stream)
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -657,26 +662,27 @@ def _fp4_half(codes, scales, name):
     """Slots, heads, elements of a row and byte strides (codes slot, head, block
     scales slot, head) of one half of a 4-bit pool: uint8 codes
     [slots, hkv, d / 2] and float8_e4m3fn block scales [slots, hkv, d / 16]."""
-    shape, sshape = tuple(codes.shape), tuple(scales.shape)
+    shape, sshape = codes.shape, scales.shape
     st, sst = codes.stride(), scales.stride()
     if len(shape) != 3 or codes.dtype != torch.uint8 or st[2] != 1 or not codes.is_cuda:
         raise ValueError(f"{name} must be a CUDA uint8 [slots, heads, dim / 2] tensor with a "
                          "contiguous last dim")
     if len(sshape) != 3 or scales.dtype != torch.float8_e4m3fn or \
-            (sst[2] != 1 and sshape[2] > 1) or scales.device != codes.device:
+            (sst[2] != 1 and sshape[2] > 1) or scales.get_device() != codes.get_device():
         raise ValueError(f"{name}'s block scales must be a float8_e4m3fn [slots, heads, dim / 16] "
                          f"tensor on {codes.device} with a contiguous last dim")
-    if sshape[:2] != shape[:2] or sshape[2] * 8 != shape[2]:
-        raise ValueError(f"{name} [slots, heads, dim / 2] {shape} and its block scales [slots, "
-                         f"heads, dim / 16] {sshape} disagree")
-    return (shape[0], shape[1], 2 * shape[2]), (st[0], st[1], sst[0], sst[1])
+    slots, heads, half = shape
+    if sshape[0] != slots or sshape[1] != heads or sshape[2] * 8 != half:
+        raise ValueError(f"{name} [slots, heads, dim / 2] {tuple(shape)} and its block scales "
+                         f"[slots, heads, dim / 16] {tuple(sshape)} disagree")
+    return (slots, heads, 2 * half), (st[0], st[1], sst[0], sst[1])
 
 
 def _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale):
     """(slots, heads, Lk, Lv), K byte strides, V byte strides."""
     kd, ks = _fp4_half(k_buffer, k_block_scale, "k_buffer")
     vd, vs = _fp4_half(v_buffer, v_block_scale, "v_buffer")
-    if vd[:2] != kd[:2] or v_buffer.device != k_buffer.device:
+    if vd[:2] != kd[:2] or v_buffer.get_device() != k_buffer.get_device():
         raise ValueError("k_buffer and v_buffer must have the same slots, heads and device")
     return (*kd, vd[2]), ks, vs
 
