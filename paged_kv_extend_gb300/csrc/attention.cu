@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   constexpr uint32_t K0 = C::OFF_K + (F16 ? C::K_BYTES : 0);
   // decode over fp8: warps 10-11 copy the codes, warps 12-13 convert the K
   // tiles and 14-15 the V tiles; extend over a 4-bit pool: warp 10 copies K,
-  // warp 11 V, warps 12-14 convert K and 14-15 V
+  // warp 11 V, warps 12-13 convert K and 14-15 V
   constexpr bool F4 = FMT == 3;
   constexpr int RAW_THREADS = 64, CONV_THREADS = 64;
   extern __shared__ uint8_t smem_raw[];
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     // stages are filled by the copy warps, or by the converting warps in
     // decode over fp8
     for (int s = 0; s < C::NK; ++s) {
-      mbar_init(&k_full[s], F4 ? 96 : F16 ? CONV_THREADS : C::COPY_THREADS);
+      mbar_init(&k_full[s], F16 || F4 ? CONV_THREADS : C::COPY_THREADS);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < C::NV; ++s) {
@@ -1754,10 +1754,9 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   } else if (F4) {
     // ---------------------- extend over a 4-bit pool (warps 10-15)
     // Warp 10 copies the K tiles into their stages and warp 11 the V tiles;
-    // warps 12-15 convert in place, K to bf16 (Q's type) and V to f16, which
-    // takes half the time: P of a pool tile is f16 too, and the output takes
-    // v_scale.  Warps 12 and 13 convert 3/8 of K each, warp 14 the rest of K
-    // and a quarter of V, warp 15 the rest of V: equal shares of the work.  Copies and conversions of
+    // warps 12-13 convert K in place to bf16 (Q's type) and 14-15 V to f16,
+    // which takes half the time: P of a pool tile is f16 too, and the output
+    // takes v_scale.  Copies and conversions of
     // K and of V thus wait for nothing of each other: with four warps that
     // copied and converted both in turn, a tile was a chain of two conversions,
     // two landings and the product that frees V's stage (678 us on
@@ -1780,19 +1779,18 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     const uint32_t d4 = (uint32_t)(q4 >> 1) * (C::BN * 128) + (uint32_t)kl * 128u;
     const uint32_t sc4 = (uint32_t)kl * 128u + (((uint32_t)(kl & 7) ^ 1u) << 4);  // block scales
     static_assert(C::K_BYTES == C::V_BYTES, "one stage size");
-    const bool is_v = warp == 11;  // of the copying warps
-    uint64_t *empty = is_v ? v_empty : k_empty;
+    const bool is_v = warp == 11 || warp >= 14;
+    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
     uint64_t *landed = is_v ? raw_full + C::NK : raw_full;
     const uint32_t n_stages = is_v ? C::NV : C::NK;
     const uint32_t stages = sbase + (is_v ? C::OFF_V : K0);
     constexpr uint32_t STAGE_BYTES = C::K_BYTES;
-    // key groups [g0, g1) (KPW keys each) of the tile in `stage`, two at a time
-    // (one where a warp's count of groups is odd).
+    // key groups [g0, g1) (KPW keys each) of the tile in `stage`, two at a time.
     // A loop, not unrolled: unrolled over a tile the code of the warps' roles
     // outgrew the instruction cache, and a word took 140 clocks.
     auto convert = [&](uint32_t stage, int g0, int g1, auto bf16_c) {
       constexpr bool BF16 = decltype(bf16_c)::value;
-      constexpr int U = HD == 128 ? 2 : 1;
+      constexpr int U = 2;
 #pragma unroll 1
       for (uint32_t at = stage + g0 * (KPW * 128); at < stage + g1 * (KPW * 128);
            at += U * KPW * 128) {
@@ -1849,85 +1847,72 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
             ok = false;
             break;
           }
-          int rows[N];
-          const int4 *ring = reinterpret_cast<const int4 *>(smem + C::OFF_I + is * C::I_BYTES) + kl * (N / 4);
-#pragma unroll
-          for (int q = 0; q < N / 4; ++q) {
-            const int4 v = ring[q];
-            rows[4 * q] = v.x;
-            rows[4 * q + 1] = v.y;
-            rows[4 * q + 2] = v.z;
-            rows[4 * q + 3] = v.w;
-          }
-          __syncwarp();  // the warp is done with the ring slot
-          if (lane == 0) mbar_arrive(&i_empty[is]);
-          ++ic;
           const uint32_t st = c % n_stages;
           if (c >= n_stages && !mbar_wait(&empty[st], ((c / n_stages) - 1) & 1u, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
-          const uint32_t at = stages + st * STAGE_BYTES + d4;
-          if (from_ext(j)) {
+          // the lane's rows are contiguous in the ring, four to a load; loops
+          // that are short in code, for the same reason as the conversion's
+          const int4 *ring =
+              reinterpret_cast<const int4 *>(smem + C::OFF_I + is * C::I_BYTES) + kl * (N / 4);
+          const uint32_t stage = stages + st * STAGE_BYTES;
+          const bool is_ext = from_ext(j);
+#pragma unroll 1
+          for (int i0 = 0; i0 < N; i0 += 4) {
+            const int4 v = ring[i0 / 4];
+            const int rows[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t dst = stage + d4 + i0 * (KPW * 128);
+            if (is_ext) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const bf16 *src = ext + (int64_t)max(rows[i], 0) * es;
-              const uint32_t n = rows[i] >= 0 ? 16u : 0u, dst = at + i * (KPW * 128);
+              for (int i = 0; i < 4; ++i) {
+                const bf16 *src = ext + (int64_t)max(rows[i], 0) * es;
 #pragma unroll
-              for (int sub = 0; sub < 4; ++sub)
-                cp_async_16(dst + ((c4 ^ sub) << 4), src + sub * 8, n);
-            }
-          } else {
+                for (int sub = 0; sub < 4; ++sub)
+                  cp_async_16(dst + i * (KPW * 128) + ((c4 ^ sub) << 4), src + sub * 8,
+                              rows[i] >= 0 ? 16u : 0u);
+              }
+            } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int64_t r = max(rows[i], 0);
-              const uint32_t dst = at + i * (KPW * 128);
-              cp_async_16(dst + (c4 << 4), pool + r * ss, rows[i] >= 0 ? 16u : 0u);
-            }
-            // block scales, one copy a key: chunk q4's lanes take every Q4-th pass
+              for (int i = 0; i < 4; ++i)
+                cp_async_16(dst + i * (KPW * 128) + (c4 << 4), pool + (int64_t)max(rows[i], 0) * ss,
+                            rows[i] >= 0 ? 16u : 0u);
+              // block scales, one copy a key: chunk q4's lanes take every Q4-th key
 #pragma unroll
-            for (int i = 0; i < N; i += Q4) {
-              int row = rows[i];
+              for (int i = 0; i < 4; i += Q4) {
+                int row = rows[i];
 #pragma unroll
-              for (int k = 1; k < Q4; ++k)
-                if (q4 == k) row = rows[i + k];
-              const uint32_t dst = stages + st * STAGE_BYTES + sc4 + (i + q4) * (KPW * 128);
-              const uint8_t *src = scales + (int64_t)max(row, 0) * sss;
-              if constexpr (HD == 128) cp_async_8_at<0>(dst, src, row >= 0 ? 8u : 0u);
-              else cp_async_4_at<0>(dst, src, row >= 0 ? 4u : 0u);
+                for (int k = 1; k < Q4; ++k)
+                  if (q4 == k) row = rows[i + k];
+                const uint32_t at = stage + sc4 + (i0 + i + q4) * (KPW * 128);
+                const uint8_t *src = scales + (int64_t)max(row, 0) * sss;
+                if constexpr (HD == 128) cp_async_8_at<0>(at, src, row >= 0 ? 8u : 0u);
+                else cp_async_4_at<0>(at, src, row >= 0 ? 4u : 0u);
+              }
             }
           }
+          __syncwarp();  // the warp is done with the ring slot
+          if (lane == 0) mbar_arrive(&i_empty[is]);
+          ++ic;
           cp_async_arrive_noinc(&landed[st]);
           ++c;
         }
       } else {
-        // K groups of warps 12, 13, 14 and V groups of warps 14, 15
-        constexpr int NG = C::BN / KPW;
-        const int k0 = warp == 12 ? 0 : warp == 13 ? NG * 3 / 8 : NG * 6 / 8;
-        const int k1 = warp == 12 ? NG * 3 / 8 : warp == 13 ? NG * 6 / 8 : NG;
-        const int v0 = warp == 14 ? 0 : NG * 2 / 8, v1 = warp == 14 ? NG * 2 / 8 : NG;
+        constexpr int HALF = C::BN / KPW / 2;  // key groups of each of the two warps
+        const int g0 = (warp & 1) * HALF;
         for (int j = 0; j < nt; ++j) {
-          const bool ext = from_ext(j);  // bf16 already: passed on
-          if (warp < 15) {
-            const uint32_t st = c % C::NK, stage = sbase + K0 + st * STAGE_BYTES;
-            if (!mbar_wait(&raw_full[st], (c / C::NK) & 1u, abort_flag, p.wait_ns)) {
-              ok = false;
-              break;
-            }
-            if (!ext) convert(stage, k0, k1, std::true_type{});
-            fence_proxy_async_smem();  // copies' and this warp's writes -> tensor-core reads
-            mbar_arrive(&k_full[st]);
+          const uint32_t st = c % n_stages;
+          if (!mbar_wait(&landed[st], (c / n_stages) & 1u, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
           }
-          if (warp >= 14) {
-            const uint32_t st = c % C::NV, stage = sbase + C::OFF_V + st * STAGE_BYTES;
-            if (!mbar_wait(&raw_full[C::NK + st], (c / C::NV) & 1u, abort_flag, p.wait_ns)) {
-              ok = false;
-              break;
-            }
-            if (!ext) convert(stage, v0, v1, std::false_type{});
-            fence_proxy_async_smem();
-            mbar_arrive(&v_full[st]);
+          if (!from_ext(j)) {  // (rows of the new tokens are bf16 already)
+            const uint32_t stage = stages + st * STAGE_BYTES;
+            if (is_v) convert(stage, g0, g0 + HALF, std::false_type{});
+            else convert(stage, g0, g0 + HALF, std::true_type{});
           }
+          fence_proxy_async_smem();  // copies' and this warp's writes -> tensor-core reads
+          mbar_arrive(&full[st]);
           ++c;
         }
       }

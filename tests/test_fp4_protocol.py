@@ -2,9 +2,8 @@
 
 Extend (attn_kernel, csrc/attention.cu): warp 10 copies K tiles and warp 11 V
 tiles into their stages once the tensor core has released them; a tile's
-landing is a phase of its stage's raw barrier, on which warps 12-13 (K), 14
-(a part of K, then a part of V) and 15 (V) wait before they convert in place
-and arrive on the stage's full barrier.  The
+landing is a phase of its stage's raw barrier, on which warps 12-13 (K) and
+14-15 (V) wait before they convert in place and mark the stage full.  The
 other roles are those of the model in test_barrier_protocol.py.
 
 Decode (decode_fp4_kernel, csrc/fp4_decode.cu): the warps of a stream copy
@@ -21,19 +20,18 @@ from test_barrier_protocol import RING, _Bar, _Model, _random_units
 class _Fp4Extend(_Model):
     def __init__(self, units, seed, mistake=None, stages=(3, 2, 3)):
         super().__init__(units, seed, mistake, stages=stages)
-        for s in range(RING):  # two warpgroups, MMA, two copying and three converting roles
-            self.bars[f"UE{s}"] = _Bar(f"UE{s}", 8)
+        for s in range(RING):  # two warpgroups, MMA, two copying and two converting roles
+            self.bars[f"UE{s}"] = _Bar(f"UE{s}", 7)
         for s in range(self.NI):
             self.bars[f"IE{s}"] = _Bar(f"IE{s}", 2)
         for pre, n in (("K", self.NK), ("V", self.NV)):
             for s in range(n):
                 self.bars[f"L{pre}{s}"] = _Bar(f"L{pre}{s}", 1)
-                self.bars[f"{pre}F{s}"] = _Bar(f"{pre}F{s}", 2)
 
     def _roles(self):
         return {"index": self._index(), "wg0": self._softmax(0), "wg1": self._softmax(1), "mma": self._mma(),
                 **{f"copy {p}": self._copy_one(p) for p in "KV"},
-                **{f"convert {p}": self._convert(p) for p in ("K", "KV", "V")}}
+                **{f"convert {p}": self._convert(p) for p in "KV"}}
 
     def _copy_one(self, pre):
         n = self.NK if pre == "K" else self.NV
@@ -54,7 +52,8 @@ class _Fp4Extend(_Model):
                 yield ("commit", f"L{pre}{c % n}")  # lands some time later
                 c += 1
 
-    def _convert(self, kinds):
+    def _convert(self, pre):
+        n = self.NK if pre == "K" else self.NV
         c = 0
         for op in self._units():
             if op[0] != "unit":
@@ -63,12 +62,10 @@ class _Fp4Extend(_Model):
             if op[1] is None:
                 return
             for _ in range(op[1]["nt"]):
-                for pre in kinds:
-                    n = self.NK if pre == "K" else self.NV
-                    if self.mistake != "converted before landing":
-                        yield self._wait(f"L{pre}{c % n}", c // n)
-                    yield ("use", f"L{pre}{c % n}", c // n)
-                    yield ("arrive", f"{pre}F{c % n}")
+                if self.mistake != "converted before landing":
+                    yield self._wait(f"L{pre}{c % n}", c // n)
+                yield ("use", f"L{pre}{c % n}", c // n)
+                yield ("arrive", f"{pre}F{c % n}")
                 c += 1
 
 
