@@ -524,7 +524,8 @@ int pkx_expand_paged_kv_indices(
  * infinity saturates; a block that holds a NaN gets the scale NaN (0x7f) and
  * reads NaN.  lk and lv are any positive multiples of 16; other arguments and
  * rules as pkx_set_kv_buffer (v may be NULL: only K is written; slots outside
- * the pool are skipped).
+ * the pool are skipped), but two tokens with the same slot leave that slot's
+ * rows undefined (one's codes may stand under the other's block scales).
  */
 int pkx_set_kv_buffer_fp4(
     const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
@@ -583,7 +584,10 @@ int pkx_decode_attention_fwd_fp4(
  * alone; k_extend / v_extend stay bf16).  With sliding_window W > 0, key j is
  * visible to the query at position P iff j <= P and (P - j <= W or
  * j < first_tokens).  first_tokens with a window and a custom mask together
- * return PKX_EUNSUPPORTED.
+ * return PKX_EUNSUPPORTED.  As in pkx_extend_attention_fwd, the rows of a
+ * block of queries share the tiles of its keys: a NaN or an infinity in the V
+ * row of a key that the masks hide from some of them reaches those rows too
+ * (decode reads visible keys alone).
  *   workspace >= pkx_extend_workspace_size(...) bytes
  */
 int pkx_extend_attention_fwd_fp4(

@@ -92,6 +92,7 @@ struct Fp4DecParams {
   int use_cap;
   float v_scale;
   uint64_t wait_ns;  // time limit of every bounded wait
+  int stall;
   int32_t *cta_err;  // [grid] status of each CTA
   int2 *entries;     // [max_shares] (sequence, parts) of the sequence split from this share on
   float *plse, *po;  // [2 max_shares][hq], [2 max_shares][hq][D]
@@ -162,12 +163,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
   __shared__ int s_seq[C::WARPS], s_tile0[C::WARPS];  // per stream: first sequence, its first tile
   __shared__ int s_err, s_abort;
   __shared__ uint64_t s_full[C::WARPS][C::STAGES], s_empty[C::WARPS][C::STAGES];  // [stream]
+  __shared__ uint64_t s_never;  // no thread arrives (the stall hook waits on it)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cta_set = blockIdx.x / p.head_groups, hg = blockIdx.x - cta_set * p.head_groups;
   // (KV head, column tile) pairs of this CTA: the warps of a stream
   const int heads = min(p.cta_heads, p.hkv * p.head_tiles - hg * p.cta_heads);
-  if (tid == 0) s_err = s_abort = 0;
+  if (tid == 0) {
+    s_err = s_abort = 0;
+    mbar_init(&s_never, 1);
+  }
   for (int i = tid; i < p.streams * C::STAGES; i += C::THREADS) {
     mbar_init(&s_full[i / C::STAGES][i % C::STAGES], heads * 32);
     mbar_init(&s_empty[i / C::STAGES][i % C::STAGES], heads);
@@ -337,7 +342,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
         if (!ok) *abort_flag = 1;
         return ok;
       };
-      while (tile < tile_end) {
+      if (p.stall) wait(&s_never, 0);  // test hook: the limit runs out
+      while (ok && tile < tile_end) {
         int gap;
         int n = visible_keys(p, b, gap, bad);
         while ((tile - base) * kTile >= n) {
@@ -773,35 +779,33 @@ __global__ void __launch_bounds__(kMergeThreads)
     gather(share, h, 0, e.y, 1, m, l, a);
     store(e.x, h, m, l, a);
   }
-  for (int k = 0; k < n_long; ++k) {
-    const int share = s_long[k];
+  for (int i = blockIdx.x; i < n_long * hq; i += gridDim.x) {
+    const int k = i / hq, h = i - k * hq, share = s_long[k];
     const int2 e = entries[share];
-    for (int h = blockIdx.x; h < hq; h += gridDim.x) {
-      float m, l, a[E];
-      gather(share, h, warp, e.y, kMergeWarps, m, l, a);
-      __syncthreads();  // the previous row's partials are read
-      if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    float m, l, a[E];
+    gather(share, h, warp, e.y, kMergeWarps, m, l, a);
+    __syncthreads();  // the previous row's partials are read
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int x = 0; x < E; ++x) s_o[warp][lane * E + x] = a[x];
+    __syncthreads();
+    if (warp == 0) {
+      m = -INFINITY;
+      for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
+      const float mr = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+#pragma unroll
+      for (int x = 0; x < E; ++x) a[x] = 0.f;
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float f = ex2_approx((s_m[w] - mr) * kLog2e);
+        l += s_l[w] * f;
+#pragma unroll
+        for (int x = 0; x < E; ++x) a[x] += s_o[w][lane * E + x] * f;
       }
-#pragma unroll
-      for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = a[k];
-      __syncthreads();
-      if (warp == 0) {
-        m = -INFINITY;
-        for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
-        const float mr = m == -INFINITY ? 0.f : m;
-        l = 0.f;
-#pragma unroll
-        for (int k = 0; k < E; ++k) a[k] = 0.f;
-        for (int w = 0; w < kMergeWarps; ++w) {
-          const float f = ex2_approx((s_m[w] - mr) * kLog2e);
-          l += s_l[w] * f;
-#pragma unroll
-          for (int k = 0; k < E; ++k) a[k] += s_o[w][lane * E + k] * f;
-        }
-        store(e.x, h, m, l, a);
-      }
+      store(e.x, h, m, l, a);
     }
   }
 }
@@ -901,8 +905,7 @@ int launch_decode_fp4(const Fp4DecodeArgs &a) {
   p.cap_pre = p.use_cap ? sm_scale / a.logit_cap : 0.f;
   p.cap_log2 = p.use_cap ? a.logit_cap * kLog2e : 0.f;
   p.v_scale = a.v_scale;
-  int stall;
-  wait_settings(&p.wait_ns, &stall);
+  wait_settings(&p.wait_ns, &p.stall);
   p.cta_err = reinterpret_cast<int32_t *>(ws + L.err);
   p.entries = reinterpret_cast<int2 *>(ws + L.entries);
   p.plse = reinterpret_cast<float *>(ws + L.plse);

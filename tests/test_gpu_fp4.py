@@ -324,10 +324,12 @@ def test_decode_repeats_and_streams_and_graph():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], full)
 
 
-def test_decode_many_split_sequences():
+@pytest.mark.parametrize("hq,hkv,long", [(32, 4, []), (8, 1, [30000, 7, 25000])])
+def test_decode_many_split_sequences(hq, hkv, long):
     """More sequences that several shares hold than a CTA of the merge takes
-    rows: every one is merged, in repeated calls on one workspace."""
-    c = Decode(64, 32, 4, [700 + 13 * i for i in range(90)], seed=15)
+    rows: every one is merged, in repeated calls on one workspace.  One KV
+    head: 16 shares a CTA, and some sequences of more than 32 parts."""
+    c = Decode(64, hq, hkv, [700 + 13 * i for i in range(90)] + long, seed=15)
     ref, ws = c.reference(), None
     for _ in range(20):
         o, lse, ws = c.run(ws=ws)
@@ -365,3 +367,51 @@ def test_write_then_decode():
                 ok = R.visible(torch.tensor([step]), step + 1, 16, 2)
                 ref = R.attend(q[i:i + 1].double(), kk, vv, ok, 1 / math.sqrt(d))
                 R.check(o[i:i + 1], lse[i:i + 1], ref, d, 1 / math.sqrt(d), F16_STEP)
+
+
+def test_offsets_past_32_bits():
+    """Slots whose bytes lie past 4 GB in every tensor of the pool: write, read
+    back, decode and extend."""
+    g = _gen(16)
+    d, hq, hkv, n, step = 128, 8, 2, 40, 1 << 27  # slots 128 MB apart
+    big = torch.zeros(n * step + 4096, dtype=torch.uint8, device=DEV)
+    at = lambda off, w: big[off:].as_strided((n, hkv, w), (step, w, 1))
+    kc, vc = at(0, d // 2), at(512, d // 2)
+    kb, vb = (at(o, d // 16).view(torch.float8_e4m3fn) for o in (1024, 1536))
+    k, v = _bf16(g, n, hkv, d), _bf16(g, n, hkv, d)
+    loc = torch.randperm(n, generator=g)
+    pkx.set_kv_buffer_fp4(kc, kb, vc, vb, loc.to(DEV), k.to(DEV), v.to(DEV))
+    kk, vv = R.unpack(*R.pack(k, 1.0)), R.unpack(*R.pack(v, 1.0))
+    idx = loc.to(torch.int32).to(DEV)
+    gk, gv = pkx.get_kv_buffer_fp4(kc, kb, vc, vb, idx)
+    assert torch.equal(gk.cpu(), kk.bfloat16()) and torch.equal(gv.cpu(), vv.bfloat16())
+    q, e = _bf16(g, 1, hq, d), _bf16(g, 3, hq, d)
+    ke, ve = _bf16(g, 3, hkv, d), _bf16(g, 3, hkv, d)
+    ptr = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    o, lse = torch.empty(1, hq, d, dtype=torch.bfloat16, device=DEV), torch.empty(1, hq, device=DEV)
+    pkx.decode_attention_fwd_fp4(q.to(DEV), o, kc, kb, vc, vb, ptr, idx, lse=lse)
+    ok = torch.ones(1, n, dtype=torch.bool)
+    R.check(o, lse, R.attend(q.double(), kk, vv, ok, d ** -0.5), d, d ** -0.5, F16_STEP)
+    o, lse = torch.empty(3, hq, d, dtype=torch.bfloat16, device=DEV), torch.empty(3, hq, device=DEV)
+    qo = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    pkx.extend_attention_fwd_fp4(e.to(DEV), ke.to(DEV), ve.to(DEV), o, kc, kb, vc, vb, qo, ptr, idx, lse=lse)
+    ref = R.attend(e.double(), torch.cat([kk, ke.double()]), torch.cat([vv, ve.double()]),
+                   R.visible(torch.arange(3) + n, n + 3, -1, 0), d ** -0.5)
+    R.check(o, lse, ref, d, d ** -0.5, 2.0 ** -8)
+
+
+def test_decode_wait_that_runs_out_is_reported():
+    """The stall hook makes a wait run out: the status says so, the context
+    stays usable and the next call is whole again."""
+    c = Decode(128, 32, 8, [4000, 900], seed=18)
+    want, wl, _ = c.run()
+    pkx.set_wait_limit_ns(20_000_000)
+    pkx.set_stall_injection(True)
+    try:
+        _, _, ws = c.run()
+        assert pkx.workspace_status(ws) == pkx.PKX_ETIMEOUT
+    finally:
+        pkx.set_stall_injection(False)
+        pkx.set_wait_limit_ns(0)
+    o, lse, ws = c.run(ws=ws)
+    assert pkx.workspace_status(ws) == 0 and torch.equal(o, want) and torch.equal(lse, wl)

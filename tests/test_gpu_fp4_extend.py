@@ -170,3 +170,19 @@ def test_serving_turns():
     # bf16 of an fp32 product: within half a step of bf16 (and of fp32)
     for got, want in ((k, kk), (v, vv)):
         assert ((got.cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -23) * want.abs()).all()
+
+
+def test_rows_behind_the_last_sequence_stay():
+    """A padded batch: query rows past qo_indptr's end and sequences without
+    new tokens."""
+    c = Case(64, 8, 2, [100, 50], [20, 30], 19)
+    want, wl_, _ = c.run()
+    pad = lambda x: torch.cat([x, torch.ones(7, *x.shape[1:], dtype=x.dtype, device=DEV)])
+    qo = torch.cat([c.qo, c.qo[-1:], c.qo[-1:]])
+    ptr = torch.cat([c.ptr, c.ptr[-1:], c.ptr[-1:]])
+    q = pad(c.q)
+    o, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 6.0, device=DEV)
+    ws = pkx.extend_attention_fwd_fp4(q, pad(c.ke), pad(c.ve), o, *c.pool, qo, ptr, c.idx, c.wl.sm_scale, lse=lse)
+    assert pkx.workspace_status(ws) == 0
+    assert torch.equal(o[:50], want) and torch.equal(lse[:50], wl_)
+    assert (o[50:] == 5.0).all() and (lse[50:] == 6.0).all()
