@@ -715,6 +715,13 @@ __device__ __forceinline__ void tile_keys(const WorkUnit &w, int j, int &kb, int
   }
 }
 
+// The bits [from, from + n) of a word (those below 32; none for n <= 0).
+__device__ __forceinline__ uint32_t bit_range(int from, int n) {
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(r) : "r"(from), "r"(max(n, 0)));
+  return r;
+}
+
 __device__ __forceinline__ void abort_cta(volatile int *abort_flag, int32_t *status, int code) {
   *abort_flag = 1;
   record_status(status, code);
@@ -848,6 +855,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
   // tiles and 14-15 the V tiles; extend over a 4-bit pool: warp 10 copies K,
   // warp 11 V, warps 12-13 convert K and 14-15 V
   constexpr bool F4 = FMT == 3;
+  constexpr bool BITS = FIRST || F4;  // masked tiles by words of bits
   constexpr int RAW_THREADS = 64, CONV_THREADS = 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -1100,18 +1108,29 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
               }
               sc = 1.0f;
             }
-          } else if (FIRST && need_mask) {
+          } else if (BITS && need_mask) {
             // numbers of the row's last key (causal, end of the tile) and of
-            // the first one in its window
-            const int vhi =
-                min(ke - 1, qpos - gap >= p.first ? qpos - gap : min(qpos, p.first - 1));
-            const int vlo = qpos - p.window - gap;
-#pragma unroll
-            for (int i = 0; i < C::BN; ++i) {
-              const int v = kb + i;
-              x[i] = v <= vhi && (v < p.first || v >= vlo) ? x[i] * sc : -INFINITY;
+            // the first one in its window; a word of bits for every 32 keys of
+            // the tile, tested one by one.  The logits keep their scale (it is
+            // positive), so a hidden one is -inf before it.  Three comparisons
+            // and a product a key took 45 of 179 us on 16 sequences of up to
+            // (4096 + 1024) tokens with a window of 1024.
+            int vhi = qpos, vlo = p.window > 0 ? qpos - p.window : 0;
+            uint32_t bits[4];
+            if constexpr (FIRST) {
+              vhi = qpos - gap >= p.first ? qpos - gap : min(qpos, p.first - 1);
+              vlo -= gap;
             }
-            sc = 1.0f;
+            vhi = min(vhi, ke - 1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int k0 = kb + 32 * q, lo = max(vlo - k0, 0);
+              bits[q] = bit_range(lo, vhi + 1 - k0 - lo);
+              if constexpr (FIRST) bits[q] |= bit_range(0, min(p.first, vhi + 1) - k0);
+            }
+#pragma unroll
+            for (int i = 0; i < C::BN; ++i)
+              if (!((bits[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
           } else if (need_mask) {
 #pragma unroll
             for (int i = 0; i < C::BN; ++i) {
@@ -2727,6 +2746,10 @@ int launch_attention(const AttnArgs &a) {
   kp.cap_pre = kp.use_cap ? sm_scale / a.logit_cap : 0.f;
   kp.cap_log2 = kp.use_cap ? a.logit_cap * log2e : 0.f;
   kp.scale_log2_k = kp.scale_log2 * a.k_scale;
+  if (sp.first > 0 || a.kv_fmt == kKvFp4) {  // never 0: a hidden logit is -inf before its scale
+    kp.scale_log2 = std::max(kp.scale_log2, 1e-37f);
+    kp.scale_log2_k = std::max(kp.scale_log2_k, 1e-37f);
+  }
   kp.cap_pre_k = kp.cap_pre * a.k_scale;
   kp.custom_mask = a.custom_mask;
   kp.mask_indptr = a.mask_indptr;
