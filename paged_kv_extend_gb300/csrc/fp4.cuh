@@ -27,9 +27,10 @@ __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t two) {
 // The eight e2m1 codes of a word as four f16 pairs (out[i]: the codes of byte
 // i, low nibble in the low half), by the hardware's converter.  Spreading the
 // codes' bits by hand (sign to bit 15, magnitude to bits 11..9: the value
-// times 2^-14) takes four integer operations a pair; decode over 64 x 8192
-// keys ran in 162 us with that, 149 us with half of each and 138 us with the
-// converter alone.
+// times 2^-14) takes four integer operations a pair: decode over 64 x 8192
+// keys ran in 162 us with that, 149 us with half of each, 138 us with the
+// converter alone and shifts for its bytes, and 122 us with the bytes taken
+// apart as operands, as here.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t x, uint32_t (&out)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"

@@ -9,8 +9,8 @@
 // What bounds it.  A key of one KV head is 2 * (D / 2 + D / 16) bytes (144 at
 // D = 128), and every one of its 2 D codes has to become a 16-bit number
 // before a product: at the copy bandwidth an SM receives 41 elements a clock,
-// and the conversion alone takes about four integer operations for two
-// elements.  So a code is converted once, in registers, straight into the
+// and two elements take a conversion (two clocks of a quarter SM) and a product
+// with their scale.  So a code is converted once, in registers, straight into the
 // operand fragment of the product that uses it, and never goes back to shared
 // memory (a tcgen05 product would need the converted tile there or in tensor
 // memory: 82 bytes a clock written and 82 read back beside the copies).  The
@@ -31,13 +31,15 @@
 //    times 2^-8 relative to the row's maximum, error 2^-11).
 //  * O^T = V^T P^T.  P^T is S^T's accumulator layout transposed 8 x 8
 //    (movmatrix).  Lane g holds D / 8 dims of the keys whose P its t holds;
-//    two keys' words are interleaved by half words, so the conversion yields
-//    (key, next key) pairs of one dim.
-//  * Every warp is on its own: a warp is one (KV head, eight query heads) and
-//    a contiguous share of the batch's key tiles (32 keys); the warps of a
-//    CTA take the KV heads of the same keys, so that a slot's row is read as
-//    one run.  A warp stages its tiles by cp.async in a private ring; no
-//    barrier is shared, nothing spins.
+//    two keys' words are interleaved by codes, so the conversion yields (key,
+//    next key) pairs of one dim.
+//  * A warp is one (KV head, eight query heads) and a contiguous share of the
+//    batch's key tiles (32 keys), with its own softmax state; the warps of a
+//    CTA that share keys (a stream, one warp a KV head) copy each slot's rows
+//    together, by cp.async into a ring of tiles with full / empty barriers.
+//  * Measured, 64 x 8192 keys, 32 query and 8 KV heads of 128: 122 us, 5.0 TB/s
+//    (0.73 of the copy bandwidth), bound by issue: 667 instructions a tile and
+//    head, 65 % of the slots, ALU pipe 55 %, tensor pipe 25 %.
 //  * The shares are equal (sizes differ by one tile), computed on the device
 //    from kv_indptr by every CTA.  A sequence that lies in one share is
 //    finished by its warp; the parts of one that several shares hold go to
@@ -811,7 +813,12 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // ===================================================================== host
-// How the (KV head, column tile) pairs lie over CTAs and warps.
+// How the (KV head, column tile) pairs lie over CTAs and warps.  Groups of more
+// than eight heads give a warp two column tiles: a code is converted once for
+// both, but the registers leave room for eight warps an SM instead of sixteen.
+// 64 x 8192 keys, 64 query and 4 KV heads: 102 us against 124 us with one
+// column tile (D = 64: 78 against 89; 128 query heads and one KV head: 186
+// against 247).
 struct Fp4DecPlan {
   int nt, warps, head_tiles, cta_heads, head_groups, streams, sets, max_shares, grid;
 };
