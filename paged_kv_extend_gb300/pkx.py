@@ -687,6 +687,12 @@ def _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale):
     return (*kd, vd[2]), ks, vs
 
 
+def _c_int(x):
+    """A window or a count as a C int: what lies past its range is as good as
+    its limit (ctypes would cut off the high bits)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def _one_device(dev, **tensors):
     for name, t in tensors.items():  # (indices first: cheap, and enough between GPUs)
         if t is not None and t.get_device() != dev.index:
@@ -809,7 +815,7 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(k_block_scale), _ptr(v_buffer),
         _ptr(v_block_scale), _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, b,
         hq, hkv, lq, lv, *ks, *vs, dims[0], float(sm_scale or 0.0),
-        float(logit_cap or 0.0), int(sliding_window), int(first_tokens), float(k_scale),
+        float(logit_cap or 0.0), _c_int(sliding_window), _c_int(first_tokens), float(k_scale),
         float(v_scale), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
     return ws
 
@@ -866,7 +872,7 @@ def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k
         _ptr(k_block_scale), _ptr(v_buffer), _ptr(v_block_scale), _ptr(qo_indptr),
         _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq,
         lv, *ke, *ve, *ks, *vs, dims[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
-        int(sliding_window), int(first_tokens),
+        _c_int(sliding_window), _c_int(first_tokens),
         *_mask_sinks(custom_mask, mask_indptr, sinks), float(k_scale), float(v_scale), _ptr(lse),
         _ptr(ws), ws.numel() * ws.element_size()))
     return ws
@@ -907,7 +913,7 @@ def extend_attention_fwd_streaming(q_extend, k_extend, v_extend, o_extend, k_buf
         _ptr(v_buffer), _ptr(qo_indptr), _ptr(kv_indptr),
         _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq, lv, *ke, *ve,
         *strides, k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
-        int(sliding_window), int(first_tokens), _mask_sinks(None, None, sinks)[2], _ptr(lse),
+        _c_int(sliding_window), _c_int(first_tokens), _mask_sinks(None, None, sinks)[2], _ptr(lse),
         _ptr(ws), ws.numel() * ws.element_size()))
     return ws
 
@@ -933,6 +939,6 @@ def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indic
         q.device, lib.pkx_decode_attention_fwd_streaming,
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(v_buffer), _ptr(kv_indptr),
         _ptr(kv_indices) if kv_indices.numel() else None, b, hq, hkv, lq, lv, *strides,
-        k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), int(sliding_window),
-        int(first_tokens), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
+        k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), _c_int(sliding_window),
+        _c_int(first_tokens), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
     return ws

@@ -132,3 +132,7 @@ def test_binding_refuses():
     ptr = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
         pkx.decode_attention_fwd_fp4(x, x, kc, kb, kc, kb, ptr, ptr)
+
+
+def test_windows_past_the_int_range():
+    assert pkx._c_int(2 ** 32 + 5) == 2 ** 31 - 1 and pkx._c_int(-2 ** 40) == -2 ** 31 and pkx._c_int(7) == 7
