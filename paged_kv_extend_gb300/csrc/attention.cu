@@ -802,6 +802,13 @@ __device__ __forceinline__ uint4 fp8x8_to_f16x8(uint2 raw) {
 // keeps any bf16 of magnitude below 2^24 inside the f16 range; the logit
 // scale takes the 2^8 back.
 constexpr float kQF16Down = 0x1p-8f, kQF16Up = 256.0f;
+// 4-bit pool: P is in f16, whose normal range ends at 2^-14, so a key some 12
+// nats below its row's largest would lose bits, and one at 17 nats all of them
+// (they are the output when the largest is a first token with a small value).
+// P is therefore taken 2^11 times too large (the sum takes the same factor,
+// which cancels) and the running maximum may lag by 2^4 at most: P stays below
+// 2^15, and a key keeps bf16's 8 bits down to 2^-28 of the largest.
+constexpr float kF4Shift = 11.0f, kF4Lag = 4.0f;
 __device__ __forceinline__ uint4 bf16x8_to_f16x8_scaled(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t out[4];
@@ -1168,8 +1175,8 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           // Rescale only when the max grows by more than 2^8: exponents of
           // the stale max stay below 256, which fp32 sums and bf16 P hold.
           // (S_full of this tile completes after the previous PV, so O is
-          // quiescent here.)
-          const bool grow = m_new > m + 8.0f;
+          // quiescent here.  A 4-bit pool: kF4Lag.)
+          const bool grow = m_new > m + (F4 ? kF4Lag : 8.0f);
           const float alpha = grow ? ex2_approx(m - m_new) : 1.0f;
           const bool o_needs = grow && j > j0 && l > 0.f;
           if (grow) {
@@ -1182,6 +1189,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           float lscale = 1.0f;
           if constexpr (FMT != 0 && !F16) {
             if constexpr (F4) {
+              nm += kF4Shift;
               // the output takes v_scale; P of a tile of extend rows is
               // divided by it (bf16 has the range, the f16 P of a pool tile
               // has not)
@@ -1249,6 +1257,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       ++o_cnt;
       tc_fence_after();
       if (warp_active) {
+        if constexpr (F4) m -= kF4Shift;  // l and O are 2^kF4Shift times too large
         float inv = l > 0.f ? 1.0f / l : 0.f;
         float lse_v = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         if (p.sinks && w.slot < 0) {

@@ -26,9 +26,13 @@
 //    permuted once to match.  Each element is multiplied by its block scale
 //    (exact in f16).
 //  * The online softmax keeps one running maximum per head in all lanes and
-//    moves it only when a logit exceeds it by 2^8 (in log2), which a vote
-//    finds; sums and outputs are fp32, P is rounded to f16 (values in [0, 2^8]
-//    times 2^-8 relative to the row's maximum, error 2^-11).
+//    moves it only when a logit exceeds it by kPLag (in log2), which a vote
+//    finds; sums and outputs are fp32, P is rounded to f16 (error 2^-11).
+//    f16's normal range ends at 2^-14, and a first token with a large logit
+//    and a small value leaves the output to keys far below the maximum: P is
+//    taken 2^kPShift times too large (the sum too, so the factor cancels), so
+//    that it stays below 2^15 and keeps its 11 bits down to 2^-26 of the
+//    maximum (18 nats).
 //  * O^T = V^T P^T.  P^T is S^T's accumulator layout transposed 8 x 8
 //    (movmatrix).  Lane g holds D / 8 dims of the keys whose P its t holds;
 //    two keys' words are interleaved by codes, so the conversion yields (key,
@@ -56,6 +60,7 @@ namespace pkx {
 
 constexpr int kTile = 32;          // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kPShift = 12.0f, kPLag = 3.0f;  // P <= 2^(kPShift + kPLag)
 
 template <int D, int NT>  // head dim; column tiles of eight query heads
 struct DecCfg {
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
               mul[c][j] = p.use_cap ? 1.0f : mult[c][j];
               mx[c][j] = mul[c][j] * fmaxf(fmaxf(s[0][c][j], s[0][c][2 + j]),
                                            fmaxf(s[1][c][j], s[1][c][2 + j]));
-              grow |= mx[c][j] > m[c][j] + 8.0f;
+              grow |= mx[c][j] > m[c][j] + kPLag;
             }
           }
           if (__any_sync(0xffffffffu, grow)) {
@@ -521,7 +526,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
           for (int c = 0; c < NT; ++c) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float nm = m[c][j] == -INFINITY ? 0.f : -m[c][j];
+              const float nm = m[c][j] == -INFINITY ? 0.f : kPShift - m[c][j];
 #pragma unroll
               for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1)
             if (head >= p.group) continue;
             const int hqi = kvh * p.group + head;
             const float inv = ls == 0.f ? 0.f : p.v_scale / ls;  // a NaN sum stays NaN
-            const float lse = ls == 0.f ? -INFINITY : (m[c][j] + __log2f(ls)) * kLn2;
+            const float lse = ls == 0.f ? -INFINITY : (m[c][j] - kPShift + __log2f(ls)) * kLn2;
             float x[D / 8];
 #pragma unroll
             for (int w = 0; w < VW; ++w)

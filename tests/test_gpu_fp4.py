@@ -225,6 +225,28 @@ def test_decode(d, hq, hkv, lens, cap, window, first, ks, vs):
     assert pkx.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("d,hq,hkv,lens,at,nats", [
+    (128, 8, 2, [3000, 40], 0, 17.0), (64, 12, 4, [900, 2000], 500, 17.0), (128, 16, 1, [30000], 3, 14.0)])
+def test_decode_dominant_key_with_a_zero_value(d, hq, hkv, lens, at, nats):
+    """One key takes nearly all of the weight and its value is zero, so that
+    the output is made of keys with weights of 2^-20 to 2^-25: they keep P's
+    11 bits."""
+    c = Decode(d, hq, hkv, lens, seed=d + at)
+    g = _gen(at)
+    slots = c.k[0].shape[0]
+    c.q = _bf16(g, 1, hkv, 1, d).expand(len(lens), hkv, hq // hkv, d).reshape(len(lens), hq, d).contiguous()
+    k, v = _bf16(g, slots, hkv, d, amp=0.1), _bf16(g, slots, hkv, d) + 0.5
+    q = c.q[0].float().view(hkv, hq // hkv, d)[:, 0]
+    for b in range(len(lens)):
+        slot = int(c.idx[int(c.indptr[b]) + min(at, lens[b] - 1)])
+        k[slot] = (q * (nats / c.scale / q.square().sum(-1, keepdim=True))).bfloat16()
+        v[slot] = 0
+    c.k, c.v = R.pack(k, 1.0), R.pack(v, 1.0)
+    c.dev[:4] = [x.to(DEV) for x in (*_to_dev(*c.k), *_to_dev(*c.v))]
+    o, lse, _ = c.run()
+    R.check(o, lse, c.reference(), d, c.scale, F16_STEP)
+
+
 @pytest.mark.parametrize("qamp", [1e-20, 3e-3, 60.0])
 def test_decode_query_range(qamp):
     """Queries far outside f16's range keep their bits."""

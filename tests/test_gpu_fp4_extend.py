@@ -78,6 +78,38 @@ def test_extend(d, hq, hkv, prefix, extend, cap, window, first, ks, vs, sinks):
     assert pkx.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("d,hq,hkv,prefix,extend,at,nats,sinks", [
+    (128, 8, 2, [2000, 300], [40, 3], 0, 16.0, False), (64, 4, 4, [900, 5000], [1, 130], 200, 16.0, True)])
+def test_dominant_key_with_a_zero_value(d, hq, hkv, prefix, extend, at, nats, sinks):
+    """One key of the pool takes nearly all of the weight and its value is
+    zero, so that the output is made of keys with weights near 2^-23: they
+    keep P's bits."""
+    c = Case(d, hq, hkv, prefix, extend, d)
+    wl, g = c.wl, torch.Generator().manual_seed(d)
+    q = torch.randn(hkv, 1, d, generator=g).bfloat16()
+    wl.q[:] = q.expand(hkv, hq // hkv, d).reshape(hq, d)
+    c.q = wl.q.to(DEV)
+    k = (torch.randn(sum(prefix), hkv, d, generator=g) * 0.1).bfloat16()
+    v = (torch.randn(sum(prefix), hkv, d, generator=g) + 0.5).bfloat16()
+    q = q[:, 0].float()
+    p0 = 0
+    for p in prefix:
+        k[p0 + at] = (q * (nats / wl.sm_scale / q.square().sum(-1, keepdim=True))).bfloat16()
+        v[p0 + at] = 0
+        p0 += p
+    c.rows = []
+    slots = wl.kv_indices.long().to(DEV)
+    for i, x in enumerate((k, v)):
+        codes, scales = R.pack(x, 1.0)
+        c.rows.append(R.unpack(codes, scales, 1.0))
+        c.pool[2 * i][slots] = codes.to(DEV)
+        c.pool[2 * i + 1].view(torch.uint8)[slots] = scales.to(DEV)
+    c.ke *= 0.05
+    sk = torch.randn(hq, generator=g) if sinks else None
+    o, lse, _ = c.run(sinks=sk.to(DEV) if sinks else None)
+    R.check(o, lse, c.reference(sinks=sk), d, wl.sm_scale, BF16_STEP)
+
+
 @pytest.mark.parametrize("d,window,sinks", [(128, -1, False), (64, 50, True)])
 def test_extend_with_a_custom_mask(d, window, sinks):
     from gpu_cases import random_masks
