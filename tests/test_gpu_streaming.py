@@ -84,6 +84,18 @@ def test_extend_without_window_or_first_is_the_plain_call():
         assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+def test_window_and_first_tokens_of_any_size():
+    """Past the C int range, and at its limit, they mean all keys."""
+    c = Extend(_draw(128, 8, 2, [300, 5], [40, 2], seed=8))
+    want, wl_, _ = c.run(-1, 0)
+    ref = R.extend(c.wl, *_prefix_rows(c.wl), c.ke.cpu(), c.ve.cpu())
+    R.check(want, wl_, ref, 128, c.wl.sm_scale, BF16_STEP)
+    for window, first in ((2 ** 32 + 5, 0), (2 ** 31 - 1, 2 ** 31 - 1), (7, 2 ** 40), (-2 ** 40, 3)):
+        o, lse, ws = c.run(window, first)
+        R.check(o, lse, ref, 128, c.wl.sm_scale, BF16_STEP, f"{window} {first}")
+        assert pkx.workspace_status(ws) == 0
+
+
 def test_extend_reads_nothing_in_the_gap():
     """Keys between the first tokens and every window may hold NaN or bad
     slots; the first tokens and the window may not."""
