@@ -509,7 +509,8 @@ int pkx_expand_paged_kv_indices(
  * All strides of a 4-bit pool are in BYTES.  The write and the read back need
  * code bases and strides that are multiples of 8 bytes; the attention calls
  * need multiples of 16 bytes, block-scale bases and strides that are multiples
- * of d / 16 bytes, and slot strides below 2^31 bytes.
+ * of d / 16 bytes, slot strides below 2^31 bytes, and k_scale and v_scale in
+ * [2^-64, 2^64].
  */
 
 /*

@@ -615,7 +615,13 @@ static int check_fp4_attention(int hq, int hkv, int lq, int lv, float k_scale,
   if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
   if (!((lq == 64 && lv == 64) || (lq == 128 && lv == 128)))
     return set_error(PKX_EUNSUPPORTED, "a 4-bit pool is built for Lq = Lv = 64 or 128");
-  return check_fp4_scales(k_scale, v_scale);
+  if ((rc = check_fp4_scales(k_scale, v_scale))) return rc;
+  // the scales join fp32 factors of logits, sums and outputs, which they must
+  // not drive out of range (extend divides P of its new rows by v_scale)
+  if (k_scale < 0x1p-64f || k_scale > 0x1p64f || v_scale < 0x1p-64f || v_scale > 0x1p64f)
+    return set_error(PKX_EUNSUPPORTED, "k_scale and v_scale of attention over a 4-bit pool must "
+                     "lie in [2^-64, 2^64]");
+  return PKX_OK;
 }
 
 static int check_fp4_attention_rows(const Fp4Pool &p, int d) {

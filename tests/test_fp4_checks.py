@@ -100,6 +100,7 @@ def _decode(lib, **over):
     (dict(hq=258, hkv=2), pkx.PKX_EUNSUPPORTED), (dict(lq=576, lv=512), pkx.PKX_EUNSUPPORTED),
     (dict(lq=192, lv=128), pkx.PKX_EUNSUPPORTED), (dict(lq=96, lv=96), pkx.PKX_EUNSUPPORTED),
     (dict(ks=-1.0), pkx.PKX_EINVAL), (dict(scale=float("nan")), pkx.PKX_EINVAL),
+    (dict(ks=2.0 ** -65), pkx.PKX_EUNSUPPORTED), (dict(vs=2.0 ** 65), pkx.PKX_EUNSUPPORTED),
     (dict(first=-1), pkx.PKX_EINVAL), (dict(q=None), pkx.PKX_EINVAL), (dict(o=P + 8), pkx.PKX_EINVAL),
     (dict(kc=P + 8), pkx.PKX_EINVAL), (dict(kb=P + 4), pkx.PKX_EINVAL), (dict(vc=None), pkx.PKX_EINVAL),
     (dict(st=(128, 72, 16, 8, 128, 64, 16, 8)), pkx.PKX_EINVAL),

@@ -217,6 +217,8 @@ class Decode:
     (64, 8, 2, [1] * 700, 0.0, -1, 0, 1.0, 1.0),            # more sequences than threads
     (128, 4, 1, [50, 60], 0.0, 1000, 10, 1.0, 1.0),         # a window longer than the keys
     (128, 8, 2, [400, 33], 0.0, 100, 100000, 1.0, 1.0),     # first tokens past the keys
+    (128, 8, 2, [700, 33], 0.0, -1, 0, 2.0 ** -64, 2.0 ** 64),   # the scales' limits
+    (64, 8, 2, [700, 33], 3.0, -1, 0, 2.0 ** -64, 2.0 ** -64),
 ])
 def test_decode(d, hq, hkv, lens, cap, window, first, ks, vs):
     c = Decode(d, hq, hkv, lens, seed=d + hq + sum(lens), ks=ks, vs=vs)

@@ -68,6 +68,8 @@ class Case:
     (128, 128, 1, [900, 128], [40, 1], 0.0, -1, 0, 1.0, 1.0, False),
     (128, 2, 2, [0], [129], 0.0, -1, 0, 1.0, 1.0, False),   # no prefix at all
     (128, 6, 2, [127, 128, 129], [1, 1, 1], 0.0, -1, 0, 2.0, 0.5, False),
+    (128, 8, 2, [200, 0, 700], [30, 140, 1], 0.0, -1, 0, 2.0 ** -64, 2.0 ** 64, False),  # the scales' limits
+    (64, 8, 2, [200, 0, 1000], [30, 140, 1], 0.0, 300, 0, 2.0 ** -64, 2.0 ** -64, True),
 ])
 def test_extend(d, hq, hkv, prefix, extend, cap, window, first, ks, vs, sinks):
     c = Case(d, hq, hkv, prefix, extend, sum(prefix) + d, ks, vs)
