@@ -690,13 +690,21 @@ def _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale):
 def _c_int(x):
     """A window or a count as a C int: what lies past its range is as good as
     its limit (ctypes would cut off the high bits)."""
-    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+    x = int(x)
+    return x if -2147483648 <= x <= 2147483647 else 2147483647 if x > 0 else -2147483648
 
 
 def _one_device(dev, **tensors):
-    for name, t in tensors.items():  # (indices first: cheap, and enough between GPUs)
-        if t is not None and t.get_device() != dev.index:
+    """All on the GPU ``dev``: their addresses may be taken as they are."""
+    index = dev.index  # (comparing indices is cheap, and enough between GPUs)
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _address(t):
+    """Address of a tensor whose device is checked, or None."""
+    return None if t is None else t.data_ptr()
 
 
 def set_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, cache_loc, k, v=None,
@@ -721,15 +729,15 @@ def set_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, cache_lo
         if tuple(v.shape) != (n, hkv, row_v):
             raise ValueError(f"v {tuple(v.shape)} does not fit k {tuple(k.shape)} and v_buffer's "
                              f"rows of {row_v} elements")
-        v_buffer_ptr, v_scale_ptr = _ptr(v_buffer), _ptr(v_block_scale)
+        v_buffer_ptr, v_scale_ptr = v_buffer.data_ptr(), v_block_scale.data_ptr()
     if row != [hkv, lk]:
         raise ValueError(f"k {tuple(k.shape)} does not fit k_buffer's rows of {row} heads and elements")
     _one_device(k.device, k_buffer=k_buffer, cache_loc=cache_loc, v=v)
     _check(_on(
         k.device, lib.pkx_set_kv_buffer_fp4,
-        _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _ptr(cache_loc) if n else None, n, hkv,
-        lk, lv, float(k_scale), float(v_scale), _ptr(k_buffer), kb[0], kb[1],
-        _ptr(k_block_scale), kb[2], kb[3], v_buffer_ptr, vb[0], vb[1], v_scale_ptr, vb[2], vb[3],
+        k.data_ptr(), ks[0], ks[1], _address(v), vs[0], vs[1], cache_loc.data_ptr(), n, hkv,
+        lk, lv, float(k_scale), float(v_scale), k_buffer.data_ptr(), kb[0], kb[1],
+        k_block_scale.data_ptr(), kb[2], kb[3], v_buffer_ptr, vb[0], vb[1], v_scale_ptr, vb[2], vb[3],
         slots))
     return k_buffer, k_block_scale, v_buffer, v_block_scale
 
@@ -750,7 +758,7 @@ def get_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, kv_indic
         v_scale_ptr = None
     else:
         (slots, hkv, lk, lv), kb, vb = _fp4_pools(k_buffer, k_block_scale, v_buffer, v_block_scale)
-        v_scale_ptr = _ptr(v_block_scale)
+        v_scale_ptr = v_block_scale.data_ptr()
 
     def output(t, d, name):
         if t is None:
@@ -766,10 +774,10 @@ def get_kv_buffer_fp4(k_buffer, k_block_scale, v_buffer, v_block_scale, kv_indic
     _one_device(dev, kv_indices=kv_indices)
     _check(_on(
         dev, lib.pkx_get_kv_buffer_fp4,
-        _ptr(k_buffer), kb[0], kb[1], _ptr(k_block_scale), kb[2], kb[3],
-        _ptr(v_buffer), vb[0], vb[1], v_scale_ptr, vb[2], vb[3], slots,
-        _ptr(kv_indices) if n else None, n, hkv, lk, lv, float(k_scale), float(v_scale),
-        _ptr(k_out) if n else None, ks[0], ks[1], _ptr(v_out), vs[0], vs[1]))
+        k_buffer.data_ptr(), kb[0], kb[1], k_block_scale.data_ptr(), kb[2], kb[3],
+        _address(v_buffer), vb[0], vb[1], v_scale_ptr, vb[2], vb[3], slots,
+        kv_indices.data_ptr(), n, hkv, lk, lv, float(k_scale), float(v_scale),
+        k_out.data_ptr(), ks[0], ks[1], _address(v_out), vs[0], vs[1]))
     return k_out, v_out
 
 
@@ -812,11 +820,11 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
     ws = _own_workspace(workspace, decode_fp4_workspace_size, q.device, b, hq, hkv, lq, lv)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd_fp4,
-        _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(k_block_scale), _ptr(v_buffer),
-        _ptr(v_block_scale), _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, b,
+        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), k_block_scale.data_ptr(), v_buffer.data_ptr(),
+        v_block_scale.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), b,
         hq, hkv, lq, lv, *ks, *vs, dims[0], float(sm_scale or 0.0),
         float(logit_cap or 0.0), _c_int(sliding_window), _c_int(first_tokens), float(k_scale),
-        float(v_scale), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
+        float(v_scale), _address(lse), ws.data_ptr(), ws.numel() * ws.element_size()))
     return ws
 
 
@@ -868,13 +876,13 @@ def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k
     ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
     _check(_on(
         dev, lib.pkx_extend_attention_fwd_fp4,
-        _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
-        _ptr(k_block_scale), _ptr(v_buffer), _ptr(v_block_scale), _ptr(qo_indptr),
-        _ptr(kv_indptr), _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq,
+        q_extend.data_ptr(), k_extend.data_ptr(), v_extend.data_ptr(), o_extend.data_ptr(), k_buffer.data_ptr(),
+        k_block_scale.data_ptr(), v_buffer.data_ptr(), v_block_scale.data_ptr(), qo_indptr.data_ptr(),
+        kv_indptr.data_ptr(), kv_indices.data_ptr(), batch, n, hq, hkv, lq,
         lv, *ke, *ve, *ks, *vs, dims[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
         _c_int(sliding_window), _c_int(first_tokens),
-        *_mask_sinks(custom_mask, mask_indptr, sinks), float(k_scale), float(v_scale), _ptr(lse),
-        _ptr(ws), ws.numel() * ws.element_size()))
+        *_mask_sinks(custom_mask, mask_indptr, sinks), float(k_scale), float(v_scale), _address(lse),
+        ws.data_ptr(), ws.numel() * ws.element_size()))
     return ws
 
 
@@ -909,12 +917,12 @@ def extend_attention_fwd_streaming(q_extend, k_extend, v_extend, o_extend, k_buf
     ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
     _check(_on(
         dev, lib.pkx_extend_attention_fwd_streaming,
-        _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
-        _ptr(v_buffer), _ptr(qo_indptr), _ptr(kv_indptr),
-        _ptr(kv_indices) if kv_indices.numel() else None, batch, n, hq, hkv, lq, lv, *ke, *ve,
+        q_extend.data_ptr(), k_extend.data_ptr(), v_extend.data_ptr(), o_extend.data_ptr(), k_buffer.data_ptr(),
+        v_buffer.data_ptr(), qo_indptr.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), batch, n, hq, hkv, lq, lv, *ke, *ve,
         *strides, k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0),
-        _c_int(sliding_window), _c_int(first_tokens), _mask_sinks(None, None, sinks)[2], _ptr(lse),
-        _ptr(ws), ws.numel() * ws.element_size()))
+        _c_int(sliding_window), _c_int(first_tokens), _mask_sinks(None, None, sinks)[2], _address(lse),
+        ws.data_ptr(), ws.numel() * ws.element_size()))
     return ws
 
 
@@ -937,8 +945,8 @@ def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indic
     ws = _own_workspace(workspace, decode_workspace_size, q.device, b, hq, hkv, lq, lv)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd_streaming,
-        _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(v_buffer), _ptr(kv_indptr),
-        _ptr(kv_indices) if kv_indices.numel() else None, b, hq, hkv, lq, lv, *strides,
+        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), b, hq, hkv, lq, lv, *strides,
         k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), _c_int(sliding_window),
-        _c_int(first_tokens), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size()))
+        _c_int(first_tokens), _address(lse), ws.data_ptr(), ws.numel() * ws.element_size()))
     return ws
