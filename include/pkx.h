@@ -26,6 +26,11 @@
  *    dereferenced: the kernel reads a zero row instead and records
  *    PKX_EDEVICE in the workspace's status word, which
  *    pkx_workspace_status() reads back.
+ *  - A row of an attention call that sees a NaN (its query, or a visible key's
+ *    K) is NaN in o and in lse; o = 0 with lse = -inf means that it sees no
+ *    key.  In the extend forms the rows of a block of queries share the tiles
+ *    of its keys: a NaN or an infinity in the V row of a key that the masks
+ *    hide from some of them reaches those rows' o too.
  *  - Array extents are the caller's: an array described by an indptr (for
  *    example kv_indices[kv_indptr[b] .. kv_indptr[b+1])) must hold every
  *    entry the indptr names, as a C array argument must; its length is not

@@ -1258,8 +1258,9 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       tc_fence_after();
       if (warp_active) {
         if constexpr (F4) m -= kF4Shift;  // l and O are 2^kF4Shift times too large
-        float inv = l > 0.f ? 1.0f / l : 0.f;
-        float lse_v = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        // a sum of 0: no visible key; a NaN sum (a NaN query or key) stays NaN
+        float inv = l == 0.f ? 0.f : 1.0f / l;
+        float lse_v = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
         if (p.sinks && w.slot < 0) {
           // the head's sink joins the denominator (a split row gets it in
           // the combine): with M = max(m, sink), l' = l 2^(m-M) + 2^(sink-M)
@@ -2332,14 +2333,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const WsHeader *hdr, const
              r;
     };
     float mx = -INFINITY;
-    for (int i = 0; i < n_part; ++i) mx = fmaxf(mx, plse[prow(i)]);
+    bool empty = true;  // every partial is -inf (fmaxf drops a NaN one)
+    for (int i = 0; i < n_part; ++i) {
+      const float x = plse[prow(i)];
+      mx = fmaxf(mx, x);
+      empty &= x == -INFINITY;
+    }
     const int t = r / group, g = r - t * group;
     const int64_t orow = (int64_t)(E.q_tok0 + t) * hq + E.kvh * group + g;
     // a sink (natural-log logit of the head) joins the denominator once
     const float sink = sinks ? __ldg(sinks + E.kvh * group + g) : -INFINITY;
-    const float mx_p = mx;
     mx = fmaxf(mx, sink);
-    if (mx_p == -INFINITY) {
+    if (empty) {
       for (int c = lane * 4; c < hdv; c += 128)
         *reinterpret_cast<uint2 *>(o + orow * hdv + c) = make_uint2(0, 0);
       if (lane == 0 && lse) lse[orow] = sink;  // -inf without a sink

@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(MlaPairCfg::THREADS, 1) mla_pair_kernel(const 
       pv_base += nt;
       tc_fence_after();
       if (warp_active) {
-        float inv = l > 0.f ? 1.0f / l : 0.f;
-        float lse_v = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        // a sum of 0: no visible key; a NaN sum (a NaN query or key) stays NaN
+        float inv = l == 0.f ? 0.f : 1.0f / l;
+        float lse_v = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
         if (p.sinks && w.slot < 0) {
           const float s2 = __ldg(p.sinks + w.kvh * G + g) * 1.4426950408889634f;
           const float M = fmaxf(m, s2);
