@@ -516,6 +516,9 @@ int pkx_expand_paged_kv_indices(
  * need multiples of 16 bytes, block-scale bases and strides that are multiples
  * of d / 16 bytes, slot strides below 2^31 bytes, and k_scale and v_scale in
  * [2^-64, 2^64].
+ * The write and the read back take fewer than 2^40 tokens or rows a call, and
+ * rows whose blocks of 16 (write) or chunks of 8 (read back) of all KV heads
+ * of K and V together number 2^20 at most.
  */
 
 /*

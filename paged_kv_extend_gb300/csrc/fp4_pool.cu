@@ -30,6 +30,7 @@ namespace pkx {
 
 constexpr int kFp4Threads = 256;
 constexpr int kMaxPlaces = 1 << 20;  // grid y stays below its limit
+constexpr int64_t kMaxRows = 1ll << 40;  // (offsets are 64-bit: more than any device holds)
 
 // How `places` (a token's blocks or chunks) lie over CTAs: tokens of a CTA's
 // pass, and CTAs (grid y) that share a token's places.
@@ -229,8 +230,8 @@ int launch_set_kv_buffer_fp4(const void *k, int64_t k_ts, int64_t k_hs, const vo
   const int64_t places = (int64_t)hkv * (a.nk + a.nv);
   if (places > kMaxPlaces)
     return set_error(PKX_EUNSUPPORTED, "set_kv_buffer_fp4: more than %d blocks a token", kMaxPlaces);
-  if (n_tokens >= (1ll << 31) / places)
-    return set_error(PKX_EUNSUPPORTED, "set_kv_buffer_fp4: 2^31 or more blocks in one call");
+  if (n_tokens >= kMaxRows)
+    return set_error(PKX_EUNSUPPORTED, "set_kv_buffer_fp4: 2^40 tokens or more");
   a.places = fp4_places(places);
   cudaError_t e = launch_pdl(set_kv_buffer_fp4_kernel,
                              wave_grid(set_kv_buffer_fp4_kernel, a.places, n_tokens, kWriteUnroll),
@@ -324,8 +325,8 @@ int launch_get_kv_buffer_fp4(const Fp4Pool &pool, const int32_t *kv_indices, int
   const int64_t places = (int64_t)hkv * (a.ck + a.cv);
   if (places > kMaxPlaces)
     return set_error(PKX_EUNSUPPORTED, "get_kv_buffer_fp4: more than %d chunks a token", kMaxPlaces);
-  if (n_rows >= (1ll << 31) / places)
-    return set_error(PKX_EUNSUPPORTED, "get_kv_buffer_fp4: 2^31 or more chunks in one call");
+  if (n_rows >= kMaxRows)
+    return set_error(PKX_EUNSUPPORTED, "get_kv_buffer_fp4: 2^40 rows or more");
   a.places = fp4_places(places);
   cudaError_t e = launch_pdl(get_kv_buffer_fp4_kernel,
                              wave_grid(get_kv_buffer_fp4_kernel, a.places, n_rows, kReadUnroll),
