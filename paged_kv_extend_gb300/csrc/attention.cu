@@ -2484,9 +2484,18 @@ static int make_q_map(CUtensorMap *m, const void *q, int64_t n, int hq, int lq, 
   cuuint64_t strides[2] = {(cuuint64_t)lq * 2, (cuuint64_t)hq * lq * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tok};
   cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // a thread's first CUDA call: the runtime binds the device's context to a
+    // thread when a call needs it, the driver's own call does not
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
   if (r != CUDA_SUCCESS) return set_error(PKX_EINVAL, "q tensor map rejected: %d", (int)r);
   return PKX_OK;
 }
