@@ -2393,8 +2393,6 @@ int tokens_per_block(int group) { return group >= 1 && group <= kBlockM ? kBlock
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-constexpr int kMaxDevicesCfg = 64;
-
 // Rows of one split-KV partial slot: both Q tiles of an extend block, or the
 // group's rows of a decode query.
 bool split_head_dims(int lq, int lv) { return (lq == 192 && lv == 128) || (lq == 288 && lv == 256); }
@@ -2449,29 +2447,28 @@ WsLayout ws_layout(int batch, int num_q_tokens, int hkv, int group, int lq, int 
 }
 
 // Whether a kernel's dynamic shared-memory limit has been raised on the
-// current device (the attribute is per device; one flag array per kernel).
-static bool needs_config(bool (&done)[kMaxDevicesCfg]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesCfg) return true;
-  return !done[dev];
+// current device (the attribute is per device; one set of flags per kernel).
+static bool needs_config(PerDevice &done) {
+  std::atomic<int> *here = done.here();
+  return !here || here->load(std::memory_order_acquire) == 0;
 }
-static void mark_configured(bool (&done)[kMaxDevicesCfg]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevicesCfg) done[dev] = true;
+static void mark_configured(PerDevice &done) {
+  if (std::atomic<int> *here = done.here()) here->store(1, std::memory_order_release);
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once.
+// cuTensorMapEncodeTiled from the driver, kept once it is found.
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+  if (!fn) {
     void *f = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
                                          &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+      known.store(fn, std::memory_order_release);
+    }
   }
   return fn;
 }
@@ -2503,7 +2500,7 @@ static int make_q_map(CUtensorMap *m, const void *q, int64_t n, int hq, int lq, 
 template <int HD, int MODE, bool MASK = false, int FMT = 0, bool FIRST = false>
 static int launch_attn_kernel(const TMaps &tmaps, const KParams &kp, int grid, cudaStream_t s) {
   using C = Cfg<HD>;
-  static bool configured[kMaxDevicesCfg] = {};  // per instantiation and device
+  static PerDevice configured;  // per instantiation
   if (needs_config(configured)) {
     cudaError_t e = cudaFuncSetAttribute(attn_kernel<HD, MODE, MASK, FMT, FIRST>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -2554,7 +2551,7 @@ static cudaError_t launch_pair(int pairs, cudaStream_t s, const KParams &kp, boo
                                int *max_pairs) {
   using C = std::conditional_t<SG, std::conditional_t<FMT != 0, MlaPairDec8Cfg, MlaPairDecCfg>,
                                MlaPairCfg>;
-  static bool configured[kMaxDevicesCfg] = {};
+  static PerDevice configured;
   if (needs_config(configured)) {
     cudaError_t e = cudaFuncSetAttribute(mla_pair_kernel<MODE, MASK, FMT, SG>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -2584,17 +2581,16 @@ static cudaError_t launch_pair(int pairs, cudaStream_t s, const KParams &kp, boo
 // group with an odd count of free SMs leaves one idle), queried once per
 // device; 0 on error.
 static int mla_pairs(int nsm) {
-  static int cached[kMaxDevicesCfg] = {};
-  int dev = 0;
-  const bool cache = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevicesCfg;
-  if (cache && cached[dev] > 0) return cached[dev];
-  int n = 0;
+  static PerDevice known;
+  std::atomic<int> *here = known.here();
+  int n = here ? here->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   if (launch_pair<kUnified, false>(nsm / 2, nullptr, KParams{}, true, &n) != cudaSuccess) {
     set_error(PKX_ECUDA, "cudaOccupancyMaxActiveClusters(mla_pair_kernel) failed");
     return 0;
   }
   n = std::min(n, nsm / 2);
-  if (cache && n > 0) cached[dev] = n;
+  if (here && n > 0) here->store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -2717,7 +2713,7 @@ int launch_attention(const AttnArgs &a) {
     if (sp.seq_in_smem) sched_smem += seq_b;
     sp.blk_in_smem = sched_smem + blk_b <= (size_t)kSchedSmemMax;
     if (sp.blk_in_smem) sched_smem += blk_b;
-    static bool configured[kMaxDevicesCfg] = {};
+    static PerDevice configured;
     if (needs_config(configured)) {
       cudaError_t e = cudaFuncSetAttribute(sched_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kSchedSmemMax);

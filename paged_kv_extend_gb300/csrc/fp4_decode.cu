@@ -869,16 +869,13 @@ template <int D, int NT>
 static cudaError_t launch_decode(const Fp4DecParams &p, int grid, cudaStream_t st) {
   using C = DecCfg<D, NT>;
   // the shared-memory limit is a property of the device's copy of the kernel
-  constexpr int kDevices = 64;
-  static bool configured[kDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kDevices || !configured[dev]) {
-    e = cudaFuncSetAttribute(decode_fp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM);
+  static PerDevice configured;
+  std::atomic<int> *done = configured.here();
+  if (!done || done->load(std::memory_order_acquire) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        decode_fp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kDevices) configured[dev] = true;
+    if (done) done->store(1, std::memory_order_release);
   }
   return launch_pdl(decode_fp4_kernel<D, NT>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
 }

@@ -56,14 +56,8 @@ __device__ __forceinline__ int fp4_place(const Fp4Places &p, int64_t &token, int
 // CTAs over the tokens: one resident wave of `kernel`, `unroll` tokens a thread.
 template <typename K>
 static dim3 wave_grid(K kernel, const Fp4Places &p, int64_t n_tokens, int unroll) {
-  static int resident = 0;  // CTAs per SM (one kernel per argument type)
-  if (resident == 0) {
-    int r = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kernel, kFp4Threads, 0) != cudaSuccess ||
-        r < 1)
-      r = 4;
-    resident = r;
-  }
+  static PerDevice known;  // (one kernel per argument type)
+  const int resident = resident_ctas(kernel, kFp4Threads, known);
   const int64_t cap = std::max<int64_t>((int64_t)num_sms_current_device() * resident / p.slices, 1);
   const int64_t need = (n_tokens + (int64_t)p.tokens * unroll - 1) / ((int64_t)p.tokens * unroll);
   return dim3((unsigned)std::max<int64_t>(std::min(need, cap), 1), (unsigned)p.slices);

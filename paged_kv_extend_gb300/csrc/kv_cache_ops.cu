@@ -113,14 +113,8 @@ int launch_set_kv_buffer(const void *k, int64_t k_ts, int64_t k_hs, const void *
     return set_error(PKX_EUNSUPPORTED, "set_kv_buffer: 2^31 or more 16-byte chunks in one call");
   const int nsm = num_sms_current_device();
   const uint64_t need = (a.total + kKvThreads * kUnroll - 1) / (kKvThreads * kUnroll);
-  static int resident = 0;  // CTAs per SM at this kernel's register count
-  if (resident == 0) {
-    int r = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, set_kv_buffer_kernel, kKvThreads, 0) !=
-            cudaSuccess || r < 1)
-      r = 4;
-    resident = r;
-  }
+  static PerDevice known;
+  const int resident = resident_ctas(set_kv_buffer_kernel, kKvThreads, known);
   const uint64_t cap = (uint64_t)nsm * resident;  // one resident wave
   const unsigned grid = (unsigned)(need < cap ? need : cap);
   set_kv_buffer_kernel<<<grid, kKvThreads, 0, st>>>(a);

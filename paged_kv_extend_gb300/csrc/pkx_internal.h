@@ -2,6 +2,7 @@
 // (host side): error reporting, workspace layout and the kernel launchers.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -104,6 +105,30 @@ struct WsLayout {
 };
 
 int num_sms_current_device();
+
+// A host-side number for each device, 0 until it is known; host threads that
+// fill it at once store the same value.
+struct PerDevice {
+  std::atomic<int> value[64];
+  // The current device's entry, or null beyond the last.
+  std::atomic<int> *here() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? &value[dev] : nullptr;
+  }
+};
+
+// CTAs of `kernel` that an SM holds at once; looked up once per device in
+// `known` (4 where the look-up fails, which is not kept).
+template <typename K>
+int resident_ctas(K kernel, int threads, PerDevice &known) {
+  std::atomic<int> *here = known.here();
+  int r = here ? here->load(std::memory_order_relaxed) : 0;
+  if (r > 0) return r;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kernel, threads, 0) != cudaSuccess || r < 1)
+    return 4;
+  if (here) here->store(r, std::memory_order_relaxed);
+  return r;
+}
 
 // Launch `kernel` with programmatic stream serialization: it may start while
 // the previous kernel on the stream runs, and waits for it in-kernel

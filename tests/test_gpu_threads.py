@@ -105,3 +105,56 @@ def test_first_cuda_call_of_a_thread(form):
     torch.cuda.synchronize()
     assert isinstance(outs[1], torch.Tensor), outs[1]
     assert outs[0].any() and torch.equal(outs[0], outs[1])
+
+
+WRITES_AND_DECODES = r"""
+import threading, torch
+from paged_kv_extend_gb300 import pkx
+
+N, SLOTS, HKV, D = 12, 700, 2, 128
+dev = torch.device("cuda:0")
+g = torch.Generator().manual_seed(4)
+rows = torch.randn(300, HKV, D, generator=g).bfloat16().to(dev)
+q = torch.randn(3, 8, D, generator=g).bfloat16().to(dev)
+loc = torch.randperm(SLOTS, generator=g)[:300].to(dev)
+idx, ptr = loc.to(torch.int32), torch.tensor([0, 120, 121, 300], dtype=torch.int32, device=dev)
+pools = [[t for _ in range(2) for t in (
+    torch.zeros(SLOTS, HKV, D // 2, dtype=torch.uint8, device=dev),
+    torch.zeros(SLOTS, HKV, D // 16, dtype=torch.float8_e4m3fn, device=dev))] for _ in range(N)]
+wide = [torch.zeros(2, SLOTS, HKV, D, dtype=torch.bfloat16, device=dev) for _ in range(N)]
+o, streams = [torch.zeros_like(q) for _ in range(N)], [torch.cuda.Stream() for _ in range(N)]
+back = [torch.zeros_like(rows) for _ in range(2 * N)]
+space = [torch.empty(pkx.decode_fp4_workspace_size(3, 8, HKV, D, D), dtype=torch.uint8, device=dev) for _ in range(N)]
+torch.cuda.synchronize()
+gate, errors = threading.Barrier(N), []
+
+def call(i):
+    try:
+        with torch.cuda.stream(streams[i]):
+            gate.wait()
+            pkx.set_kv_buffer_fp4(*pools[i], loc, rows, rows, 0.3, 0.5)
+            pkx.get_kv_buffer_fp4(*pools[i], idx, 0.3, 0.5, back[2 * i], back[2 * i + 1])
+            pkx.decode_attention_fwd_fp4(q, o[i], *pools[i], ptr, idx, workspace=space[i], k_scale=0.3, v_scale=0.5)
+            pkx.set_kv_buffer(wide[i][0], wide[i][1], loc, rows, rows)
+    except Exception as e:
+        errors.append(repr(e))
+
+for _ in range(4):
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(N)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for i in range(1, N):
+        assert torch.equal(o[i], o[0]) and torch.equal(wide[i], wide[0]), i
+        assert torch.equal(back[2 * i], back[0]) and torch.equal(back[2 * i + 1], back[1]), i
+    assert o[0].any() and back[0].any() and torch.equal(wide[0][0][loc], rows)
+    assert all(pkx.workspace_status(w) == 0 for w in space)
+print("same results")
+"""
+
+
+def test_writes_and_decodes_from_several_threads():
+    r = subprocess.run([sys.executable, "-c", WRITES_AND_DECODES], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same results" in r.stdout, r.stdout + r.stderr
