@@ -111,6 +111,8 @@ size_t pkx_decode_workspace_min_size(int batch, int hq, int hkv, int lq, int lv)
  * Device status word of the last attention call that used `workspace`:
  * copies it to the host (synchronising `stream`) and returns PKX_OK,
  * PKX_EDEVICE or PKX_ETIMEOUT.  Returns PKX_ECUDA if the copy fails.
+ * A call with nothing to do (a batch or a token count of 0) does not use its
+ * workspace and leaves it as it is.
  */
 int pkx_workspace_status(const void *workspace, void *stream);
 

@@ -280,11 +280,13 @@ def _check_len(t, n, name):
         raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
 
 
-def _workspace(ws, nbytes, dev):
+def _workspace(ws, nbytes, dev, work=True):
     """The caller's workspace (its size is checked by the library), or a new
-    one of the size the library asks for."""
+    one of the size the library asks for.  A call without ``work`` launches
+    nothing that would set a new workspace's status word."""
     if ws is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        new = torch.empty if work else torch.zeros
+        return new(max(nbytes, 256), dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -317,7 +319,8 @@ def extend_attention_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, v_buf
         if not t.is_contiguous() or t.dtype != torch.bfloat16:
             raise ValueError(f"{nm} must be contiguous bf16")
     _i32(qo_indptr, "qo_indptr"), _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
-    ws = _workspace(workspace, extend_workspace_size(batch, n, hq, hkv, lq, lv), q_extend.device)
+    ws = _workspace(workspace, extend_workspace_size(batch, n, hq, hkv, lq, lv), q_extend.device,
+                    batch and n)
     args = [
         _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
         _ptr(v_buffer), _ptr(qo_indptr), _ptr(kv_indptr),
@@ -368,7 +371,7 @@ def extend_attention_fwd_ragged_paged(q_extend, k_extend, v_extend, o_extend, k_
             raise ValueError(f"{nm} must be contiguous bf16")
     _i32(qo_indptr, "qo_indptr"), _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
     ws = _workspace(workspace, ragged_paged_workspace_size(batch, n, hq, hkv, lq, lv),
-                    q_extend.device)
+                    q_extend.device, batch and n)
     _check(_on(
         q_extend.device, lib.pkx_extend_attention_fwd_ragged_paged,
         _ptr(q_extend), _ptr(k_extend), _ptr(v_extend), _ptr(o_extend), _ptr(k_buffer),
@@ -399,7 +402,7 @@ def extend_attention_fwd_unified(q, o, k_buffer, v_buffer, qo_indptr, kv_indptr,
     if kv_indices.dtype != torch.int64 or not kv_indices.is_contiguous():
         raise ValueError("kv_indices must be contiguous int64")
     _i32(qo_indptr, "qo_indptr"), _i32(kv_indptr, "kv_indptr"), _i32(prefix_lens, "prefix_lens")
-    ws = _workspace(workspace, extend_workspace_size(batch, n, hq, hkv, lq, lv), q.device)
+    ws = _workspace(workspace, extend_workspace_size(batch, n, hq, hkv, lq, lv), q.device, batch and n)
     _check(_on(
         q.device, lib.pkx_extend_attention_fwd_unified,
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(v_buffer), _ptr(qo_indptr), _ptr(kv_indptr),
@@ -427,7 +430,7 @@ def decode_attention_fwd(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, sm_sca
     _check_len(kv_indptr, b + 1, "kv_indptr")
     kb, vb, kv_dtype = _pool_rows(k_buffer, v_buffer)
     _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
-    ws = _workspace(workspace, decode_workspace_size(b, hq, hkv, lq, lv), q.device)
+    ws = _workspace(workspace, decode_workspace_size(b, hq, hkv, lq, lv), q.device, b)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd,
         _ptr(q), _ptr(o), _ptr(k_buffer), _ptr(v_buffer), _ptr(kv_indptr),
@@ -817,7 +820,7 @@ def decode_attention_fwd_fp4(q, o, k_buffer, k_block_scale, v_buffer, v_block_sc
     _check_len(kv_indptr, b + 1, "kv_indptr")
     _one_device(q.device, o=o, k_buffer=k_buffer, kv_indptr=kv_indptr, kv_indices=kv_indices,
                 lse=lse, workspace=workspace)
-    ws = _own_workspace(workspace, decode_fp4_workspace_size, q.device, b, hq, hkv, lq, lv)
+    ws = _own_workspace(workspace, decode_fp4_workspace_size, q.device, b, b, hq, hkv, lq, lv)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd_fp4,
         q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), k_block_scale.data_ptr(), v_buffer.data_ptr(),
@@ -846,12 +849,13 @@ def _one_sink_per_head(sinks, hq):
         _check_len(sinks, hq, "sinks")
 
 
-def _own_workspace(workspace, size_fn, dev, *shape):
-    """The caller's workspace, or a new one of size_fn(*shape) bytes on ``dev``."""
+def _own_workspace(workspace, size_fn, dev, work, *shape):
+    """The caller's workspace, or a new one of size_fn(*shape) bytes on ``dev``
+    (``work`` as in _workspace)."""
     if workspace is not None:
         return workspace
     with torch.cuda.device(dev):
-        return _workspace(None, size_fn(*shape), dev)
+        return _workspace(None, size_fn(*shape), dev, work)
 
 
 def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k_block_scale,
@@ -873,7 +877,7 @@ def extend_attention_fwd_fp4(q_extend, k_extend, v_extend, o_extend, k_buffer, k
                 qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, lse=lse,
                 workspace=workspace, custom_mask=custom_mask, mask_indptr=mask_indptr, sinks=sinks)
     _one_sink_per_head(sinks, hq)
-    ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
+    ws = _own_workspace(workspace, extend_workspace_size, dev, batch and n, batch, n, hq, hkv, lq, lv)
     _check(_on(
         dev, lib.pkx_extend_attention_fwd_fp4,
         q_extend.data_ptr(), k_extend.data_ptr(), v_extend.data_ptr(), o_extend.data_ptr(), k_buffer.data_ptr(),
@@ -914,7 +918,7 @@ def extend_attention_fwd_streaming(q_extend, k_extend, v_extend, o_extend, k_buf
                 v_buffer=v_buffer, qo_indptr=qo_indptr, kv_indptr=kv_indptr,
                 kv_indices=kv_indices, lse=lse, workspace=workspace, sinks=sinks)
     _one_sink_per_head(sinks, hq)
-    ws = _own_workspace(workspace, extend_workspace_size, dev, batch, n, hq, hkv, lq, lv)
+    ws = _own_workspace(workspace, extend_workspace_size, dev, batch and n, batch, n, hq, hkv, lq, lv)
     _check(_on(
         dev, lib.pkx_extend_attention_fwd_streaming,
         q_extend.data_ptr(), k_extend.data_ptr(), v_extend.data_ptr(), o_extend.data_ptr(), k_buffer.data_ptr(),
@@ -942,7 +946,7 @@ def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indic
     _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
     _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
                 kv_indices=kv_indices, lse=lse, workspace=workspace)
-    ws = _own_workspace(workspace, decode_workspace_size, q.device, b, hq, hkv, lq, lv)
+    ws = _own_workspace(workspace, decode_workspace_size, q.device, b, b, hq, hkv, lq, lv)
     _check(_on(
         q.device, lib.pkx_decode_attention_fwd_streaming,
         q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
