@@ -15,10 +15,11 @@
 // division once, and walks over the tokens with it: no division per block, and
 // a warp's accesses are runs of whole rows.  Several tokens' loads are in
 // flight per thread; the grid is one resident wave.  Measured for 8 KV heads of
-// 128 (K and V): write and read back of 16384 tokens 35 us together (5.0 TB/s;
-// 70 us with a division per block), read back of 131072 rows 120 us (5.7 TB/s,
-// 0.84 of the copy bandwidth).  The write's bound is issue (52 % of the slots,
-// ALU pipe 60 %), the read back's HBM.
+// 128 (K and V): write of 16384 tokens 18 us with a power-of-two tensor scale
+// (4.7 TB/s, 0.70 of the copy bandwidth; 63 % of the issue slots) and 41 us with
+// another one (2.1 TB/s, 76 % of the issue slots, which bound it); the write and
+// the read back together 35 us, 70 us with a division per block; read back of
+// 131072 rows 120 us (5.7 TB/s, 0.84 of the copy bandwidth), bound by HBM.
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -116,7 +117,7 @@ __device__ __forceinline__ uint32_t sign_nibbles(uint32_t a, uint32_t b, uint32_
 // multiple of 2^-18 by adding and taking away 48, is on the right side of
 // every midpoint and exactly on it where q / s is, and the hardware's rounding
 // gives the definition's code.  Any other scale compares q with the midpoints
-// times s (exact too, about twice the instructions).
+// times s (exact too, 2.9 times the instructions and 2.3 times the time).
 template <bool POW2>
 __device__ __forceinline__ uint2 quantise_block(const uint4 (&in)[2], float tensor_scale,
                                                 uint8_t &scale_code) {
