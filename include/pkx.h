@@ -644,6 +644,155 @@ int pkx_decode_attention_fwd_streaming(
     int sliding_window, int first_tokens, float *lse_out, void *workspace,
     size_t workspace_bytes, void *stream);
 
+/*
+ * A decode step around the paged pool.  The pages' engine normalises and
+ * rotates queries and keys before set_kv_buffer and reads every cached key;
+ * the calls below are this library's own additions.
+ */
+
+/*
+ * Per-head RMS norm and position rotation of queries and keys, and the KV
+ * write of the result, in one pass.  A row x (one token, one head, d
+ * elements) becomes
+ *   y = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *                                  (q_weight / k_weight; NULL: y = x)
+ * and then pair i < rotary_dim / 2 of y, (y[i], y[i + rotary_dim / 2]) or,
+ * with `interleaved`, (y[2i], y[2i + 1]), becomes (a c - b s, b c + a s) with
+ *   c = cos_sin[p, i],  s = cos_sin[p, rotary_dim / 2 + i],
+ *   p = positions[pair_axis[i], t]   (axis 0 without pair_axis).
+ * Elements from rotary_dim on are not rotated.  Computed in fp32 and rounded
+ * once to bf16.  With cache_loc the k_out row is also stored at that slot of
+ * k_buffer and v's row at that slot of v_buffer, as pkx_set_kv_buffer (or
+ * pkx_set_kv_buffer_fp8 for an fp8 pool) stores rows.
+ *   q, k       bf16 [n_tokens, hq / hkv, d], strides (ts, hs)
+ *   v          bf16 [n_tokens, hkv, d], or NULL (only keys are written);
+ *              needs cache_loc
+ *   q_out, k_out  bf16, as q and k; each may be its input (the same address
+ *              and strides) but overlap no other tensor
+ *   positions  int64 [num_axes, n_tokens] (num_axes = 1 for text; time, height
+ *              and width for video); a token with a position outside
+ *              [0, max_position), or a pair with an axis outside
+ *              [0, num_axes), gets NaN in those pairs
+ *   pair_axis  uint8 [rotary_dim / 2], NULL for a single axis
+ *   cos_sin    fp32 [max_position, rotary_dim], 16-byte aligned
+ *   q_weight, k_weight  bf16 [d] or NULL, 16-byte aligned
+ *   cache_loc  int64 [n_tokens] or NULL (no KV write); a slot outside the pool
+ *              is skipped
+ * d is a multiple of 8 up to 256, rotary_dim a multiple of 16 up to d (0: no
+ * rotation; positions, cos_sin and pair_axis are then ignored).
+ */
+int pkx_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts,
+                     int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs, int64_t n_tokens,
+                     int hq, int hkv, int d, const int64_t *positions, int num_axes,
+                     const uint8_t *pair_axis, const float *cos_sin, int64_t max_position,
+                     int rotary_dim, int interleaved, const void *q_weight, const void *k_weight,
+                     float eps, float weight_offset, void *q_out, int64_t qo_ts, int64_t qo_hs,
+                     void *k_out, int64_t ko_ts, int64_t ko_hs, const int64_t *cache_loc,
+                     void *k_buffer, int64_t kb_ss, int64_t kb_sh, void *v_buffer, int64_t vb_ss,
+                     int64_t vb_sh, int64_t num_slots, int kv_dtype, float k_scale, float v_scale,
+                     void *stream);
+
+/*
+ * Bounds of pages.  The pool is a pool of num_pages * page_size slots at least;
+ * page P is the slots P * page_size ... .  For every listed page and KV head,
+ *   bounds[page, h, 0, :] = min, bounds[page, h, 1, :] = max
+ * over the first page_lens[i] slots (at most page_size; all of them where
+ * page_lens is NULL) of k_buffer, per dim (NaN where a key is NaN; of an fp8
+ * pool the codes' values without k_scale).  A page outside [0, num_pages) or
+ * with no slots is skipped; other pages' bounds are left as they were.  A page
+ * listed twice must have the same length both times.
+ *   page_ids, page_lens  int32 [n_pages]
+ *   bounds     bf16 [num_pages, hkv, 2, d] contiguous, 16-byte aligned
+ * d is a multiple of 8.
+ */
+int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, int kv_dtype,
+                           int page_size, int64_t num_pages, int hkv, int d,
+                           const int32_t *page_ids, const int32_t *page_lens, int64_t n_pages,
+                           void *bounds, void *stream);
+
+/*
+ * Selection of the pages that a decode step reads, for d = 64 or 128.  With
+ * qp[j] = the sum over a KV head's query heads, in order, of max(q[j], 0) and qn[j]
+ * that of min(q[j], 0), each sum rounded to fp32, a page's score is
+ *   tree(qn[j] * bounds[page, h, 0, j]) + tree(qp[j] * bounds[page, h, 1, j]),
+ * where tree() adds neighbours pairwise over the dims (0 + 1, 2 + 3, ..., then
+ * the sums likewise) and every product and sum is rounded to fp32: the sum
+ * over the query heads of an upper bound of <q, k> over the page's keys.
+ * selected[b, h, :] are the numbers of the pages within the sequence,
+ * ascending: all of them, then -1, for a sequence of at most top_k pages;
+ * otherwise its first first_pages and last last_pages pages and the others
+ * with the largest scores (of equal scores the lower page; NaN above all).
+ *   q          bf16 [batch, hq, d] contiguous
+ *   kv_indptr  int32 [batch + 1] over kv_indices; kv_indices int32
+ *              [n_indices] page ids (entries past kv_indptr[batch] are not
+ *              read for any sequence)
+ *   selected   int32 [batch, hkv, top_k] (written)
+ *   workspace  >= pkx_select_pages_workspace_size(hkv, n_indices) bytes,
+ *              256-byte aligned; pkx_workspace_status reports a candidate page
+ *              outside [0, num_pages) (it ranks last) and an indptr that
+ *              decreases or passes n_indices (that sequence selects nothing)
+ * first_pages + last_pages <= top_k <= 8192.
+ */
+size_t pkx_select_pages_workspace_size(int hkv, int64_t n_indices);
+int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
+                     const int32_t *kv_indptr, const int32_t *kv_indices, int64_t n_indices,
+                     int batch, int hq, int hkv, int d, int top_k, int first_pages, int last_pages,
+                     int32_t *selected, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Decode attention over selected pages: pkx_decode_attention_fwd in which
+ * query head h of sequence b attends to the keys of the pages
+ * selected[b, h / (hq / hkv), :] alone.  The sequence's pages are
+ * kv_indices[kv_indptr[b] ..), page_size slots each, kv_last_page_len[b] in
+ * the last one (the paged format of pkx_expand_paged_kv_indices).  Entries
+ * below 0 are ignored; entries may come in any order, one listed twice counts
+ * twice.  A row without keys gets o = 0 and lse = -inf.  For (lq, lv) =
+ * (64, 64) and (128, 128), bf16 and fp8 pools.
+ *   n_indices  entries of kv_indices
+ *   selected   int32 [batch, hkv, top_k], top_k <= 8192
+ *   workspace  >= pkx_decode_pages_workspace_size(...) bytes, 256-byte aligned
+ * batch * hkv * top_k * page_size < 2^31.  pkx_workspace_status reports a
+ * page outside the pool (its keys read as zero rows), a selected number past
+ * the sequence's pages (ignored), a last page length outside [0, page_size]
+ * (held at its limit), and an indptr that decreases or passes n_indices (that
+ * sequence has no keys).
+ */
+size_t pkx_decode_pages_workspace_size(int batch, int hq, int hkv, int lq, int lv, int page_size,
+                                       int top_k);
+int pkx_decode_attention_fwd_pages(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int64_t n_indices, const int32_t *kv_last_page_len, int page_size,
+    const int32_t *selected, int top_k, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss,
+    int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int kv_dtype, float k_scale, float v_scale, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/*
+ * Decode attention for sequences in groups that share a prefix:
+ * pkx_decode_attention_fwd (without a window) for batches in which the
+ * sequences group_indptr[g] .. group_indptr[g+1] - 1 have their first
+ * shared_lens[g] keys in common.  Those are read once a group, through the
+ * group's first sequence's kv_indices; the other sequences' entries there are
+ * not read.  A group shares at most its shortest sequence's keys.  Sequences
+ * before group_indptr[0] or from group_indptr[num_groups] on stand alone.
+ * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools.
+ *   group_indptr  int32 [num_groups + 1], non-decreasing within [0, batch]
+ *   shared_lens   int32 [num_groups], >= 0
+ *                 (both NULL when num_groups is 0; if either is out of range,
+ *                 nothing is shared and pkx_workspace_status reports it)
+ *   workspace     >= pkx_decode_shared_workspace_size(...) bytes, 256-byte
+ *                 aligned
+ */
+size_t pkx_decode_shared_workspace_size(int batch, int num_groups, int hq, int hkv, int lq,
+                                        int lv);
+int pkx_decode_attention_fwd_shared(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
+    const int32_t *kv_indices, const int32_t *group_indptr, const int32_t *shared_lens,
+    int num_groups, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
+    int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
+    float k_scale, float v_scale, float *lse_out, void *workspace, size_t workspace_bytes,
+    void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,16 +44,19 @@ def needs_build() -> bool:
 
 
 # Kernels that hand registers between warpgroups with setmaxnreg, and the
-# source file that states the launch register count the split assumes.
-SPLIT_KERNELS = (("attn_kernel", "attention.cu"), ("mla_pair_kernel", "mla_pair_kernel.cuh"))
+# source file that states the launch register count the split assumes; by the
+# translation unit that instantiates them.
+ATTN_KERNEL = ("attn_kernel", "attn_kernel.cuh")
+SPLIT_KERNELS = {"attention.cu": (ATTN_KERNEL, ("mla_pair_kernel", "mla_pair_kernel.cuh")),
+                 "listed_attention.cu": (ATTN_KERNEL,)}
 
 
-def check_attention_registers(ptxas_log: str) -> None:
+def check_attention_registers(unit: str, ptxas_log: str) -> None:
     """The attention kernels hand registers between warpgroups with
     setmaxnreg; the split adds up only if every instantiation launches with
     exactly the register count the kernel source assumes (REGS_LAUNCH).
     Refuse to build otherwise: a wrong split would stall the kernel."""
-    for kernel, fname in SPLIT_KERNELS:
+    for kernel, fname in SPLIT_KERNELS[unit]:
         src = open(os.path.join(CSRC, fname)).read()
         m = re.search(r"REGS_LAUNCH = (\d+)", src)
         if not m:
@@ -90,7 +93,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [nvcc, *NVCC_FLAGS, "-c", src, "-o", obj]
-        if os.path.basename(src) == "attention.cu":
+        if os.path.basename(src) in SPLIT_KERNELS:
             cmd.insert(1, "-Xptxas=-v")
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
@@ -101,8 +104,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append((src, out.decode(errors="replace")))
         else:
-            if os.path.basename(src) == "attention.cu":
-                check_attention_registers(out.decode(errors="replace"))
+            if os.path.basename(src) in SPLIT_KERNELS:
+                check_attention_registers(os.path.basename(src), out.decode(errors="replace"))
             if verbose and out:
                 print(out.decode(errors="replace"), file=sys.stderr)
     if failed:

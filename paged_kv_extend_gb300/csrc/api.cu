@@ -851,3 +851,269 @@ int pkx_decode_attention_fwd_streaming(
 }
 
 }  // extern "C"
+
+// ------------------------------------ a decode step around the paged pool
+static int check_pool_format(const char *what, int kv_dtype, float k_scale, float v_scale) {
+  if (kv_dtype == kKvBf16) return PKX_OK;
+  if (kv_dtype != kKvFp8E4M3 && kv_dtype != kKvFp8E5M2)
+    return set_error(PKX_EINVAL, "%s: kv_dtype %d is not a PKX_KV_* value", what, kv_dtype);
+  if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return set_error(PKX_EINVAL, "%s: k_scale and v_scale must be positive and finite", what);
+  return PKX_OK;
+}
+
+// Heads of the forms built for Lq = Lv = 64 or 128.
+static int check_equal_heads(const char *what, int hq, int hkv, int lq, int lv) {
+  int rc;
+  if ((rc = check_heads(hq, hkv, lq, lv))) return rc;
+  if (lq != lv || (lq != 64 && lq != 128))
+    return set_error(PKX_EUNSUPPORTED, "%s is built for Lq = Lv = 64 or 128", what);
+  return PKX_OK;
+}
+
+// Pages of one call: a selection fits the listing kernel's shared memory.
+constexpr int kMaxTopK = 8192;
+static int check_top_k(int top_k) {
+  if (top_k <= 0) return set_error(PKX_EINVAL, "top_k must be positive");
+  if (top_k > kMaxTopK) return set_error(PKX_EUNSUPPORTED, "top_k %d > %d", top_k, kMaxTopK);
+  return PKX_OK;
+}
+
+// What the two listed decode forms share, after decode_args().
+static ListedArgs listed_args(const AttnArgs &a, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  ListedArgs l{};
+  l.q = a.q; l.o = a.o; l.lse = a.lse;
+  l.k_buf = a.k_buf; l.v_buf = a.v_buf;
+  l.kb_ss = a.kb_ss; l.kb_sh = a.kb_sh; l.vb_ss = a.vb_ss; l.vb_sh = a.vb_sh;
+  l.num_slots = a.num_slots;
+  l.kv_indptr = a.kv_indptr;
+  l.kv_indices = static_cast<const int32_t *>(a.kv_indices);
+  l.batch = a.batch; l.hq = a.hq; l.hkv = a.hkv; l.d = a.lq;
+  l.sm_scale = a.sm_scale; l.logit_cap = a.logit_cap;
+  l.kv_fmt = a.kv_fmt; l.k_scale = a.k_scale; l.v_scale = a.v_scale;
+  l.workspace = workspace; l.workspace_bytes = workspace_bytes;
+  l.stream = static_cast<cudaStream_t>(stream);
+  return l;
+}
+
+extern "C" {
+
+int pkx_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts,
+                     int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs, int64_t n_tokens,
+                     int hq, int hkv, int d, const int64_t *positions, int num_axes,
+                     const uint8_t *pair_axis, const float *cos_sin, int64_t max_position,
+                     int rotary_dim, int interleaved, const void *q_weight, const void *k_weight,
+                     float eps, float weight_offset, void *q_out, int64_t qo_ts, int64_t qo_hs,
+                     void *k_out, int64_t ko_ts, int64_t ko_hs, const int64_t *cache_loc,
+                     void *k_buffer, int64_t kb_ss, int64_t kb_sh, void *v_buffer, int64_t vb_ss,
+                     int64_t vb_sh, int64_t num_slots, int kv_dtype, float k_scale, float v_scale,
+                     void *stream) {
+  int rc;
+  if (n_tokens < 0 || hq <= 0 || hkv <= 0)
+    return set_error(PKX_EINVAL, "qk_norm_rope: n_tokens >= 0, hq > 0 and hkv > 0");
+  if (n_tokens >= (1ll << 40) || hq > (1 << 20) || hkv > (1 << 20))
+    return set_error(PKX_EUNSUPPORTED, "qk_norm_rope: 2^40 tokens or more than 2^20 heads");
+  if (d <= 0 || d % 8) return set_error(PKX_EINVAL, "qk_norm_rope: d must be a multiple of 8");
+  if (d > 256) return set_error(PKX_EUNSUPPORTED, "qk_norm_rope: d %d > 256", d);
+  if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 16)
+    return set_error(PKX_EINVAL, "qk_norm_rope: rotary_dim must be a multiple of 16 up to d");
+  if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(weight_offset))
+    return set_error(PKX_EINVAL, "qk_norm_rope: eps must be finite and not negative, "
+                                 "weight_offset finite");
+  if (n_tokens == 0) return PKX_OK;
+  if (v && !cache_loc)
+    return set_error(PKX_EINVAL, "qk_norm_rope: v is only written to the pool: cache_loc is null");
+  if (rotary_dim > 0) {
+    if (!positions || !aligned(positions, 8))
+      return set_error(PKX_EINVAL, "qk_norm_rope: positions null or misaligned");
+    if (!cos_sin || !aligned(cos_sin, 16) || max_position <= 0)
+      return set_error(PKX_EINVAL, "qk_norm_rope: cos_sin null, misaligned or without rows");
+    if (num_axes <= 0 || (num_axes > 1 && !pair_axis))
+      return set_error(PKX_EINVAL, "qk_norm_rope: several axes need pair_axis");
+  }
+  if ((rc = check_rows("q", q, q_ts, q_hs))) return rc;
+  if ((rc = check_rows("k", k, k_ts, k_hs))) return rc;
+  if ((rc = check_rows("q_out", q_out, qo_ts, qo_hs))) return rc;
+  if ((rc = check_rows("k_out", k_out, ko_ts, ko_hs))) return rc;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return set_error(PKX_EINVAL, "qk_norm_rope: weights must be 16-byte aligned");
+  if (cache_loc) {
+    if ((rc = check_pool_format("qk_norm_rope", kv_dtype, k_scale, v_scale))) return rc;
+    if (!aligned(cache_loc, 8)) return set_error(PKX_EINVAL, "qk_norm_rope: cache_loc misaligned");
+    if (num_slots < 0) return set_error(PKX_EINVAL, "qk_norm_rope: negative num_slots");
+    if ((rc = check_rows("k_buffer", k_buffer, kb_ss, kb_sh))) return rc;
+    if (v) {
+      if ((rc = check_rows("v", v, v_ts, v_hs))) return rc;
+      if ((rc = check_rows("v_buffer", v_buffer, vb_ss, vb_sh))) return rc;
+    }
+  }
+  RopeArgs a{};
+  auto in = [](const void *p) { return static_cast<const uint16_t *>(p); };
+  a.q = in(q); a.k = in(k); a.v = in(v);
+  a.q_out = static_cast<uint16_t *>(q_out); a.k_out = static_cast<uint16_t *>(k_out);
+  a.q_ts = q_ts; a.q_hs = q_hs; a.k_ts = k_ts; a.k_hs = k_hs; a.v_ts = v_ts; a.v_hs = v_hs;
+  a.qo_ts = qo_ts; a.qo_hs = qo_hs; a.ko_ts = ko_ts; a.ko_hs = ko_hs;
+  a.n_tokens = n_tokens;
+  a.hq = hq; a.hkv = hkv; a.d = d; a.rotary = rotary_dim;
+  a.positions = positions; a.axes = num_axes;
+  a.pair_axis = pair_axis; a.cos_sin = cos_sin; a.max_position = max_position;
+  a.interleaved = interleaved;
+  a.q_weight = in(q_weight); a.k_weight = in(k_weight);
+  a.eps = eps; a.weight_offset = weight_offset;
+  a.cache_loc = cache_loc;
+  a.k_buffer = k_buffer; a.v_buffer = v_buffer;
+  a.kb_ss = kb_ss; a.kb_hs = kb_sh; a.vb_ss = vb_ss; a.vb_hs = vb_sh;
+  a.num_slots = num_slots;
+  a.kv_fmt = cache_loc ? kv_dtype : kKvBf16;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  return launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, int kv_dtype,
+                           int page_size, int64_t num_pages, int hkv, int d,
+                           const int32_t *page_ids, const int32_t *page_lens, int64_t n_pages,
+                           void *bounds, void *stream) {
+  int rc;
+  if ((rc = check_pool_format("update_page_bounds", kv_dtype, 1.f, 1.f))) return rc;
+  if (page_size <= 0 || num_pages < 0 || n_pages < 0)
+    return set_error(PKX_EINVAL, "update_page_bounds: page_size > 0, no negative counts");
+  if (hkv <= 0 || d <= 0 || d % 8)
+    return set_error(PKX_EINVAL, "update_page_bounds: hkv > 0, d a multiple of 8");
+  if (hkv > (1 << 20) || d > (1 << 10))
+    return set_error(PKX_EUNSUPPORTED, "update_page_bounds: more than 2^20 heads or d > 1024");
+  if (n_pages == 0) return PKX_OK;
+  if ((rc = check_rows("k_buffer", k_buffer, kb_ss, kb_sh))) return rc;
+  if (!bounds || !aligned(bounds, 16))
+    return set_error(PKX_EINVAL, "update_page_bounds: bounds null or misaligned");
+  if (!page_ids || !aligned(page_ids, 4) || !aligned(page_lens, 4))
+    return set_error(PKX_EINVAL, "update_page_bounds: page_ids null or misaligned");
+  return launch_update_page_bounds(k_buffer, kb_ss, kb_sh, kv_dtype, page_size, num_pages, hkv, d,
+                                   page_ids, page_lens, n_pages, bounds,
+                                   static_cast<cudaStream_t>(stream));
+}
+
+size_t pkx_select_pages_workspace_size(int hkv, int64_t n_indices) {
+  if (hkv <= 0 || n_indices < 0) return 0;
+  return select_pages_workspace(hkv, n_indices);
+}
+
+int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
+                     const int32_t *kv_indptr, const int32_t *kv_indices, int64_t n_indices,
+                     int batch, int hq, int hkv, int d, int top_k, int first_pages, int last_pages,
+                     int32_t *selected, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc;
+  if (batch < 0) return set_error(PKX_EINVAL, "negative batch");
+  if ((rc = check_equal_heads("select_pages", hq, hkv, d, d))) return rc;
+  if ((rc = check_top_k(top_k))) return rc;
+  if (first_pages < 0 || last_pages < 0 || (int64_t)first_pages + last_pages > top_k)
+    return set_error(PKX_EINVAL, "select_pages: first_pages + last_pages must be in [0, top_k]");
+  if (num_pages < 0 || n_indices < 0)
+    return set_error(PKX_EINVAL, "select_pages: negative count of pages");
+  if (n_indices >= (1ll << 31))
+    return set_error(PKX_EUNSUPPORTED, "select_pages: 2^31 or more pages in one call");
+  if (batch == 0) return PKX_OK;
+  if ((rc = check_rows("q", q, 8, 8))) return rc;
+  if (num_pages > 0 && (!bounds || !aligned(bounds, 16)))
+    return set_error(PKX_EINVAL, "select_pages: bounds null or misaligned");
+  if (!kv_indptr || !aligned(kv_indptr, 4))
+    return set_error(PKX_EINVAL, "kv_indptr null or misaligned");
+  if (n_indices > 0 && (!kv_indices || !aligned(kv_indices, 4)))
+    return set_error(PKX_EINVAL, "kv_indices null or misaligned");
+  if (!selected || !aligned(selected, 4))
+    return set_error(PKX_EINVAL, "select_pages: selected null or misaligned");
+  const size_t need = select_pages_workspace(hkv, n_indices);
+  if (!workspace || workspace_bytes < need)
+    return set_error(PKX_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes,
+                     need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return set_error(PKX_EINVAL, "workspace must be 256-byte aligned");
+  SelectArgs a{};
+  a.q = q; a.bounds = bounds; a.num_pages = num_pages;
+  a.kv_indptr = kv_indptr; a.kv_indices = kv_indices; a.n_indices = n_indices;
+  a.batch = batch; a.hq = hq; a.hkv = hkv; a.d = d;
+  a.top_k = top_k; a.first_pages = first_pages; a.last_pages = last_pages;
+  a.selected = selected;
+  a.workspace = workspace; a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_select_pages(a);
+}
+
+size_t pkx_decode_pages_workspace_size(int batch, int hq, int hkv, int lq, int lv, int page_size,
+                                       int top_k) {
+  if (batch < 0 || hkv <= 0 || hq <= 0 || hq % hkv || hq / hkv > kBlockM || lq != lv ||
+      (lq != 64 && lq != 128) || page_size <= 0 || top_k <= 0 || top_k > kMaxTopK ||
+      (int64_t)top_k * page_size >= (1ll << 31))
+    return 0;
+  return pages_decode_workspace(batch, hq, hkv, lq, page_size, top_k, num_sms_current_device());
+}
+
+int pkx_decode_attention_fwd_pages(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
+    const int32_t *kv_indices, int64_t n_indices, const int32_t *kv_last_page_len, int page_size,
+    const int32_t *selected, int top_k, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss,
+    int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int kv_dtype, float k_scale, float v_scale, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream) {
+  int rc;
+  if ((rc = check_equal_heads("decode over selected pages", hq, hkv, lq, lv))) return rc;
+  if ((rc = check_top_k(top_k))) return rc;
+  if (page_size <= 0) return set_error(PKX_EINVAL, "page_size must be positive");
+  if (n_indices < 0) return set_error(PKX_EINVAL, "negative n_indices");
+  AttnArgs a{};
+  bool done;
+  rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,
+                   kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, -1, kv_dtype,
+                   k_scale, v_scale, lse_out, &done);
+  if (rc != PKX_OK || done) return rc;
+  if (n_indices > 0 && !kv_indices) return set_error(PKX_EINVAL, "kv_indices is null");
+  if (!kv_last_page_len || !aligned(kv_last_page_len, 4))
+    return set_error(PKX_EINVAL, "kv_last_page_len null or misaligned");
+  if (!selected || !aligned(selected, 4))
+    return set_error(PKX_EINVAL, "selected null or misaligned");
+  if (num_slots >= INT32_MAX) return set_error(PKX_EUNSUPPORTED, "more than 2^31 pool slots");
+  ListedArgs l = listed_args(a, workspace, workspace_bytes, stream);
+  l.last_page_len = kv_last_page_len;
+  l.selected = selected;
+  l.page_size = page_size;
+  l.top_k = top_k;
+  l.n_indices = n_indices;
+  return launch_decode_pages(l);
+}
+
+size_t pkx_decode_shared_workspace_size(int batch, int num_groups, int hq, int hkv, int lq,
+                                        int lv) {
+  if (batch < 0 || num_groups < 0 || hkv <= 0 || hq <= 0 || hq % hkv || hq / hkv > kBlockM ||
+      lq != lv || (lq != 64 && lq != 128))
+    return 0;
+  return shared_decode_workspace(batch, num_groups, hq, hkv, lq, num_sms_current_device());
+}
+
+int pkx_decode_attention_fwd_shared(
+    const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
+    const int32_t *kv_indices, const int32_t *group_indptr, const int32_t *shared_lens,
+    int num_groups, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
+    int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
+    float k_scale, float v_scale, float *lse_out, void *workspace, size_t workspace_bytes,
+    void *stream) {
+  int rc;
+  if ((rc = check_equal_heads("decode with shared prefixes", hq, hkv, lq, lv))) return rc;
+  if (num_groups < 0) return set_error(PKX_EINVAL, "negative num_groups");
+  AttnArgs a{};
+  bool done;
+  rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,
+                   kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, -1, kv_dtype,
+                   k_scale, v_scale, lse_out, &done);
+  if (rc != PKX_OK || done) return rc;
+  if (num_groups > 0 && (!group_indptr || !shared_lens || !aligned(group_indptr, 4) ||
+                         !aligned(shared_lens, 4)))
+    return set_error(PKX_EINVAL, "group_indptr or shared_lens null or misaligned");
+  if (num_slots >= INT32_MAX) return set_error(PKX_EUNSUPPORTED, "more than 2^31 pool slots");
+  ListedArgs l = listed_args(a, workspace, workspace_bytes, stream);
+  l.group_indptr = group_indptr;
+  l.shared_lens = shared_lens;
+  l.num_groups = num_groups;
+  return launch_decode_shared(l);
+}
+
+}  // extern "C"

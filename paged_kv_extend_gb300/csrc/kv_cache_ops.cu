@@ -24,10 +24,9 @@
 // evenly over the CTAs, so one long sequence does not serialise on one CTA as
 // it would with a CTA per sequence.  A thread finds the sequence of its entry
 // by binary search in the shared running sum.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "fp8.cuh"
 #include "pkx_internal.h"
 
 namespace pkx {
@@ -139,22 +138,6 @@ struct KvWriteFp8Args {
   uint64_t total;
   float k_scale, v_scale;
 };
-
-template <int FMT>
-__device__ __forceinline__ uint2 bf16x8_to_fp8x8(uint4 in, float scale) {
-  constexpr __nv_fp8_interpretation_t kind = FMT == 1 ? __NV_E4M3 : __NV_E5M2;
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  uint32_t out[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
-    const float2 f = __bfloat1622float2(b);
-    const float2 q = make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, kind);
-    out[i >> 1] |= (two & 0xFFFFu) << (16 * (i & 1));
-  }
-  return make_uint2(out[0], out[1]);
-}
 
 template <int FMT>
 __global__ void __launch_bounds__(kKvThreads) set_kv_buffer_fp8_kernel(const KvWriteFp8Args a) {

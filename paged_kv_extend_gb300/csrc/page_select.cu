@@ -1,0 +1,450 @@
+// page_select.cu -- which pages of a paged KV cache a decode step reads: the
+// bounds of every page's keys, and the selection by them.
+//
+// Bounds.  For page P and KV head h, per dim d: lo = min and hi = max of
+// k[d] over the page's keys.  They are elements of K, so bf16 holds them
+// exactly (an fp8 pool's codes too; its k_scale, a positive factor of every
+// score, is left out).
+//
+// Score.  max over the box of <q, k> is sum_d max(q_d lo_d, q_d hi_d) =
+// sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d, an upper bound of the logit of
+// every key in the page.  Summed over the query heads of a KV head the q factors
+// add up first:
+//   score = sum_d qn_d lo_d + sum_d qp_d hi_d,  qp = sum_g max(q_g, 0), ...
+// so that a page costs one product a bound whatever the group.  The order of the
+// sums is part of the definition (each product and sum rounded to fp32, dims
+// added pairwise: 0 + 1, 2 + 3, then those), so that the selection does not
+// depend on how the work is split: a lane adds its 8 dims as a tree, and a
+// butterfly over the lanes goes on with it.
+//
+// What bounds it: the bounds are read once, 4 d bytes a page and KV head
+// (1/32 of K and V at pages of 64 bf16 keys); 4 operations an element stay
+// below a third of the issue slots.  The scores go to the workspace as
+// ordered 32-bit keys and a second kernel, one CTA for each (sequence, KV
+// head), finds the threshold of the top k by halving the key range two bits a
+// round with counts over the CTA (a histogram by shared atomics would
+// serialise: the scores share their exponents) and writes the pages in order,
+// so equal scores go to the lower page and no atomic decides.
+#include <cuda_runtime.h>
+
+#include "fp8.cuh"
+#include "pkx_internal.h"
+#include "ptx.cuh"
+
+namespace pkx {
+
+// ------------------------------------------------------------------ bounds
+constexpr int kBoundThreads = 256;
+constexpr int kBoundUnroll = 8;
+
+struct BoundParams {
+  const uint8_t *k;
+  int64_t kb_ss, kb_hs;  // bytes
+  const int32_t *page_ids, *page_lens;
+  int64_t n_pages, num_pages;
+  int page_size, hkv, d;
+  int slices;  // runs of 32 chunks of a slot's row (all heads)
+  uint4 *bounds;  // [num_pages][hkv][2][d / 8]
+};
+
+template <int FMT>
+__device__ __forceinline__ uint4 load_keys(const uint8_t *p) {
+  if constexpr (FMT == 0) return __ldg(reinterpret_cast<const uint4 *>(p));
+  else return fp8x8_to_bf16x8<FMT>(__ldg(reinterpret_cast<const uint2 *>(p)));
+}
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // NaN if either is
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint4 min8(uint4 a, uint4 b) {
+  return make_uint4(min2(a.x, b.x), min2(a.y, b.y), min2(a.z, b.z), min2(a.w, b.w));
+}
+__device__ __forceinline__ uint4 max8(uint4 a, uint4 b) {
+  return make_uint4(max2(a.x, b.x), max2(a.y, b.y), max2(a.z, b.z), max2(a.w, b.w));
+}
+
+// One CTA: a page and 32 neighbouring 8-element chunks of its slots' rows (a
+// lane each); the eight warps take slots in turn and meet in shared memory.
+template <int FMT>
+__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundParams p) {
+  constexpr int WARPS = kBoundThreads / 32;
+  __shared__ uint4 s_lo[WARPS][32], s_hi[WARPS][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t item = blockIdx.x / p.slices;
+  const int chunk = (int)(blockIdx.x - item * p.slices) * 32 + lane;
+  const int cph = p.d / 8;
+  const int page = __ldg(p.page_ids + item);
+  int len = p.page_lens ? min(__ldg(p.page_lens + item), p.page_size) : p.page_size;
+  if (page < 0 || page >= p.num_pages || len <= 0) return;  // (the same for the whole CTA)
+  const int h = chunk / cph, c = chunk - h * cph;
+  const bool have = h < p.hkv;
+  const uint8_t *src = p.k + (int64_t)page * p.page_size * p.kb_ss + (have ? h : 0) * p.kb_hs +
+                       c * (FMT == 0 ? 16 : 8);
+  const uint32_t inf2 = 0x7F807F80u, ninf2 = 0xFF80FF80u;
+  uint4 lo = make_uint4(inf2, inf2, inf2, inf2), hi = make_uint4(ninf2, ninf2, ninf2, ninf2);
+  for (int s0 = warp; s0 < len; s0 += WARPS * kBoundUnroll) {
+    uint4 x[kBoundUnroll];
+    // (a slot past the end repeats the first one)
+#pragma unroll
+    for (int u = 0; u < kBoundUnroll; ++u) {
+      const int s = s0 + u * WARPS;
+      if (have) x[u] = load_keys<FMT>(src + (int64_t)(s < len ? s : s0) * p.kb_ss);
+    }
+    if (have) {
+#pragma unroll
+      for (int u = 0; u < kBoundUnroll; ++u) {
+        lo = min8(lo, x[u]);
+        hi = max8(hi, x[u]);
+      }
+    }
+  }
+  s_lo[warp][lane] = lo;
+  s_hi[warp][lane] = hi;
+  __syncthreads();
+  if (warp < 2 && have) {
+    uint4 r = warp == 0 ? s_lo[0][lane] : s_hi[0][lane];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) r = warp == 0 ? min8(r, s_lo[w][lane]) : max8(r, s_hi[w][lane]);
+    p.bounds[(((int64_t)page * p.hkv + h) * 2 + warp) * cph + c] = r;
+  }
+}
+
+int launch_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_hs, int kv_fmt,
+                              int page_size, int64_t num_pages, int hkv, int d,
+                              const int32_t *page_ids, const int32_t *page_lens, int64_t n_pages,
+                              void *bounds, cudaStream_t st) {
+  if (n_pages == 0) return PKX_OK;
+  const int size = kv_fmt == kKvBf16 ? 2 : 1;
+  BoundParams p;
+  p.k = static_cast<const uint8_t *>(k_buffer);
+  p.kb_ss = kb_ss * size;
+  p.kb_hs = kb_hs * size;
+  p.page_ids = page_ids;
+  p.page_lens = page_lens;
+  p.n_pages = n_pages;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.hkv = hkv;
+  p.d = d;
+  p.slices = (hkv * (d / 8) + 31) / 32;
+  p.bounds = static_cast<uint4 *>(bounds);
+  if (n_pages * p.slices >= (1ll << 31))
+    return set_error(PKX_EUNSUPPORTED, "update_page_bounds: too many pages in one call");
+  auto kernel = kv_fmt == kKvBf16      ? page_bounds_kernel<0>
+                : kv_fmt == kKvFp8E4M3 ? page_bounds_kernel<1>
+                                       : page_bounds_kernel<2>;
+  cudaError_t e = launch_pdl(kernel, dim3((unsigned)(n_pages * p.slices)), dim3(kBoundThreads), 0,
+                             st, p);
+  if (e != cudaSuccess)
+    return set_error(PKX_ECUDA, "update_page_bounds launch: %s", cudaGetErrorString(e));
+  return PKX_OK;
+}
+
+// ------------------------------------------------------------------- score
+constexpr int kScoreThreads = 256;
+constexpr int kScoreUnroll = 4;
+
+struct ScoreParams {
+  const uint16_t *q;
+  const uint4 *bounds;
+  int64_t num_pages;
+  const int32_t *kv_indptr, *kv_indices;
+  int64_t n_indices;
+  int batch, hq, hkv, group, top_k;
+  int run;         // page steps of a warp
+  int64_t runs;    // runs of a KV head
+  uint32_t *keys;  // [hkv][n_indices]
+  WsHeader *hdr;
+};
+
+// A score as an unsigned key of the same order: NaN above everything, equal
+// zeros equal.  0 stands for a page outside the bounds (no score maps there).
+__device__ __forceinline__ uint32_t score_key(float s) {
+  if (s != s) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(s + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// A warp: one KV head and a run of consecutive entries of kv_indices.  D / 4
+// lanes hold a page's two bounds, 8 dims each; neighbouring warps take the
+// heads of the same pages.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreParams p) {
+  constexpr int LP = D / 4;        // lanes of a page
+  constexpr int PPW = 32 / LP;     // pages of a warp's step
+  constexpr int CH = D / 8;        // lanes of one bound
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->status = 0;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+  if (w >= p.runs * p.hkv) return;
+  const int h = (int)(w % p.hkv);
+  const int64_t e0 = (w / p.hkv) * p.run * PPW;
+  const int sub = lane / LP, l = lane - sub * LP;
+  const bool is_hi = l >= CH;
+  const int c = is_hi ? l - CH : l;
+  const int64_t e_end = min(e0 + (int64_t)p.run * PPW, p.n_indices);
+  int b = -1;
+  int64_t b_end = 0;  // entries before b_end belong to sequence b
+  bool scored = false;
+  float f[8];
+  for (int64_t s0 = e0; s0 < e_end; s0 += PPW * kScoreUnroll) {
+    int64_t pg[kScoreUnroll];
+    uint4 x[kScoreUnroll];
+#pragma unroll
+    for (int u = 0; u < kScoreUnroll; ++u) {
+      const int64_t e = s0 + u * PPW + sub;
+      pg[u] = e < e_end ? __ldg(p.kv_indices + e) : -1;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (pg[u] >= 0 && pg[u] < p.num_pages)
+        x[u] = __ldg(p.bounds + (pg[u] * p.hkv + h) * LP + l);
+      else
+        pg[u] = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kScoreUnroll; ++u) {
+      const int64_t e = s0 + u * PPW + sub;
+      // the entry's sequence and the sum of its query heads (the lanes of a
+      // page take the same branch)
+      if (e < e_end && e >= b_end) {
+        int lo = max(b, 0), hi = p.batch - 1;  // last b with kv_indptr[b] <= e
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (__ldg(p.kv_indptr + mid) <= e) lo = mid;
+          else hi = mid - 1;
+        }
+        b = lo;
+        const int64_t first = __ldg(p.kv_indptr + b);
+        b_end = max((int64_t)__ldg(p.kv_indptr + b + 1), e + 1);
+        const int64_t end = __ldg(p.kv_indptr + b + 1);
+        scored = e >= first && e < end && end - first > p.top_k;  // else: every page, or none
+        if (e >= end || e < first) b_end = e + 1;
+        if (scored) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = 0.f;
+          const uint4 *row = reinterpret_cast<const uint4 *>(
+              p.q + ((int64_t)b * p.hq + (int64_t)h * p.group) * D) + c;
+          for (int g = 0; g < p.group; ++g) {
+            const uint4 v = __ldg(row + g * CH);
+            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float qv = __uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16);
+              f[i] = __fadd_rn(f[i], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
+            }
+          }
+        }
+      }
+      const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        t[i] = __fmul_rn(__uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16),
+                         scored ? f[i] : 0.f);
+#pragma unroll
+      for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
+      float s = t[0];
+#pragma unroll
+      for (int o = 1; o < LP; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      if (l == 0 && e < e_end && scored)
+        p.keys[(int64_t)h * p.n_indices + e] = pg[u] < 0 ? 0u : score_key(s);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ select
+struct SelectParams {
+  const int32_t *kv_indptr;
+  int64_t n_indices;
+  int batch, hkv, top_k, first_pages, last_pages;
+  const uint32_t *keys;
+  int32_t *selected;
+  WsHeader *hdr;
+};
+
+// One CTA for each (sequence, KV head).  A thread keeps kHeld keys in
+// registers (keys i = r * THREADS + tid); those of longer sequences are read
+// again each round.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams p) {
+  constexpr int kHeld = 16, WARPS = THREADS / 32;
+  __shared__ int s_cnt[2][WARPS][3];
+  __shared__ int s_scan[2][WARPS];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.hkv, h = blockIdx.x - b * p.hkv;
+  const int64_t at = __ldg(p.kv_indptr + b);
+  const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
+  int32_t *out = p.selected + (int64_t)blockIdx.x * p.top_k;
+  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
+  if (bad && tid == 0) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
+  const int n = bad ? 0 : (int)n64;
+  if (n <= p.top_k) {  // every page
+    for (int i = tid; i < p.top_k; i += THREADS) out[i] = i < n ? i : -1;
+    return;
+  }
+  // candidates: the pages between the first and the last ones
+  const int lo = p.first_pages, m = n - p.first_pages - p.last_pages;
+  const int want = p.top_k - p.first_pages - p.last_pages;  // 0 <= want < m
+  const uint32_t *keys = p.keys + (int64_t)h * p.n_indices + at + lo;
+  uint32_t held[kHeld];
+  bool lost = false;  // a page outside the bounds
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r) {
+    const int i = r * THREADS + tid;
+    held[r] = i < m ? __ldg(keys + i) : 0u;
+    lost |= i < m && held[r] == 0u;
+  }
+  for (int i = kHeld * THREADS + tid; i < m; i += THREADS) lost |= __ldg(keys + i) == 0u;
+  if (lost) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
+
+  // the largest key T with count(key >= T) >= want, two bits a round
+  uint32_t T = 0;
+  int above = 0;  // count(key > T) at the end
+  if (want > 0) {
+    int parity = 0;
+    for (int shift = 30; shift >= 0; shift -= 2, parity ^= 1) {
+      const uint32_t t1 = T + (1u << shift), t2 = T + (2u << shift), t3 = T + (3u << shift);
+      int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+      for (int r = 0; r < kHeld; ++r) {  // (an absent key is 0, below every bound)
+        c1 += held[r] >= t1;
+        c2 += held[r] >= t2;
+        c3 += held[r] >= t3;
+      }
+      for (int i = kHeld * THREADS + tid; i < m; i += THREADS) {
+        const uint32_t k = __ldg(keys + i);
+        c1 += k >= t1;
+        c2 += k >= t2;
+        c3 += k >= t3;
+      }
+      c1 = __reduce_add_sync(0xffffffffu, c1);
+      c2 = __reduce_add_sync(0xffffffffu, c2);
+      c3 = __reduce_add_sync(0xffffffffu, c3);
+      if (lane == 0) {
+        s_cnt[parity][warp][0] = c1;
+        s_cnt[parity][warp][1] = c2;
+        s_cnt[parity][warp][2] = c3;
+      }
+      __syncthreads();
+      c1 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][0] : 0);
+      c2 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][1] : 0);
+      c3 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][2] : 0);
+      if (c3 >= want) T = t3;
+      else if (c2 >= want) T = t2, above = c3;
+      else if (c1 >= want) T = t1, above = c2;
+      else above = c1;
+    }
+  }
+  const int ties = want - above;  // keys equal to T that are taken, lowest first
+
+  for (int i = tid; i < p.first_pages; i += THREADS) out[i] = i;
+  for (int i = tid; i < p.last_pages; i += THREADS)
+    out[p.top_k - p.last_pages + i] = n - p.last_pages + i;
+  // the others in order: a running count of keys above T and equal to it
+  int gt = 0, eq = 0, parity = 0;
+  if (want > 0) {
+    for (int r = 0; r * THREADS < m; ++r, parity ^= 1) {
+      const int i = r * THREADS + tid;
+      uint32_t k = 0;
+      if (r < kHeld) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (j == r) k = held[j];
+      } else if (i < m) {
+        k = __ldg(keys + i);
+      }
+      const unsigned g = __ballot_sync(0xffffffffu, i < m && k > T);
+      const unsigned q = __ballot_sync(0xffffffffu, i < m && k == T);
+      if (lane == 0) s_scan[parity][warp] = __popc(g) | (__popc(q) << 16);
+      __syncthreads();
+      int x = lane < WARPS ? s_scan[parity][lane] : 0;
+      const int all = __reduce_add_sync(0xffffffffu, x);
+      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+      const unsigned below = (1u << lane) - 1u;
+      const int my_gt = gt + (before & 0xFFFF) + __popc(g & below);
+      const int my_eq = eq + (before >> 16) + __popc(q & below);
+      if (i < m && (k > T || (k == T && my_eq < ties)))
+        out[lo + my_gt + min(my_eq, ties)] = lo + i;
+      gt += all & 0xFFFF;
+      eq += all >> 16;
+    }
+  }
+}
+
+size_t select_pages_workspace(int hkv, int64_t n_indices) {
+  return 256 + ((sizeof(uint32_t) * (size_t)hkv * (size_t)n_indices + 255) & ~(size_t)255);
+}
+
+int launch_select_pages(const SelectArgs &a) {
+  if (a.batch == 0) return PKX_OK;
+  const int nsm = num_sms_current_device();
+  if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
+  WsHeader *hdr = static_cast<WsHeader *>(a.workspace);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.workspace) + 256);
+  ScoreParams p;
+  p.q = static_cast<const uint16_t *>(a.q);
+  p.bounds = static_cast<const uint4 *>(a.bounds);
+  p.num_pages = a.num_pages;
+  p.kv_indptr = a.kv_indptr;
+  p.kv_indices = a.kv_indices;
+  p.n_indices = a.n_indices;
+  p.batch = a.batch;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.group = a.hq / a.hkv;
+  p.top_k = a.top_k;
+  p.keys = keys;
+  p.hdr = hdr;
+  // a warp's run: about 32 warps an SM, 4 to 32 steps each (a run reads the
+  // group's query rows once)
+  const int ppw = 128 / a.d;
+  const int64_t steps = (a.n_indices + ppw - 1) / ppw;
+  int64_t run = steps * a.hkv / ((int64_t)nsm * 32);
+  run = run < kScoreUnroll ? kScoreUnroll : run > 32 ? 32 : run / kScoreUnroll * kScoreUnroll;
+  p.run = (int)run;
+  p.runs = (steps + run - 1) / run;
+  int64_t grid = (p.runs * a.hkv + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+  if (grid < 1) grid = 1;  // (the status word)
+  if (grid >= (1ll << 31) || (int64_t)a.batch * a.hkv >= (1ll << 31))
+    return set_error(PKX_EUNSUPPORTED, "select_pages: too many pages in one call");
+  cudaError_t e = launch_pdl(a.d == 128 ? page_score_kernel<128> : page_score_kernel<64>,
+                             dim3((unsigned)grid), dim3(kScoreThreads), 0, a.stream, p);
+  if (e != cudaSuccess)
+    return set_error(PKX_ECUDA, "page_score launch: %s", cudaGetErrorString(e));
+  SelectParams s;
+  s.kv_indptr = a.kv_indptr;
+  s.n_indices = a.n_indices;
+  s.batch = a.batch;
+  s.hkv = a.hkv;
+  s.top_k = a.top_k;
+  s.first_pages = a.first_pages;
+  s.last_pages = a.last_pages;
+  s.keys = keys;
+  s.selected = a.selected;
+  s.hdr = hdr;
+  // 256 threads hold 4096 keys, 1024 hold 16384: by the batch's average
+  const dim3 pairs((unsigned)(a.batch * a.hkv));
+  if (a.n_indices / a.batch <= 4096)
+    e = launch_pdl(page_select_kernel<256>, pairs, dim3(256), 0, a.stream, s);
+  else
+    e = launch_pdl(page_select_kernel<1024>, pairs, dim3(1024), 0, a.stream, s);
+  if (e != cudaSuccess)
+    return set_error(PKX_ECUDA, "page_select launch: %s", cudaGetErrorString(e));
+  return PKX_OK;
+}
+
+}  // namespace pkx

@@ -20,6 +20,8 @@ enum KeyMode : int {
   kTwoStage = 0,  // prefix via int32 kv_indices, extend rows from k/v_extend
   kUnified = 1,   // every key via int64 kv_indices, prefix_lens given
   kDecode = 2,    // every key via int32 kv_indices, query at position T-1
+  kListed = 3,    // units listed by the caller: every key via int32 kv_indices and
+                  // visible, every unit writes partials (listed_attention.cu)
 };
 
 // Element format of the KV pool (the values of include/pkx.h's PKX_KV_*).
@@ -238,6 +240,81 @@ struct Fp4DecodeArgs {
 };
 size_t fp4_decode_workspace(int hq, int hkv, int d);
 int launch_decode_fp4(const Fp4DecodeArgs &a);
+// Arguments of one query / key norm, rotation and KV write (rope.cu); strides
+// in elements of the tensor (a pool's: of the pool).
+struct RopeArgs {
+  const uint16_t *q, *k, *v;  // v: null without the KV write of values
+  uint16_t *q_out, *k_out;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+  int64_t n_tokens;
+  int hq, hkv, d, rotary;  // rotary 0: no rotation
+  const int64_t *positions;  // [axes][n_tokens]
+  int axes;
+  const float *cos_sin;  // [max_position][rotary]
+  int64_t max_position;
+  const uint8_t *pair_axis;  // null: every pair on axis 0
+  int interleaved;
+  const uint16_t *q_weight, *k_weight;
+  float eps, weight_offset;
+  const int64_t *cache_loc;  // null: no KV write
+  void *k_buffer, *v_buffer;
+  int64_t kb_ss, kb_hs, vb_ss, vb_hs, num_slots;
+  int kv_fmt;
+  float k_scale, v_scale;
+};
+int launch_qk_norm_rope(const RopeArgs &a, cudaStream_t s);
+
+// Page bounds and the selection of pages (page_select.cu).
+int launch_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_hs, int kv_fmt,
+                              int page_size, int64_t num_pages, int hkv, int d,
+                              const int32_t *page_ids, const int32_t *page_lens, int64_t n_pages,
+                              void *bounds, cudaStream_t s);
+struct SelectArgs {
+  const void *q;
+  const void *bounds;
+  int64_t num_pages;
+  const int32_t *kv_indptr, *kv_indices;
+  int64_t n_indices;
+  int batch, hq, hkv, d;
+  int top_k, first_pages, last_pages;
+  int32_t *selected;
+  void *workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+size_t select_pages_workspace(int hkv, int64_t n_indices);
+int launch_select_pages(const SelectArgs &a);
+
+// Decode attention whose work is listed by schedulers of its own
+// (listed_attention.cu): sequences in groups that share a prefix, or selected
+// pages of each KV head.  Lq = Lv = d.
+struct ListedArgs {
+  const void *q;
+  void *o;
+  float *lse;
+  const void *k_buf, *v_buf;
+  int64_t kb_ss, kb_sh, vb_ss, vb_sh, num_slots;
+  const int32_t *kv_indptr, *kv_indices;  // tokens (shared) or pages
+  int batch, hq, hkv, d;
+  float sm_scale, logit_cap;
+  int kv_fmt;
+  float k_scale, v_scale;
+  // shared prefixes
+  const int32_t *group_indptr = nullptr, *shared_lens = nullptr;
+  int num_groups = 0;
+  // selected pages
+  const int32_t *last_page_len = nullptr, *selected = nullptr;
+  int page_size = 0, top_k = 0;
+  int64_t n_indices = 0;  // entries of kv_indices
+  void *workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+size_t shared_decode_workspace(int batch, int num_groups, int hq, int hkv, int d, int num_sms);
+int launch_decode_shared(const ListedArgs &a);
+size_t pages_decode_workspace(int batch, int hq, int hkv, int d, int page_size, int top_k,
+                              int num_sms);
+int launch_decode_pages(const ListedArgs &a);
 // Largest batch the index gather takes (its running sum lives in 48 KB of
 // shared memory).
 constexpr int kGatherMaxBatch = 12000;

@@ -105,6 +105,23 @@ _SIGS = {
     "pkx_decode_attention_fwd_streaming": (_i, [
         _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i,
         _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _i, _p, _p, _sz, _p]),
+    "pkx_qk_norm_rope": (_i, [
+        _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64, _i, _i, _i, _p, _i, _p, _p, _i64,
+        _i, _i, _p, _p, _f, _f, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64,
+        _i64, _i64, _i, _f, _f, _p]),
+    "pkx_update_page_bounds": (_i, [
+        _p, _i64, _i64, _i, _i, _i64, _i, _i, _p, _p, _i64, _p, _p]),
+    "pkx_select_pages_workspace_size": (_sz, [_i, _i64]),
+    "pkx_select_pages": (_i, [
+        _p, _p, _i64, _p, _p, _i64, _i, _i, _i, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "pkx_decode_pages_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "pkx_decode_attention_fwd_pages": (_i, [
+        _p, _p, _p, _p, _p, _p, _i64, _p, _i, _p, _i, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _f, _f, _p, _p, _sz, _p]),
+    "pkx_decode_shared_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "pkx_decode_attention_fwd_shared": (_i, [
+        _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i,
+        _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _f, _f, _p, _p, _sz, _p]),
 }
 
 
@@ -953,4 +970,242 @@ def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indic
         kv_indices.data_ptr(), b, hq, hkv, lq, lv, *strides,
         k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), _c_int(sliding_window),
         _c_int(first_tokens), _address(lse), ws.data_ptr(), ws.numel() * ws.element_size()))
+    return ws
+
+
+# ------------------------------------------- a decode step around the paged pool
+def _row_output(out, like, name):
+    """The output for rows shaped as ``like``: ``out``, or a new tensor."""
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape or out.get_device() != like.get_device():
+        raise ValueError(f"{name} is {tuple(out.shape)} on {out.device}, expected "
+                         f"{tuple(like.shape)} on {like.device}")
+    return out
+
+
+def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_weight=None,
+                 k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False, pair_axis=None,
+                 cache_loc=None, v=None, k_buffer=None, v_buffer=None, k_scale=1.0, v_scale=1.0):
+    """Per-head RMS norm (``q_weight`` / ``k_weight`` bf16 [d], None: none) and
+    position rotation of queries [n, hq, d] and keys [n, hkv, d], and the KV
+    write of the result (pkx_qk_norm_rope).  ``positions`` int64 [n], or
+    [axes, n] with ``pair_axis`` uint8 [rotary / 2]; ``cos_sin`` float32
+    [max_position, rotary] (None: no rotation).  With ``cache_loc`` int64 [n]
+    the new keys (and ``v``) also go to that slot of ``k_buffer`` (and
+    ``v_buffer``), bf16 or fp8.  ``q_out`` / ``k_out`` may be ``q`` / ``k``.
+    Returns (q_out, k_out)."""
+    lib = load_library()
+    qs, ks = _rows(q, "q"), _rows(k, "k")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    if tuple(k.shape) != (n, hkv, d):
+        raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
+    dev = q.device
+    q_out, k_out = _row_output(q_out, q, "q_out"), _row_output(k_out, k, "k_out")
+    qo, ko = _rows(q_out, "q_out"), _rows(k_out, "k_out")
+    axes, rotary, rows = 1, 0, 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_position, rotary] tensor")
+        rows, rotary = cos_sin.shape
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        _i64_vec(positions, "positions")
+        if positions.dim() not in (1, 2) or positions.shape[-1] != n:
+            raise ValueError(f"positions must be [{n}] or [axes, {n}], got {tuple(positions.shape)}")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        if pair_axis is not None:
+            if pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
+                raise ValueError("pair_axis must be a contiguous uint8 tensor")
+            _check_len(pair_axis, rotary // 2, "pair_axis")
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need cos_sin")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if w.dtype != torch.bfloat16 or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 tensor")
+            _check_len(w, d, name)
+    vs, kb, vb, fmt, slots = (0, 0), (0, 0), (0, 0), PKX_KV_BF16, 0
+    if cache_loc is None:
+        if v is not None or k_buffer is not None or v_buffer is not None:
+            raise ValueError("the KV write needs cache_loc")
+    else:
+        _i64_vec(cache_loc, "cache_loc")
+        _check_len(cache_loc, n, "cache_loc")
+        if k_buffer is None or (v is None) != (v_buffer is None):
+            raise ValueError("the KV write needs k_buffer, and v and v_buffer together")
+        if v is None:
+            kb, _, fmt = _pool_rows(k_buffer, k_buffer)
+        else:
+            kb, vb, fmt = _pool_rows(k_buffer, v_buffer)
+            vs = _rows(v, "v")
+            if tuple(v.shape) != (n, hkv, d) or v_buffer.shape != k_buffer.shape:
+                raise ValueError("v and v_buffer must be shaped as k and k_buffer")
+        slots = k_buffer.shape[0]
+        if tuple(k_buffer.shape[1:]) != (hkv, d):
+            raise ValueError(f"k_buffer {tuple(k_buffer.shape)} does not fit k {tuple(k.shape)}")
+    _one_device(dev, k=k, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
+                k_weight=k_weight, pair_axis=pair_axis, cache_loc=cache_loc, v=v,
+                k_buffer=k_buffer, v_buffer=v_buffer)
+    _check(_on(
+        dev, lib.pkx_qk_norm_rope,
+        q.data_ptr(), *qs, k.data_ptr(), *ks, _address(v), *vs, n, hq, hkv, d,
+        _address(positions), axes, _address(pair_axis), _address(cos_sin), rows, rotary,
+        1 if interleaved else 0, _address(q_weight), _address(k_weight), float(eps),
+        float(weight_offset), q_out.data_ptr(), *qo, k_out.data_ptr(), *ko, _address(cache_loc),
+        _address(k_buffer), *kb, _address(v_buffer), *vb, slots, fmt, float(k_scale),
+        float(v_scale)))
+    return q_out, k_out
+
+
+def _check_bounds(bounds, hkv, d):
+    """Pages of a bounds tensor bf16 [pages, hkv, 2, d]."""
+    if bounds.dtype != torch.bfloat16 or not bounds.is_contiguous() or bounds.dim() != 4 or \
+            tuple(bounds.shape[1:]) != (hkv, 2, d):
+        raise ValueError(f"bounds must be a contiguous bf16 [pages, {hkv}, 2, {d}] tensor, got "
+                         f"{bounds.dtype} {tuple(bounds.shape)}")
+    return bounds.shape[0]
+
+
+def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
+    """Smallest and largest key value of each listed page, per KV head and dim
+    (pkx_update_page_bounds): bounds[page, h, 0 / 1, :], in place.  The pool
+    (bf16 or fp8) is [pages * page_size or more slots, hkv, d]; ``page_ids``
+    int32 [n], ``page_lens`` int32 [n] (the slots in use; None: all).  Returns
+    ``bounds``."""
+    lib = load_library()
+    kb, _, fmt = _pool_rows(k_buffer, k_buffer)
+    slots, hkv, d = k_buffer.shape
+    pages = _check_bounds(bounds, hkv, d)
+    page_size = int(page_size)
+    if page_size < 1 or pages * page_size > slots:
+        raise ValueError(f"{pages} pages of {page_size} slots do not fit a pool of {slots} slots")
+    _i32(page_ids, "page_ids")
+    n = page_ids.numel()
+    if page_lens is not None:
+        _i32(page_lens, "page_lens")
+        _check_len(page_lens, n, "page_lens")
+    _one_device(k_buffer.device, bounds=bounds, page_ids=page_ids, page_lens=page_lens)
+    _check(_on(
+        k_buffer.device, lib.pkx_update_page_bounds, k_buffer.data_ptr(), *kb, fmt, page_size,
+        pages, hkv, d, page_ids.data_ptr(), _address(page_lens), n, bounds.data_ptr()))
+    return bounds
+
+
+def select_pages_workspace_size(hkv, n_indices) -> int:
+    return int(load_library().pkx_select_pages_workspace_size(hkv, n_indices))
+
+
+def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pages=1,
+                 selected=None, workspace=None):
+    """The pages whose bounds promise the largest logits, for each sequence and
+    KV head (pkx_select_pages): q [B, hq, d], bounds of update_page_bounds,
+    kv_indptr / kv_indices over pages.  Returns (selected int32
+    [B, hkv, top_k], workspace)."""
+    lib = load_library()
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda:
+        raise ValueError("q must be a contiguous CUDA bf16 [batch, heads, dim] tensor")
+    b, hq, d = q.shape
+    hkv = bounds.shape[1] if bounds.dim() == 4 else 0
+    pages = _check_bounds(bounds, hkv, d)
+    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
+    _check_len(kv_indptr, b + 1, "kv_indptr")
+    top_k = int(top_k)
+    if selected is None:
+        selected = torch.empty(b, hkv, max(top_k, 0), dtype=torch.int32, device=q.device)
+    else:
+        _i32(selected, "selected")
+        if tuple(selected.shape) != (b, hkv, top_k):
+            raise ValueError(f"selected is {tuple(selected.shape)}, expected {(b, hkv, top_k)}")
+    _one_device(q.device, bounds=bounds, kv_indptr=kv_indptr, kv_indices=kv_indices,
+                selected=selected, workspace=workspace)
+    n = kv_indices.numel()
+    ws = _own_workspace(workspace, select_pages_workspace_size, q.device, b, hkv, n)
+    _check(_on(
+        q.device, lib.pkx_select_pages, q.data_ptr(), bounds.data_ptr(), pages,
+        kv_indptr.data_ptr(), kv_indices.data_ptr(), n, b, hq, hkv, d, top_k, int(first_pages),
+        int(last_pages), selected.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()))
+    return selected, ws
+
+
+def _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr, kv_indices):
+    """Checks shared by the two decode forms below: (tokens, hq, hkv, lq, lv),
+    pool strides, pool format."""
+    kb, vb, fmt = _pool_rows(k_buffer, v_buffer)
+    if k_buffer.shape[:2] != v_buffer.shape[:2]:
+        raise ValueError("k_buffer and v_buffer must have the same slots and heads")
+    dims = (*k_buffer.shape, v_buffer.shape[2])
+    out = _check_fp4_attn(q, o, lse, dims)
+    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
+    _check_len(kv_indptr, out[0] + 1, "kv_indptr")
+    return out, (*kb, *vb), fmt
+
+
+def decode_pages_workspace_size(batch, hq, hkv, lq, lv, page_size, top_k) -> int:
+    return int(load_library().pkx_decode_pages_workspace_size(batch, hq, hkv, lq, lv, page_size,
+                                                              top_k))
+
+
+def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, kv_last_page_len,
+                               page_size, selected, sm_scale=None, logit_cap=0.0, lse=None,
+                               workspace=None, k_scale=1.0, v_scale=1.0):
+    """Decode attention over the selected pages of each sequence and KV head
+    (pkx_decode_attention_fwd_pages): ``selected`` int32 [B, hkv, top_k] as
+    select_pages gives, the paged format of expand_paged_kv_indices.  Writes o
+    (and lse) in place; other arguments as decode_attention_fwd.  Returns the
+    workspace."""
+    lib = load_library()
+    (b, hq, hkv, lq, lv), strides, fmt = _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr,
+                                                       kv_indices)
+    _i32(kv_last_page_len, "kv_last_page_len"), _i32(selected, "selected")
+    _check_len(kv_last_page_len, b, "kv_last_page_len")
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (b, hkv):
+        raise ValueError(f"selected is {tuple(selected.shape)}, expected [{b}, {hkv}, top_k]")
+    top_k, page_size = selected.shape[2], int(page_size)
+    _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
+                kv_indices=kv_indices, kv_last_page_len=kv_last_page_len, selected=selected,
+                lse=lse, workspace=workspace)
+    ws = _own_workspace(workspace, decode_pages_workspace_size, q.device, b, b, hq, hkv, lq, lv,
+                        page_size, top_k)
+    _check(_on(
+        q.device, lib.pkx_decode_attention_fwd_pages,
+        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_indices.numel(), kv_last_page_len.data_ptr(), page_size,
+        selected.data_ptr(), top_k, b, hq, hkv, lq, lv, *strides, k_buffer.shape[0],
+        float(sm_scale or 0.0), float(logit_cap or 0.0), fmt, float(k_scale), float(v_scale),
+        _address(lse), ws.data_ptr(), ws.numel() * ws.element_size()))
+    return ws
+
+
+def decode_shared_workspace_size(batch, num_groups, hq, hkv, lq, lv) -> int:
+    return int(load_library().pkx_decode_shared_workspace_size(batch, num_groups, hq, hkv, lq, lv))
+
+
+def decode_attention_fwd_shared(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, group_indptr,
+                                shared_lens, sm_scale=None, logit_cap=0.0, lse=None,
+                                workspace=None, k_scale=1.0, v_scale=1.0):
+    """Decode attention for sequences in groups that share a prefix, whose keys
+    are read once a group (pkx_decode_attention_fwd_shared): the sequences
+    group_indptr[g] .. group_indptr[g + 1] - 1 have their first shared_lens[g]
+    keys in common; both int32.  Other arguments as decode_attention_fwd.
+    Returns the workspace."""
+    lib = load_library()
+    (b, hq, hkv, lq, lv), strides, fmt = _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr,
+                                                       kv_indices)
+    _i32(group_indptr, "group_indptr"), _i32(shared_lens, "shared_lens")
+    groups = shared_lens.numel()
+    _check_len(group_indptr, groups + 1, "group_indptr")
+    _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
+                kv_indices=kv_indices, group_indptr=group_indptr, shared_lens=shared_lens,
+                lse=lse, workspace=workspace)
+    ws = _own_workspace(workspace, decode_shared_workspace_size, q.device, b, b, groups, hq, hkv,
+                        lq, lv)
+    _check(_on(
+        q.device, lib.pkx_decode_attention_fwd_shared,
+        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), group_indptr.data_ptr(), shared_lens.data_ptr(), groups, b, hq, hkv,
+        lq, lv, *strides, k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), fmt,
+        float(k_scale), float(v_scale), _address(lse), ws.data_ptr(),
+        ws.numel() * ws.element_size()))
     return ws
