@@ -731,7 +731,7 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
  *              256-byte aligned; pkx_workspace_status reports a candidate page
  *              outside [0, num_pages) (it ranks last) and an indptr that
  *              decreases or passes n_indices (that sequence selects nothing)
- * first_pages + last_pages <= top_k <= 8192.
+ * first_pages + last_pages <= top_k <= 4096.
  */
 size_t pkx_select_pages_workspace_size(int hkv, int64_t n_indices);
 int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
@@ -749,7 +749,7 @@ int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
  * twice.  A row without keys gets o = 0 and lse = -inf.  For (lq, lv) =
  * (64, 64) and (128, 128), bf16 and fp8 pools.
  *   n_indices  entries of kv_indices
- *   selected   int32 [batch, hkv, top_k], top_k <= 8192
+ *   selected   int32 [batch, hkv, top_k], top_k <= 4096
  *   workspace  >= pkx_decode_pages_workspace_size(...) bytes, 256-byte aligned
  * batch * hkv * top_k * page_size < 2^31.  pkx_workspace_status reports a
  * page outside the pool (its keys read as zero rows), a selected number past

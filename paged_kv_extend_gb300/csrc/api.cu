@@ -872,7 +872,7 @@ static int check_equal_heads(const char *what, int hq, int hkv, int lq, int lv) 
 }
 
 // Pages of one call: a selection fits the listing kernel's shared memory.
-constexpr int kMaxTopK = 8192;
+constexpr int kMaxTopK = 4096;
 static int check_top_k(int top_k) {
   if (top_k <= 0) return set_error(PKX_EINVAL, "top_k must be positive");
   if (top_k > kMaxTopK) return set_error(PKX_EUNSUPPORTED, "top_k %d > %d", top_k, kMaxTopK);

@@ -14,11 +14,18 @@
 //    first kernel writes its list of pool slots, and the units follow from the
 //    batch alone (equal shares of the longest list), so no scan is needed.
 //
+// One-token units (own keys, selected pages) of groups of at most 16 query
+// heads run in rows_kernel, a warp a unit: 128 rows of the tensor core would be
+// padding for them, and a unit's way through the pipeline of the tile kernel
+// (claim, query load, two tiles in flight, epilogue) takes 3 us of an SM however
+// short it is (256 sequences of 32 own keys behind a shared prefix: 2048 units,
+// 40 us).  Larger groups and the prefixes run in the tile kernel.
+//
 // Partials are fp32 (o normalised, lse in natural logs) and merged as
 //   lse = log sum_i exp(lse_i),  o = sum_i exp(lse_i - lse) o_i.
 // A unit's partial rows lie in granules of Hq / Hkv rows (one token's heads of
-// one KV head): n_tok granules a key stream, so that a one-token unit takes two
-// and not two whole tiles.
+// one KV head): n_tok granules a key stream, so that a one-token unit takes one
+// (rows_kernel) or two (the tile kernel's two streams) and not two whole tiles.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -34,9 +41,16 @@ namespace pkx {
 // mask applies.
 constexpr int kPastAll = 1 << 30;
 
+// Groups of at most this many query heads take one-token units to rows_kernel.
+constexpr int kRowsGroup = 16;
+// Keys that a one-token unit of rows_kernel is cut at, and the fewest such runs
+// it holds.
+constexpr int kRowRun = 64, kMinRuns = 2;
+constexpr int kRowsWarps = 8;  // of a CTA, one CTA an SM
+
 // Where a token's partials lie: granule a + kvh * a_head + i * a_step + s *
-// a_stream for its prefix (i < a_n splits, s < a_streams), likewise b for its own
-// keys (two streams, one granule apart).
+// a_stream for its prefix (i < a_n splits, s < a_streams), likewise b + kvh *
+// b_head + i * b_step + s for its own keys (the launch's b_head, b_step).
 struct __align__(16) ListedRow {
   int32_t a, a_n, a_head, a_step, a_streams, a_stream, b, b_n;
 };
@@ -46,7 +60,6 @@ struct ListedLayout {
       po_off, total;
   int unit_max;
   int64_t gran_max;
-  int unit_target;
 };
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -58,7 +71,7 @@ template <int D>
 __global__ void __launch_bounds__(256) listed_combine_kernel(
     const ListedRow *__restrict__ rows, const float *__restrict__ plse,
     const float *__restrict__ po, bf16 *__restrict__ o, float *__restrict__ lse, int batch, int hq,
-    int group, int b_head, int b_step, const int32_t *__restrict__ err, int n_err,
+    int group, int b_head, int b_step, int b_streams, const int32_t *__restrict__ err, int n_err,
     int32_t *status) {
   grid_dep_wait();
   grid_dep_launch();
@@ -72,15 +85,15 @@ __global__ void __launch_bounds__(256) listed_combine_kernel(
     const int t = (int)(r / hq), head = (int)(r - (int64_t)t * hq);
     const int kvh = head / group, g = head - kvh * group;
     const ListedRow R = rows[t];
-    const int na = R.a_n * R.a_streams, n = na + 2 * R.b_n;
+    const int na = R.a_n * R.a_streams, n = na + b_streams * R.b_n;
     auto row_of = [&](int i) -> int64_t {
       int64_t gr;
       if (i < na) {
         const int sp = R.a_streams == 2 ? i >> 1 : i, s = i - sp * R.a_streams;
         gr = (int64_t)R.a + (int64_t)kvh * R.a_head + (int64_t)sp * R.a_step + s * R.a_stream;
       } else {
-        const int j = i - na;
-        gr = (int64_t)R.b + (int64_t)kvh * b_head + (int64_t)(j >> 1) * b_step + (j & 1);
+        const int j = i - na, sp = b_streams == 2 ? j >> 1 : j;
+        gr = (int64_t)R.b + (int64_t)kvh * b_head + (int64_t)sp * b_step + (j - sp * b_streams);
       }
       return gr * group + g;
     };
@@ -140,22 +153,316 @@ __global__ void __launch_bounds__(256) listed_combine_kernel(
   }
 }
 
+// Fields of the header's padding: first unit, units and claim counter of rows_kernel.
+enum { kRowsFirst = 0, kRowsCount = 1, kRowsNext = 2 };
+
+// --------------------------------------------------------- one-token units
+// A warp a unit: the 16 rows of mma.sync m16n8k16 are the query heads of one KV
+// head (zero rows behind the group), 16 keys a step.
+//  * S = Q K^T: Q's fragments stay in registers; K rows come from the warp's own
+//    ring in shared memory (cp.async, 16-byte chunks in an order that spreads
+//    eight rows over the banks) as ldmatrix pairs.
+//  * The online softmax keeps one maximum a row, moved only when a logit passes it
+//    by kRowsLag (in log2), which a vote finds; P (bf16) is S's accumulator
+//    packed, already the A fragment of P V.
+//  * An fp8 row's codes become bf16 (exact) on the way into the fragments.  A lane
+//    holds four neighbouring codes of a key for K, so a step's 16 dims run in the
+//    order (4 t, 4 t + 1 | 4 t + 2, 4 t + 3) for both factors; for V two
+//    neighbouring dims of two keys, which are regrouped by bytes into the two
+//    tiles of even and of odd dims.
+// Nothing is shared between the warps: no barriers, no waits but cp.async's.
+// What bounds it: the rows' bytes; the ring holds 192 KB an SM.  A step of 8 KB
+// takes about 230 instructions, a sixth of the issue slots of the time that
+// its bytes need.
+constexpr float kRowsLag = 8.0f;
+
+template <int D, int FMT>
+struct RowsCfg {
+  static constexpr int ROW = D * (FMT == 0 ? 2 : 1);  // bytes of a K or V row
+  static constexpr int CPR = ROW / 16;                // chunks of a row
+  static constexpr int STAGE = 2 * 16 * ROW;          // 16 K rows, 16 V rows
+  static constexpr int STAGES = STAGE == 8192 ? 3 : STAGE == 4096 ? 6 : 8;
+  static constexpr int SMEM = kRowsWarps * STAGES * STAGE;
+};
+
+struct RowsParams {
+  const bf16 *q;
+  const uint8_t *k, *v;
+  int64_t k_ss, k_sh, v_ss, v_sh;  // bytes
+  int64_t num_slots;
+  const int32_t *kv_indptr, *kv_indices;
+  const WorkUnit *units;
+  WsHeader *hdr;
+  float *plse, *po;
+  int hq, group;
+  float scale_log2, cap_pre, cap_log2, v_scale;
+  int use_cap;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two fp8 codes (the low 16 bits) as two bf16.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t codes) {
+  constexpr __nv_fp8_interpretation_t kind = FMT == 1 ? __NV_E4M3 : __NV_E5M2;
+  const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), kind));
+  const float2 f = __half22float2(h);
+  return pack_bf16(f.x, f.y);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsParams p) {
+  using C = RowsCfg<D, FMT>;
+  constexpr int RP = 32 / C::CPR;  // rows of one copy instruction
+  extern __shared__ __align__(128) uint8_t smem[];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
+  // chunk c of row r in a stage: c ^ r % 8 (rows of 64 bytes: two to a line)
+  auto spread = [](int r, int c) { return C::CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); };
+  const int first = p.hdr->pad[kRowsFirst], count = p.hdr->pad[kRowsCount];
+  const int warps = gridDim.x * kRowsWarps;
+  bool bad = false;
+  // the first unit by the warp's number (neighbouring units, which share a
+  // sequence's slots, on different SMs), the others claimed
+  for (int u = warp * gridDim.x + blockIdx.x; u < count;) {
+    const WorkUnit w = p.units[first + u];
+    const int n = w.k_end - w.k_begin, steps = (n + 15) / 16;
+    const int32_t *idx = p.kv_indices + __ldg(p.kv_indptr + w.b) + w.k_begin;
+    const int row = lane / C::CPR, chunk = lane % C::CPR;  // of this lane's copies
+    const uint8_t *kp = p.k + w.kvh * p.k_sh + chunk * 16, *vp = p.v + w.kvh * p.v_sh + chunk * 16;
+    // slots of 32 keys at a time, one block ahead: `slots` of the block that the
+    // copies are in, `coming` of the next
+    auto fetch = [&](int block) {
+      const int i = block * 32 + lane;
+      return i < n ? __ldg(idx + i) : -1;
+    };
+    int slots = fetch(0), coming = fetch(1);
+    auto checked = [&](int s, int block) {
+      if ((uint32_t)s >= (uint64_t)p.num_slots) {
+        bad |= block * 32 + lane < n;
+        return -1;
+      }
+      return s;
+    };
+    slots = checked(slots, 0);
+    auto issue = [&](int step) {
+      if (step < steps) {
+        if ((step & 1) == 0 && step > 0) {
+          slots = checked(coming, step >> 1);
+          coming = fetch((step >> 1) + 1);
+        }
+        const uint32_t stage = ring + (step % C::STAGES) * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < 16 / RP; ++i) {
+          const int r = i * RP + row;
+          const int s = __shfl_sync(0xffffffffu, slots, (step & 1) * 16 + r);
+          const uint32_t at = stage + r * C::ROW + spread(r, chunk) * 16;
+          const int64_t s0 = max(s, 0);
+          cp_async_16(at, kp + s0 * p.k_ss, s >= 0 ? 16u : 0u);
+          cp_async_16(at + 16 * C::ROW, vp + s0 * p.v_ss, s >= 0 ? 16u : 0u);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) issue(s);
+    // Q's fragments: rows g and g + 8
+    uint32_t qa[D / 16][4];
+    {
+      const uint32_t *q0 = reinterpret_cast<const uint32_t *>(
+          p.q + ((int64_t)w.q_tok0 * p.hq + (int64_t)w.kvh * p.group + g) * D);
+      const uint32_t *q1 = q0 + 8 * (D / 2);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const int lo = s * 8 + (FMT == 0 ? t : 2 * t), hi = s * 8 + (FMT == 0 ? t + 4 : 2 * t + 1);
+        qa[s][0] = g < p.group ? __ldg(q0 + lo) : 0u;
+        qa[s][1] = g + 8 < p.group ? __ldg(q1 + lo) : 0u;
+        qa[s][2] = g < p.group ? __ldg(q0 + hi) : 0u;
+        qa[s][3] = g + 8 < p.group ? __ldg(q1 + hi) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int mr = lane & 7, mi = lane >> 3;  // row and matrix of this lane's ldmatrix address
+    for (int step = 0; step < steps; ++step) {
+      cp_async_wait_group<C::STAGES - 2>();
+      __syncwarp();  // the step's rows are here, and all lanes are done with the step before
+      issue(step + C::STAGES - 1);
+      const uint32_t sk = ring + (step % C::STAGES) * C::STAGE, sv = sk + 16 * C::ROW;
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0-7, 8-15
+      if constexpr (FMT == 0) {
+        const int r = (mi >> 1) * 8 + mr;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          uint32_t b[4];
+          ldmatrix4(b, sk + r * C::ROW + spread(r, 2 * s + (mi & 1)) * 16);
+          mma_bf16(s0, qa[s], b[0], b[1]);
+          mma_bf16(s1, qa[s], b[2], b[3]);
+        }
+      } else {
+        const int r = (mi & 1) * 8 + mr;
+#pragma unroll
+        for (int s = 0; s < D / 16; s += 2) {
+          uint32_t b[4];
+          ldmatrix4(b, sk + r * C::ROW + spread(r, s + (mi >> 1)) * 16);
+          mma_bf16(s0, qa[s], fp8x2_to_bf16x2<FMT>(b[0] & 0xFFFFu), fp8x2_to_bf16x2<FMT>(b[0] >> 16));
+          mma_bf16(s1, qa[s], fp8x2_to_bf16x2<FMT>(b[1] & 0xFFFFu), fp8x2_to_bf16x2<FMT>(b[1] >> 16));
+          mma_bf16(s0, qa[s + 1], fp8x2_to_bf16x2<FMT>(b[2] & 0xFFFFu),
+                   fp8x2_to_bf16x2<FMT>(b[2] >> 16));
+          mma_bf16(s1, qa[s + 1], fp8x2_to_bf16x2<FMT>(b[3] & 0xFFFFu),
+                   fp8x2_to_bf16x2<FMT>(b[3] >> 16));
+        }
+      }
+      // logits in log2; keys behind the unit's last are -inf
+      float x[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = p.use_cap ? p.cap_log2 * tanh_approx(x[i] * p.cap_pre) : x[i] * p.scale_log2;
+      if (step * 16 + 16 > n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (step * 16 + ((i >> 1) & 1) * 8 + 2 * t + (i & 1) >= n) x[i] = -INFINITY;
+      }
+      float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      float t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+      if (__any_sync(0xffffffffu, t0 > m0 + kRowsLag || t1 > m1 + kRowsLag)) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+        const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+        // (an old maximum of -inf goes with sums of 0)
+        const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0);
+        const float a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= a0;
+          o[j][1] *= a0;
+          o[j][2] *= a1;
+          o[j][3] *= a1;
+        }
+      }
+      const float c0 = m0 == -INFINITY ? 0.f : m0, c1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = ex2_approx(x[i] - c0);
+        x[4 + i] = ex2_approx(x[4 + i] - c1);
+        l0 += x[i];
+        l1 += x[4 + i];
+      }
+      const uint32_t pa[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[4], x[5]), pack_bf16(x[2], x[3]),
+                              pack_bf16(x[6], x[7])};
+      const int r = (mi & 1) * 8 + mr;
+      if constexpr (FMT == 0) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, sv + r * C::ROW + spread(r, 2 * j + (mi >> 1)) * 16);
+          mma_bf16(o[2 * j], pa, b[0], b[1]);
+          mma_bf16(o[2 * j + 1], pa, b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, sv + r * C::ROW + spread(r, j + (mi >> 1)) * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // bytes: (key, dims 2 g and 2 g + 1), (next key, the same dims)
+            const uint32_t x0 = __byte_perm(b[2 * i], 0u, 0x3120);
+            const uint32_t x1 = __byte_perm(b[2 * i + 1], 0u, 0x3120);
+            mma_bf16(o[2 * (j + i)], pa, fp8x2_to_bf16x2<FMT>(x0 & 0xFFFFu),
+                     fp8x2_to_bf16x2<FMT>(x1 & 0xFFFFu));
+            mma_bf16(o[2 * (j + i) + 1], pa, fp8x2_to_bf16x2<FMT>(x0 >> 16),
+                     fp8x2_to_bf16x2<FMT>(x1 >> 16));
+          }
+        }
+      }
+    }
+    __syncwarp();  // the ring is free
+    // the partial: o / l and lse of rows g and g + 8
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int head = g + 8 * half;
+      if (head >= p.group) continue;
+      const float l = half ? l1 : l0, m = half ? m1 : m0;
+      const float inv = (l == 0.f ? 0.f : 1.0f / l) * p.v_scale;
+      const int64_t out = (int64_t)w.slot * p.group + head;
+      float *dst = p.po + out * D;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const float e0 = o[2 * j][2 * half] * inv, e1 = o[2 * j][2 * half + 1] * inv;
+        const float f0 = o[2 * j + 1][2 * half] * inv, f1 = o[2 * j + 1][2 * half + 1] * inv;
+        if constexpr (FMT == 0) {
+          *reinterpret_cast<float2 *>(dst + 16 * j + 2 * t) = make_float2(e0, e1);
+          *reinterpret_cast<float2 *>(dst + 16 * j + 8 + 2 * t) = make_float2(f0, f1);
+        } else {  // tiles of even and of odd dims
+          *reinterpret_cast<float4 *>(dst + 16 * j + 4 * t) = make_float4(e0, f0, e1, f1);
+        }
+      }
+      if (t == 0)
+        p.plse[out] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+    }
+    int next = 0;
+    if (lane == 0) next = atomicAdd(&p.hdr->pad[kRowsNext], 1);
+    u = warps + __shfl_sync(0xffffffffu, next, 0);
+  }
+  if (bad) record_status(&p.hdr->status, PKX_EDEVICE);
+  cp_async_wait_all();
+}
+
 // --------------------------------------------------------- shared prefixes
 struct SharedParams {
   const int32_t *kv_indptr, *group_indptr, *shared_lens;
   int batch, num_groups, hkv;
   int tok;          // tokens of a query tile
-  int target;       // units wanted
+  int sms;
+  int own_run;      // keys that own keys are cut at
+  int own_least;    // fewest such runs of a unit
+  int own_target;   // units of own keys wanted
+  int own_gran;     // granules of one
+  int rows;         // own keys go to rows_kernel
   int unit_max;
   int64_t gran_max;
   int32_t *seq;     // [3][batch + 1]: keys, shared keys, first unit of own keys
-  int32_t *grp;     // [3][num_groups + 1]: shared keys, first unit, first granule
+  int32_t *grp;     // [4][num_groups + 1]: shared keys, first sequence, first unit, first granule
+  int in_smem;      // those arrays in dynamic shared memory instead
   WorkUnit *units;
   int32_t *order;
-  ListedRow *rows;
+  ListedRow *rows_out;
   WsHeader *hdr;
 };
-
 // Exclusive sum over a block of 1024 threads of one value each, and the total.
 __device__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -181,17 +488,24 @@ __device__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
 // One CTA of 1024 threads: the units of every group's prefix and of every
 // sequence's own keys.  A group shares min(shared_lens, the shortest of its
 // sequences) keys, nothing if that is less than a tile of keys or if it has one
-// sequence.  Key ranges are cut into equal pieces of at most C tiles, C chosen
-// for about `target` units.
+// sequence.  A prefix is cut into equal pieces of at most C tiles.  The units
+// are few and long, so C is the one of up to 64 candidates (the longest prefix
+// in 1, 2, ... pieces) whose rounds over the SMs take least, a unit counting
+// C + kUnitTiles tiles (its query load, pipeline fill and partials).  Own keys
+// are cut for a given number of units.
+constexpr int kUnitTiles = 3;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {
+  extern __shared__ int32_t s_dyn[];
   __shared__ int64_t sh[32];
-  __shared__ int s_bad;
+  __shared__ int64_t s_best[32];
+  __shared__ int s_bad, s_longest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.batch, NG = p.num_groups;
-  int32_t *sT = p.seq, *sS = p.seq + (B + 1), *sU = p.seq + 2 * (B + 1);
-  int32_t *gS = p.grp, *gU = p.grp + (NG + 1), *gG = p.grp + 2 * (NG + 1);
+  int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + 3 * (B + 1) : p.grp;
+  int32_t *sT = seq, *sS = seq + (B + 1), *sU = seq + 2 * (B + 1);
+  int32_t *gS = grp, *gB = grp + (NG + 1), *gU = grp + 2 * (NG + 1), *gG = grp + 3 * (NG + 1);
   const int blk = 2 * p.tok;  // tokens of a prefix unit
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_longest = 0;
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
@@ -206,92 +520,121 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   }
   // groups: consecutive runs of sequences, else nothing is shared
   bool bad_groups = false;
-  for (int g = tid; g < NG; g += 1024) {
-    const int lo = p.group_indptr[g], hi = p.group_indptr[g + 1];
-    bad_groups |= lo < 0 || hi < lo || hi > B || p.shared_lens[g] < 0;
+  for (int g = tid; g <= NG && NG > 0; g += 1024) {
+    const int lo = p.group_indptr[g], hi = g < NG ? p.group_indptr[g + 1] : lo;
+    const int s = g < NG ? p.shared_lens[g] : 0;
+    bad_groups |= lo < 0 || hi < lo || hi > B || s < 0;
+    gB[g] = lo;
+    gS[g] = s;
   }
   if (bad_groups) s_bad = 1;
   bad |= bad_groups;
   if (tid == 0) {
     p.hdr->status = 0;
     p.hdr->next_unit = 0;
+    p.hdr->pad[kRowsNext] = 0;
   }
   __syncthreads();
   if (bad) record_status(&p.hdr->status, PKX_EDEVICE);
   const bool share = s_bad == 0;
+  auto tiles = [](int keys) { return keys / kBlockN + (keys % kBlockN != 0); };
   // shared keys of each group (a warp each)
   for (int g = warp; g < NG; g += 32) {
     int S = 0;
     if (share) {
-      const int lo = p.group_indptr[g], hi = p.group_indptr[g + 1];
-      int least = p.shared_lens[g];
+      const int lo = gB[g], hi = gB[g + 1];
+      int least = gS[g];
       for (int b = lo + lane; b < hi; b += 32) least = min(least, sT[b]);
       least = __reduce_min_sync(0xffffffffu, least);
       if (hi - lo >= 2 && least >= kBlockN) S = least;
       for (int b = lo + lane; b < hi; b += 32) sS[b] = S;
     }
-    if (lane == 0) gS[g] = S;
+    __syncwarp();
+    if (lane == 0) {
+      gS[g] = S;
+      atomicMax(&s_longest, tiles(S));
+    }
   }
   __syncthreads();
-  // size of a piece
-  auto tiles = [](int keys) { return keys / kBlockN + (keys % kBlockN != 0); };
-  auto group_blocks = [&](int g) {
-    return gS[g] > 0 ? (p.group_indptr[g + 1] - p.group_indptr[g] + blk - 1) / blk : 0;
+  auto runs = [&](int b) {
+    const int n = sT[b] - sS[b];
+    return n / p.own_run + (n % p.own_run != 0);
   };
-  int64_t cost = 0;
-  for (int b = tid; b < B; b += 1024) cost += tiles(sT[b] - sS[b]);
-  for (int g = tid; g < NG; g += 1024) cost += (int64_t)group_blocks(g) * tiles(gS[g]);
-  int64_t all_cost;
-  block_sum_before(cost, sh, all_cost);
-  const int64_t c64 = (all_cost * p.hkv + p.target - 1) / p.target;
-  const int C = (int)max(c64, (int64_t)kMinSplitTiles);
-  auto pieces = [&](int nt) { return (nt + C - 1) / C; };
+  auto group_blocks = [&](int g) { return gS[g] > 0 ? (gB[g + 1] - gB[g] + blk - 1) / blk : 0; };
   // granules of a group's piece (all its blocks, one KV head): two streams of
   // partials where the block is one tile of rows
   auto group_granules = [&](int g) {
-    const int nb = group_blocks(g);
-    const int last = p.group_indptr[g + 1] - p.group_indptr[g] - (nb - 1) * blk;
+    const int nb = group_blocks(g), last = gB[g + 1] - gB[g] - (nb - 1) * blk;
     return (nb - 1) * blk + (last <= p.tok ? 2 * last : last);
   };
-  // first unit and granule of each group, first unit of each sequence
-  const int gc = (NG + 1023) / 1024, g0 = min(NG, tid * gc), g1 = min(NG, g0 + gc);
-  int64_t nu = 0, ng = 0;
-  for (int g = g0; g < g1; ++g) {
-    if (gS[g] <= 0) continue;
-    const int s = pieces(tiles(gS[g]));
-    nu += (int64_t)s * group_blocks(g) * p.hkv;
-    ng += (int64_t)s * p.hkv * group_granules(g);
+  int64_t cost = 0, own = 0, all_cost, all_own;
+  for (int b = tid; b < B; b += 1024) own += runs(b);
+  for (int g = tid; g < NG; g += 1024) cost += (int64_t)group_blocks(g) * tiles(gS[g]);
+  block_sum_before(own, sh, all_own);
+  const int R = (int)max((all_own * p.hkv + p.own_target - 1) / p.own_target, (int64_t)p.own_least);
+  auto own_pieces = [&](int b) { return (runs(b) + R - 1) / R; };
+  int C = 1;
+  int64_t pre_units = 0, pre_gran = 0;
+  if (s_longest > 0) {
+    block_sum_before(cost, sh, all_cost);
+    // (at most four units an SM and one more a block)
+    const int least = (int)max((all_cost * p.hkv + 4 * p.sms - 1) / (4 * p.sms), (int64_t)kMinSplitTiles);
+    int64_t best = INT64_MAX;
+    for (int j = warp + 1; j <= 64; j += 32) {
+      const int c = max((s_longest + j - 1) / j, least);
+      int64_t n = 0;
+      for (int g = lane; g < NG; g += 32)
+        n += (int64_t)group_blocks(g) * ((tiles(gS[g]) + c - 1) / c);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      const int64_t rounds = (n * p.hkv + p.sms - 1) / p.sms;
+      best = min(best, (rounds * (c + kUnitTiles) << 24) + min(c, (1 << 24) - 1));
+    }
+    if (lane == 0) s_best[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < 32; ++w) best = min(best, s_best[w]);
+    C = (int)(best & ((1 << 24) - 1));
   }
-  int64_t pre_units, pre_gran, own_units;
-  nu = block_sum_before(nu, sh, pre_units);
-  ng = block_sum_before(ng, sh, pre_gran);
+  auto pieces = [&](int g) { return (tiles(gS[g]) + C - 1) / C; };
+  // first unit and granule of each group, first unit of each sequence
+  if (s_longest > 0) {
+    const int gc = (NG + 1023) / 1024, g0 = min(NG, tid * gc), g1 = min(NG, g0 + gc);
+    int64_t nu = 0, ng = 0;
+    for (int g = g0; g < g1; ++g) {
+      if (gS[g] <= 0) continue;
+      nu += (int64_t)pieces(g) * group_blocks(g) * p.hkv;
+      ng += (int64_t)pieces(g) * p.hkv * group_granules(g);
+    }
+    nu = block_sum_before(nu, sh, pre_units);
+    ng = block_sum_before(ng, sh, pre_gran);
+    for (int g = g0; g < g1; ++g) {
+      gU[g] = (int)min(nu, (int64_t)INT_MAX);
+      gG[g] = (int)min(ng, (int64_t)INT_MAX);
+      if (gS[g] <= 0) continue;
+      nu += (int64_t)pieces(g) * group_blocks(g) * p.hkv;
+      ng += (int64_t)pieces(g) * p.hkv * group_granules(g);
+    }
+  }
   const int bc = (B + 1023) / 1024, b0 = min(B, tid * bc), b1 = min(B, b0 + bc);
-  int64_t bu = 0;
-  for (int b = b0; b < b1; ++b) bu += pieces(tiles(sT[b] - sS[b]));
+  int64_t bu = 0, own_units;
+  for (int b = b0; b < b1; ++b) bu += own_pieces(b);
   bu = block_sum_before(bu, sh, own_units);
   own_units *= p.hkv;
   // (cannot be false: the workspace is sized for the largest counts)
   const bool fits = pre_units + own_units <= p.unit_max &&
-                    pre_gran + 2 * own_units <= p.gran_max;
+                    pre_gran + p.own_gran * own_units <= p.gran_max;
   if (!fits) {
     if (tid == 0) {
       record_status(&p.hdr->status, PKX_EDEVICE);
       p.hdr->n_units = 0;
+      p.hdr->pad[kRowsCount] = 0;
     }
-    for (int b = tid; b < B; b += 1024) p.rows[b] = ListedRow{};
+    for (int b = tid; b < B; b += 1024) p.rows_out[b] = ListedRow{};
     return;
-  }
-  for (int g = g0; g < g1; ++g) {
-    gU[g] = (int)nu;
-    gG[g] = (int)ng;
-    if (gS[g] <= 0) continue;
-    const int s = pieces(tiles(gS[g]));
-    nu += (int64_t)s * group_blocks(g) * p.hkv;
-    ng += (int64_t)s * p.hkv * group_granules(g);
   }
   for (int b = b0; b < b1; ++b) {
     sU[b] = (int)bu;
-    bu += pieces(tiles(sT[b] - sS[b]));
+    bu += own_pieces(b);
   }
   __syncthreads();
   // units of the prefixes: group, piece, KV head, block (blocks of one piece
@@ -303,12 +646,12 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       if (gU[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
-    const int g = lo, nb = group_blocks(g), nt = tiles(gS[g]), S = pieces(nt);
+    const int g = lo, nb = group_blocks(g), nt = tiles(gS[g]), S = pieces(g);
     int r = u - gU[g];
     const int k = r % nb;
     r /= nb;
     const int kvh = r % p.hkv, sp = r / p.hkv;
-    const int first = p.group_indptr[g], n = p.group_indptr[g + 1] - first;
+    const int first = gB[g], n = gB[g + 1] - first;
     WorkUnit w;
     w.q_tok0 = first + k * blk;
     w.n_tok = min(blk, n - k * blk);
@@ -333,65 +676,82 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       if (sU[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    const int b = lo, nt = tiles(sT[b] - sS[b]), S = pieces(nt), sp = x - sU[b];
+    const int b = lo, nr = runs(b), S = own_pieces(b), sp = x - sU[b];
     WorkUnit w;
     w.q_tok0 = b;
     w.n_tok = 1;
     w.qpos0 = kPastAll;
     w.kvh = kvh;
-    w.k_begin = (int)min((int64_t)sT[b], sS[b] + (int64_t)sp * nt / S * kBlockN);
-    w.k_end = (int)min((int64_t)sT[b], sS[b] + (int64_t)(sp + 1) * nt / S * kBlockN);
+    w.k_begin = (int)min((int64_t)sT[b], sS[b] + (int64_t)sp * nr / S * p.own_run);
+    w.k_end = (int)min((int64_t)sT[b], sS[b] + (int64_t)(sp + 1) * nr / S * p.own_run);
     w.k_split = INT_MAX;
     w.n_tiles = tiles(w.k_end - w.k_begin);
     w.b = b;
-    w.slot = (int)pre_gran + 2 * i;
+    w.slot = (int)pre_gran + p.own_gran * i;
     w.dq = w.claim = 0;
     p.units[(int)pre_units + i] = w;
     p.order[(int)pre_units + i] = (int)pre_units + i;
   }
   // where each token's partials lie
   for (int b = tid; b < B; b += 1024) {
-    ListedRow R{};
+    ListedRow r{};
     if (sS[b] > 0) {
-      int lo = 0, hi = NG - 1;  // last g with group_indptr[g] <= b
+      int lo = 0, hi = NG - 1;  // last g with gB[g] <= b
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.group_indptr[mid] <= b) lo = mid;
+        if (gB[mid] <= b) lo = mid;
         else hi = mid - 1;
       }
-      const int g = lo, i = b - p.group_indptr[g], k = i / blk;
-      const int n_tok = min(blk, p.group_indptr[g + 1] - p.group_indptr[g] - k * blk);
-      R.a = gG[g] + i;
-      R.a_n = pieces(tiles(gS[g]));
-      R.a_head = group_granules(g);
-      R.a_step = p.hkv * R.a_head;
-      R.a_streams = n_tok <= p.tok ? 2 : 1;
-      R.a_stream = n_tok;
+      const int g = lo, i = b - gB[g], k = i / blk;
+      const int n_tok = min(blk, gB[g + 1] - gB[g] - k * blk);
+      r.a = gG[g] + i;
+      r.a_n = pieces(g);
+      r.a_head = group_granules(g);
+      r.a_step = p.hkv * r.a_head;
+      r.a_streams = n_tok <= p.tok ? 2 : 1;
+      r.a_stream = n_tok;
     }
-    R.b = (int)pre_gran + 2 * sU[b] * p.hkv;
-    R.b_n = pieces(tiles(sT[b] - sS[b]));
-    p.rows[b] = R;
+    r.b = (int)pre_gran + p.own_gran * sU[b] * p.hkv;
+    r.b_n = own_pieces(b);
+    p.rows_out[b] = r;
   }
-  if (tid == 0) p.hdr->n_units = (int)(pre_units + own_units);
+  if (tid == 0) {
+    p.hdr->n_units = (int)(p.rows ? pre_units : pre_units + own_units);
+    p.hdr->pad[kRowsFirst] = (int)pre_units;
+    p.hdr->pad[kRowsCount] = (int)(p.rows ? own_units : 0);
+  }
+}
+
+// Units of own keys wanted, the keys they are cut at, the fewest of those runs,
+// and granules of a unit: three for each warp of rows_kernel, or three tile
+// units an SM.
+struct OwnUnits {
+  int target, run, least, gran;
+};
+static OwnUnits own_units(int group, int num_sms) {
+  const int n = num_sms > 0 ? num_sms : 160;
+  return group <= kRowsGroup ? OwnUnits{3 * kRowsWarps * n, kRowRun, kMinRuns, 1}
+                             : OwnUnits{3 * n, kBlockN, kMinSplitTiles, 2};
 }
 
 static ListedLayout shared_layout(int batch, int num_groups, int hkv, int group, int d,
                                   int num_sms) {
   ListedLayout L{};
   const int tok = tokens_per_block(group), blk = 2 * tok;
-  L.unit_target = 3 * (num_sms > 0 ? num_sms : 160);
+  const int n = num_sms > 0 ? num_sms : 160;
+  const OwnUnits own = own_units(group, num_sms);
   // blocks: at most one partly filled a group (of two sequences or more)
   const int64_t blocks = batch / blk + std::min(num_groups, batch / 2);
-  const int64_t units = L.unit_target + (int64_t)hkv * (blocks + batch);
+  const int64_t units = 4ll * n + own.target + (int64_t)hkv * (blocks + batch);
   L.unit_max = (int)std::min<int64_t>(units, INT_MAX / 4);
-  // a prefix unit has at most blk granules, and a block's first piece twice
-  // its tokens; a unit of own keys has two
-  L.gran_max = (int64_t)L.unit_target * (blk + 2) + 4 * (int64_t)hkv * batch;
+  // four prefix units an SM of blk granules and, a block's first piece, twice
+  // its tokens; the units of own keys
+  L.gran_max = 4ll * n * blk + 2ll * hkv * batch + own.gran * (own.target + (int64_t)hkv * batch);
   size_t off = up256(sizeof(WsHeader));
   L.seq_off = off;
   off = up256(off + sizeof(int32_t) * 3 * (size_t)(batch + 1));
   L.grp_off = off;
-  off = up256(off + sizeof(int32_t) * 3 * (size_t)(num_groups + 1));
+  off = up256(off + sizeof(int32_t) * 4 * (size_t)(num_groups + 1));
   L.units_off = off;
   off = up256(off + sizeof(WorkUnit) * (size_t)L.unit_max);
   L.order_off = off;
@@ -416,13 +776,16 @@ struct PagesParams {
   int64_t n_indices, num_slots;
   int batch, hkv, page_size, top_k;
   int pieces;      // units of a (sequence, KV head)
+  int run;         // keys they are cut at
+  int gran;        // granules of one
+  int rows;        // they go to rows_kernel
   int cap;         // keys of its list: top_k * page_size
   int32_t *slots;  // [batch * hkv][cap]
   int32_t *ptr;    // [batch * hkv] first key of each list
   int32_t *err;    // [batch * hkv]
   WorkUnit *units;
   int32_t *order;
-  ListedRow *rows;
+  ListedRow *rows_out;
   WsHeader *hdr;
 };
 
@@ -430,6 +793,7 @@ struct PagesParams {
 // one after another, and its units (equal shares of the list).
 __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
   extern __shared__ int s_first[];  // [top_k + 1] first key of each entry
+  int *s_slot = s_first + p.top_k + 1;  // [top_k] its first pool slot, or -1
   __shared__ int s_warp[8];
   __shared__ int s_run, s_bad;
   grid_dep_wait();
@@ -448,14 +812,22 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     s_bad = 0;
   }
   __syncthreads();
-  // first key of each entry: a running sum of the entries' lengths
+  // first key of each entry (a running sum of the entries' lengths) and its
+  // page's first slot
+  const int64_t pages = p.num_slots / p.page_size;
   for (int e0 = 0; e0 < p.top_k; e0 += 256) {
     const int e = e0 + tid;
     int len = 0;
     if (e < p.top_k) {
       const int s = sel[e];
       bad |= s >= n;
-      if (s >= 0 && s < n) len = s == n - 1 ? min(max(last, 0), p.page_size) : p.page_size;
+      int slot = -1;
+      if (s >= 0 && s < n) {
+        const int page = __ldg(p.kv_indices + at + s);
+        if (page >= 0 && page < pages) slot = page * p.page_size;
+        len = s == n - 1 ? min(max(last, 0), p.page_size) : p.page_size;
+      }
+      s_slot[e] = slot;
     }
     int x = len;
 #pragma unroll
@@ -482,16 +854,19 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     if (pair == 0) {
       p.hdr->status = 0;
       p.hdr->next_unit = 0;
-      p.hdr->n_units = gridDim.x * p.pieces;
+      p.hdr->n_units = p.rows ? 0 : gridDim.x * p.pieces;
+      p.hdr->pad[kRowsFirst] = 0;
+      p.hdr->pad[kRowsCount] = p.rows ? gridDim.x * p.pieces : 0;
+      p.hdr->pad[kRowsNext] = 0;
     }
     if (kvh == 0) {
       ListedRow R{};
-      R.b = pair * p.pieces * 2;
+      R.b = pair * p.pieces * p.gran;
       R.b_n = p.pieces;
-      p.rows[b] = R;
+      p.rows_out[b] = R;
     }
   }
-  const int nt = (keys + kBlockN - 1) / kBlockN;
+  const int nt = (keys + p.run - 1) / p.run;
   for (int s = tid; s < p.pieces; s += 256) {
     const int u = pair * p.pieces + s;
     WorkUnit w;
@@ -499,44 +874,42 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     w.n_tok = 1;
     w.qpos0 = kPastAll;
     w.kvh = kvh;
-    w.k_begin = (int)min((int64_t)keys, (int64_t)s * nt / p.pieces * kBlockN);
-    w.k_end = (int)min((int64_t)keys, (int64_t)(s + 1) * nt / p.pieces * kBlockN);
+    w.k_begin = (int)min((int64_t)keys, (int64_t)s * nt / p.pieces * p.run);
+    w.k_end = (int)min((int64_t)keys, (int64_t)(s + 1) * nt / p.pieces * p.run);
     w.k_split = INT_MAX;
     w.n_tiles = (w.k_end - w.k_begin + kBlockN - 1) / kBlockN;
     w.b = pair;
-    w.slot = 2 * u;
+    w.slot = p.gran * u;
     w.dq = w.claim = 0;
     p.units[u] = w;
     p.order[u] = u;
   }
-  // the slots; a page outside the pool is listed as -1, which the attention
-  // kernel reads as a zero row and reports
+  // the slots, a warp an entry; a page outside the pool is listed as -1, which
+  // the attention kernel reads as a zero row and reports
   int32_t *out = p.slots + (int64_t)pair * p.cap;
-  const int64_t pages = p.num_slots / p.page_size;
-  for (int i = tid; i < p.top_k * p.page_size; i += 256) {
-    const int e = i / p.page_size, j = i - e * p.page_size;
-    if (j >= s_first[e + 1] - s_first[e]) continue;
-    const int page = __ldg(p.kv_indices + at + sel[e]);
-    out[s_first[e] + j] = page >= 0 && page < pages ? page * p.page_size + j : -1;
+  for (int e = warp; e < p.top_k; e += 8) {
+    const int first = s_first[e], len = s_first[e + 1] - first, slot = s_slot[e];
+    for (int i = lane; i < len; i += 32) out[first + i] = slot < 0 ? -1 : slot + i;
   }
 }
 
-// Units of a (sequence, KV head): at least kMinSplitTiles tiles each, and no
-// more than make four units an SM.
-static int pages_pieces(int batch, int hkv, int page_size, int top_k, int num_sms) {
-  const int64_t nt = ((int64_t)top_k * page_size + kBlockN - 1) / kBlockN;
-  const int64_t pairs = (int64_t)batch * hkv;
-  const int64_t want = (4ll * (num_sms > 0 ? num_sms : 160) + pairs - 1) / std::max<int64_t>(pairs, 1);
-  return (int)std::max<int64_t>(1, std::min(want, nt / kMinSplitTiles));
+// Units of a (sequence, KV head): as many as own_units() wants, of at least its
+// fewest runs.
+static int pages_pieces(int batch, int hkv, int group, int page_size, int top_k, int num_sms) {
+  const OwnUnits own = own_units(group, num_sms);
+  const int64_t nr = ((int64_t)top_k * page_size + own.run - 1) / own.run;
+  const int64_t pairs = std::max<int64_t>((int64_t)batch * hkv, 1);
+  const int64_t want = (own.target + pairs - 1) / pairs;
+  return (int)std::max<int64_t>(1, std::min(want, nr / own.least));
 }
 
 static ListedLayout pages_layout(int batch, int hkv, int group, int d, int page_size, int top_k,
                                  int num_sms) {
   ListedLayout L{};
   const int64_t pairs = (int64_t)batch * hkv;
-  const int64_t units = pairs * pages_pieces(batch, hkv, page_size, top_k, num_sms);
+  const int64_t units = pairs * pages_pieces(batch, hkv, group, page_size, top_k, num_sms);
   L.unit_max = (int)std::min<int64_t>(units, INT_MAX / 4);
-  L.gran_max = 2 * units;
+  L.gran_max = own_units(group, num_sms).gran * units;
   size_t off = up256(sizeof(WsHeader));
   L.units_off = off;
   off = up256(off + sizeof(WorkUnit) * (size_t)units);
@@ -581,10 +954,60 @@ static int launch_listed(int fmt, const ListedMaps &tm, const KParams &kp, int g
   return launch_attn_kernel<D, kListed>(tm, kp, grid, s);
 }
 
-// The attention kernel and the combine over the units in the workspace.
+template <int D, int FMT>
+static int launch_rows_as(const RowsParams &p, int nsm, cudaStream_t s) {
+  static PerDevice configured;
+  if (needs_config(configured)) {
+    cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, FMT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         RowsCfg<D, FMT>::SMEM);
+    if (e != cudaSuccess)
+      return set_error(PKX_ECUDA, "cudaFuncSetAttribute(rows_kernel): %s", cudaGetErrorString(e));
+    mark_configured(configured);
+  }
+  cudaError_t e = launch_pdl(rows_kernel<D, FMT>, dim3(nsm), dim3(kRowsWarps * 32),
+                             RowsCfg<D, FMT>::SMEM, s, p);
+  if (e != cudaSuccess) return set_error(PKX_ECUDA, "rows_kernel launch: %s", cudaGetErrorString(e));
+  return PKX_OK;
+}
+
+template <int D>
+static int launch_rows(const ListedArgs &a, const KParams &kp, int nsm) {
+  const int size = a.kv_fmt == kKvBf16 ? 2 : 1;
+  RowsParams p;
+  p.q = kp.q;
+  p.k = static_cast<const uint8_t *>(a.k_buf);
+  p.v = static_cast<const uint8_t *>(a.v_buf);
+  p.k_ss = a.kb_ss * size;
+  p.k_sh = a.kb_sh * size;
+  p.v_ss = a.vb_ss * size;
+  p.v_sh = a.vb_sh * size;
+  p.num_slots = a.num_slots;
+  p.kv_indptr = kp.kv_indptr;
+  p.kv_indices = static_cast<const int32_t *>(kp.kv_indices);
+  p.units = kp.units;
+  p.hdr = static_cast<WsHeader *>(a.workspace);
+  p.plse = kp.plse;
+  p.po = kp.po;
+  p.hq = a.hq;
+  p.group = kp.group;
+  const bool fp8 = a.kv_fmt != kKvBf16;
+  p.use_cap = kp.use_cap;
+  p.scale_log2 = fp8 ? kp.scale_log2_k : kp.scale_log2;
+  p.cap_pre = fp8 ? kp.cap_pre_k : kp.cap_pre;
+  p.cap_log2 = kp.cap_log2;
+  p.v_scale = fp8 ? a.v_scale : 1.0f;
+  if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1>(p, nsm, a.stream);
+  if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2>(p, nsm, a.stream);
+  return launch_rows_as<D, 0>(p, nsm, a.stream);
+}
+
+// The attention kernels and the combine over the units in the workspace: the
+// tile kernel where there may be units for it, rows_kernel for groups of at
+// most kRowsGroup heads.
 static int run_listed(const ListedArgs &a, const ListedMaps &tm, const ListedLayout &L, int nsm,
-                      const int32_t *kv_indptr, const int32_t *kv_indices, int b_head, int b_step,
-                      const int32_t *err, int n_err) {
+                      const int32_t *kv_indptr, const int32_t *kv_indices, bool tile_units,
+                      int b_head, int b_step, const int32_t *err, int n_err) {
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
   const int group = a.hq / a.hkv;
@@ -629,16 +1052,23 @@ static int run_listed(const ListedArgs &a, const ListedMaps &tm, const ListedLay
   cudaEvent_t ev_before = nullptr, ev_after = nullptr;
   attention_events(&ev_before, &ev_after);
   if (ev_before) cudaEventRecord(ev_before, a.stream);
-  const int rc = a.d == 128 ? launch_listed<128>(a.kv_fmt, tm, kp, nsm, a.stream)
-                            : launch_listed<64>(a.kv_fmt, tm, kp, nsm, a.stream);
+  int rc = PKX_OK;
+  if (tile_units)
+    rc = a.d == 128 ? launch_listed<128>(a.kv_fmt, tm, kp, nsm, a.stream)
+                    : launch_listed<64>(a.kv_fmt, tm, kp, nsm, a.stream);
   if (rc != PKX_OK) return rc;
+  if (group <= kRowsGroup) {
+    rc = a.d == 128 ? launch_rows<128>(a, kp, nsm) : launch_rows<64>(a, kp, nsm);
+    if (rc != PKX_OK) return rc;
+  }
   if (ev_after) cudaEventRecord(ev_after, a.stream);
   const int64_t ctas = ((int64_t)a.batch * a.hq + 7) / 8;
   const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)nsm * 8);
   cudaError_t e = launch_pdl(
       a.d == 128 ? listed_combine_kernel<128> : listed_combine_kernel<64>, dim3(grid), dim3(256), 0,
       a.stream, reinterpret_cast<const ListedRow *>(ws + L.rows_off), (const float *)kp.plse,
-      (const float *)kp.po, kp.o, a.lse, a.batch, a.hq, group, b_head, b_step, err, n_err,
+      (const float *)kp.po, kp.o, a.lse, a.batch, a.hq, group, b_head, b_step,
+      group <= kRowsGroup ? 1 : 2, err, n_err,
       &hdr->status);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "listed_combine launch: %s", cudaGetErrorString(e));
@@ -672,19 +1102,29 @@ int launch_decode_shared(const ListedArgs &a) {
   p.num_groups = a.num_groups;
   p.hkv = a.hkv;
   p.tok = tokens_per_block(group);
-  p.target = L.unit_target;
+  p.sms = nsm;
+  const OwnUnits own = own_units(group, nsm);
+  p.own_run = own.run;
+  p.own_least = own.least;
+  p.own_target = own.target;
+  p.own_gran = own.gran;
+  p.rows = group <= kRowsGroup;
   p.unit_max = L.unit_max;
   p.gran_max = L.gran_max;
   p.seq = reinterpret_cast<int32_t *>(ws + L.seq_off);
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
+  size_t smem = sizeof(int32_t) * (3 * (size_t)(a.batch + 1) + 4 * (size_t)(a.num_groups + 1));
+  p.in_smem = smem <= 40 * 1024;
+  if (!p.in_smem) smem = 0;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
   p.order = reinterpret_cast<int32_t *>(ws + L.order_off);
-  p.rows = reinterpret_cast<ListedRow *>(ws + L.rows_off);
+  p.rows_out = reinterpret_cast<ListedRow *>(ws + L.rows_off);
   p.hdr = reinterpret_cast<WsHeader *>(ws);
-  cudaError_t e = launch_pdl(shared_sched_kernel, dim3(1), dim3(1024), 0, a.stream, p);
+  cudaError_t e = launch_pdl(shared_sched_kernel, dim3(1), dim3(1024), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "shared_sched launch: %s", cudaGetErrorString(e));
-  return run_listed(a, tm, L, nsm, a.kv_indptr, a.kv_indices, 2, 2 * a.hkv, nullptr, 0);
+  return run_listed(a, tm, L, nsm, a.kv_indptr, a.kv_indices, a.num_groups > 0 || !p.rows, own.gran,
+                    own.gran * a.hkv, nullptr, 0);
 }
 
 int launch_decode_pages(const ListedArgs &a) {
@@ -692,7 +1132,7 @@ int launch_decode_pages(const ListedArgs &a) {
   if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   const int group = a.hq / a.hkv;
   const int64_t pairs = (int64_t)a.batch * a.hkv;
-  if (pairs * a.top_k * a.page_size >= INT_MAX)
+  if (pairs * a.top_k * a.page_size >= INT_MAX)  // (units and granules are fewer)
     return set_error(PKX_EUNSUPPORTED,
                      "decode_pages: batch * hkv * top_k * page_size must be below 2^31");
   const ListedLayout L = pages_layout(a.batch, a.hkv, group, a.d, a.page_size, a.top_k, nsm);
@@ -712,20 +1152,25 @@ int launch_decode_pages(const ListedArgs &a) {
   p.hkv = a.hkv;
   p.page_size = a.page_size;
   p.top_k = a.top_k;
-  p.pieces = pages_pieces(a.batch, a.hkv, a.page_size, a.top_k, nsm);
+  p.pieces = pages_pieces(a.batch, a.hkv, group, a.page_size, a.top_k, nsm);
+  const OwnUnits own = own_units(group, nsm);
+  p.run = own.run;
+  p.gran = own.gran;
+  p.rows = group <= kRowsGroup;
   p.cap = a.top_k * a.page_size;
   p.slots = reinterpret_cast<int32_t *>(ws + L.idx_off);
   p.ptr = reinterpret_cast<int32_t *>(ws + L.ptr_off);
   p.err = reinterpret_cast<int32_t *>(ws + L.err_off);
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
   p.order = reinterpret_cast<int32_t *>(ws + L.order_off);
-  p.rows = reinterpret_cast<ListedRow *>(ws + L.rows_off);
+  p.rows_out = reinterpret_cast<ListedRow *>(ws + L.rows_off);
   p.hdr = reinterpret_cast<WsHeader *>(ws);
-  const size_t smem = sizeof(int) * ((size_t)a.top_k + 1);
+  const size_t smem = sizeof(int) * (2 * (size_t)a.top_k + 1);
   cudaError_t e = launch_pdl(list_pages_kernel, dim3((unsigned)pairs), dim3(256), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "list_pages launch: %s", cudaGetErrorString(e));
-  return run_listed(a, tm, L, nsm, p.ptr, p.slots, 2 * p.pieces, 2, p.err, (int)pairs);
+  return run_listed(a, tm, L, nsm, p.ptr, p.slots, !p.rows, own.gran * p.pieces, own.gran, p.err,
+                    (int)pairs);
 }
 
 }  // namespace pkx

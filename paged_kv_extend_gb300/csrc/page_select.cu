@@ -151,7 +151,7 @@ int launch_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_hs
 
 // ------------------------------------------------------------------- score
 constexpr int kScoreThreads = 256;
-constexpr int kScoreUnroll = 4;
+constexpr int kScoreUnroll = 8;
 
 struct ScoreParams {
   const uint16_t *q;
@@ -160,7 +160,7 @@ struct ScoreParams {
   const int32_t *kv_indptr, *kv_indices;
   int64_t n_indices;
   int batch, hq, hkv, group, top_k;
-  int run;         // page steps of a warp
+  int run;         // entries of a warp, at most 32
   int64_t runs;    // runs of a KV head
   uint32_t *keys;  // [hkv][n_indices]
   WsHeader *hdr;
@@ -174,9 +174,10 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// A warp: one KV head and a run of consecutive entries of kv_indices.  D / 4
-// lanes hold a page's two bounds, 8 dims each; neighbouring warps take the
-// heads of the same pages.
+// A warp: one KV head and a run of up to 32 consecutive entries of kv_indices,
+// whose page ids its lanes fetch together; neighbouring warps take the heads
+// of the same pages.  D / 4 lanes hold a page's two bounds, 8 dims each,
+// kScoreUnroll steps in flight.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreParams p) {
   constexpr int LP = D / 4;        // lanes of a page
@@ -188,79 +189,79 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
   if (w >= p.runs * p.hkv) return;
-  const int h = (int)(w % p.hkv);
-  const int64_t e0 = (w / p.hkv) * p.run * PPW;
+  const int64_t r = w / p.hkv;
+  const int h = (int)(w - r * p.hkv);
+  const int64_t e0 = r * p.run;
   const int sub = lane / LP, l = lane - sub * LP;
   const bool is_hi = l >= CH;
   const int c = is_hi ? l - CH : l;
-  const int64_t e_end = min(e0 + (int64_t)p.run * PPW, p.n_indices);
-  int b = -1;
-  int64_t b_end = 0;  // entries before b_end belong to sequence b
-  bool scored = false;
-  float f[8];
-  for (int64_t s0 = e0; s0 < e_end; s0 += PPW * kScoreUnroll) {
-    int64_t pg[kScoreUnroll];
-    uint4 x[kScoreUnroll];
-#pragma unroll
-    for (int u = 0; u < kScoreUnroll; ++u) {
-      const int64_t e = s0 + u * PPW + sub;
-      pg[u] = e < e_end ? __ldg(p.kv_indices + e) : -1;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (pg[u] >= 0 && pg[u] < p.num_pages)
-        x[u] = __ldg(p.bounds + (pg[u] * p.hkv + h) * LP + l);
-      else
-        pg[u] = -1;
+  const int64_t e_end = min(e0 + p.run, p.n_indices);
+  int my_page = e0 + lane < e_end ? __ldg(p.kv_indices + e0 + lane) : -1;
+  if (my_page >= p.num_pages) my_page = -1;
+  for (int64_t e = e0; e < e_end;) {
+    // the sequence of entry e: the last b with kv_indptr[b] <= e, by 32 probes
+    // at a time
+    int b = 0;
+    for (int span = p.batch; span > 1;) {
+      const int step = (span + 31) / 32;
+      const int at = lane * step;
+      const bool before = at < span && (at == 0 || __ldg(p.kv_indptr + b + at) <= e);
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
+      b += last * step;
+      span = min(step, span - last * step);
     }
+    const int64_t first = __ldg(p.kv_indptr + b), end = __ldg(p.kv_indptr + b + 1);
+    if (first > e || end <= e) break;  // behind the last sequence
+    const int64_t seg = min(end, e_end);
+    if (end - first <= p.top_k) {  // all of its pages are taken
+      e = seg;
+      continue;
+    }
+    float f[8];
 #pragma unroll
-    for (int u = 0; u < kScoreUnroll; ++u) {
-      const int64_t e = s0 + u * PPW + sub;
-      // the entry's sequence and the sum of its query heads (the lanes of a
-      // page take the same branch)
-      if (e < e_end && e >= b_end) {
-        int lo = max(b, 0), hi = p.batch - 1;  // last b with kv_indptr[b] <= e
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (__ldg(p.kv_indptr + mid) <= e) lo = mid;
-          else hi = mid - 1;
-        }
-        b = lo;
-        const int64_t first = __ldg(p.kv_indptr + b);
-        b_end = max((int64_t)__ldg(p.kv_indptr + b + 1), e + 1);
-        const int64_t end = __ldg(p.kv_indptr + b + 1);
-        scored = e >= first && e < end && end - first > p.top_k;  // else: every page, or none
-        if (e >= end || e < first) b_end = e + 1;
-        if (scored) {
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    const uint4 *row =
+        reinterpret_cast<const uint4 *>(p.q + ((int64_t)b * p.hq + (int64_t)h * p.group) * D) + c;
+    for (int g = 0; g < p.group; ++g) {
+      const uint4 v = __ldg(row + g * CH);
+      const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = 0.f;
-          const uint4 *row = reinterpret_cast<const uint4 *>(
-              p.q + ((int64_t)b * p.hq + (int64_t)h * p.group) * D) + c;
-          for (int g = 0; g < p.group; ++g) {
-            const uint4 v = __ldg(row + g * CH);
-            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float qv = __uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16);
-              f[i] = __fadd_rn(f[i], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
-            }
-          }
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float qv = __uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16);
+        f[i] = __fadd_rn(f[i], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
       }
-      const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        t[i] = __fmul_rn(__uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16),
-                         scored ? f[i] : 0.f);
-#pragma unroll
-      for (int n = 4; n > 0; n >>= 1)
-#pragma unroll
-        for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
-      float s = t[0];
-#pragma unroll
-      for (int o = 1; o < LP; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-      if (l == 0 && e < e_end && scored)
-        p.keys[(int64_t)h * p.n_indices + e] = pg[u] < 0 ? 0u : score_key(s);
     }
+    for (; e < seg; e += PPW * kScoreUnroll) {
+      uint4 x[kScoreUnroll];
+      int page[kScoreUnroll];
+#pragma unroll
+      for (int u = 0; u < kScoreUnroll; ++u) {
+        const int i = (int)(e - e0) + u * PPW + sub;
+        page[u] = __shfl_sync(0xffffffffu, my_page, i & 31);
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (e + u * PPW + sub < seg && page[u] >= 0)
+          x[u] = __ldg(p.bounds + ((int64_t)page[u] * p.hkv + h) * LP + l);
+      }
+#pragma unroll
+      for (int u = 0; u < kScoreUnroll; ++u) {
+        const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          t[i] = __fmul_rn(__uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16), f[i]);
+#pragma unroll
+        for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+          for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
+        float s = t[0];
+#pragma unroll
+        for (int o = 1; o < LP; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+        const int64_t at = e + u * PPW + sub;
+        if (l == 0 && at < seg)
+          p.keys[(int64_t)h * p.n_indices + at] = page[u] < 0 ? 0u : score_key(s);
+      }
+    }
+    e = seg;
   }
 }
 
@@ -304,6 +305,8 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
   bool lost = false;  // a page outside the bounds
 #pragma unroll
   for (int r = 0; r < kHeld; ++r) {
+    held[r] = 0u;
+    if (r * THREADS >= m) continue;
     const int i = r * THREADS + tid;
     held[r] = i < m ? __ldg(keys + i) : 0u;
     lost |= i < m && held[r] == 0u;
@@ -321,6 +324,7 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
       int c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll
       for (int r = 0; r < kHeld; ++r) {  // (an absent key is 0, below every bound)
+        if (r * THREADS >= m) break;
         c1 += held[r] >= t1;
         c2 += held[r] >= t2;
         c3 += held[r] >= t3;
@@ -409,14 +413,12 @@ int launch_select_pages(const SelectArgs &a) {
   p.top_k = a.top_k;
   p.keys = keys;
   p.hdr = hdr;
-  // a warp's run: about 32 warps an SM, 4 to 32 steps each (a run reads the
-  // group's query rows once)
-  const int ppw = 128 / a.d;
-  const int64_t steps = (a.n_indices + ppw - 1) / ppw;
-  int64_t run = steps * a.hkv / ((int64_t)nsm * 32);
-  run = run < kScoreUnroll ? kScoreUnroll : run > 32 ? 32 : run / kScoreUnroll * kScoreUnroll;
+  // a warp's run: 32 entries, or fewer where that leaves less than 16 warps an
+  // SM (a run reads the group's query rows once)
+  int64_t run = a.n_indices * a.hkv / ((int64_t)nsm * 16);
+  run = run < 8 ? 8 : run > 32 ? 32 : run / 8 * 8;
   p.run = (int)run;
-  p.runs = (steps + run - 1) / run;
+  p.runs = (a.n_indices + run - 1) / run;
   int64_t grid = (p.runs * a.hkv + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
   if (grid < 1) grid = 1;  // (the status word)
   if (grid >= (1ll << 31) || (int64_t)a.batch * a.hkv >= (1ll << 31))
