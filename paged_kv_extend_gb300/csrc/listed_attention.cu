@@ -62,13 +62,20 @@ struct ListedLayout {
   int64_t gran_max;
 };
 
+// First key of piece i when n runs of `run` keys, `keys` in all, are cut into S
+// pieces (sizes differ by one run).
+__device__ __forceinline__ int piece_at(int i, int n, int S, int run, int keys) {
+  const int q = n / S;
+  return (int)min((int64_t)(i * q + min(i, n - q * S)) * run, (int64_t)keys);
+}
+
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // ------------------------------------------------------------------ combine
 // One warp a (token, head) row: the lanes hold up to 32 partials' weights, the
 // row's dims are split over the lanes (float4 each).
 template <int D>
-__global__ void __launch_bounds__(256) listed_combine_kernel(
+__global__ void __launch_bounds__(256, 4) listed_combine_kernel(
     const ListedRow *__restrict__ rows, const float *__restrict__ plse,
     const float *__restrict__ po, bf16 *__restrict__ o, float *__restrict__ lse, int batch, int hq,
     int group, int b_head, int b_step, int b_streams, const int32_t *__restrict__ err, int n_err,
@@ -122,16 +129,16 @@ __global__ void __launch_bounds__(256) listed_combine_kernel(
       const float w = have ? exp2f((plse[row] - mx) * kLog2e) : 0.f;
       wsum += w;
       const int m = min(32, n - i0);
-      for (int i = 0; i < m; i += 8) {
-        float4 v[8];
+      for (int i = 0; i < m; i += 4) {
+        float4 v[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const int64_t at = __shfl_sync(0xffffffffu, row, (i + u) & 31);
           if (i + u < m && lane * 4 < D)
             v[u] = *reinterpret_cast<const float4 *>(po + at * D + lane * 4);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const float wi = __shfl_sync(0xffffffffu, w, (i + u) & 31);
           // (a stream without keys has weight 0 and a row of zeros)
           if (i + u < m && lane * 4 < D) {
@@ -464,7 +471,7 @@ struct SharedParams {
   WsHeader *hdr;
 };
 // Exclusive sum over a block of 1024 threads of one value each, and the total.
-__device__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
+__device__ __forceinline__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
 #pragma unroll
@@ -474,14 +481,14 @@ __device__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
   }
   if (lane == 31) sh[warp] = x;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < 32; ++w) {
-    const int64_t y = sh[w];
-    if (w < warp) before += y;
-    all += y;
+  int64_t t = sh[lane], before = lane < warp ? t : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   __syncthreads();
-  total = all;
+  total = t;
   return before + x - v;
 }
 
@@ -592,7 +599,9 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     }
     if (lane == 0) s_best[warp] = best;
     __syncthreads();
-    for (int w = 0; w < 32; ++w) best = min(best, s_best[w]);
+    best = s_best[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = min(best, (int64_t)__shfl_xor_sync(0xffffffffu, best, o));
     C = (int)(best & ((1 << 24) - 1));
   }
   auto pieces = [&](int g) { return (tiles(gS[g]) + C - 1) / C; };
@@ -657,8 +666,8 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.n_tok = min(blk, n - k * blk);
     w.qpos0 = kPastAll;
     w.kvh = kvh;
-    w.k_begin = (int)min((int64_t)gS[g], (int64_t)sp * nt / S * kBlockN);
-    w.k_end = (int)min((int64_t)gS[g], (int64_t)(sp + 1) * nt / S * kBlockN);
+    w.k_begin = piece_at(sp, nt, S, kBlockN, gS[g]);
+    w.k_end = piece_at(sp + 1, nt, S, kBlockN, gS[g]);
     w.k_split = INT_MAX;
     w.n_tiles = tiles(w.k_end - w.k_begin);
     w.b = first;
@@ -682,8 +691,8 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.n_tok = 1;
     w.qpos0 = kPastAll;
     w.kvh = kvh;
-    w.k_begin = (int)min((int64_t)sT[b], sS[b] + (int64_t)sp * nr / S * p.own_run);
-    w.k_end = (int)min((int64_t)sT[b], sS[b] + (int64_t)(sp + 1) * nr / S * p.own_run);
+    w.k_begin = sS[b] + piece_at(sp, nr, S, p.own_run, sT[b] - sS[b]);
+    w.k_end = sS[b] + piece_at(sp + 1, nr, S, p.own_run, sT[b] - sS[b]);
     w.k_split = INT_MAX;
     w.n_tiles = tiles(w.k_end - w.k_begin);
     w.b = b;
@@ -874,8 +883,8 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     w.n_tok = 1;
     w.qpos0 = kPastAll;
     w.kvh = kvh;
-    w.k_begin = (int)min((int64_t)keys, (int64_t)s * nt / p.pieces * p.run);
-    w.k_end = (int)min((int64_t)keys, (int64_t)(s + 1) * nt / p.pieces * p.run);
+    w.k_begin = piece_at(s, nt, p.pieces, p.run, keys);
+    w.k_end = piece_at(s + 1, nt, p.pieces, p.run, keys);
     w.k_split = INT_MAX;
     w.n_tiles = (w.k_end - w.k_begin + kBlockN - 1) / kBlockN;
     w.b = pair;

@@ -198,6 +198,9 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
   const int64_t e_end = min(e0 + p.run, p.n_indices);
   int my_page = e0 + lane < e_end ? __ldg(p.kv_indices + e0 + lane) : -1;
   if (my_page >= p.num_pages) my_page = -1;
+  uint32_t *keys = p.keys + (int64_t)h * p.n_indices + e0;
+  const uint4 *box = p.bounds + (int64_t)h * LP + l;
+  const int64_t page_chunks = (int64_t)p.hkv * LP;
   for (int64_t e = e0; e < e_end;) {
     // the sequence of entry e: the last b with kv_indptr[b] <= e, by 32 probes
     // at a time
@@ -231,17 +234,18 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
         f[i] = __fadd_rn(f[i], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
       }
     }
-    for (; e < seg; e += PPW * kScoreUnroll) {
+    // (an entry behind the run's end, or a page outside the bounds, reads page 0
+    // and its result is dropped: the loads go out without a branch)
+    const int i1 = (int)(seg - e0);
+    for (int i0 = (int)(e - e0); i0 < i1 && p.num_pages > 0; i0 += PPW * kScoreUnroll) {
       uint4 x[kScoreUnroll];
       int page[kScoreUnroll];
 #pragma unroll
-      for (int u = 0; u < kScoreUnroll; ++u) {
-        const int i = (int)(e - e0) + u * PPW + sub;
-        page[u] = __shfl_sync(0xffffffffu, my_page, i & 31);
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (e + u * PPW + sub < seg && page[u] >= 0)
-          x[u] = __ldg(p.bounds + ((int64_t)page[u] * p.hkv + h) * LP + l);
-      }
+      for (int u = 0; u < kScoreUnroll; ++u)
+        page[u] = __shfl_sync(0xffffffffu, my_page, (i0 + u * PPW + sub) & 31);
+#pragma unroll
+      for (int u = 0; u < kScoreUnroll; ++u)
+        x[u] = __ldg(box + (int64_t)max(page[u], 0) * page_chunks);
 #pragma unroll
       for (int u = 0; u < kScoreUnroll; ++u) {
         const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
@@ -256,11 +260,11 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
         float s = t[0];
 #pragma unroll
         for (int o = 1; o < LP; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-        const int64_t at = e + u * PPW + sub;
-        if (l == 0 && at < seg)
-          p.keys[(int64_t)h * p.n_indices + at] = page[u] < 0 ? 0u : score_key(s);
+        const int i = i0 + u * PPW + sub;
+        if (l == 0 && i < i1) keys[i] = page[u] < 0 ? 0u : score_key(s);
       }
     }
+    if (p.num_pages == 0 && lane >= (int)(e - e0) && lane < i1) keys[lane] = 0u;
     e = seg;
   }
 }
@@ -275,14 +279,63 @@ struct SelectParams {
   WsHeader *hdr;
 };
 
-// One CTA for each (sequence, KV head).  A thread keeps kHeld keys in
-// registers (keys i = r * THREADS + tid); those of longer sequences are read
-// again each round.
+// The threshold of the `want` largest of the CTA's keys: the largest T with
+// count(key >= T) >= want, two bits a round, and `above` = count(key > T).  HELD
+// keys a thread in registers (an absent one is 0, below every bound tried);
+// keys from HELD * THREADS on are read again each round.
+template <int THREADS, int HELD>
+__device__ __forceinline__ void threshold(const uint32_t *keys, int m, int want,
+                                          const uint32_t (&held)[16], int (*s_cnt)[32][3],
+                                          uint32_t &T, int &above) {
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  T = 0;
+  above = 0;
+  int parity = 0;
+  for (int shift = 30; shift >= 0; shift -= 2, parity ^= 1) {
+    const uint32_t t1 = T + (1u << shift), t2 = T + (2u << shift), t3 = T + (3u << shift);
+    int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+    for (int r = 0; r < HELD; ++r) {
+      c1 += held[r] >= t1;
+      c2 += held[r] >= t2;
+      c3 += held[r] >= t3;
+    }
+    if constexpr (HELD == 16)
+      for (int i = HELD * THREADS + tid; i < m; i += THREADS) {
+        const uint32_t k = __ldg(keys + i);
+        c1 += k >= t1;
+        c2 += k >= t2;
+        c3 += k >= t3;
+      }
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    if constexpr (WARPS > 1) {
+      if (lane == 0) {
+        s_cnt[parity][warp][0] = c1;
+        s_cnt[parity][warp][1] = c2;
+        s_cnt[parity][warp][2] = c3;
+      }
+      __syncthreads();
+      c1 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][0] : 0);
+      c2 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][1] : 0);
+      c3 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][2] : 0);
+    }
+    if (c3 >= want) T = t3;
+    else if (c2 >= want) T = t2, above = c3;
+    else if (c1 >= want) T = t1, above = c2;
+    else above = c1;
+  }
+}
+
+// One CTA for each (sequence, KV head).  A thread keeps 16 keys in registers
+// (keys i = r * THREADS + tid).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams p) {
   constexpr int kHeld = 16, WARPS = THREADS / 32;
-  __shared__ int s_cnt[2][WARPS][3];
-  __shared__ int s_scan[2][WARPS];
+  __shared__ int s_cnt[2][32][3];
+  __shared__ int s_scan[2][32];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -305,87 +358,54 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
   bool lost = false;  // a page outside the bounds
 #pragma unroll
   for (int r = 0; r < kHeld; ++r) {
-    held[r] = 0u;
-    if (r * THREADS >= m) continue;
     const int i = r * THREADS + tid;
     held[r] = i < m ? __ldg(keys + i) : 0u;
     lost |= i < m && held[r] == 0u;
   }
   for (int i = kHeld * THREADS + tid; i < m; i += THREADS) lost |= __ldg(keys + i) == 0u;
   if (lost) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
-
-  // the largest key T with count(key >= T) >= want, two bits a round
-  uint32_t T = 0;
-  int above = 0;  // count(key > T) at the end
-  if (want > 0) {
-    int parity = 0;
-    for (int shift = 30; shift >= 0; shift -= 2, parity ^= 1) {
-      const uint32_t t1 = T + (1u << shift), t2 = T + (2u << shift), t3 = T + (3u << shift);
-      int c1 = 0, c2 = 0, c3 = 0;
-#pragma unroll
-      for (int r = 0; r < kHeld; ++r) {  // (an absent key is 0, below every bound)
-        if (r * THREADS >= m) break;
-        c1 += held[r] >= t1;
-        c2 += held[r] >= t2;
-        c3 += held[r] >= t3;
-      }
-      for (int i = kHeld * THREADS + tid; i < m; i += THREADS) {
-        const uint32_t k = __ldg(keys + i);
-        c1 += k >= t1;
-        c2 += k >= t2;
-        c3 += k >= t3;
-      }
-      c1 = __reduce_add_sync(0xffffffffu, c1);
-      c2 = __reduce_add_sync(0xffffffffu, c2);
-      c3 = __reduce_add_sync(0xffffffffu, c3);
-      if (lane == 0) {
-        s_cnt[parity][warp][0] = c1;
-        s_cnt[parity][warp][1] = c2;
-        s_cnt[parity][warp][2] = c3;
-      }
-      __syncthreads();
-      c1 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][0] : 0);
-      c2 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][1] : 0);
-      c3 = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_cnt[parity][lane][2] : 0);
-      if (c3 >= want) T = t3;
-      else if (c2 >= want) T = t2, above = c3;
-      else if (c1 >= want) T = t1, above = c2;
-      else above = c1;
-    }
-  }
-  const int ties = want - above;  // keys equal to T that are taken, lowest first
-
   for (int i = tid; i < p.first_pages; i += THREADS) out[i] = i;
   for (int i = tid; i < p.last_pages; i += THREADS)
     out[p.top_k - p.last_pages + i] = n - p.last_pages + i;
-  // the others in order: a running count of keys above T and equal to it
-  int gt = 0, eq = 0, parity = 0;
-  if (want > 0) {
-    for (int r = 0; r * THREADS < m; ++r, parity ^= 1) {
-      const int i = r * THREADS + tid;
-      uint32_t k = 0;
-      if (r < kHeld) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-          if (j == r) k = held[j];
-      } else if (i < m) {
-        k = __ldg(keys + i);
-      }
-      const unsigned g = __ballot_sync(0xffffffffu, i < m && k > T);
-      const unsigned q = __ballot_sync(0xffffffffu, i < m && k == T);
-      if (lane == 0) s_scan[parity][warp] = __popc(g) | (__popc(q) << 16);
+  if (want == 0) return;
+
+  uint32_t T;
+  int above;
+  if (m <= THREADS) threshold<THREADS, 1>(keys, m, want, held, s_cnt, T, above);
+  else if (m <= 2 * THREADS) threshold<THREADS, 2>(keys, m, want, held, s_cnt, T, above);
+  else if (m <= 4 * THREADS) threshold<THREADS, 4>(keys, m, want, held, s_cnt, T, above);
+  else if (m <= 8 * THREADS) threshold<THREADS, 8>(keys, m, want, held, s_cnt, T, above);
+  else threshold<THREADS, 16>(keys, m, want, held, s_cnt, T, above);
+  const int ties = want - above;  // keys equal to T that are taken, lowest first
+
+  // the pages in order: a running count of keys above T and equal to it
+  int gt = 0, eq = 0;
+  auto place = [&](int r, uint32_t k) {
+    const int i = r * THREADS + tid;
+    const unsigned g = __ballot_sync(0xffffffffu, i < m && k > T);
+    const unsigned q = __ballot_sync(0xffffffffu, i < m && k == T);
+    int all = __popc(g) | (__popc(q) << 16), before = 0;
+    if constexpr (WARPS > 1) {
+      if (lane == 0) s_scan[r & 1][warp] = all;
       __syncthreads();
-      int x = lane < WARPS ? s_scan[parity][lane] : 0;
-      const int all = __reduce_add_sync(0xffffffffu, x);
-      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-      const unsigned below = (1u << lane) - 1u;
-      const int my_gt = gt + (before & 0xFFFF) + __popc(g & below);
-      const int my_eq = eq + (before >> 16) + __popc(q & below);
-      if (i < m && (k > T || (k == T && my_eq < ties)))
-        out[lo + my_gt + min(my_eq, ties)] = lo + i;
-      gt += all & 0xFFFF;
-      eq += all >> 16;
+      const int x = lane < WARPS ? s_scan[r & 1][lane] : 0;
+      all = __reduce_add_sync(0xffffffffu, x);
+      before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
     }
+    const unsigned below = (1u << lane) - 1u;
+    const int my_gt = gt + (before & 0xFFFF) + __popc(g & below);
+    const int my_eq = eq + (before >> 16) + __popc(q & below);
+    if (i < m && (k > T || (k == T && my_eq < ties)))
+      out[lo + my_gt + min(my_eq, ties)] = lo + i;
+    gt += all & 0xFFFF;
+    eq += all >> 16;
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r * THREADS < m) place(r, held[r]);
+  for (int r = kHeld; r * THREADS < m; ++r) {
+    const int i = r * THREADS + tid;
+    place(r, i < m ? __ldg(keys + i) : 0u);
   }
 }
 
@@ -438,9 +458,13 @@ int launch_select_pages(const SelectArgs &a) {
   s.keys = keys;
   s.selected = a.selected;
   s.hdr = hdr;
-  // 256 threads hold 4096 keys, 1024 hold 16384: by the batch's average
+  // By the batch's average: a warp holds 512 keys and needs no barrier, 256
+  // threads hold 4096, 1024 hold 16384.
   const dim3 pairs((unsigned)(a.batch * a.hkv));
-  if (a.n_indices / a.batch <= 4096)
+  const int64_t mean = a.n_indices / a.batch;
+  if (mean <= 512)
+    e = launch_pdl(page_select_kernel<32>, pairs, dim3(32), 0, a.stream, s);
+  else if (mean <= 4096)
     e = launch_pdl(page_select_kernel<256>, pairs, dim3(256), 0, a.stream, s);
   else
     e = launch_pdl(page_select_kernel<1024>, pairs, dim3(1024), 0, a.stream, s);

@@ -31,17 +31,16 @@
 
 namespace pkx {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRows = 4;  // row steps in flight
 
 struct RopeParams {
   RopeArgs a;
   int64_t warps;  // tokens * parts
   int parts;      // warps that share a token's rows
-  int log_lanes;  // lanes of a row: 1 << log_lanes
   int chunks;     // d / 8: lanes that hold elements
   int turned;     // rotary / 8: lanes whose elements are rotated
-  int q_steps, k_steps, steps;  // row steps of q, of q and k, of all rows
+  int q_steps, k_steps;  // row steps of q and of k (v has k's)
   float inv_d;
 };
 
@@ -83,23 +82,46 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int second, uint4 v, flo
   }
 }
 
+// What a lane does to the rows of q or of k, for its four pairs: with e, f a
+// pair's elements, (e A - f B, f C + e D), where the norm's weights are
+// multiplied into the cosines and sines; without rotation (e A, f C).
+struct Turn {
+  float A[4], B[4], C[4], D[4];
+};
+
+template <bool LEAVED>
+__device__ __forceinline__ Turn make_turn(uint4 weight, bool weighted, float offset, bool turned,
+                                          const float (&cs)[4], const float (&sn)[4]) {
+  float w[8];
+  unpack8(weight, w);
+  Turn r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = LEAVED ? 2 * i : i, n = LEAVED ? 2 * i + 1 : i + 4;
+    const float we = weighted ? w[m] + offset : 1.0f, wf = weighted ? w[n] + offset : 1.0f;
+    r.A[i] = turned ? we * cs[i] : we;
+    r.B[i] = wf * sn[i];
+    r.C[i] = turned ? wf * cs[i] : wf;
+    r.D[i] = we * sn[i];
+  }
+  return r;
+}
+
 // FMT: the pool's element format (0 bf16, 1 e4m3, 2 e5m2).  LEAVED: pairs of
-// neighbouring elements.
-template <int FMT, bool LEAVED>
-__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const RopeParams p) {
+// neighbouring elements.  LOG: a row takes 1 << LOG lanes.
+template <int FMT, bool LEAVED, int LOG>
+__global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const RopeParams p) {
+  constexpr int LANES = 1 << LOG, ROWS = 32 / LANES;  // rows of a warp's step
+  constexpr int BYTES = FMT == 0 ? 2 : 1;
   grid_dep_wait();
   grid_dep_launch();
   const RopeArgs &a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int lanes = 1 << p.log_lanes, rows = 32 >> p.log_lanes;  // rows of a warp's step
-  const int c = lane & (lanes - 1), sub = lane >> p.log_lanes;
+  const int lane = threadIdx.x & 31, c = lane % LANES, sub = lane / LANES;
   const bool in_row = c < p.chunks, turned = c < p.turned;
   const int half = a.rotary >> 1;
   // this lane's elements: run of four at `at`, the other `second` further on
   const int at = !LEAVED && turned ? 4 * c : 8 * c;
   const int second = turned ? half : 4;
-  const bool norm = a.q_weight || a.k_weight;
-
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
   if (a.q_weight && in_row) wq = load_row<LEAVED>(a.q_weight + at, second);
   if (a.k_weight && in_row) wk = load_row<LEAVED>(a.k_weight + at, second);
@@ -108,115 +130,150 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const Rop
   for (; w < p.warps; w += (int64_t)gridDim.x * (kRopeThreads / 32)) {
     const int64_t tok = p.parts == 1 ? w : w / p.parts;
     const int part = (int)(w - tok * p.parts);
-    const uint16_t *qp = a.q + tok * a.q_ts + at, *kp = a.k + tok * a.k_ts + at;
-    const uint16_t *vp = a.v + tok * a.v_ts + at;
-    uint16_t *qo = a.q_out + tok * a.qo_ts + at, *ko = a.k_out + tok * a.ko_ts + at;
+    // rows of q are taken from step `part` on, those of k and v where q's end
+    const int k_part = (part + p.parts - p.q_steps % p.parts) % p.parts;
+    const int v_part = (k_part + p.parts - p.k_steps % p.parts) % p.parts;
+    const int stride = p.parts * ROWS;  // rows between a warp's steps
+    uint4 val[kRows];
+    auto load = [&](const uint16_t *x, int64_t hs, int heads, int h0) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int h = h0 + u * stride + sub;
+        val[u] = make_uint4(0, 0, 0, 0);
+        if (in_row && h < heads) val[u] = load_row<LEAVED>(x + h * hs, second);
+      }
+    };
+    const uint16_t *qp = a.q + tok * a.q_ts + at;
+    load(qp, a.q_hs, a.hq, part * ROWS);
     int64_t slot = -1;
     if (a.cache_loc) {
       slot = __ldg(a.cache_loc + tok);
       if (slot >= a.num_slots) slot = -1;
     }
-    constexpr int BYTES = FMT == 0 ? 2 : 1;
-    uint8_t *kc = static_cast<uint8_t *>(a.k_buffer) + (slot * a.kb_ss + at) * BYTES;
-    uint8_t *vc = static_cast<uint8_t *>(a.v_buffer) + (slot * a.vb_ss + at) * BYTES;
-    float cs[4], sn[4];
-    bool have_angles = false;
-    for (int s0 = part; s0 < p.steps; s0 += p.parts * kRows) {
-      uint4 val[kRows];
+    // the four pairs' cosines and sines; NaN for a position outside the table
+    // or no such axis
+    float cs[4] = {0.f, 0.f, 0.f, 0.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (turned) {
+      const float nan = __int_as_float(0x7fffffff);
+      if (!a.pair_axis) {
+        const int64_t pos = __ldg(a.positions + tok);
+        const bool ok = pos >= 0 && pos < a.max_position;
+        const float *row = a.cos_sin + (ok ? pos : 0) * a.rotary + 4 * c;
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(row));
+        const float4 y = __ldg(reinterpret_cast<const float4 *>(row + half));
+        cs[0] = ok ? x.x : nan; cs[1] = ok ? x.y : nan;
+        cs[2] = ok ? x.z : nan; cs[3] = ok ? x.w : nan;
+        sn[0] = y.x; sn[1] = y.y; sn[2] = y.z; sn[3] = y.w;
+      } else {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const int st = s0 + u * p.parts;
-        val[u] = make_uint4(0, 0, 0, 0);
-        if (st < p.q_steps) {
-          const int h = st * rows + sub;
-          if (in_row && h < a.hq) val[u] = load_row<LEAVED>(qp + h * a.q_hs, second);
-        } else if (st < p.steps) {
-          const bool is_k = st < p.k_steps;
-          const int h = (st - (is_k ? p.q_steps : p.k_steps)) * rows + sub;
-          if (in_row && h < a.hkv)
-            val[u] = load_row<LEAVED>(is_k ? kp + h * a.k_hs : vp + h * a.v_hs, second);
-        }
-      }
-      if (!have_angles && turned) {
-        // the four pairs' cosines and sines (after the first rows' loads have
-        // gone out); NaN for a position outside the table or no such axis
-        have_angles = true;
-        const float nan = __int_as_float(0x7fffffff);
-        if (!a.pair_axis) {
-          const int64_t pos = __ldg(a.positions + tok);
-          const bool ok = pos >= 0 && pos < a.max_position;
-          const float *row = a.cos_sin + (ok ? pos : 0) * a.rotary + 4 * c;
-          const float4 x = __ldg(reinterpret_cast<const float4 *>(row));
-          const float4 y = __ldg(reinterpret_cast<const float4 *>(row + half));
-          cs[0] = ok ? x.x : nan; cs[1] = ok ? x.y : nan;
-          cs[2] = ok ? x.z : nan; cs[3] = ok ? x.w : nan;
-          sn[0] = y.x; sn[1] = y.y; sn[2] = y.z; sn[3] = y.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int axis = __ldg(a.pair_axis + 4 * c + i);
-            const int64_t pos = axis < a.axes ? __ldg(a.positions + axis * a.n_tokens + tok) : -1;
-            cs[i] = sn[i] = nan;
-            if (pos >= 0 && pos < a.max_position) {
-              cs[i] = __ldg(a.cos_sin + pos * a.rotary + 4 * c + i);
-              sn[i] = __ldg(a.cos_sin + pos * a.rotary + half + 4 * c + i);
-            }
+        for (int i = 0; i < 4; ++i) {
+          const int axis = __ldg(a.pair_axis + 4 * c + i);
+          const int64_t pos = axis < a.axes ? __ldg(a.positions + axis * a.n_tokens + tok) : -1;
+          cs[i] = sn[i] = nan;
+          if (pos >= 0 && pos < a.max_position) {
+            cs[i] = __ldg(a.cos_sin + pos * a.rotary + 4 * c + i);
+            sn[i] = __ldg(a.cos_sin + pos * a.rotary + half + 4 * c + i);
           }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        const int st = s0 + u * p.parts;  // (the same for the whole warp)
-        if (st >= p.steps) break;
-        uint4 out = val[u];
-        const bool is_q = st < p.q_steps;
-        if (st < p.k_steps) {
-          float x[8];
-          unpack8(out, x);
-          if (norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-            for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-              const float inv = rsqrtf(ss * p.inv_d + a.eps);
-              float wt[8];
-              unpack8(is_q ? wq : wk, wt);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] *= inv * (wt[i] + a.weight_offset);
-            }
-          }
-          if (turned) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int m = LEAVED ? 2 * i : i, n = LEAVED ? 2 * i + 1 : i + 4;
-              const float e = x[m], f = x[n];
-              x[m] = e * cs[i] - f * sn[i];
-              x[n] = f * cs[i] + e * sn[i];
-            }
-          }
-          out = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                           pack_bf16(x[6], x[7]));
-        }
-        if (!in_row) continue;
-        if (is_q) {
-          const int h = st * rows + sub;
-          if (h < a.hq) store_row<LEAVED>(qo + h * a.qo_hs, second, out);
-          continue;
-        }
-        const bool is_k = st < p.k_steps;
-        const int h = (st - (is_k ? p.q_steps : p.k_steps)) * rows + sub;
-        if (h >= a.hkv) continue;
-        if (is_k) store_row<LEAVED>(ko + h * a.ko_hs, second, out);
-        if (slot >= 0) {
-          uint8_t *dst = is_k ? kc + h * a.kb_hs * BYTES : vc + h * a.vb_hs * BYTES;
-          if constexpr (FMT == 0)
-            store_row<LEAVED>(reinterpret_cast<uint16_t *>(dst), second, out);
-          else
-            store_codes<LEAVED, FMT>(dst, second, out, is_k ? a.k_scale : a.v_scale);
         }
       }
     }
+    // one row: norm and rotation (all lanes of the warp)
+    auto turn_row = [&](uint4 in, bool norm, const Turn &T) {
+      float x[8];
+      unpack8(in, x);
+      float inv = 1.0f;
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        inv = rsqrtf(ss * p.inv_d + a.eps);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = LEAVED ? 2 * i : i, n = LEAVED ? 2 * i + 1 : i + 4;
+        const float e = x[m], f = x[n];
+        x[m] = e * T.A[i];
+        x[n] = f * T.C[i];
+        if (turned) {
+          x[m] -= f * T.B[i];
+          x[n] += e * T.D[i];
+        }
+      }
+      if (norm) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= inv;
+      }
+      return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                        pack_bf16(x[6], x[7]));
+    };
+    auto store_pool = [&](void *pool, int64_t row, uint4 v, float scale) {
+      uint8_t *dst = static_cast<uint8_t *>(pool) + (row + at) * BYTES;
+      if constexpr (FMT == 0) store_row<LEAVED>(reinterpret_cast<uint16_t *>(dst), second, v);
+      else store_codes<LEAVED, FMT>(dst, second, v, scale);
+    };
+    {
+      const bool norm = a.q_weight != nullptr;
+      const Turn T = make_turn<LEAVED>(wq, norm, a.weight_offset, turned, cs, sn);
+      uint16_t *out = a.q_out + tok * a.qo_ts + at;
+      for (int h0 = part * ROWS; h0 < a.hq; h0 += kRows * stride) {
+        if (h0 != part * ROWS) load(qp, a.q_hs, a.hq, h0);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          if (h0 + u * stride >= a.hq) break;  // (the same for the whole warp)
+          const int h = h0 + u * stride + sub;
+          const uint4 r = turn_row(val[u], norm, T);
+          if (in_row && h < a.hq) store_row<LEAVED>(out + h * a.qo_hs, second, r);
+        }
+      }
+    }
+    {
+      const bool norm = a.k_weight != nullptr;
+      const Turn T = make_turn<LEAVED>(wk, norm, a.weight_offset, turned, cs, sn);
+      const uint16_t *kp = a.k + tok * a.k_ts + at;
+      uint16_t *out = a.k_out + tok * a.ko_ts + at;
+      for (int h0 = k_part * ROWS; h0 < a.hkv; h0 += kRows * stride) {
+        load(kp, a.k_hs, a.hkv, h0);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          if (h0 + u * stride >= a.hkv) break;
+          const int h = h0 + u * stride + sub;
+          const uint4 r = turn_row(val[u], norm, T);
+          if (!in_row || h >= a.hkv) continue;
+          store_row<LEAVED>(out + h * a.ko_hs, second, r);
+          if (slot >= 0) store_pool(a.k_buffer, slot * a.kb_ss + h * a.kb_hs, r, a.k_scale);
+        }
+      }
+    }
+    if (a.v && slot >= 0) {
+      const uint16_t *vp = a.v + tok * a.v_ts + at;
+      for (int h0 = v_part * ROWS; h0 < a.hkv; h0 += kRows * stride) {
+        load(vp, a.v_hs, a.hkv, h0);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int h = h0 + u * stride + sub;
+          if (in_row && h < a.hkv)
+            store_pool(a.v_buffer, slot * a.vb_ss + h * a.vb_hs, val[u], a.v_scale);
+        }
+      }
+    }
+  }
+}
+
+template <bool LEAVED, int LOG>
+static void (*rope_kernel(int fmt))(const RopeParams) {
+  return fmt == kKvBf16      ? qk_norm_rope_kernel<0, LEAVED, LOG>
+         : fmt == kKvFp8E4M3 ? qk_norm_rope_kernel<1, LEAVED, LOG>
+                             : qk_norm_rope_kernel<2, LEAVED, LOG>;
+}
+template <bool LEAVED>
+static void (*rope_kernel(int fmt, int log))(const RopeParams) {
+  switch (log) {
+    case 3: return rope_kernel<LEAVED, 3>(fmt);
+    case 4: return rope_kernel<LEAVED, 4>(fmt);
+    case 5: return rope_kernel<LEAVED, 5>(fmt);
+    default: return rope_kernel<LEAVED, 2>(fmt);  // d <= 32 (lanes may be idle)
   }
 }
 
@@ -225,30 +282,24 @@ int launch_qk_norm_rope(const RopeArgs &a, cudaStream_t st) {
   RopeParams p;
   p.a = a;
   p.chunks = a.d / 8;
-  p.log_lanes = 0;
-  while ((1 << p.log_lanes) < p.chunks) ++p.log_lanes;
+  int log = 2;
+  while ((1 << log) < p.chunks) ++log;
   p.turned = a.rotary / 8;
   p.inv_d = 1.0f / (float)a.d;
   const int nsm = num_sms_current_device();
   if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   // Warps that share a token's rows: enough that the GPU holds about 16 warps
   // an SM, at most one a row step.
-  const int rows = 32 >> p.log_lanes;
+  const int rows = 32 >> log;
   p.q_steps = (a.hq + rows - 1) / rows;
-  p.k_steps = p.q_steps + (a.hkv + rows - 1) / rows;
-  p.steps = p.k_steps + (a.v ? (a.hkv + rows - 1) / rows : 0);
+  p.k_steps = (a.hkv + rows - 1) / rows;
+  const int steps = p.q_steps + p.k_steps * (a.v ? 2 : 1);
   const int64_t want = ((int64_t)nsm * 16 + a.n_tokens - 1) / a.n_tokens;
-  p.parts = (int)(want < p.steps ? want : p.steps);
+  p.parts = (int)(want < steps ? want : steps);
   p.warps = a.n_tokens * p.parts;
   const int64_t need = (p.warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   const unsigned grid = (unsigned)(need < (1 << 30) ? need : (1 << 30));
-  auto kernel = a.interleaved
-                    ? (a.kv_fmt == kKvBf16      ? qk_norm_rope_kernel<0, true>
-                       : a.kv_fmt == kKvFp8E4M3 ? qk_norm_rope_kernel<1, true>
-                                                : qk_norm_rope_kernel<2, true>)
-                    : (a.kv_fmt == kKvBf16      ? qk_norm_rope_kernel<0, false>
-                       : a.kv_fmt == kKvFp8E4M3 ? qk_norm_rope_kernel<1, false>
-                                                : qk_norm_rope_kernel<2, false>);
+  auto kernel = a.interleaved ? rope_kernel<true>(a.kv_fmt, log) : rope_kernel<false>(a.kv_fmt, log);
   cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kRopeThreads), 0, st, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));

@@ -974,14 +974,75 @@ def decode_attention_fwd_streaming(q, o, k_buffer, v_buffer, kv_indptr, kv_indic
 
 
 # ------------------------------------------- a decode step around the paged pool
-def _row_output(out, like, name):
-    """The output for rows shaped as ``like``: ``out``, or a new tensor."""
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if out.shape != like.shape or out.get_device() != like.get_device():
-        raise ValueError(f"{name} is {tuple(out.shape)} on {out.device}, expected "
-                         f"{tuple(like.shape)} on {like.device}")
-    return out
+# These calls are made for every layer of every decode step, often with a few
+# microseconds of GPU work each, so each tensor is looked at once: a helper checks it
+# and returns its address.
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(index, fn, *args):
+    """_on for a device index."""
+    if _current_device() == index:
+        return _check(fn(*args, _raw_stream(index)))
+    with torch.cuda.device(index):
+        return _check(fn(*args, torch.cuda.current_stream(index).cuda_stream))
+
+
+def _gpu(t, name):
+    """Index of the GPU that ``t`` is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    return index
+
+
+def _flat_at(t, dtype, n, index, name):
+    """Address of a contiguous tensor of ``n`` entries."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} entries on "
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _dense_at(t, dtype, shape, index, name):
+    """Address of a contiguous tensor of ``shape``."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(shape)} on "
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows_at(t, shape, index, name):
+    """Address, row stride and head stride of bf16 rows [n, heads, dim]."""
+    st = t.stride()
+    if t.dtype is not _BF16 or t.shape != shape or st[2] != 1 or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor {tuple(shape)} on cuda:{index} with a "
+                         f"contiguous last dim, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _pool_at(t, index, name):
+    """Address, slot stride, head stride, (slots, heads, dim) and PKX_KV_*
+    format of a bf16 or fp8 pool."""
+    shape, st, fmt = t.shape, t.stride(), _KV_CODES.get(t.dtype)
+    if fmt is None or len(shape) != 3 or st[2] != 1 or t.get_device() != index:
+        raise ValueError(f"{name} must be a bf16 or fp8 [slots, heads, dim] tensor on cuda:{index} "
+                         f"with a contiguous last dim, got {t.dtype} {tuple(shape)} on {t.device}")
+    return t.data_ptr(), st[0], st[1], shape, fmt
+
+
+def _workspace_at(ws, index, size_fn, work, *shape):
+    """(workspace, its address, its bytes): the caller's, or a new one of
+    size_fn(*shape) bytes on GPU ``index`` (``work`` as in _workspace)."""
+    if ws is None:
+        with torch.cuda.device(index):
+            ws = _workspace(None, size_fn(*shape), torch.device("cuda", index), work)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{index}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_weight=None,
@@ -995,101 +1056,78 @@ def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_w
     the new keys (and ``v``) also go to that slot of ``k_buffer`` (and
     ``v_buffer``), bf16 or fp8.  ``q_out`` / ``k_out`` may be ``q`` / ``k``.
     Returns (q_out, k_out)."""
-    lib = load_library()
-    qs, ks = _rows(q, "q"), _rows(k, "k")
-    n, hq, d = q.shape
-    hkv = k.shape[1]
-    if tuple(k.shape) != (n, hkv, d):
-        raise ValueError(f"k {tuple(k.shape)} does not fit q {tuple(q.shape)}")
-    dev = q.device
-    q_out, k_out = _row_output(q_out, q, "q_out"), _row_output(k_out, k, "k_out")
-    qo, ko = _rows(q_out, "q_out"), _rows(k_out, "k_out")
+    lib = _lib or load_library()
+    index = _gpu(q, "q")
+    q_shape, k_shape = q.shape, k.shape
+    if len(q_shape) != 3 or len(k_shape) != 3:
+        raise ValueError("q and k must be [n, heads, dim]")
+    n, hq, d = q_shape
+    hkv = k_shape[1]
+    if k_shape[0] != n or k_shape[2] != d:
+        raise ValueError(f"k {tuple(k_shape)} does not fit q {tuple(q_shape)}")
+    q_at, k_at = _rows_at(q, q_shape, index, "q"), _rows_at(k, k_shape, index, "k")
+    if q_out is None:
+        q_out = torch.empty(q_shape, dtype=_BF16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k_shape, dtype=_BF16, device=k.device)
+    pos_at = axis_at = table_at = None
     axes, rotary, rows = 1, 0, 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 [max_position, rotary] tensor")
-        rows, rotary = cos_sin.shape
         if positions is None:
             raise ValueError("cos_sin needs positions")
-        _i64_vec(positions, "positions")
-        if positions.dim() not in (1, 2) or positions.shape[-1] != n:
-            raise ValueError(f"positions must be [{n}] or [axes, {n}], got {tuple(positions.shape)}")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
+        rows, rotary = cos_sin.shape
+        table_at = _dense_at(cos_sin, _F32, (rows, rotary), index, "cos_sin")
+        pos_shape = positions.shape
+        if len(pos_shape) == 2:
+            axes = pos_shape[0]
+        pos_at = _dense_at(positions, _I64, (n,) if len(pos_shape) == 1 else (axes, n), index,
+                           "positions")
         if pair_axis is not None:
-            if pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
-                raise ValueError("pair_axis must be a contiguous uint8 tensor")
-            _check_len(pair_axis, rotary // 2, "pair_axis")
+            axis_at = _flat_at(pair_axis, _U8, rotary // 2, index, "pair_axis")
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need cos_sin")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if w.dtype != torch.bfloat16 or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous bf16 tensor")
-            _check_len(w, d, name)
-    vs, kb, vb, fmt, slots = (0, 0), (0, 0), (0, 0), PKX_KV_BF16, 0
-    if cache_loc is None:
-        if v is not None or k_buffer is not None or v_buffer is not None:
-            raise ValueError("the KV write needs cache_loc")
-    else:
-        _i64_vec(cache_loc, "cache_loc")
-        _check_len(cache_loc, n, "cache_loc")
+    qw_at = None if q_weight is None else _flat_at(q_weight, _BF16, d, index, "q_weight")
+    kw_at = None if k_weight is None else _flat_at(k_weight, _BF16, d, index, "k_weight")
+    v_at, kb, vb = (None, 0, 0), (None, 0, 0), (None, 0, 0)
+    loc_at, fmt, slots = None, PKX_KV_BF16, 0
+    if cache_loc is not None:
         if k_buffer is None or (v is None) != (v_buffer is None):
             raise ValueError("the KV write needs k_buffer, and v and v_buffer together")
-        if v is None:
-            kb, _, fmt = _pool_rows(k_buffer, k_buffer)
-        else:
-            kb, vb, fmt = _pool_rows(k_buffer, v_buffer)
-            vs = _rows(v, "v")
-            if tuple(v.shape) != (n, hkv, d) or v_buffer.shape != k_buffer.shape:
-                raise ValueError("v and v_buffer must be shaped as k and k_buffer")
-        slots = k_buffer.shape[0]
-        if tuple(k_buffer.shape[1:]) != (hkv, d):
-            raise ValueError(f"k_buffer {tuple(k_buffer.shape)} does not fit k {tuple(k.shape)}")
-    _one_device(dev, k=k, positions=positions, cos_sin=cos_sin, q_weight=q_weight,
-                k_weight=k_weight, pair_axis=pair_axis, cache_loc=cache_loc, v=v,
-                k_buffer=k_buffer, v_buffer=v_buffer)
-    _check(_on(
-        dev, lib.pkx_qk_norm_rope,
-        q.data_ptr(), *qs, k.data_ptr(), *ks, _address(v), *vs, n, hq, hkv, d,
-        _address(positions), axes, _address(pair_axis), _address(cos_sin), rows, rotary,
-        1 if interleaved else 0, _address(q_weight), _address(k_weight), float(eps),
-        float(weight_offset), q_out.data_ptr(), *qo, k_out.data_ptr(), *ko, _address(cache_loc),
-        _address(k_buffer), *kb, _address(v_buffer), *vb, slots, fmt, float(k_scale),
-        float(v_scale)))
+        loc_at = _flat_at(cache_loc, _I64, n, index, "cache_loc")
+        *kb, shape, fmt = _pool_at(k_buffer, index, "k_buffer")
+        slots = shape[0]
+        if shape[1] != hkv or shape[2] != d:
+            raise ValueError(f"k_buffer {tuple(shape)} does not fit k {tuple(k_shape)}")
+        if v is not None:
+            v_at = _rows_at(v, k_shape, index, "v")
+            *vb, v_shape, v_fmt = _pool_at(v_buffer, index, "v_buffer")
+            if v_shape != shape or v_fmt != fmt:
+                raise ValueError("k_buffer and v_buffer must have the same shape and type")
+    elif v is not None or k_buffer is not None or v_buffer is not None:
+        raise ValueError("the KV write needs cache_loc")
+    _call(index, lib.pkx_qk_norm_rope, *q_at, *k_at, *v_at, n, hq, hkv, d, pos_at, axes, axis_at,
+          table_at, rows, rotary, 1 if interleaved else 0, qw_at, kw_at, eps, weight_offset,
+          *_rows_at(q_out, q_shape, index, "q_out"), *_rows_at(k_out, k_shape, index, "k_out"),
+          loc_at, *kb, *vb, slots, fmt, k_scale, v_scale)
     return q_out, k_out
-
-
-def _check_bounds(bounds, hkv, d):
-    """Pages of a bounds tensor bf16 [pages, hkv, 2, d]."""
-    if bounds.dtype != torch.bfloat16 or not bounds.is_contiguous() or bounds.dim() != 4 or \
-            tuple(bounds.shape[1:]) != (hkv, 2, d):
-        raise ValueError(f"bounds must be a contiguous bf16 [pages, {hkv}, 2, {d}] tensor, got "
-                         f"{bounds.dtype} {tuple(bounds.shape)}")
-    return bounds.shape[0]
 
 
 def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
     """Smallest and largest key value of each listed page, per KV head and dim
-    (pkx_update_page_bounds): bounds[page, h, 0 / 1, :], in place.  The pool
-    (bf16 or fp8) is [pages * page_size or more slots, hkv, d]; ``page_ids``
-    int32 [n], ``page_lens`` int32 [n] (the slots in use; None: all).  Returns
-    ``bounds``."""
-    lib = load_library()
-    kb, _, fmt = _pool_rows(k_buffer, k_buffer)
-    slots, hkv, d = k_buffer.shape
-    pages = _check_bounds(bounds, hkv, d)
-    page_size = int(page_size)
+    (pkx_update_page_bounds): bounds[page, h, 0 / 1, :], in place, bf16
+    [pages, hkv, 2, d].  The pool (bf16 or fp8) is [pages * page_size or more
+    slots, hkv, d]; ``page_ids`` int32 [n], ``page_lens`` int32 [n] (the slots
+    in use; None: all).  Returns ``bounds``."""
+    lib = _lib or load_library()
+    index = _gpu(k_buffer, "k_buffer")
+    *kb, (slots, hkv, d), fmt = _pool_at(k_buffer, index, "k_buffer")
+    pages, page_size, n = bounds.shape[0], int(page_size), page_ids.numel()
+    bounds_at = _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds")
     if page_size < 1 or pages * page_size > slots:
         raise ValueError(f"{pages} pages of {page_size} slots do not fit a pool of {slots} slots")
-    _i32(page_ids, "page_ids")
-    n = page_ids.numel()
-    if page_lens is not None:
-        _i32(page_lens, "page_lens")
-        _check_len(page_lens, n, "page_lens")
-    _one_device(k_buffer.device, bounds=bounds, page_ids=page_ids, page_lens=page_lens)
-    _check(_on(
-        k_buffer.device, lib.pkx_update_page_bounds, k_buffer.data_ptr(), *kb, fmt, page_size,
-        pages, hkv, d, page_ids.data_ptr(), _address(page_lens), n, bounds.data_ptr()))
+    lens_at = None if page_lens is None else _flat_at(page_lens, _I32, n, index, "page_lens")
+    _call(index, lib.pkx_update_page_bounds, *kb, fmt, page_size, pages, hkv, d,
+          _flat_at(page_ids, _I32, n, index, "page_ids"), lens_at, n, bounds_at)
     return bounds
 
 
@@ -1103,43 +1141,42 @@ def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pa
     KV head (pkx_select_pages): q [B, hq, d], bounds of update_page_bounds,
     kv_indptr / kv_indices over pages.  Returns (selected int32
     [B, hkv, top_k], workspace)."""
-    lib = load_library()
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda:
-        raise ValueError("q must be a contiguous CUDA bf16 [batch, heads, dim] tensor")
-    b, hq, d = q.shape
-    hkv = bounds.shape[1] if bounds.dim() == 4 else 0
-    pages = _check_bounds(bounds, hkv, d)
-    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
-    _check_len(kv_indptr, b + 1, "kv_indptr")
-    top_k = int(top_k)
+    lib = _lib or load_library()
+    index = _gpu(q, "q")
+    q_shape, b_shape, top_k = q.shape, bounds.shape, int(top_k)
+    if len(q_shape) != 3 or len(b_shape) != 4:
+        raise ValueError("q must be [batch, heads, dim] and bounds [pages, heads, 2, dim]")
+    b, hq, d = q_shape
+    pages, hkv = b_shape[0], b_shape[1]
     if selected is None:
-        selected = torch.empty(b, hkv, max(top_k, 0), dtype=torch.int32, device=q.device)
-    else:
-        _i32(selected, "selected")
-        if tuple(selected.shape) != (b, hkv, top_k):
-            raise ValueError(f"selected is {tuple(selected.shape)}, expected {(b, hkv, top_k)}")
-    _one_device(q.device, bounds=bounds, kv_indptr=kv_indptr, kv_indices=kv_indices,
-                selected=selected, workspace=workspace)
+        selected = torch.empty((b, hkv, max(top_k, 0)), dtype=_I32, device=q.device)
     n = kv_indices.numel()
-    ws = _own_workspace(workspace, select_pages_workspace_size, q.device, b, hkv, n)
-    _check(_on(
-        q.device, lib.pkx_select_pages, q.data_ptr(), bounds.data_ptr(), pages,
-        kv_indptr.data_ptr(), kv_indices.data_ptr(), n, b, hq, hkv, d, top_k, int(first_pages),
-        int(last_pages), selected.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()))
+    ws, ws_at, ws_bytes = _workspace_at(workspace, index, select_pages_workspace_size, b, hkv, n)
+    _call(index, lib.pkx_select_pages, _dense_at(q, _BF16, q_shape, index, "q"),
+          _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds"), pages,
+          _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"),
+          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n, b, hq, hkv, d, top_k,
+          int(first_pages), int(last_pages),
+          _dense_at(selected, _I32, (b, hkv, max(top_k, 0)), index, "selected"), ws_at, ws_bytes)
     return selected, ws
 
 
-def _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr, kv_indices):
-    """Checks shared by the two decode forms below: (tokens, hq, hkv, lq, lv),
-    pool strides, pool format."""
-    kb, vb, fmt = _pool_rows(k_buffer, v_buffer)
-    if k_buffer.shape[:2] != v_buffer.shape[:2]:
-        raise ValueError("k_buffer and v_buffer must have the same slots and heads")
-    dims = (*k_buffer.shape, v_buffer.shape[2])
-    out = _check_fp4_attn(q, o, lse, dims)
-    _i32(kv_indptr, "kv_indptr"), _i32(kv_indices, "kv_indices")
-    _check_len(kv_indptr, out[0] + 1, "kv_indptr")
-    return out, (*kb, *vb), fmt
+def _listed_at(q, o, lse, k_buffer, v_buffer, kv_indptr, index):
+    """Checks shared by the two decode forms below.  Returns the shapes
+    (batch, hq, hkv, lq, lv), the addresses (q, o, lse, kv_indptr), K's and V's
+    (address, slot stride, head stride), slots and the pool's format."""
+    *kb, (slots, hkv, lq), fmt = _pool_at(k_buffer, index, "k_buffer")
+    *vb, (v_slots, v_heads, lv), v_fmt = _pool_at(v_buffer, index, "v_buffer")
+    if v_slots != slots or v_heads != hkv or v_fmt != fmt:
+        raise ValueError("k_buffer and v_buffer must have the same slots, heads and type")
+    q_shape = q.shape
+    if len(q_shape) != 3 or q_shape[2] != lq:
+        raise ValueError(f"q must be [batch, heads, {lq}] as k_buffer's rows, got {tuple(q_shape)}")
+    b, hq, _ = q_shape
+    lse_at = None if lse is None else _dense_at(lse, _F32, (b, hq), index, "lse")
+    return ((b, hq, hkv, lq, lv), _dense_at(q, _BF16, q_shape, index, "q"),
+            _dense_at(o, _BF16, (b, hq, lv), index, "o"), lse_at,
+            _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"), kb, vb, slots, fmt)
 
 
 def decode_pages_workspace_size(batch, hq, hkv, lq, lv, page_size, top_k) -> int:
@@ -1155,26 +1192,19 @@ def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, 
     select_pages gives, the paged format of expand_paged_kv_indices.  Writes o
     (and lse) in place; other arguments as decode_attention_fwd.  Returns the
     workspace."""
-    lib = load_library()
-    (b, hq, hkv, lq, lv), strides, fmt = _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr,
-                                                       kv_indices)
-    _i32(kv_last_page_len, "kv_last_page_len"), _i32(selected, "selected")
-    _check_len(kv_last_page_len, b, "kv_last_page_len")
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (b, hkv):
-        raise ValueError(f"selected is {tuple(selected.shape)}, expected [{b}, {hkv}, top_k]")
-    top_k, page_size = selected.shape[2], int(page_size)
-    _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
-                kv_indices=kv_indices, kv_last_page_len=kv_last_page_len, selected=selected,
-                lse=lse, workspace=workspace)
-    ws = _own_workspace(workspace, decode_pages_workspace_size, q.device, b, b, hq, hkv, lq, lv,
-                        page_size, top_k)
-    _check(_on(
-        q.device, lib.pkx_decode_attention_fwd_pages,
-        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
-        kv_indices.data_ptr(), kv_indices.numel(), kv_last_page_len.data_ptr(), page_size,
-        selected.data_ptr(), top_k, b, hq, hkv, lq, lv, *strides, k_buffer.shape[0],
-        float(sm_scale or 0.0), float(logit_cap or 0.0), fmt, float(k_scale), float(v_scale),
-        _address(lse), ws.data_ptr(), ws.numel() * ws.element_size()))
+    lib = _lib or load_library()
+    index = _gpu(q, "q")
+    dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
+        q, o, lse, k_buffer, v_buffer, kv_indptr, index)
+    b, n, top_k, page_size = dims[0], kv_indices.numel(), selected.shape[-1], int(page_size)
+    ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_pages_workspace_size, b, *dims,
+                                        page_size, top_k)
+    _call(index, lib.pkx_decode_attention_fwd_pages, q_at, o_at, kb[0], vb[0], ptr_at,
+          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n,
+          _flat_at(kv_last_page_len, _I32, b, index, "kv_last_page_len"), page_size,
+          _dense_at(selected, _I32, (b, dims[2], top_k), index, "selected"), top_k, *dims, kb[1],
+          kb[2], vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale, v_scale,
+          lse_at, ws_at, ws_bytes)
     return ws
 
 
@@ -1190,22 +1220,17 @@ def decode_attention_fwd_shared(q, o, k_buffer, v_buffer, kv_indptr, kv_indices,
     group_indptr[g] .. group_indptr[g + 1] - 1 have their first shared_lens[g]
     keys in common; both int32.  Other arguments as decode_attention_fwd.
     Returns the workspace."""
-    lib = load_library()
-    (b, hq, hkv, lq, lv), strides, fmt = _check_listed(q, o, lse, k_buffer, v_buffer, kv_indptr,
-                                                       kv_indices)
-    _i32(group_indptr, "group_indptr"), _i32(shared_lens, "shared_lens")
-    groups = shared_lens.numel()
-    _check_len(group_indptr, groups + 1, "group_indptr")
-    _one_device(q.device, o=o, k_buffer=k_buffer, v_buffer=v_buffer, kv_indptr=kv_indptr,
-                kv_indices=kv_indices, group_indptr=group_indptr, shared_lens=shared_lens,
-                lse=lse, workspace=workspace)
-    ws = _own_workspace(workspace, decode_shared_workspace_size, q.device, b, b, groups, hq, hkv,
-                        lq, lv)
-    _check(_on(
-        q.device, lib.pkx_decode_attention_fwd_shared,
-        q.data_ptr(), o.data_ptr(), k_buffer.data_ptr(), v_buffer.data_ptr(), kv_indptr.data_ptr(),
-        kv_indices.data_ptr(), group_indptr.data_ptr(), shared_lens.data_ptr(), groups, b, hq, hkv,
-        lq, lv, *strides, k_buffer.shape[0], float(sm_scale or 0.0), float(logit_cap or 0.0), fmt,
-        float(k_scale), float(v_scale), _address(lse), ws.data_ptr(),
-        ws.numel() * ws.element_size()))
+    lib = _lib or load_library()
+    index = _gpu(q, "q")
+    dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
+        q, o, lse, k_buffer, v_buffer, kv_indptr, index)
+    b, groups = dims[0], shared_lens.numel()
+    ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_shared_workspace_size, b, b,
+                                        groups, *dims[1:])
+    _call(index, lib.pkx_decode_attention_fwd_shared, q_at, o_at, kb[0], vb[0], ptr_at,
+          _flat_at(kv_indices, _I32, kv_indices.numel(), index, "kv_indices"),
+          _flat_at(group_indptr, _I32, groups + 1, index, "group_indptr"),
+          _flat_at(shared_lens, _I32, groups, index, "shared_lens"), groups, *dims, kb[1], kb[2],
+          vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale, v_scale, lse_at,
+          ws_at, ws_bytes)
     return ws
