@@ -78,20 +78,33 @@ template <int D>
 __global__ void __launch_bounds__(256, 4) listed_combine_kernel(
     const ListedRow *__restrict__ rows, const float *__restrict__ plse,
     const float *__restrict__ po, bf16 *__restrict__ o, float *__restrict__ lse, int batch, int hq,
-    int group, int b_head, int b_step, int b_streams, const int32_t *__restrict__ err, int n_err,
-    int32_t *status) {
+    int group, int b_head, int b_step, int b_streams, int b_n, const int32_t *__restrict__ err,
+    int n_err, int err_sets, int32_t *status) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr float kLog2e = 1.4426950408889634f;
-  if (err && blockIdx.x == 0)  // errors that the listing kernel's CTAs found
-    for (int i = threadIdx.x; i < n_err; i += blockDim.x)
-      if (err[i]) record_status(status, PKX_EDEVICE);
+  if (err && blockIdx.x == 0) {  // errors that the warps or CTAs before found
+    int bad = 0;
+    for (int i = threadIdx.x; i < n_err; i += blockDim.x) bad |= err[i];
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+      if (err_sets) *status = bad ? PKX_EDEVICE : PKX_OK;
+      else if (bad) record_status(status, PKX_EDEVICE);
+    }
+  }
   const int lane = threadIdx.x & 31;
   const int nw = (gridDim.x * blockDim.x) >> 5;
   for (int64_t r = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < (int64_t)batch * hq; r += nw) {
     const int t = (int)(r / hq), head = (int)(r - (int64_t)t * hq);
     const int kvh = head / group, g = head - kvh * group;
-    const ListedRow R = rows[t];
+    // (without a table: b_n pieces of each of the token's KV heads in turn)
+    ListedRow R{};
+    if (rows) {
+      R = rows[t];
+    } else {
+      R.b = t * (hq / group) * b_head;
+      R.b_n = b_n;
+    }
     const int na = R.a_n * R.a_streams, n = na + b_streams * R.b_n;
     auto row_of = [&](int i) -> int64_t {
       int64_t gr;
@@ -160,8 +173,9 @@ __global__ void __launch_bounds__(256, 4) listed_combine_kernel(
   }
 }
 
-// Fields of the header's padding: first unit, units and claim counter of rows_kernel.
-enum { kRowsFirst = 0, kRowsCount = 1, kRowsNext = 2 };
+// Fields of the header's padding: first granule, units and claim counter of
+// rows_kernel.
+enum { kRowsGran = 0, kRowsCount = 1, kRowsNext = 2 };
 
 // --------------------------------------------------------- one-token units
 // A warp a unit: the 16 rows of mma.sync m16n8k16 are the query heads of one KV
@@ -198,12 +212,18 @@ struct RowsParams {
   int64_t k_ss, k_sh, v_ss, v_sh;  // bytes
   int64_t num_slots;
   const int32_t *kv_indptr, *kv_indices;
-  const WorkUnit *units;
   WsHeader *hdr;
   float *plse, *po;
-  int hq, group;
+  int batch, hq, hkv, group;
   float scale_log2, cap_pre, cap_log2, v_scale;
   int use_cap;
+  // own keys: first key, and first piece of each sequence [batch + 1]
+  const int32_t *own_begin, *own_first;
+  // selected pages
+  const int32_t *selected, *last_page_len;
+  int64_t n_indices;
+  int top_k, page_size, pieces;
+  int32_t *err;  // [units]
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -235,11 +255,15 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t codes) {
   return pack_bf16(f.x, f.y);
 }
 
-template <int D, int FMT>
+// The unit's keys: own keys (units are pieces of the sequences, KV heads
+// innermost), or (PAGES) top_k * page_size places for keys of selected pages, of
+// which an entry below 0 or a part of the last page leaves some empty.
+template <int D, int FMT, bool PAGES>
 __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsParams p) {
   using C = RowsCfg<D, FMT>;
   constexpr int RP = 32 / C::CPR;  // rows of one copy instruction
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_empty[kRowsWarps][C::STAGES];  // places without a key, a bit each
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -247,41 +271,94 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
   // chunk c of row r in a stage: c ^ r % 8 (rows of 64 bytes: two to a line)
   auto spread = [](int r, int c) { return C::CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); };
-  const int first = p.hdr->pad[kRowsFirst], count = p.hdr->pad[kRowsCount];
+  const int count = PAGES ? p.batch * p.hkv * p.pieces : p.hdr->pad[kRowsCount];
+  const int gran0 = PAGES ? 0 : p.hdr->pad[kRowsGran];
   const int warps = gridDim.x * kRowsWarps;
-  bool bad = false;
   // the first unit by the warp's number (neighbouring units, which share a
-  // sequence's slots, on different SMs), the others claimed
+  // sequence's slots, on different SMs); then own keys are claimed (ragged), and
+  // pages, of equal sizes, taken in turn
   for (int u = warp * gridDim.x + blockIdx.x; u < count;) {
-    const WorkUnit w = p.units[first + u];
-    const int n = w.k_end - w.k_begin, steps = (n + 15) / 16;
-    const int32_t *idx = p.kv_indices + __ldg(p.kv_indptr + w.b) + w.k_begin;
+    int b, kvh, k_begin, k_end, at, n_pages = 0, last_len = 0;
+    bool bad = false;
+    const int32_t *sel = nullptr;
+    if constexpr (PAGES) {
+      const int pair = u / p.pieces, sp = u - pair * p.pieces;
+      b = pair / p.hkv;
+      kvh = pair - b * p.hkv;
+      const int places = p.top_k * p.page_size, runs = (places + kRowRun - 1) / kRowRun;
+      k_begin = piece_at(sp, runs, p.pieces, kRowRun, places);
+      k_end = piece_at(sp + 1, runs, p.pieces, kRowRun, places);
+      sel = p.selected + (int64_t)pair * p.top_k;
+      at = __ldg(p.kv_indptr + b);
+      n_pages = __ldg(p.kv_indptr + b + 1) - at;
+      if (at < 0 || n_pages < 0 || (int64_t)at + n_pages > p.n_indices) {
+        bad = true;
+        n_pages = 0;
+      }
+      if (n_pages > 0) {
+        last_len = __ldg(p.last_page_len + b);
+        bad |= last_len < 0 || last_len > p.page_size;
+        last_len = min(max(last_len, 0), p.page_size);
+      }
+    } else {
+      const int x = u / p.hkv;
+      kvh = u - x * p.hkv;
+      b = 0;  // the last sequence whose first piece is at most x, by 32 probes at a time
+      for (int span = p.batch; span > 1;) {
+        const int step = (span + 31) / 32, i = lane * step;
+        const bool before = i < span && (i == 0 || __ldg(p.own_first + b + i) <= x);
+        const int top = 31 - __clz(__ballot_sync(0xffffffffu, before));
+        b += top * step;
+        span = min(step, span - top * step);
+      }
+      const int first = __ldg(p.own_first + b), S = __ldg(p.own_first + b + 1) - first;
+      at = __ldg(p.kv_indptr + b);
+      const int begin = __ldg(p.own_begin + b), keys = __ldg(p.kv_indptr + b + 1) - at - begin;
+      const int runs = keys / kRowRun + (keys % kRowRun != 0);
+      k_begin = begin + piece_at(x - first, runs, S, kRowRun, keys);
+      k_end = begin + piece_at(x - first + 1, runs, S, kRowRun, keys);
+    }
+    const int n = k_end - k_begin, steps = (n + 15) / 16;
     const int row = lane / C::CPR, chunk = lane % C::CPR;  // of this lane's copies
-    const uint8_t *kp = p.k + w.kvh * p.k_sh + chunk * 16, *vp = p.v + w.kvh * p.v_sh + chunk * 16;
+    const uint8_t *kp = p.k + kvh * p.k_sh + chunk * 16, *vp = p.v + kvh * p.v_sh + chunk * 16;
     // slots of 32 keys at a time, one block ahead: `slots` of the block that the
-    // copies are in, `coming` of the next
+    // copies are in, `coming` of the next; kNone: no key, kOutside: outside the pool
+    constexpr int kNone = -1, kOutside = -2;
     auto fetch = [&](int block) {
       const int i = block * 32 + lane;
-      return i < n ? __ldg(idx + i) : -1;
+      if (i >= n) return kNone;
+      if constexpr (PAGES) {
+        const int e = (k_begin + i) / p.page_size, off = k_begin + i - e * p.page_size;
+        const int s = __ldg(sel + e);
+        bad |= s >= n_pages;
+        if (s < 0 || s >= n_pages || (s == n_pages - 1 && off >= last_len)) return kNone;
+        const int page = __ldg(p.kv_indices + at + s);
+        const int64_t slot = (int64_t)page * p.page_size + off;
+        // (a page is inside the pool as a whole or not at all)
+        return page < 0 || slot - off + p.page_size > p.num_slots ? kOutside : (int)slot;
+      } else {
+        const int s = __ldg(p.kv_indices + at + k_begin + i);
+        return (uint32_t)s < (uint64_t)p.num_slots ? s : kOutside;
+      }
     };
     int slots = fetch(0), coming = fetch(1);
-    auto checked = [&](int s, int block) {
-      if ((uint32_t)s >= (uint64_t)p.num_slots) {
-        bad |= block * 32 + lane < n;
-        return -1;
-      }
-      return s;
-    };
-    slots = checked(slots, 0);
+    bad |= slots == kOutside;
     auto issue = [&](int step) {
       if (step < steps) {
         if ((step & 1) == 0 && step > 0) {
-          slots = checked(coming, step >> 1);
+          slots = coming;
+          bad |= slots == kOutside;
           coming = fetch((step >> 1) + 1);
         }
+        uint32_t none = 0;
+        if constexpr (PAGES) {
+          none = (__ballot_sync(0xffffffffu, slots == kNone) >> ((step & 1) * 16)) & 0xFFFFu;
+          if (lane == 0) s_empty[warp][step % C::STAGES] = none;
+        }
         const uint32_t stage = ring + (step % C::STAGES) * C::STAGE;
+        // (a step of empty places is passed over)
 #pragma unroll
-        for (int i = 0; i < 16 / RP; ++i) {
+        for (int i = 0; i < 16 / RP && none != 0xFFFFu; ++i) {
           const int r = i * RP + row;
           const int s = __shfl_sync(0xffffffffu, slots, (step & 1) * 16 + r);
           const uint32_t at = stage + r * C::ROW + spread(r, chunk) * 16;
@@ -298,7 +375,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
     uint32_t qa[D / 16][4];
     {
       const uint32_t *q0 = reinterpret_cast<const uint32_t *>(
-          p.q + ((int64_t)w.q_tok0 * p.hq + (int64_t)w.kvh * p.group + g) * D);
+          p.q + ((int64_t)b * p.hq + (int64_t)kvh * p.group + g) * D);
       const uint32_t *q1 = q0 + 8 * (D / 2);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
@@ -317,7 +394,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
     for (int step = 0; step < steps; ++step) {
       cp_async_wait_group<C::STAGES - 2>();
       __syncwarp();  // the step's rows are here, and all lanes are done with the step before
+      uint32_t empty = 0;
+      if constexpr (PAGES) empty = s_empty[warp][step % C::STAGES];
       issue(step + C::STAGES - 1);
+      if (PAGES && empty == 0xFFFFu) continue;
       const uint32_t sk = ring + (step % C::STAGES) * C::STAGE, sv = sk + 16 * C::ROW;
       float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // keys 0-7, 8-15
       if constexpr (FMT == 0) {
@@ -343,15 +423,19 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
                    fp8x2_to_bf16x2<FMT>(b[3] >> 16));
         }
       }
-      // logits in log2; keys behind the unit's last are -inf
+      // logits in log2; places without a key are -inf
       float x[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         x[i] = p.use_cap ? p.cap_log2 * tanh_approx(x[i] * p.cap_pre) : x[i] * p.scale_log2;
-      if (step * 16 + 16 > n) {
+      if constexpr (!PAGES) {
+        const int left = n - step * 16;
+        if (left < 16) empty = 0xFFFFu << left;
+      }
+      if (empty != 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (step * 16 + ((i >> 1) & 1) * 8 + 2 * t + (i & 1) >= n) x[i] = -INFINITY;
+          if ((empty >> (((i >> 1) & 1) * 8 + 2 * t + (i & 1))) & 1u) x[i] = -INFINITY;
       }
       float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       float t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
@@ -425,7 +509,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
       if (head >= p.group) continue;
       const float l = half ? l1 : l0, m = half ? m1 : m0;
       const float inv = (l == 0.f ? 0.f : 1.0f / l) * p.v_scale;
-      const int64_t out = (int64_t)w.slot * p.group + head;
+      const int64_t out = (int64_t)(gran0 + u) * p.group + head;
       float *dst = p.po + out * D;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
@@ -441,11 +525,19 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
       if (t == 0)
         p.plse[out] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
-    int next = 0;
-    if (lane == 0) next = atomicAdd(&p.hdr->pad[kRowsNext], 1);
-    u = warps + __shfl_sync(0xffffffffu, next, 0);
+    bad = __any_sync(0xffffffffu, bad);
+    if constexpr (PAGES) {
+      if (lane == 0) p.err[u] = bad;
+      u += warps;
+    } else {
+      int next = 0;
+      if (lane == 0) {
+        if (bad) record_status(&p.hdr->status, PKX_EDEVICE);
+        next = atomicAdd(&p.hdr->pad[kRowsNext], 1);
+      }
+      u = warps + __shfl_sync(0xffffffffu, next, 0);
+    }
   }
-  if (bad) record_status(&p.hdr->status, PKX_EDEVICE);
   cp_async_wait_all();
 }
 
@@ -462,7 +554,8 @@ struct SharedParams {
   int rows;         // own keys go to rows_kernel
   int unit_max;
   int64_t gran_max;
-  int32_t *seq;     // [3][batch + 1]: keys, shared keys, first unit of own keys
+  int32_t *seq;     // [2][batch + 1]: keys, shared keys
+  int32_t *own_begin, *own_first;  // [batch + 1] first own key; first piece
   int32_t *grp;     // [4][num_groups + 1]: shared keys, first sequence, first unit, first granule
   int in_smem;      // those arrays in dynamic shared memory instead
   WorkUnit *units;
@@ -470,26 +563,31 @@ struct SharedParams {
   ListedRow *rows_out;
   WsHeader *hdr;
 };
-// Exclusive sum over a block of 1024 threads of one value each, and the total.
-__device__ __forceinline__ int64_t block_sum_before(int64_t v, int64_t *sh, int64_t &total) {
+// Exclusive sum over a block of 1024 threads of one value in [0, kMany] each, and
+// the total; sums are held at kMany, far above any count that the workspace
+// takes (an indptr that decreases can make them larger than 32 bits).
+constexpr uint32_t kMany = 1u << 30;
+__device__ __forceinline__ uint32_t add_held(uint32_t a, uint32_t b) { return min(a + b, kMany); }
+__device__ __forceinline__ uint32_t block_sum_before(uint32_t v, uint32_t *sh, uint32_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = add_held(x, y);
   }
   if (lane == 31) sh[warp] = x;
+  const uint32_t up = __shfl_up_sync(0xffffffffu, x, 1);
   __syncthreads();
-  int64_t t = sh[lane], before = lane < warp ? t : 0;
+  uint32_t t = sh[lane], before = lane < warp ? t : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    t += __shfl_xor_sync(0xffffffffu, t, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+    t = add_held(t, __shfl_xor_sync(0xffffffffu, t, o));
+    before = add_held(before, __shfl_xor_sync(0xffffffffu, before, o));
   }
   __syncthreads();
   total = t;
-  return before + x - v;
+  return lane == 0 ? before : add_held(before, up);
 }
 
 // One CTA of 1024 threads: the units of every group's prefix and of every
@@ -503,30 +601,20 @@ __device__ __forceinline__ int64_t block_sum_before(int64_t v, int64_t *sh, int6
 constexpr int kUnitTiles = 3;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {
   extern __shared__ int32_t s_dyn[];
-  __shared__ int64_t sh[32];
+  __shared__ uint32_t sh[32];
   __shared__ int64_t s_best[32];
-  __shared__ int s_bad, s_longest;
+  __shared__ int s_longest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.batch, NG = p.num_groups;
-  int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + 3 * (B + 1) : p.grp;
-  int32_t *sT = seq, *sS = seq + (B + 1), *sU = seq + 2 * (B + 1);
+  int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + 2 * (B + 1) : p.grp;
+  int32_t *sT = seq, *sS = seq + (B + 1);
   int32_t *gS = grp, *gB = grp + (NG + 1), *gU = grp + 2 * (NG + 1), *gG = grp + 3 * (NG + 1);
   const int blk = 2 * p.tok;  // tokens of a prefix unit
-  if (tid == 0) s_bad = s_longest = 0;
+  if (tid == 0) s_longest = 0;
   grid_dep_wait();
   grid_dep_launch();
-  __syncthreads();
-  bool bad = false;
-  // sequences
-  for (int b = tid; b < B; b += 1024) {
-    const int k0 = p.kv_indptr[b], T = p.kv_indptr[b + 1] - k0;
-    const bool ok = k0 >= 0 && T >= 0;
-    bad |= !ok;
-    sT[b] = ok ? T : 0;
-    sS[b] = 0;
-  }
-  // groups: consecutive runs of sequences, else nothing is shared
-  bool bad_groups = false;
+  // groups are consecutive runs of sequences, else nothing is shared
+  bool bad = false, bad_groups = false;
   for (int g = tid; g <= NG && NG > 0; g += 1024) {
     const int lo = p.group_indptr[g], hi = g < NG ? p.group_indptr[g + 1] : lo;
     const int s = g < NG ? p.shared_lens[g] : 0;
@@ -534,16 +622,20 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     gB[g] = lo;
     gS[g] = s;
   }
-  if (bad_groups) s_bad = 1;
-  bad |= bad_groups;
+  for (int b = tid; b < B; b += 1024) {
+    const int k0 = p.kv_indptr[b], T = p.kv_indptr[b + 1] - k0;
+    const bool ok = k0 >= 0 && T >= 0;
+    bad |= !ok;
+    sT[b] = ok ? T : 0;
+    sS[b] = 0;
+  }
   if (tid == 0) {
     p.hdr->status = 0;
     p.hdr->next_unit = 0;
     p.hdr->pad[kRowsNext] = 0;
   }
-  __syncthreads();
-  if (bad) record_status(&p.hdr->status, PKX_EDEVICE);
-  const bool share = s_bad == 0;
+  const bool share = __syncthreads_or(bad_groups) == 0;
+  if (bad || bad_groups) record_status(&p.hdr->status, PKX_EDEVICE);
   auto tiles = [](int keys) { return keys / kBlockN + (keys % kBlockN != 0); };
   // shared keys of each group (a warp each)
   for (int g = warp; g < NG; g += 32) {
@@ -559,7 +651,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     __syncwarp();
     if (lane == 0) {
       gS[g] = S;
-      atomicMax(&s_longest, tiles(S));
+      if (S > 0) atomicMax(&s_longest, tiles(S));
     }
   }
   __syncthreads();
@@ -574,27 +666,27 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     const int nb = group_blocks(g), last = gB[g + 1] - gB[g] - (nb - 1) * blk;
     return (nb - 1) * blk + (last <= p.tok ? 2 * last : last);
   };
-  int64_t cost = 0, own = 0, all_cost, all_own;
-  for (int b = tid; b < B; b += 1024) own += runs(b);
-  for (int g = tid; g < NG; g += 1024) cost += (int64_t)group_blocks(g) * tiles(gS[g]);
-  block_sum_before(own, sh, all_own);
-  const int R = (int)max((all_own * p.hkv + p.own_target - 1) / p.own_target, (int64_t)p.own_least);
-  auto own_pieces = [&](int b) { return (runs(b) + R - 1) / R; };
+  auto held = [](int64_t x) { return (uint32_t)min(x, (int64_t)kMany); };
   int C = 1;
-  int64_t pre_units = 0, pre_gran = 0;
+  uint32_t pre_units = 0, pre_gran = 0;
+  auto pieces = [&](int g) { return (tiles(gS[g]) + C - 1) / C; };
   if (s_longest > 0) {
+    uint32_t cost = 0, all_cost;
+    for (int g = tid; g < NG; g += 1024)
+      cost = add_held(cost, held((int64_t)group_blocks(g) * tiles(gS[g])));
     block_sum_before(cost, sh, all_cost);
     // (at most four units an SM and one more a block)
-    const int least = (int)max((all_cost * p.hkv + 4 * p.sms - 1) / (4 * p.sms), (int64_t)kMinSplitTiles);
+    const int least = max((int)(((int64_t)all_cost * p.hkv + 4 * p.sms - 1) / (4 * p.sms)),
+                          kMinSplitTiles);
     int64_t best = INT64_MAX;
     for (int j = warp + 1; j <= 64; j += 32) {
       const int c = max((s_longest + j - 1) / j, least);
-      int64_t n = 0;
+      uint32_t n = 0;
       for (int g = lane; g < NG; g += 32)
-        n += (int64_t)group_blocks(g) * ((tiles(gS[g]) + c - 1) / c);
+        n = add_held(n, held((int64_t)group_blocks(g) * ((tiles(gS[g]) + c - 1) / c)));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      const int64_t rounds = (n * p.hkv + p.sms - 1) / p.sms;
+      for (int o = 16; o > 0; o >>= 1) n = add_held(n, __shfl_xor_sync(0xffffffffu, n, o));
+      const int64_t rounds = ((int64_t)n * p.hkv + p.sms - 1) / p.sms;
       best = min(best, (rounds * (c + kUnitTiles) << 24) + min(c, (1 << 24) - 1));
     }
     if (lane == 0) s_best[warp] = best;
@@ -603,33 +695,37 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = min(best, (int64_t)__shfl_xor_sync(0xffffffffu, best, o));
     C = (int)(best & ((1 << 24) - 1));
-  }
-  auto pieces = [&](int g) { return (tiles(gS[g]) + C - 1) / C; };
-  // first unit and granule of each group, first unit of each sequence
-  if (s_longest > 0) {
+    // first unit and granule of each group
     const int gc = (NG + 1023) / 1024, g0 = min(NG, tid * gc), g1 = min(NG, g0 + gc);
-    int64_t nu = 0, ng = 0;
+    uint32_t nu = 0, ng = 0;
     for (int g = g0; g < g1; ++g) {
       if (gS[g] <= 0) continue;
-      nu += (int64_t)pieces(g) * group_blocks(g) * p.hkv;
-      ng += (int64_t)pieces(g) * p.hkv * group_granules(g);
+      nu = add_held(nu, held((int64_t)pieces(g) * group_blocks(g) * p.hkv));
+      ng = add_held(ng, held((int64_t)pieces(g) * p.hkv * group_granules(g)));
     }
     nu = block_sum_before(nu, sh, pre_units);
     ng = block_sum_before(ng, sh, pre_gran);
     for (int g = g0; g < g1; ++g) {
-      gU[g] = (int)min(nu, (int64_t)INT_MAX);
-      gG[g] = (int)min(ng, (int64_t)INT_MAX);
+      gU[g] = (int)nu;
+      gG[g] = (int)ng;
       if (gS[g] <= 0) continue;
-      nu += (int64_t)pieces(g) * group_blocks(g) * p.hkv;
-      ng += (int64_t)pieces(g) * p.hkv * group_granules(g);
+      nu = add_held(nu, held((int64_t)pieces(g) * group_blocks(g) * p.hkv));
+      ng = add_held(ng, held((int64_t)pieces(g) * p.hkv * group_granules(g)));
     }
   }
+  // own keys: pieces of R runs, about own_target of them
+  uint32_t own = 0, all_own;
   const int bc = (B + 1023) / 1024, b0 = min(B, tid * bc), b1 = min(B, b0 + bc);
-  int64_t bu = 0, own_units;
-  for (int b = b0; b < b1; ++b) bu += own_pieces(b);
-  bu = block_sum_before(bu, sh, own_units);
-  own_units *= p.hkv;
-  // (cannot be false: the workspace is sized for the largest counts)
+  for (int b = b0; b < b1; ++b) own = add_held(own, (uint32_t)runs(b));
+  block_sum_before(own, sh, all_own);
+  const int R = max((int)(((int64_t)all_own * p.hkv + p.own_target - 1) / p.own_target), p.own_least);
+  auto own_pieces = [&](int b) { return (runs(b) + R - 1) / R; };
+  uint32_t bu = 0, own_all;
+  for (int b = b0; b < b1; ++b) bu = add_held(bu, (uint32_t)own_pieces(b));
+  bu = block_sum_before(bu, sh, own_all);
+  const int64_t own_units = (int64_t)own_all * p.hkv;
+  // (false only for an indptr that decreases: the workspace is sized for the
+  // largest counts)
   const bool fits = pre_units + own_units <= p.unit_max &&
                     pre_gran + p.own_gran * own_units <= p.gran_max;
   if (!fits) {
@@ -642,8 +738,36 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     return;
   }
   for (int b = b0; b < b1; ++b) {
-    sU[b] = (int)bu;
-    bu += own_pieces(b);
+    p.own_first[b] = (int)bu;
+    p.own_begin[b] = sS[b];
+    // where the token's partials lie
+    ListedRow r{};
+    r.b = (int)pre_gran + p.own_gran * (int)bu * p.hkv;
+    r.b_n = own_pieces(b);
+    bu += r.b_n;
+    if (sS[b] > 0) {
+      int lo = 0, hi = NG - 1;  // last g with gB[g] <= b
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (gB[mid] <= b) lo = mid;
+        else hi = mid - 1;
+      }
+      const int g = lo, i = b - gB[g], k = i / blk;
+      const int n_tok = min(blk, gB[g + 1] - gB[g] - k * blk);
+      r.a = gG[g] + i;
+      r.a_n = pieces(g);
+      r.a_head = group_granules(g);
+      r.a_step = p.hkv * r.a_head;
+      r.a_streams = n_tok <= p.tok ? 2 : 1;
+      r.a_stream = n_tok;
+    }
+    p.rows_out[b] = r;
+  }
+  if (tid == 0) {
+    p.own_first[B] = (int)own_all;
+    p.hdr->n_units = (int)(p.rows ? pre_units : pre_units + own_units);
+    p.hdr->pad[kRowsGran] = (int)pre_gran;
+    p.hdr->pad[kRowsCount] = (int)(p.rows ? own_units : 0);
   }
   __syncthreads();
   // units of the prefixes: group, piece, KV head, block (blocks of one piece
@@ -676,16 +800,17 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     p.units[u] = w;
     p.order[u] = u;
   }
+  if (p.rows) return;  // (rows_kernel finds its units itself)
   // units of the sequences' own keys: sequence, piece, KV head
   for (int i = tid; i < (int)own_units; i += 1024) {
     const int x = i / p.hkv, kvh = i - x * p.hkv;
-    int lo = 0, hi = B - 1;  // last b with sU[b] <= x
+    int lo = 0, hi = B - 1;  // last b with own_first[b] <= x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sU[mid] <= x) lo = mid;
+      if (p.own_first[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    const int b = lo, nr = runs(b), S = own_pieces(b), sp = x - sU[b];
+    const int b = lo, nr = runs(b), S = own_pieces(b), sp = x - p.own_first[b];
     WorkUnit w;
     w.q_tok0 = b;
     w.n_tok = 1;
@@ -700,34 +825,6 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.dq = w.claim = 0;
     p.units[(int)pre_units + i] = w;
     p.order[(int)pre_units + i] = (int)pre_units + i;
-  }
-  // where each token's partials lie
-  for (int b = tid; b < B; b += 1024) {
-    ListedRow r{};
-    if (sS[b] > 0) {
-      int lo = 0, hi = NG - 1;  // last g with gB[g] <= b
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (gB[mid] <= b) lo = mid;
-        else hi = mid - 1;
-      }
-      const int g = lo, i = b - gB[g], k = i / blk;
-      const int n_tok = min(blk, gB[g + 1] - gB[g] - k * blk);
-      r.a = gG[g] + i;
-      r.a_n = pieces(g);
-      r.a_head = group_granules(g);
-      r.a_step = p.hkv * r.a_head;
-      r.a_streams = n_tok <= p.tok ? 2 : 1;
-      r.a_stream = n_tok;
-    }
-    r.b = (int)pre_gran + p.own_gran * sU[b] * p.hkv;
-    r.b_n = own_pieces(b);
-    p.rows_out[b] = r;
-  }
-  if (tid == 0) {
-    p.hdr->n_units = (int)(p.rows ? pre_units : pre_units + own_units);
-    p.hdr->pad[kRowsFirst] = (int)pre_units;
-    p.hdr->pad[kRowsCount] = (int)(p.rows ? own_units : 0);
   }
 }
 
@@ -758,7 +855,7 @@ static ListedLayout shared_layout(int batch, int num_groups, int hkv, int group,
   L.gran_max = 4ll * n * blk + 2ll * hkv * batch + own.gran * (own.target + (int64_t)hkv * batch);
   size_t off = up256(sizeof(WsHeader));
   L.seq_off = off;
-  off = up256(off + sizeof(int32_t) * 3 * (size_t)(batch + 1));
+  off = up256(off + sizeof(int32_t) * 4 * (size_t)(batch + 1));
   L.grp_off = off;
   off = up256(off + sizeof(int32_t) * 4 * (size_t)(num_groups + 1));
   L.units_off = off;
@@ -787,7 +884,6 @@ struct PagesParams {
   int pieces;      // units of a (sequence, KV head)
   int run;         // keys they are cut at
   int gran;        // granules of one
-  int rows;        // they go to rows_kernel
   int cap;         // keys of its list: top_k * page_size
   int32_t *slots;  // [batch * hkv][cap]
   int32_t *ptr;    // [batch * hkv] first key of each list
@@ -863,10 +959,7 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     if (pair == 0) {
       p.hdr->status = 0;
       p.hdr->next_unit = 0;
-      p.hdr->n_units = p.rows ? 0 : gridDim.x * p.pieces;
-      p.hdr->pad[kRowsFirst] = 0;
-      p.hdr->pad[kRowsCount] = p.rows ? gridDim.x * p.pieces : 0;
-      p.hdr->pad[kRowsNext] = 0;
+      p.hdr->n_units = gridDim.x * p.pieces;
     }
     if (kvh == 0) {
       ListedRow R{};
@@ -915,23 +1008,26 @@ static int pages_pieces(int batch, int hkv, int group, int page_size, int top_k,
 static ListedLayout pages_layout(int batch, int hkv, int group, int d, int page_size, int top_k,
                                  int num_sms) {
   ListedLayout L{};
+  const bool rows = group <= kRowsGroup;  // (no units and no lists)
   const int64_t pairs = (int64_t)batch * hkv;
   const int64_t units = pairs * pages_pieces(batch, hkv, group, page_size, top_k, num_sms);
   L.unit_max = (int)std::min<int64_t>(units, INT_MAX / 4);
   L.gran_max = own_units(group, num_sms).gran * units;
   size_t off = up256(sizeof(WsHeader));
-  L.units_off = off;
-  off = up256(off + sizeof(WorkUnit) * (size_t)units);
-  L.order_off = off;
-  off = up256(off + sizeof(int32_t) * (size_t)units);
-  L.rows_off = off;
-  off = up256(off + sizeof(ListedRow) * (size_t)batch);
-  L.ptr_off = off;
-  off = up256(off + sizeof(int32_t) * (size_t)pairs);
   L.err_off = off;
-  off = up256(off + sizeof(int32_t) * (size_t)pairs);
-  L.idx_off = off;
-  off = up256(off + sizeof(int32_t) * (size_t)pairs * top_k * page_size);
+  off = up256(off + sizeof(int32_t) * (size_t)(rows ? units : pairs));
+  if (!rows) {
+    L.units_off = off;
+    off = up256(off + sizeof(WorkUnit) * (size_t)units);
+    L.order_off = off;
+    off = up256(off + sizeof(int32_t) * (size_t)units);
+    L.rows_off = off;
+    off = up256(off + sizeof(ListedRow) * (size_t)batch);
+    L.ptr_off = off;
+    off = up256(off + sizeof(int32_t) * (size_t)pairs);
+    L.idx_off = off;
+    off = up256(off + sizeof(int32_t) * (size_t)pairs * top_k * page_size);
+  }
   L.plse_off = off;
   off = up256(off + sizeof(float) * (size_t)L.gran_max * group);
   L.po_off = off;
@@ -963,27 +1059,30 @@ static int launch_listed(int fmt, const ListedMaps &tm, const KParams &kp, int g
   return launch_attn_kernel<D, kListed>(tm, kp, grid, s);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool PAGES>
 static int launch_rows_as(const RowsParams &p, int nsm, cudaStream_t s) {
   static PerDevice configured;
   if (needs_config(configured)) {
-    cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, FMT>,
+    cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, FMT, PAGES>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          RowsCfg<D, FMT>::SMEM);
     if (e != cudaSuccess)
       return set_error(PKX_ECUDA, "cudaFuncSetAttribute(rows_kernel): %s", cudaGetErrorString(e));
     mark_configured(configured);
   }
-  cudaError_t e = launch_pdl(rows_kernel<D, FMT>, dim3(nsm), dim3(kRowsWarps * 32),
+  cudaError_t e = launch_pdl(rows_kernel<D, FMT, PAGES>, dim3(nsm), dim3(kRowsWarps * 32),
                              RowsCfg<D, FMT>::SMEM, s, p);
   if (e != cudaSuccess) return set_error(PKX_ECUDA, "rows_kernel launch: %s", cudaGetErrorString(e));
   return PKX_OK;
 }
 
+// pieces > 0: selected pages, so many units a (sequence, KV head); 0: own keys.
 template <int D>
-static int launch_rows(const ListedArgs &a, const KParams &kp, int nsm) {
+static int launch_rows(const ListedArgs &a, const KParams &kp, const ListedLayout &L, int nsm,
+                       int pieces) {
   const int size = a.kv_fmt == kKvBf16 ? 2 : 1;
-  RowsParams p;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  RowsParams p{};
   p.q = kp.q;
   p.k = static_cast<const uint8_t *>(a.k_buf);
   p.v = static_cast<const uint8_t *>(a.v_buf);
@@ -992,13 +1091,14 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, int nsm) {
   p.v_ss = a.vb_ss * size;
   p.v_sh = a.vb_sh * size;
   p.num_slots = a.num_slots;
-  p.kv_indptr = kp.kv_indptr;
-  p.kv_indices = static_cast<const int32_t *>(kp.kv_indices);
-  p.units = kp.units;
-  p.hdr = static_cast<WsHeader *>(a.workspace);
+  p.kv_indptr = a.kv_indptr;
+  p.kv_indices = a.kv_indices;
+  p.hdr = reinterpret_cast<WsHeader *>(ws);
   p.plse = kp.plse;
   p.po = kp.po;
+  p.batch = a.batch;
   p.hq = a.hq;
+  p.hkv = a.hkv;
   p.group = kp.group;
   const bool fp8 = a.kv_fmt != kKvBf16;
   p.use_cap = kp.use_cap;
@@ -1006,17 +1106,40 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, int nsm) {
   p.cap_pre = fp8 ? kp.cap_pre_k : kp.cap_pre;
   p.cap_log2 = kp.cap_log2;
   p.v_scale = fp8 ? a.v_scale : 1.0f;
-  if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1>(p, nsm, a.stream);
-  if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2>(p, nsm, a.stream);
-  return launch_rows_as<D, 0>(p, nsm, a.stream);
+  if (pieces > 0) {
+    p.selected = a.selected;
+    p.last_page_len = a.last_page_len;
+    p.n_indices = a.n_indices;
+    p.top_k = a.top_k;
+    p.page_size = a.page_size;
+    p.pieces = pieces;
+    p.err = reinterpret_cast<int32_t *>(ws + L.err_off);
+    if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1, true>(p, nsm, a.stream);
+    if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, true>(p, nsm, a.stream);
+    return launch_rows_as<D, 0, true>(p, nsm, a.stream);
+  }
+  p.own_begin = reinterpret_cast<int32_t *>(ws + L.seq_off) + 2 * (size_t)(a.batch + 1);
+  p.own_first = p.own_begin + (a.batch + 1);
+  if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1, false>(p, nsm, a.stream);
+  if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, false>(p, nsm, a.stream);
+  return launch_rows_as<D, 0, false>(p, nsm, a.stream);
 }
 
-// The attention kernels and the combine over the units in the workspace: the
-// tile kernel where there may be units for it, rows_kernel for groups of at
-// most kRowsGroup heads.
-static int run_listed(const ListedArgs &a, const ListedMaps &tm, const ListedLayout &L, int nsm,
-                      const int32_t *kv_indptr, const int32_t *kv_indices, bool tile_units,
-                      int b_head, int b_step, const int32_t *err, int n_err) {
+// How the combine finds the partials of one-token units.
+struct OwnPartials {
+  const ListedRow *rows;  // or null: `pieces` a KV head, in order
+  int head, step, pieces;
+  const int32_t *err;  // errors of the warps or CTAs before (nullable)
+  int n_err;
+  int err_sets;  // nothing before has set the status word
+};
+
+// The attention kernels and the combine: the tile kernel over the units in the
+// workspace where there may be some, rows_kernel for groups of at most
+// kRowsGroup heads.
+static int run_listed(const ListedArgs &a, const ListedMaps *tm, const ListedLayout &L, int nsm,
+                      const int32_t *kv_indptr, const int32_t *kv_indices, int pieces,
+                      const OwnPartials &own) {
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
   const int group = a.hq / a.hkv;
@@ -1062,12 +1185,12 @@ static int run_listed(const ListedArgs &a, const ListedMaps &tm, const ListedLay
   attention_events(&ev_before, &ev_after);
   if (ev_before) cudaEventRecord(ev_before, a.stream);
   int rc = PKX_OK;
-  if (tile_units)
-    rc = a.d == 128 ? launch_listed<128>(a.kv_fmt, tm, kp, nsm, a.stream)
-                    : launch_listed<64>(a.kv_fmt, tm, kp, nsm, a.stream);
+  if (tm)
+    rc = a.d == 128 ? launch_listed<128>(a.kv_fmt, *tm, kp, nsm, a.stream)
+                    : launch_listed<64>(a.kv_fmt, *tm, kp, nsm, a.stream);
   if (rc != PKX_OK) return rc;
   if (group <= kRowsGroup) {
-    rc = a.d == 128 ? launch_rows<128>(a, kp, nsm) : launch_rows<64>(a, kp, nsm);
+    rc = a.d == 128 ? launch_rows<128>(a, kp, L, nsm, pieces) : launch_rows<64>(a, kp, L, nsm, pieces);
     if (rc != PKX_OK) return rc;
   }
   if (ev_after) cudaEventRecord(ev_after, a.stream);
@@ -1075,10 +1198,9 @@ static int run_listed(const ListedArgs &a, const ListedMaps &tm, const ListedLay
   const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)nsm * 8);
   cudaError_t e = launch_pdl(
       a.d == 128 ? listed_combine_kernel<128> : listed_combine_kernel<64>, dim3(grid), dim3(256), 0,
-      a.stream, reinterpret_cast<const ListedRow *>(ws + L.rows_off), (const float *)kp.plse,
-      (const float *)kp.po, kp.o, a.lse, a.batch, a.hq, group, b_head, b_step,
-      group <= kRowsGroup ? 1 : 2, err, n_err,
-      &hdr->status);
+      a.stream, own.rows, (const float *)kp.plse, (const float *)kp.po, kp.o, a.lse, a.batch, a.hq,
+      group, own.head, own.step, group <= kRowsGroup ? 1 : 2, own.pieces, own.err, own.n_err,
+      own.err_sets, &hdr->status);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "listed_combine launch: %s", cudaGetErrorString(e));
   return PKX_OK;
@@ -1121,8 +1243,10 @@ int launch_decode_shared(const ListedArgs &a) {
   p.unit_max = L.unit_max;
   p.gran_max = L.gran_max;
   p.seq = reinterpret_cast<int32_t *>(ws + L.seq_off);
+  p.own_begin = p.seq + 2 * (size_t)(a.batch + 1);
+  p.own_first = p.seq + 3 * (size_t)(a.batch + 1);
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
-  size_t smem = sizeof(int32_t) * (3 * (size_t)(a.batch + 1) + 4 * (size_t)(a.num_groups + 1));
+  size_t smem = sizeof(int32_t) * (2 * (size_t)(a.batch + 1) + 4 * (size_t)(a.num_groups + 1));
   p.in_smem = smem <= 40 * 1024;
   if (!p.in_smem) smem = 0;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
@@ -1132,8 +1256,9 @@ int launch_decode_shared(const ListedArgs &a) {
   cudaError_t e = launch_pdl(shared_sched_kernel, dim3(1), dim3(1024), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "shared_sched launch: %s", cudaGetErrorString(e));
-  return run_listed(a, tm, L, nsm, a.kv_indptr, a.kv_indices, a.num_groups > 0 || !p.rows, own.gran,
-                    own.gran * a.hkv, nullptr, 0);
+  return run_listed(a, a.num_groups > 0 || !p.rows ? &tm : nullptr, L, nsm, a.kv_indptr,
+                    a.kv_indices, 0,
+                    OwnPartials{p.rows_out, own.gran, own.gran * a.hkv, 0, nullptr, 0, 0});
 }
 
 int launch_decode_pages(const ListedArgs &a) {
@@ -1147,9 +1272,15 @@ int launch_decode_pages(const ListedArgs &a) {
   const ListedLayout L = pages_layout(a.batch, a.hkv, group, a.d, a.page_size, a.top_k, nsm);
   int rc = check_workspace(a, L);
   if (rc != PKX_OK) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  const OwnUnits own = own_units(group, nsm);
+  const int pieces = pages_pieces(a.batch, a.hkv, group, a.page_size, a.top_k, nsm);
+  int32_t *err = reinterpret_cast<int32_t *>(ws + L.err_off);
+  if (group <= kRowsGroup)
+    return run_listed(a, nullptr, L, nsm, nullptr, nullptr, pieces,
+                      OwnPartials{nullptr, pieces, 1, pieces, err, (int)pairs * pieces, 1});
   ListedMaps tm;
   if ((rc = make_maps(tm, a)) != PKX_OK) return rc;
-  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   PagesParams p;
   p.kv_indptr = a.kv_indptr;
   p.kv_indices = a.kv_indices;
@@ -1161,15 +1292,13 @@ int launch_decode_pages(const ListedArgs &a) {
   p.hkv = a.hkv;
   p.page_size = a.page_size;
   p.top_k = a.top_k;
-  p.pieces = pages_pieces(a.batch, a.hkv, group, a.page_size, a.top_k, nsm);
-  const OwnUnits own = own_units(group, nsm);
+  p.pieces = pieces;
   p.run = own.run;
   p.gran = own.gran;
-  p.rows = group <= kRowsGroup;
   p.cap = a.top_k * a.page_size;
   p.slots = reinterpret_cast<int32_t *>(ws + L.idx_off);
   p.ptr = reinterpret_cast<int32_t *>(ws + L.ptr_off);
-  p.err = reinterpret_cast<int32_t *>(ws + L.err_off);
+  p.err = err;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
   p.order = reinterpret_cast<int32_t *>(ws + L.order_off);
   p.rows_out = reinterpret_cast<ListedRow *>(ws + L.rows_off);
@@ -1178,8 +1307,8 @@ int launch_decode_pages(const ListedArgs &a) {
   cudaError_t e = launch_pdl(list_pages_kernel, dim3((unsigned)pairs), dim3(256), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "list_pages launch: %s", cudaGetErrorString(e));
-  return run_listed(a, tm, L, nsm, p.ptr, p.slots, !p.rows, own.gran * p.pieces, own.gran, p.err,
-                    (int)pairs);
+  return run_listed(a, &tm, L, nsm, p.ptr, p.slots, 0,
+                    OwnPartials{p.rows_out, own.gran * pieces, own.gran, 0, err, (int)pairs, 0});
 }
 
 }  // namespace pkx

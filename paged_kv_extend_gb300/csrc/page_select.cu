@@ -150,8 +150,8 @@ int launch_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_hs
 }
 
 // ------------------------------------------------------------------- score
-constexpr int kScoreThreads = 256;
-constexpr int kScoreUnroll = 8;
+constexpr int kScoreThreads = 128;
+constexpr int kScoreRun = 32;   // entries of a warp, at most
 
 struct ScoreParams {
   const uint16_t *q;
@@ -176,18 +176,24 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 
 // A warp: one KV head and a run of up to 32 consecutive entries of kv_indices,
 // whose page ids its lanes fetch together; neighbouring warps take the heads
-// of the same pages.  D / 4 lanes hold a page's two bounds, 8 dims each,
-// kScoreUnroll steps in flight.
+// of the same pages.  D / 4 lanes hold a page's two bounds, 8 dims each.  All of
+// the run's bounds are on their way (cp.async, each lane its own 16 bytes, so
+// nothing is shared) before the warp looks for its sequence and sums up its
+// queries: with loads into registers, 8 pages at a time, that preparation stood
+// between the loads (64 sequences of 512 pages, 8 KV heads of 128: 45 us for
+// 134 MB).
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreParams p) {
   constexpr int LP = D / 4;        // lanes of a page
-  constexpr int PPW = 32 / LP;     // pages of a warp's step
+  constexpr int PPW = 32 / LP;     // pages of a warp's copy
   constexpr int CH = D / 8;        // lanes of one bound
+  constexpr int COPIES = kScoreRun / PPW;
+  extern __shared__ __align__(16) uint8_t smem[];
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->status = 0;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = (int64_t)blockIdx.x * (kScoreThreads / 32) + warp;
   if (w >= p.runs * p.hkv) return;
   const int64_t r = w / p.hkv;
   const int h = (int)(w - r * p.hkv);
@@ -195,15 +201,23 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
   const int sub = lane / LP, l = lane - sub * LP;
   const bool is_hi = l >= CH;
   const int c = is_hi ? l - CH : l;
-  const int64_t e_end = min(e0 + p.run, p.n_indices);
-  int my_page = e0 + lane < e_end ? __ldg(p.kv_indices + e0 + lane) : -1;
+  const int n = (int)min((int64_t)p.run, p.n_indices - e0);
+  int my_page = lane < n ? __ldg(p.kv_indices + e0 + lane) : -1;
   if (my_page >= p.num_pages) my_page = -1;
-  uint32_t *keys = p.keys + (int64_t)h * p.n_indices + e0;
   const uint4 *box = p.bounds + (int64_t)h * LP + l;
-  const int64_t page_chunks = (int64_t)p.hkv * LP;
-  for (int64_t e = e0; e < e_end;) {
-    // the sequence of entry e: the last b with kv_indptr[b] <= e, by 32 probes
-    // at a time
+  const uint32_t mine = smem_u32(smem) + warp * (COPIES * 512) + lane * 16;
+#pragma unroll
+  for (int u = 0; u < COPIES; ++u) {
+    const int page = __shfl_sync(0xffffffffu, my_page, u * PPW + sub);
+    if (page >= 0) cp_async_16(mine + u * 512, box + (int64_t)page * p.hkv * LP, 16u);
+    if (u % 8 == 7) cp_async_commit();
+  }
+  uint32_t *keys = p.keys + (int64_t)h * p.n_indices + e0;
+  int landed = 0;  // copies that have
+  for (int i = 0; i < n;) {
+    // the sequence of entry e0 + i: the last b with kv_indptr[b] <= it, by 32
+    // probes at a time
+    const int64_t e = e0 + i;
     int b = 0;
     for (int span = p.batch; span > 1;) {
       const int step = (span + 31) / 32;
@@ -215,58 +229,74 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
     }
     const int64_t first = __ldg(p.kv_indptr + b), end = __ldg(p.kv_indptr + b + 1);
     if (first > e || end <= e) break;  // behind the last sequence
-    const int64_t seg = min(end, e_end);
+    const int seg = (int)min(end - e0, (int64_t)n);
     if (end - first <= p.top_k) {  // all of its pages are taken
-      e = seg;
+      i = seg;
       continue;
     }
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    for (int k = 0; k < 8; ++k) f[k] = 0.f;
     const uint4 *row =
         reinterpret_cast<const uint4 *>(p.q + ((int64_t)b * p.hq + (int64_t)h * p.group) * D) + c;
+#pragma unroll 4
     for (int g = 0; g < p.group; ++g) {
       const uint4 v = __ldg(row + g * CH);
       const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float qv = __uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16);
-        f[i] = __fadd_rn(f[i], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
+      for (int k = 0; k < 8; ++k) {
+        const float qv = __uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16);
+        f[k] = __fadd_rn(f[k], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
       }
     }
-    // (an entry behind the run's end, or a page outside the bounds, reads page 0
-    // and its result is dropped: the loads go out without a branch)
-    const int i1 = (int)(seg - e0);
-    for (int i0 = (int)(e - e0); i0 < i1 && p.num_pages > 0; i0 += PPW * kScoreUnroll) {
-      uint4 x[kScoreUnroll];
-      int page[kScoreUnroll];
+    // Eight copies at a time.  The lanes' sums meet in a butterfly in which a
+    // lane passes on the half of its values that its partner keeps, so that eight
+    // sums take 4 + 2 + 1 shuffles (and one a level from there on), each of
+    // them the sum of two neighbours of the tree; lane l ends with copy l % 8.
+    // (Entries of other sequences in a copy are left out.)
+    for (int u0 = i / PPW / 8 * 8; u0 * PPW < seg; u0 += 8) {
+      if (u0 >= landed) {
+        landed = u0 + 8;
+        switch (COPIES / 8 - landed / 8) {
+          case 3: cp_async_wait_group<3>(); break;
+          case 2: cp_async_wait_group<2>(); break;
+          case 1: cp_async_wait_group<1>(); break;
+          default: cp_async_wait_group<0>();
+        }
+      }
+      float v[8];
 #pragma unroll
-      for (int u = 0; u < kScoreUnroll; ++u)
-        page[u] = __shfl_sync(0xffffffffu, my_page, (i0 + u * PPW + sub) & 31);
-#pragma unroll
-      for (int u = 0; u < kScoreUnroll; ++u)
-        x[u] = __ldg(box + (int64_t)max(page[u], 0) * page_chunks);
-#pragma unroll
-      for (int u = 0; u < kScoreUnroll; ++u) {
-        const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      for (int u = 0; u < 8; ++u) {
+        const uint4 x = ld_shared_u4(mine + (u0 + u) * 512);
+        const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
         float t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          t[i] = __fmul_rn(__uint_as_float(i & 1 ? wd[i / 2] & 0xFFFF0000u : wd[i / 2] << 16), f[i]);
+        for (int k = 0; k < 8; ++k)
+          t[k] = __fmul_rn(__uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16), f[k]);
 #pragma unroll
-        for (int n = 4; n > 0; n >>= 1)
+        for (int m = 4; m > 0; m >>= 1)
 #pragma unroll
-          for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
-        float s = t[0];
-#pragma unroll
-        for (int o = 1; o < LP; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-        const int i = i0 + u * PPW + sub;
-        if (l == 0 && i < i1) keys[i] = page[u] < 0 ? 0u : score_key(s);
+          for (int k = 0; k < m; ++k) t[k] = __fadd_rn(t[2 * k], t[2 * k + 1]);
+        v[u] = t[0];
       }
+#pragma unroll
+      for (int o = 1, m = 4; o < 8; o <<= 1, m >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < m; ++k) {
+          const float keep = up ? v[2 * k + 1] : v[2 * k], pass = up ? v[2 * k] : v[2 * k + 1];
+          v[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, pass, o));
+        }
+      }
+#pragma unroll
+      for (int o = 8; o < LP; o <<= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+      const int at = (u0 + (lane & 7)) * PPW + sub;
+      const int page = __shfl_sync(0xffffffffu, my_page, at & 31);
+      if (l < 8 && at >= i && at < seg) keys[at] = page < 0 ? 0u : score_key(v[0]);
     }
-    if (p.num_pages == 0 && lane >= (int)(e - e0) && lane < i1) keys[lane] = 0u;
-    e = seg;
+    i = seg;
   }
+  cp_async_wait_all();
 }
 
 // ------------------------------------------------------------------ select
@@ -436,15 +466,24 @@ int launch_select_pages(const SelectArgs &a) {
   // a warp's run: 32 entries, or fewer where that leaves less than 16 warps an
   // SM (a run reads the group's query rows once)
   int64_t run = a.n_indices * a.hkv / ((int64_t)nsm * 16);
-  run = run < 8 ? 8 : run > 32 ? 32 : run / 8 * 8;
+  run = run < 8 ? 8 : run > kScoreRun ? kScoreRun : run / 8 * 8;
   p.run = (int)run;
   p.runs = (a.n_indices + run - 1) / run;
   int64_t grid = (p.runs * a.hkv + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
   if (grid < 1) grid = 1;  // (the status word)
   if (grid >= (1ll << 31) || (int64_t)a.batch * a.hkv >= (1ll << 31))
     return set_error(PKX_EUNSUPPORTED, "select_pages: too many pages in one call");
-  cudaError_t e = launch_pdl(a.d == 128 ? page_score_kernel<128> : page_score_kernel<64>,
-                             dim3((unsigned)grid), dim3(kScoreThreads), 0, a.stream, p);
+  auto score = a.d == 128 ? page_score_kernel<128> : page_score_kernel<64>;
+  const size_t smem = (size_t)(kScoreThreads / 32) * kScoreRun * a.d * 4;  // 64 KB at most
+  static PerDevice configured[2];
+  std::atomic<int> *done = configured[a.d == 128].here();
+  cudaError_t e = cudaSuccess;
+  if (!done || done->load(std::memory_order_acquire) == 0) {
+    e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && done) done->store(1, std::memory_order_release);
+  }
+  if (e == cudaSuccess)
+    e = launch_pdl(score, dim3((unsigned)grid), dim3(kScoreThreads), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "page_score launch: %s", cudaGetErrorString(e));
   SelectParams s;
