@@ -554,61 +554,77 @@ struct SharedParams {
   int rows;         // own keys go to rows_kernel
   int unit_max;
   int64_t gran_max;
-  int32_t *seq;     // [2][batch + 1]: keys, shared keys
+  int32_t *seq;     // [kSeqArrays][batch + 1]
   int32_t *own_begin, *own_first;  // [batch + 1] first own key; first piece
-  int32_t *grp;     // [4][num_groups + 1]: shared keys, first sequence, first unit, first granule
+  int32_t *grp;     // [kGroupArrays][num_groups + 1]
   int in_smem;      // those arrays in dynamic shared memory instead
   WorkUnit *units;
   int32_t *order;
   ListedRow *rows_out;
   WsHeader *hdr;
 };
-// Exclusive sum over a block of 1024 threads of one value in [0, kMany] each, and
-// the total; sums are held at kMany, far above any count that the workspace
-// takes (an indptr that decreases can make them larger than 32 bits).
+// Exclusive sums over a block of 1024 threads of two values in [0, kMany] each,
+// and the totals; sums are held at kMany, far above any count that the
+// workspace takes (an indptr that decreases can make them larger than 32 bits).
 constexpr uint32_t kMany = 1u << 30;
 __device__ __forceinline__ uint32_t add_held(uint32_t a, uint32_t b) { return min(a + b, kMany); }
-__device__ __forceinline__ uint32_t block_sum_before(uint32_t v, uint32_t *sh, uint32_t &total) {
+__device__ __forceinline__ uint32_t mul_held(uint32_t a, uint32_t b) {
+  return (uint32_t)min((uint64_t)a * b, (uint64_t)kMany);
+}
+struct Two {
+  uint32_t x, y;
+};
+__device__ __forceinline__ Two add_held(Two a, Two b) { return {add_held(a.x, b.x), add_held(a.y, b.y)}; }
+__device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  Two s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x = add_held(x, y);
+    const Two y = {__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o)};
+    if (lane >= o) s = add_held(s, y);
   }
-  if (lane == 31) sh[warp] = x;
-  const uint32_t up = __shfl_up_sync(0xffffffffu, x, 1);
+  if (lane == 31) sh[warp] = s;
+  const Two up = {__shfl_up_sync(0xffffffffu, s.x, 1), __shfl_up_sync(0xffffffffu, s.y, 1)};
   __syncthreads();
-  uint32_t t = sh[lane], before = lane < warp ? t : 0;
+  Two t = sh[lane], before = lane < warp ? t : Two{0, 0};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    t = add_held(t, __shfl_xor_sync(0xffffffffu, t, o));
-    before = add_held(before, __shfl_xor_sync(0xffffffffu, before, o));
+    t = add_held(t, Two{__shfl_xor_sync(0xffffffffu, t.x, o), __shfl_xor_sync(0xffffffffu, t.y, o)});
+    before = add_held(before, Two{__shfl_xor_sync(0xffffffffu, before.x, o),
+                                  __shfl_xor_sync(0xffffffffu, before.y, o)});
   }
   __syncthreads();
   total = t;
   return lane == 0 ? before : add_held(before, up);
 }
 
-// One CTA of 1024 threads: the units of every group's prefix and of every
-// sequence's own keys.  A group shares min(shared_lens, the shortest of its
+// One CTA of 1024 threads: the units of every group's prefix and the pieces of
+// every sequence's own keys.  A group shares min(shared_lens, the shortest of its
 // sequences) keys, nothing if that is less than a tile of keys or if it has one
 // sequence.  A prefix is cut into equal pieces of at most C tiles.  The units
 // are few and long, so C is the one of up to 64 candidates (the longest prefix
 // in 1, 2, ... pieces) whose rounds over the SMs take least, a unit counting
 // C + kUnitTiles tiles (its query load, pipeline fill and partials).  Own keys
 // are cut for a given number of units.
+//
+// The whole call waits for this one CTA, so it is a chain of few barriers with
+// no 64-bit division (a candidate in 64 bits took 2400 clocks); what a group
+// or a sequence needs later stays in shared memory.
 constexpr int kUnitTiles = 3;
+constexpr int kSeqArrays = 3, kGroupArrays = 7;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {
   extern __shared__ int32_t s_dyn[];
-  __shared__ uint32_t sh[32];
-  __shared__ int64_t s_best[32];
+  __shared__ Two sh[32];
+  __shared__ uint2 s_best[32];
   __shared__ int s_longest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int B = p.batch, NG = p.num_groups;
-  int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + 2 * (B + 1) : p.grp;
-  int32_t *sT = seq, *sS = seq + (B + 1);
-  int32_t *gS = grp, *gB = grp + (NG + 1), *gU = grp + 2 * (NG + 1), *gG = grp + 3 * (NG + 1);
+  const int B = p.batch, NG = p.num_groups, B1 = B + 1, G1 = NG + 1;
+  int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + kSeqArrays * B1 : p.grp;
+  // keys, shared keys, pieces of own keys
+  int32_t *sT = seq, *sS = seq + B1, *sN = seq + 2 * B1;
+  // shared keys, first sequence, blocks, granules and pieces; first unit, first granule
+  int32_t *gS = grp, *gB = grp + G1, *gK = grp + 2 * G1, *gR = grp + 3 * G1, *gP = grp + 4 * G1;
+  int32_t *gU = grp + 5 * G1, *gG = grp + 6 * G1;
   const int blk = 2 * p.tok;  // tokens of a prefix unit
   if (tid == 0) s_longest = 0;
   grid_dep_wait();
@@ -637,11 +653,14 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   const bool share = __syncthreads_or(bad_groups) == 0;
   if (bad || bad_groups) record_status(&p.hdr->status, PKX_EDEVICE);
   auto tiles = [](int keys) { return keys / kBlockN + (keys % kBlockN != 0); };
-  // shared keys of each group (a warp each)
+  // shared keys of each group (a warp each), its blocks of queries, and the
+  // granules of one piece of all of them for one KV head (two streams of partials
+  // where the block is one tile of rows)
   for (int g = warp; g < NG; g += 32) {
-    int S = 0;
+    int S = 0, lo = 0, hi = 0;
     if (share) {
-      const int lo = gB[g], hi = gB[g + 1];
+      lo = gB[g];
+      hi = gB[g + 1];
       int least = gS[g];
       for (int b = lo + lane; b < hi; b += 32) least = min(least, sT[b]);
       least = __reduce_min_sync(0xffffffffu, least);
@@ -650,84 +669,77 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     }
     __syncwarp();
     if (lane == 0) {
+      const int nb = S > 0 ? (hi - lo + blk - 1) / blk : 0, last = hi - lo - (nb - 1) * blk;
       gS[g] = S;
+      gK[g] = nb;
+      gR[g] = nb > 0 ? (nb - 1) * blk + (last <= p.tok ? 2 * last : last) : 0;
       if (S > 0) atomicMax(&s_longest, tiles(S));
     }
   }
   __syncthreads();
+  // totals: tiles of the prefixes, runs of own keys
   auto runs = [&](int b) {
     const int n = sT[b] - sS[b];
     return n / p.own_run + (n % p.own_run != 0);
   };
-  auto group_blocks = [&](int g) { return gS[g] > 0 ? (gB[g + 1] - gB[g] + blk - 1) / blk : 0; };
-  // granules of a group's piece (all its blocks, one KV head): two streams of
-  // partials where the block is one tile of rows
-  auto group_granules = [&](int g) {
-    const int nb = group_blocks(g), last = gB[g + 1] - gB[g] - (nb - 1) * blk;
-    return (nb - 1) * blk + (last <= p.tok ? 2 * last : last);
-  };
-  auto held = [](int64_t x) { return (uint32_t)min(x, (int64_t)kMany); };
-  int C = 1;
-  uint32_t pre_units = 0, pre_gran = 0;
-  auto pieces = [&](int g) { return (tiles(gS[g]) + C - 1) / C; };
+  const int bc = (B + 1023) / 1024, b0 = min(B, tid * bc), b1 = min(B, b0 + bc);
+  Two sum = {0, 0}, all;
+  for (int b = b0; b < b1; ++b) sum.y = add_held(sum.y, (uint32_t)runs(b));
+  for (int g = tid; g < NG; g += 1024) sum.x = add_held(sum.x, mul_held(gK[g], tiles(gS[g])));
+  block_sum_before(sum, sh, all);
+  // pieces of R runs: about own_target of them and one more a sequence at most
+  // (the quotient in fp32 is raised past its rounding)
+  const float own_each = (float)all.y * (float)p.hkv / (float)p.own_target * 1.000001f;
+  const int R = max((int)ceilf(min(own_each, 1e9f)), p.own_least);
+  Two units = {0, 0};  // of own keys
+  for (int b = b0; b < b1; ++b) {
+    sN[b] = (runs(b) + R - 1) / R;
+    units.x = add_held(units.x, (uint32_t)sN[b]);
+  }
+  Two own_all, pre = {0, 0};  // pre: prefix units, their granules
+  const Two own_before = block_sum_before(units, sh, own_all);
   if (s_longest > 0) {
-    uint32_t cost = 0, all_cost;
-    for (int g = tid; g < NG; g += 1024)
-      cost = add_held(cost, held((int64_t)group_blocks(g) * tiles(gS[g])));
-    block_sum_before(cost, sh, all_cost);
-    // (at most four units an SM and one more a block)
-    const int least = max((int)(((int64_t)all_cost * p.hkv + 4 * p.sms - 1) / (4 * p.sms)),
-                          kMinSplitTiles);
-    int64_t best = INT64_MAX;
+    // at most four units an SM and one more a block
+    const float each = (float)all.x * (float)p.hkv / (4.0f * p.sms) * 1.000001f;
+    const int least = max((int)ceilf(min(each, 1e9f)), kMinSplitTiles);
+    uint2 best = make_uint2(0xFFFFFFFFu, 0u);  // (tiles of all rounds, C)
     for (int j = warp + 1; j <= 64; j += 32) {
-      const int c = max((s_longest + j - 1) / j, least);
+      const uint32_t c = max((s_longest + j - 1) / j, least);
       uint32_t n = 0;
       for (int g = lane; g < NG; g += 32)
-        n = add_held(n, held((int64_t)group_blocks(g) * ((tiles(gS[g]) + c - 1) / c)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n = add_held(n, __shfl_xor_sync(0xffffffffu, n, o));
-      const int64_t rounds = ((int64_t)n * p.hkv + p.sms - 1) / p.sms;
-      best = min(best, (rounds * (c + kUnitTiles) << 24) + min(c, (1 << 24) - 1));
+        n = add_held(n, mul_held(gK[g], ((uint32_t)tiles(gS[g]) + c - 1) / c));
+      n = __reduce_add_sync(0xffffffffu, min(n, kMany / 32));
+      const uint32_t rounds = (mul_held(n, p.hkv) + p.sms - 1) / (uint32_t)p.sms;
+      const uint32_t t = mul_held(rounds, c + kUnitTiles);
+      if (t < best.x) best = make_uint2(t, c);
     }
     if (lane == 0) s_best[warp] = best;
     __syncthreads();
     best = s_best[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = min(best, (int64_t)__shfl_xor_sync(0xffffffffu, best, o));
-    C = (int)(best & ((1 << 24) - 1));
+    const uint32_t t = __reduce_min_sync(0xffffffffu, best.x);
+    const int C = (int)__reduce_min_sync(0xffffffffu, best.x == t ? best.y : 0xFFFFFFFFu);
     // first unit and granule of each group
     const int gc = (NG + 1023) / 1024, g0 = min(NG, tid * gc), g1 = min(NG, g0 + gc);
-    uint32_t nu = 0, ng = 0;
+    auto size = [&](int g) {  // units and granules
+      return Two{mul_held(mul_held(gP[g], gK[g]), p.hkv), mul_held(mul_held(gP[g], gR[g]), p.hkv)};
+    };
+    Two n = {0, 0};
     for (int g = g0; g < g1; ++g) {
-      if (gS[g] <= 0) continue;
-      nu = add_held(nu, held((int64_t)pieces(g) * group_blocks(g) * p.hkv));
-      ng = add_held(ng, held((int64_t)pieces(g) * p.hkv * group_granules(g)));
+      gP[g] = (tiles(gS[g]) + C - 1) / C;
+      n = add_held(n, size(g));
     }
-    nu = block_sum_before(nu, sh, pre_units);
-    ng = block_sum_before(ng, sh, pre_gran);
+    n = block_sum_before(n, sh, pre);
     for (int g = g0; g < g1; ++g) {
-      gU[g] = (int)nu;
-      gG[g] = (int)ng;
-      if (gS[g] <= 0) continue;
-      nu = add_held(nu, held((int64_t)pieces(g) * group_blocks(g) * p.hkv));
-      ng = add_held(ng, held((int64_t)pieces(g) * p.hkv * group_granules(g)));
+      gU[g] = (int)n.x;
+      gG[g] = (int)n.y;
+      n = add_held(n, size(g));
     }
   }
-  // own keys: pieces of R runs, about own_target of them
-  uint32_t own = 0, all_own;
-  const int bc = (B + 1023) / 1024, b0 = min(B, tid * bc), b1 = min(B, b0 + bc);
-  for (int b = b0; b < b1; ++b) own = add_held(own, (uint32_t)runs(b));
-  block_sum_before(own, sh, all_own);
-  const int R = max((int)(((int64_t)all_own * p.hkv + p.own_target - 1) / p.own_target), p.own_least);
-  auto own_pieces = [&](int b) { return (runs(b) + R - 1) / R; };
-  uint32_t bu = 0, own_all;
-  for (int b = b0; b < b1; ++b) bu = add_held(bu, (uint32_t)own_pieces(b));
-  bu = block_sum_before(bu, sh, own_all);
-  const int64_t own_units = (int64_t)own_all * p.hkv;
+  const int64_t own_units = (int64_t)own_all.x * p.hkv;
   // (false only for an indptr that decreases: the workspace is sized for the
   // largest counts)
-  const bool fits = pre_units + own_units <= p.unit_max &&
-                    pre_gran + p.own_gran * own_units <= p.gran_max;
+  const bool fits = pre.x + own_units <= p.unit_max &&
+                    pre.y + p.own_gran * own_units <= p.gran_max;
   if (!fits) {
     if (tid == 0) {
       record_status(&p.hdr->status, PKX_EDEVICE);
@@ -737,14 +749,17 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     for (int b = tid; b < B; b += 1024) p.rows_out[b] = ListedRow{};
     return;
   }
+  const int pre_units = (int)pre.x, pre_gran = (int)pre.y;
+  __syncthreads();  // the groups' first units and granules
+  int first_piece = (int)own_before.x;
   for (int b = b0; b < b1; ++b) {
-    p.own_first[b] = (int)bu;
+    p.own_first[b] = first_piece;
     p.own_begin[b] = sS[b];
     // where the token's partials lie
     ListedRow r{};
-    r.b = (int)pre_gran + p.own_gran * (int)bu * p.hkv;
-    r.b_n = own_pieces(b);
-    bu += r.b_n;
+    r.b = pre_gran + p.own_gran * first_piece * p.hkv;
+    r.b_n = sN[b];
+    first_piece += sN[b];
     if (sS[b] > 0) {
       int lo = 0, hi = NG - 1;  // last g with gB[g] <= b
       while (lo < hi) {
@@ -755,35 +770,31 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       const int g = lo, i = b - gB[g], k = i / blk;
       const int n_tok = min(blk, gB[g + 1] - gB[g] - k * blk);
       r.a = gG[g] + i;
-      r.a_n = pieces(g);
-      r.a_head = group_granules(g);
-      r.a_step = p.hkv * r.a_head;
+      r.a_n = gP[g];
+      r.a_head = gR[g];
+      r.a_step = p.hkv * gR[g];
       r.a_streams = n_tok <= p.tok ? 2 : 1;
       r.a_stream = n_tok;
     }
     p.rows_out[b] = r;
   }
   if (tid == 0) {
-    p.own_first[B] = (int)own_all;
+    p.own_first[B] = (int)own_all.x;
     p.hdr->n_units = (int)(p.rows ? pre_units : pre_units + own_units);
-    p.hdr->pad[kRowsGran] = (int)pre_gran;
+    p.hdr->pad[kRowsGran] = pre_gran;
     p.hdr->pad[kRowsCount] = (int)(p.rows ? own_units : 0);
   }
-  __syncthreads();
   // units of the prefixes: group, piece, KV head, block (blocks of one piece
   // and head next to each other: they read the same keys)
-  for (int u = tid; u < (int)pre_units; u += 1024) {
+  for (int u = tid; u < pre_units; u += 1024) {
     int lo = 0, hi = NG - 1;  // last g with gU[g] <= u
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (gU[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
-    const int g = lo, nb = group_blocks(g), nt = tiles(gS[g]), S = pieces(g);
-    int r = u - gU[g];
-    const int k = r % nb;
-    r /= nb;
-    const int kvh = r % p.hkv, sp = r / p.hkv;
+    const int g = lo, nb = gK[g], nt = tiles(gS[g]), S = gP[g];
+    const int r = u - gU[g], r2 = r / nb, k = r - r2 * nb, sp = r2 / p.hkv, kvh = r2 - sp * p.hkv;
     const int first = gB[g], n = gB[g + 1] - first;
     WorkUnit w;
     w.q_tok0 = first + k * blk;
@@ -795,11 +806,12 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.k_split = INT_MAX;
     w.n_tiles = tiles(w.k_end - w.k_begin);
     w.b = first;
-    w.slot = gG[g] + (sp * p.hkv + kvh) * group_granules(g) + k * blk;
+    w.slot = gG[g] + (sp * p.hkv + kvh) * gR[g] + k * blk;
     w.dq = w.claim = 0;
     p.units[u] = w;
     p.order[u] = u;
   }
+  __syncthreads();  // (own_first, for the units below)
   if (p.rows) return;  // (rows_kernel finds its units itself)
   // units of the sequences' own keys: sequence, piece, KV head
   for (int i = tid; i < (int)own_units; i += 1024) {
@@ -810,7 +822,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       if (p.own_first[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    const int b = lo, nr = runs(b), S = own_pieces(b), sp = x - p.own_first[b];
+    const int b = lo, nr = runs(b), S = sN[b], sp = x - p.own_first[b];
     WorkUnit w;
     w.q_tok0 = b;
     w.n_tok = 1;
@@ -821,10 +833,10 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.k_split = INT_MAX;
     w.n_tiles = tiles(w.k_end - w.k_begin);
     w.b = b;
-    w.slot = (int)pre_gran + p.own_gran * i;
+    w.slot = pre_gran + p.own_gran * i;
     w.dq = w.claim = 0;
-    p.units[(int)pre_units + i] = w;
-    p.order[(int)pre_units + i] = (int)pre_units + i;
+    p.units[pre_units + i] = w;
+    p.order[pre_units + i] = pre_units + i;
   }
 }
 
@@ -855,9 +867,9 @@ static ListedLayout shared_layout(int batch, int num_groups, int hkv, int group,
   L.gran_max = 4ll * n * blk + 2ll * hkv * batch + own.gran * (own.target + (int64_t)hkv * batch);
   size_t off = up256(sizeof(WsHeader));
   L.seq_off = off;
-  off = up256(off + sizeof(int32_t) * 4 * (size_t)(batch + 1));
+  off = up256(off + sizeof(int32_t) * (kSeqArrays + 2) * (size_t)(batch + 1));
   L.grp_off = off;
-  off = up256(off + sizeof(int32_t) * 4 * (size_t)(num_groups + 1));
+  off = up256(off + sizeof(int32_t) * kGroupArrays * (size_t)(num_groups + 1));
   L.units_off = off;
   off = up256(off + sizeof(WorkUnit) * (size_t)L.unit_max);
   L.order_off = off;
@@ -1118,7 +1130,7 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, const ListedLayou
     if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, true>(p, nsm, a.stream);
     return launch_rows_as<D, 0, true>(p, nsm, a.stream);
   }
-  p.own_begin = reinterpret_cast<int32_t *>(ws + L.seq_off) + 2 * (size_t)(a.batch + 1);
+  p.own_begin = reinterpret_cast<int32_t *>(ws + L.seq_off) + kSeqArrays * (size_t)(a.batch + 1);
   p.own_first = p.own_begin + (a.batch + 1);
   if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1, false>(p, nsm, a.stream);
   if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, false>(p, nsm, a.stream);
@@ -1243,10 +1255,11 @@ int launch_decode_shared(const ListedArgs &a) {
   p.unit_max = L.unit_max;
   p.gran_max = L.gran_max;
   p.seq = reinterpret_cast<int32_t *>(ws + L.seq_off);
-  p.own_begin = p.seq + 2 * (size_t)(a.batch + 1);
-  p.own_first = p.seq + 3 * (size_t)(a.batch + 1);
+  p.own_begin = p.seq + kSeqArrays * (size_t)(a.batch + 1);
+  p.own_first = p.own_begin + (a.batch + 1);
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
-  size_t smem = sizeof(int32_t) * (2 * (size_t)(a.batch + 1) + 4 * (size_t)(a.num_groups + 1));
+  size_t smem = sizeof(int32_t) * (kSeqArrays * (size_t)(a.batch + 1) +
+                                   kGroupArrays * (size_t)(a.num_groups + 1));
   p.in_smem = smem <= 40 * 1024;
   if (!p.in_smem) smem = 0;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
