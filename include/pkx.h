@@ -727,13 +727,13 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
  *              [n_indices] page ids (entries past kv_indptr[batch] are not
  *              read for any sequence)
  *   selected   int32 [batch, hkv, top_k] (written)
- *   workspace  >= pkx_select_pages_workspace_size(hkv, n_indices) bytes,
+ *   workspace  >= pkx_select_pages_workspace_size(...) bytes,
  *              256-byte aligned; pkx_workspace_status reports a candidate page
  *              outside [0, num_pages) (it ranks last) and an indptr that
  *              decreases or passes n_indices (that sequence selects nothing)
  * first_pages + last_pages <= top_k <= 4096.
  */
-size_t pkx_select_pages_workspace_size(int hkv, int64_t n_indices);
+size_t pkx_select_pages_workspace_size(int batch, int hkv, int64_t n_indices);
 int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
                      const int32_t *kv_indptr, const int32_t *kv_indices, int64_t n_indices,
                      int batch, int hq, int hkv, int d, int top_k, int first_pages, int last_pages,

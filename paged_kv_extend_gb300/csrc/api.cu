@@ -2,8 +2,10 @@
 // host-side argument validation, then the launchers.  No entry point
 // allocates device memory or synchronises the stream (except
 // pkx_workspace_status, whose job is to read the device status word).
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <cstddef>
 #include <cstdio>
 #include <cuda_runtime.h>
 
@@ -129,10 +131,25 @@ size_t pkx_decode_workspace_size(int batch, int hq, int hkv, int lq, int lv) {
 
 int pkx_workspace_status(const void *workspace, void *stream) {
   if (!workspace) return set_error(PKX_EINVAL, "workspace is null");
-  int32_t st = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemcpyAsync(&st, workspace, sizeof st, cudaMemcpyDeviceToHost, s);
+  WsHeader hdr = {};
+  const size_t used = offsetof(WsHeader, pad) + (kUnitsPlace + 1) * sizeof(int32_t);
+  cudaError_t e = cudaMemcpyAsync(&hdr, workspace, used, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  int32_t st = hdr.status;
+  if (e == cudaSuccess && st == kStatusInUnits) {  // the units' own words
+    st = PKX_OK;
+    const uint8_t *at = static_cast<const uint8_t *>(workspace) + 256 * (size_t)hdr.pad[kUnitsPlace];
+    int32_t part[1024];
+    for (int64_t i = 0; i < hdr.pad[kUnitsCount] && st == PKX_OK && e == cudaSuccess; i += 1024) {
+      const int64_t n = std::min<int64_t>(1024, hdr.pad[kUnitsCount] - i);
+      e = cudaMemcpyAsync(part, at + i * sizeof(int32_t), n * sizeof(int32_t),
+                          cudaMemcpyDeviceToHost, s);
+      if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+      for (int64_t k = 0; k < n && e == cudaSuccess; ++k)
+        if (part[k]) st = PKX_EDEVICE;
+    }
+  }
   if (e != cudaSuccess) return set_error(PKX_ECUDA, "status read: %s", cudaGetErrorString(e));
   if (st == PKX_EDEVICE) return set_error(PKX_EDEVICE, "device-side index or indptr check failed");
   if (st == PKX_ETIMEOUT) return set_error(PKX_ETIMEOUT, "a device wait ran out of time");
@@ -993,9 +1010,9 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
                                    static_cast<cudaStream_t>(stream));
 }
 
-size_t pkx_select_pages_workspace_size(int hkv, int64_t n_indices) {
-  if (hkv <= 0 || n_indices < 0) return 0;
-  return select_pages_workspace(hkv, n_indices);
+size_t pkx_select_pages_workspace_size(int batch, int hkv, int64_t n_indices) {
+  if (batch < 0 || hkv <= 0 || n_indices < 0) return 0;
+  return select_pages_workspace(batch, hkv, n_indices);
 }
 
 int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
@@ -1022,7 +1039,7 @@ int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
     return set_error(PKX_EINVAL, "kv_indices null or misaligned");
   if (!selected || !aligned(selected, 4))
     return set_error(PKX_EINVAL, "select_pages: selected null or misaligned");
-  const size_t need = select_pages_workspace(hkv, n_indices);
+  const size_t need = select_pages_workspace(batch, hkv, n_indices);
   if (!workspace || workspace_bytes < need)
     return set_error(PKX_EWORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes,
                      need);

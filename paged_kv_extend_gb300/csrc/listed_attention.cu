@@ -72,29 +72,29 @@ __device__ __forceinline__ int piece_at(int i, int n, int S, int run, int keys) 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // ------------------------------------------------------------------ combine
-// One warp a (token, head) row: the lanes hold up to 32 partials' weights, the
-// row's dims are split over the lanes (float4 each).
-template <int D>
+// WPR warps a (token, head) row: they take its partials in turn, 32 weights in a
+// warp's lanes, the row's dims split over the lanes (float4 each), four partials'
+// loads in flight, and meet in shared memory.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256, 4) listed_combine_kernel(
     const ListedRow *__restrict__ rows, const float *__restrict__ plse,
     const float *__restrict__ po, bf16 *__restrict__ o, float *__restrict__ lse, int batch, int hq,
     int group, int b_head, int b_step, int b_streams, int b_n, const int32_t *__restrict__ err,
-    int n_err, int err_sets, int32_t *status) {
+    int n_err, int32_t *status) {
+  constexpr int ROWS = 8 / WPR;  // rows of a CTA
+  __shared__ float4 s_acc[WPR > 1 ? 8 : 1][32];
+  __shared__ float2 s_mw[8];  // maximum and sum of weights
   grid_dep_wait();
   grid_dep_launch();
   constexpr float kLog2e = 1.4426950408889634f;
-  if (err && blockIdx.x == 0) {  // errors that the warps or CTAs before found
-    int bad = 0;
-    for (int i = threadIdx.x; i < n_err; i += blockDim.x) bad |= err[i];
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-      if (err_sets) *status = bad ? PKX_EDEVICE : PKX_OK;
-      else if (bad) record_status(status, PKX_EDEVICE);
-    }
-  }
-  const int lane = threadIdx.x & 31;
-  const int nw = (gridDim.x * blockDim.x) >> 5;
-  for (int64_t r = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; r < (int64_t)batch * hq; r += nw) {
+  if (err && blockIdx.x == 0)  // errors that the listing kernel's CTAs found
+    for (int i = threadIdx.x; i < n_err; i += blockDim.x)
+      if (err[i]) record_status(status, PKX_EDEVICE);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+  const int64_t n_rows = (int64_t)batch * hq;
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < n_rows; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t r = min(r0 + warp / WPR, n_rows - 1);
+    const bool own_row = r0 + warp / WPR < n_rows;
     const int t = (int)(r / hq), head = (int)(r - (int64_t)t * hq);
     const int kvh = head / group, g = head - kvh * group;
     // (without a table: b_n pieces of each of the token's KV heads in turn)
@@ -117,31 +117,28 @@ __global__ void __launch_bounds__(256, 4) listed_combine_kernel(
       }
       return gr * group + g;
     };
-    // maximum of the partials' log sums (fmaxf drops a NaN one, which comes
-    // back as a NaN weight below)
+    // this warp's partials: part, part + WPR, ...
+    const int mine = n > part ? (n - part + WPR - 1) / WPR : 0;
+    // maximum of their log sums (fmaxf drops a NaN one, which comes back as a
+    // NaN weight below)
     float mx = -INFINITY;
     bool any = false;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const float x = i0 + lane < n ? plse[row_of(i0 + lane)] : -INFINITY;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      const float x = i0 + lane < mine ? plse[row_of((i0 + lane) * WPR + part)] : -INFINITY;
       any |= !(x == -INFINITY);
       mx = fmaxf(mx, x);
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     any = __any_sync(0xffffffffu, any);
-    bf16 *orow = o + r * D;
-    if (!any) {  // no visible key
-      if (lane * 4 < D) *reinterpret_cast<uint2 *>(orow + lane * 4) = make_uint2(0, 0);
-      if (lane == 0 && lse) lse[r] = -INFINITY;
-      continue;
-    }
-    float wsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const bool have = i0 + lane < n;
-      const int64_t row = have ? row_of(i0 + lane) : 0;
+    float wsum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; any && i0 < mine; i0 += 32) {
+      const bool have = i0 + lane < mine;
+      const int64_t row = have ? row_of((i0 + lane) * WPR + part) : 0;
       const float w = have ? exp2f((plse[row] - mx) * kLog2e) : 0.f;
       wsum += w;
-      const int m = min(32, n - i0);
+      const int m = min(32, mine - i0);
       for (int i = 0; i < m; i += 4) {
         float4 v[4];
 #pragma unroll
@@ -155,21 +152,56 @@ __global__ void __launch_bounds__(256, 4) listed_combine_kernel(
           const float wi = __shfl_sync(0xffffffffu, w, (i + u) & 31);
           // (a stream without keys has weight 0 and a row of zeros)
           if (i + u < m && lane * 4 < D) {
-            acc[0] += wi * v[u].x;
-            acc[1] += wi * v[u].y;
-            acc[2] += wi * v[u].z;
-            acc[3] += wi * v[u].w;
+            acc.x += wi * v[u].x;
+            acc.y += wi * v[u].y;
+            acc.z += wi * v[u].z;
+            acc.w += wi * v[u].w;
           }
         }
       }
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, s);
-    const float inv = 1.0f / wsum;
+    if constexpr (WPR > 1) {
+      // the warps' sums, each relative to its own maximum (one without partials,
+      // or with empty ones alone, has the maximum -inf, weight 0 and zeros)
+      s_acc[warp][lane] = acc;
+      if (lane == 0) s_mw[warp] = make_float2(mx, wsum);
+      __syncthreads();
+      float all = -INFINITY, sum = 0.f;
+      bool seen = false;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        const float2 mw = s_mw[warp - part + w];
+        seen |= !(mw.x == -INFINITY && mw.y == 0.f);
+        all = fmaxf(all, mw.x);
+      }
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        const float2 mw = s_mw[warp - part + w];
+        if (mw.x == -INFINITY && mw.y == 0.f) continue;
+        const float f = exp2f((mw.x - all) * kLog2e);
+        const float4 x = s_acc[warp - part + w][lane];
+        sum += f * mw.y;
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+      mx = all;
+      wsum = sum;
+      any = seen;
+      __syncthreads();
+    }
+    if (!own_row || part != 0) continue;
+    bf16 *orow = o + r * D;
+    const float inv = any ? 1.0f / wsum : 0.f;  // no visible key: 0 and -inf
     if (lane * 4 < D)
       *reinterpret_cast<uint2 *>(orow + lane * 4) =
-          make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    if (lane == 0 && lse) lse[r] = mx + logf(wsum);
+          any ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv))
+              : make_uint2(0, 0);
+    if (lane == 0 && lse) lse[r] = any ? mx + logf(wsum) : -INFINITY;
   }
 }
 
@@ -224,6 +256,8 @@ struct RowsParams {
   int64_t n_indices;
   int top_k, page_size, pieces;
   int32_t *err;  // [units]
+  bf16 *o;       // one unit a (sequence, KV head): the outputs themselves, or null
+  float *lse;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -273,6 +307,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
   auto spread = [](int r, int c) { return C::CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); };
   const int count = PAGES ? p.batch * p.hkv * p.pieces : p.hdr->pad[kRowsCount];
   const int gran0 = PAGES ? 0 : p.hdr->pad[kRowsGran];
+  if (PAGES && blockIdx.x == 0 && threadIdx.x == 0) set_status_in_units(p.hdr, p.err, count);
   const int warps = gridDim.x * kRowsWarps;
   // the first unit by the warp's number (neighbouring units, which share a
   // sequence's slots, on different SMs); then own keys are claimed (ragged), and
@@ -509,6 +544,25 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
       if (head >= p.group) continue;
       const float l = half ? l1 : l0, m = half ? m1 : m0;
       const float inv = (l == 0.f ? 0.f : 1.0f / l) * p.v_scale;
+      const float lse = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+      if (PAGES && p.o) {
+        const int64_t out = (int64_t)b * p.hq + (int64_t)kvh * p.group + head;
+        bf16 *dst = p.o + out * D;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const float e0 = o[2 * j][2 * half] * inv, e1 = o[2 * j][2 * half + 1] * inv;
+          const float f0 = o[2 * j + 1][2 * half] * inv, f1 = o[2 * j + 1][2 * half + 1] * inv;
+          if constexpr (FMT == 0) {
+            *reinterpret_cast<uint32_t *>(dst + 16 * j + 2 * t) = pack_bf16(e0, e1);
+            *reinterpret_cast<uint32_t *>(dst + 16 * j + 8 + 2 * t) = pack_bf16(f0, f1);
+          } else {
+            *reinterpret_cast<uint2 *>(dst + 16 * j + 4 * t) =
+                make_uint2(pack_bf16(e0, f0), pack_bf16(e1, f1));
+          }
+        }
+        if (t == 0 && p.lse) p.lse[out] = lse;
+        continue;
+      }
       const int64_t out = (int64_t)(gran0 + u) * p.group + head;
       float *dst = p.po + out * D;
 #pragma unroll
@@ -522,8 +576,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
           *reinterpret_cast<float4 *>(dst + 16 * j + 4 * t) = make_float4(e0, f0, e1, f1);
         }
       }
-      if (t == 0)
-        p.plse[out] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+      if (t == 0) p.plse[out] = lse;
     }
     bad = __any_sync(0xffffffffu, bad);
     if constexpr (PAGES) {
@@ -1126,6 +1179,8 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, const ListedLayou
     p.page_size = a.page_size;
     p.pieces = pieces;
     p.err = reinterpret_cast<int32_t *>(ws + L.err_off);
+    p.o = pieces == 1 ? kp.o : nullptr;
+    p.lse = a.lse;
     if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1, true>(p, nsm, a.stream);
     if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, true>(p, nsm, a.stream);
     return launch_rows_as<D, 0, true>(p, nsm, a.stream);
@@ -1141,10 +1196,30 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, const ListedLayou
 struct OwnPartials {
   const ListedRow *rows;  // or null: `pieces` a KV head, in order
   int head, step, pieces;
-  const int32_t *err;  // errors of the warps or CTAs before (nullable)
+  const int32_t *err;  // errors of the listing kernel's CTAs (nullable)
   int n_err;
-  int err_sets;  // nothing before has set the status word
 };
+
+// One warp a row where the rows fill the GPU (32 warps an SM), else up to eight.
+template <int D>
+static int launch_combine(const ListedArgs &a, const KParams &kp, const OwnPartials &own, int nsm) {
+  const int64_t rows = (int64_t)a.batch * a.hq, full = (int64_t)nsm * 32;
+  const int wpr = rows * 8 <= full ? 8 : rows * 4 <= full ? 4 : rows * 2 <= full ? 2 : 1;
+  auto kernel = wpr == 8   ? listed_combine_kernel<D, 8>
+                : wpr == 4 ? listed_combine_kernel<D, 4>
+                : wpr == 2 ? listed_combine_kernel<D, 2>
+                           : listed_combine_kernel<D, 1>;
+  const int64_t ctas = (rows * wpr + 7) / 8;
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)nsm * 8);
+  WsHeader *hdr = static_cast<WsHeader *>(a.workspace);
+  cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(256), 0, a.stream, own.rows,
+                             (const float *)kp.plse, (const float *)kp.po, kp.o, a.lse, a.batch,
+                             a.hq, kp.group, own.head, own.step, kp.group <= kRowsGroup ? 1 : 2,
+                             own.pieces, own.err, own.n_err, &hdr->status);
+  if (e != cudaSuccess)
+    return set_error(PKX_ECUDA, "listed_combine launch: %s", cudaGetErrorString(e));
+  return PKX_OK;
+}
 
 // The attention kernels and the combine: the tile kernel over the units in the
 // workspace where there may be some, rows_kernel for groups of at most
@@ -1206,16 +1281,8 @@ static int run_listed(const ListedArgs &a, const ListedMaps *tm, const ListedLay
     if (rc != PKX_OK) return rc;
   }
   if (ev_after) cudaEventRecord(ev_after, a.stream);
-  const int64_t ctas = ((int64_t)a.batch * a.hq + 7) / 8;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)nsm * 8);
-  cudaError_t e = launch_pdl(
-      a.d == 128 ? listed_combine_kernel<128> : listed_combine_kernel<64>, dim3(grid), dim3(256), 0,
-      a.stream, own.rows, (const float *)kp.plse, (const float *)kp.po, kp.o, a.lse, a.batch, a.hq,
-      group, own.head, own.step, group <= kRowsGroup ? 1 : 2, own.pieces, own.err, own.n_err,
-      own.err_sets, &hdr->status);
-  if (e != cudaSuccess)
-    return set_error(PKX_ECUDA, "listed_combine launch: %s", cudaGetErrorString(e));
-  return PKX_OK;
+  if (own.pieces == 1) return PKX_OK;  // rows_kernel has written the outputs
+  return a.d == 128 ? launch_combine<128>(a, kp, own, nsm) : launch_combine<64>(a, kp, own, nsm);
 }
 
 static int make_maps(ListedMaps &tm, const ListedArgs &a) {
@@ -1271,7 +1338,7 @@ int launch_decode_shared(const ListedArgs &a) {
     return set_error(PKX_ECUDA, "shared_sched launch: %s", cudaGetErrorString(e));
   return run_listed(a, a.num_groups > 0 || !p.rows ? &tm : nullptr, L, nsm, a.kv_indptr,
                     a.kv_indices, 0,
-                    OwnPartials{p.rows_out, own.gran, own.gran * a.hkv, 0, nullptr, 0, 0});
+                    OwnPartials{p.rows_out, own.gran, own.gran * a.hkv, 0, nullptr, 0});
 }
 
 int launch_decode_pages(const ListedArgs &a) {
@@ -1291,7 +1358,7 @@ int launch_decode_pages(const ListedArgs &a) {
   int32_t *err = reinterpret_cast<int32_t *>(ws + L.err_off);
   if (group <= kRowsGroup)
     return run_listed(a, nullptr, L, nsm, nullptr, nullptr, pieces,
-                      OwnPartials{nullptr, pieces, 1, pieces, err, (int)pairs * pieces, 1});
+                      OwnPartials{nullptr, pieces, 1, pieces, nullptr, 0});
   ListedMaps tm;
   if ((rc = make_maps(tm, a)) != PKX_OK) return rc;
   PagesParams p;
@@ -1321,7 +1388,7 @@ int launch_decode_pages(const ListedArgs &a) {
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "list_pages launch: %s", cudaGetErrorString(e));
   return run_listed(a, &tm, L, nsm, p.ptr, p.slots, 0,
-                    OwnPartials{p.rows_out, own.gran * pieces, own.gran, 0, err, (int)pairs, 0});
+                    OwnPartials{p.rows_out, own.gran * pieces, own.gran, 0, err, (int)pairs});
 }
 
 }  // namespace pkx

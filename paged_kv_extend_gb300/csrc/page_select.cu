@@ -174,6 +174,65 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+// A lane's part of the q sums of one (sequence, KV head): chunk c (8 dims) of qp
+// (`is_hi`) or qn.
+template <int D>
+__device__ __forceinline__ void query_sums(const uint16_t *q, int64_t first_row, int group, int c,
+                                           bool is_hi, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = 0.f;
+  const uint4 *row = reinterpret_cast<const uint4 *>(q + first_row * D) + c;
+#pragma unroll 4
+  for (int g = 0; g < group; ++g) {
+    const uint4 v = __ldg(row + g * (D / 8));
+    const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float qv = __uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16);
+      f[k] = __fadd_rn(f[k], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
+    }
+  }
+}
+
+// The scores of eight copies (a copy: 512 bytes, the bounds of 128 / D pages, 16
+// bytes a lane): lane l ends with the score of copy l % 8 (and its own page of
+// the copy).  The lanes' sums meet in a butterfly in which a lane passes on the
+// half of its values that its partner keeps, so that eight sums take 4 + 2 + 1
+// shuffles (and one a level from there on), each of them the sum of two
+// neighbours of the tree.
+template <int D, typename F>
+__device__ __forceinline__ float eight_scores(const float (&f)[8], F &&copy) {
+  constexpr int LP = D / 4;  // lanes of a page
+  const int lane = threadIdx.x & 31;
+  float v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint4 x = copy(u);
+    const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      t[k] = __fmul_rn(__uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16), f[k]);
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1)
+#pragma unroll
+      for (int k = 0; k < m; ++k) t[k] = __fadd_rn(t[2 * k], t[2 * k + 1]);
+    v[u] = t[0];
+  }
+#pragma unroll
+  for (int o = 1, m = 4; o < 8; o <<= 1, m >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < m; ++k) {
+      const float keep = up ? v[2 * k + 1] : v[2 * k], pass = up ? v[2 * k] : v[2 * k + 1];
+      v[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, pass, o));
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < LP; o <<= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
 // A warp: one KV head and a run of up to 32 consecutive entries of kv_indices,
 // whose page ids its lanes fetch together; neighbouring warps take the heads
 // of the same pages.  D / 4 lanes hold a page's two bounds, 8 dims each.  All of
@@ -235,25 +294,8 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
       continue;
     }
     float f[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = 0.f;
-    const uint4 *row =
-        reinterpret_cast<const uint4 *>(p.q + ((int64_t)b * p.hq + (int64_t)h * p.group) * D) + c;
-#pragma unroll 4
-    for (int g = 0; g < p.group; ++g) {
-      const uint4 v = __ldg(row + g * CH);
-      const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float qv = __uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16);
-        f[k] = __fadd_rn(f[k], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
-      }
-    }
-    // Eight copies at a time.  The lanes' sums meet in a butterfly in which a
-    // lane passes on the half of its values that its partner keeps, so that eight
-    // sums take 4 + 2 + 1 shuffles (and one a level from there on), each of
-    // them the sum of two neighbours of the tree; lane l ends with copy l % 8.
-    // (Entries of other sequences in a copy are left out.)
+    query_sums<D>(p.q, (int64_t)b * p.hq + (int64_t)h * p.group, p.group, c, is_hi, f);
+    // eight copies at a time (entries of other sequences in a copy are left out)
     for (int u0 = i / PPW / 8 * 8; u0 * PPW < seg; u0 += 8) {
       if (u0 >= landed) {
         landed = u0 + 8;
@@ -264,35 +306,11 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
           default: cp_async_wait_group<0>();
         }
       }
-      float v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint4 x = ld_shared_u4(mine + (u0 + u) * 512);
-        const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-        float t[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          t[k] = __fmul_rn(__uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16), f[k]);
-#pragma unroll
-        for (int m = 4; m > 0; m >>= 1)
-#pragma unroll
-          for (int k = 0; k < m; ++k) t[k] = __fadd_rn(t[2 * k], t[2 * k + 1]);
-        v[u] = t[0];
-      }
-#pragma unroll
-      for (int o = 1, m = 4; o < 8; o <<= 1, m >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int k = 0; k < m; ++k) {
-          const float keep = up ? v[2 * k + 1] : v[2 * k], pass = up ? v[2 * k] : v[2 * k + 1];
-          v[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, pass, o));
-        }
-      }
-#pragma unroll
-      for (int o = 8; o < LP; o <<= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+      const float score =
+          eight_scores<D>(f, [&](int u) { return ld_shared_u4(mine + (u0 + u) * 512); });
       const int at = (u0 + (lane & 7)) * PPW + sub;
       const int page = __shfl_sync(0xffffffffu, my_page, at & 31);
-      if (l < 8 && at >= i && at < seg) keys[at] = page < 0 ? 0u : score_key(v[0]);
+      if (l < 8 && at >= i && at < seg) keys[at] = page < 0 ? 0u : score_key(score);
     }
     i = seg;
   }
@@ -306,6 +324,7 @@ struct SelectParams {
   int batch, hkv, top_k, first_pages, last_pages;
   const uint32_t *keys;
   int32_t *selected;
+  int32_t *err;  // [batch * hkv] (the fused kernel)
   WsHeader *hdr;
 };
 
@@ -333,7 +352,7 @@ __device__ __forceinline__ void threshold(const uint32_t *keys, int m, int want,
     }
     if constexpr (HELD == 16)
       for (int i = HELD * THREADS + tid; i < m; i += THREADS) {
-        const uint32_t k = __ldg(keys + i);
+        const uint32_t k = keys[i];
         c1 += k >= t1;
         c2 += k >= t2;
         c3 += k >= t3;
@@ -359,45 +378,30 @@ __device__ __forceinline__ void threshold(const uint32_t *keys, int m, int want,
   }
 }
 
-// One CTA for each (sequence, KV head).  A thread keeps 16 keys in registers
-// (keys i = r * THREADS + tid).
+// Numbers of the pages of a sequence of n > top_k pages, by a CTA: `keys` are the
+// ordered scores of the pages between the first and the last ones.  A thread
+// keeps 16 keys in registers (keys i = r * THREADS + tid).  Returns whether this
+// thread saw a page outside the bounds.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams p) {
+__device__ __forceinline__ bool select_top(const SelectParams &p, int n, const uint32_t *keys,
+                                           int32_t *out, int (*s_cnt)[32][3], int (*s_scan)[32]) {
   constexpr int kHeld = 16, WARPS = THREADS / 32;
-  __shared__ int s_cnt[2][32][3];
-  __shared__ int s_scan[2][32];
-  grid_dep_wait();
-  grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.hkv, h = blockIdx.x - b * p.hkv;
-  const int64_t at = __ldg(p.kv_indptr + b);
-  const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
-  int32_t *out = p.selected + (int64_t)blockIdx.x * p.top_k;
-  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
-  if (bad && tid == 0) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
-  const int n = bad ? 0 : (int)n64;
-  if (n <= p.top_k) {  // every page
-    for (int i = tid; i < p.top_k; i += THREADS) out[i] = i < n ? i : -1;
-    return;
-  }
-  // candidates: the pages between the first and the last ones
   const int lo = p.first_pages, m = n - p.first_pages - p.last_pages;
   const int want = p.top_k - p.first_pages - p.last_pages;  // 0 <= want < m
-  const uint32_t *keys = p.keys + (int64_t)h * p.n_indices + at + lo;
   uint32_t held[kHeld];
-  bool lost = false;  // a page outside the bounds
+  bool lost = false;
 #pragma unroll
   for (int r = 0; r < kHeld; ++r) {
     const int i = r * THREADS + tid;
-    held[r] = i < m ? __ldg(keys + i) : 0u;
+    held[r] = i < m ? keys[i] : 0u;
     lost |= i < m && held[r] == 0u;
   }
-  for (int i = kHeld * THREADS + tid; i < m; i += THREADS) lost |= __ldg(keys + i) == 0u;
-  if (lost) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
+  for (int i = kHeld * THREADS + tid; i < m; i += THREADS) lost |= keys[i] == 0u;
   for (int i = tid; i < p.first_pages; i += THREADS) out[i] = i;
   for (int i = tid; i < p.last_pages; i += THREADS)
     out[p.top_k - p.last_pages + i] = n - p.last_pages + i;
-  if (want == 0) return;
+  if (want == 0) return lost;
 
   uint32_t T;
   int above;
@@ -425,8 +429,10 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
     const unsigned below = (1u << lane) - 1u;
     const int my_gt = gt + (before & 0xFFFF) + __popc(g & below);
     const int my_eq = eq + (before >> 16) + __popc(q & below);
-    if (i < m && (k > T || (k == T && my_eq < ties)))
-      out[lo + my_gt + min(my_eq, ties)] = lo + i;
+    // (my_gt + my_eq < want always, but for keys that another CTA changes: an
+    // indptr that decreases can give two sequences the same ones)
+    const int pos = my_gt + min(my_eq, ties);
+    if (i < m && (k > T || (k == T && my_eq < ties)) && pos < want) out[lo + pos] = lo + i;
     gt += all & 0xFFFF;
     eq += all >> 16;
   };
@@ -435,12 +441,107 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
     if (r * THREADS < m) place(r, held[r]);
   for (int r = kHeld; r * THREADS < m; ++r) {
     const int i = r * THREADS + tid;
-    place(r, i < m ? __ldg(keys + i) : 0u);
+    place(r, i < m ? keys[i] : 0u);
+  }
+  return lost;
+}
+
+// One CTA for each (sequence, KV head): its pages' numbers from the keys in the
+// workspace.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams p) {
+  __shared__ int s_cnt[2][32][3];
+  __shared__ int s_scan[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.x / p.hkv, h = blockIdx.x - b * p.hkv;
+  const int64_t at = __ldg(p.kv_indptr + b);
+  const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
+  int32_t *out = p.selected + (int64_t)blockIdx.x * p.top_k;
+  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
+  bool lost = bad;
+  const int n = bad ? 0 : (int)n64;
+  if (n <= p.top_k) {  // every page
+    for (int i = threadIdx.x; i < p.top_k; i += THREADS) out[i] = i < n ? i : -1;
+  } else {
+    lost = select_top<THREADS>(p, n, p.keys + (int64_t)h * p.n_indices + at + p.first_pages, out,
+                               s_cnt, s_scan);
+  }
+  if (lost) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
+}
+
+// Scores and selection in one: a CTA for each (sequence, KV head), whose eight
+// warps take eight copies of bounds at a time and leave the keys in shared memory
+// (in the workspace past kFusedKeys pages).  The queries are summed once a CTA
+// and the keys make no round trip; it needs CTAs enough to fill the GPU.
+constexpr int kFusedThreads = 256, kFusedKeys = 4096;
+template <int D>
+__global__ void __launch_bounds__(kFusedThreads, 4) page_score_select_kernel(const ScoreParams p,
+                                                                             const SelectParams sp) {
+  constexpr int LP = D / 4, PPW = 32 / LP, CH = D / 8, WARPS = kFusedThreads / 32;
+  constexpr int STEP = 8 * PPW;  // pages of a warp's step
+  __shared__ uint32_t s_keys[kFusedKeys];
+  __shared__ int s_cnt[2][32][3];
+  __shared__ int s_scan[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x / p.hkv, h = blockIdx.x - b * p.hkv;
+  const int64_t at = __ldg(p.kv_indptr + b);
+  const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
+  int32_t *out = sp.selected + (int64_t)blockIdx.x * p.top_k;
+  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
+  bool lost = bad;
+  const int n = bad ? 0 : (int)n64;
+  if (n <= p.top_k) {  // every page
+    for (int i = threadIdx.x; i < p.top_k; i += kFusedThreads) out[i] = i < n ? i : -1;
+  } else {
+    const int sub = lane / LP, l = lane - sub * LP;
+    const bool is_hi = l >= CH;
+    const int32_t *ids = p.kv_indices + at + sp.first_pages;
+    const int m = n - sp.first_pages - sp.last_pages;
+    uint32_t *keys = m <= kFusedKeys ? s_keys : p.keys + (int64_t)h * p.n_indices + at;
+    auto fetch = [&](int i0) {  // page ids of a step, a lane each
+      const int i = i0 + lane;
+      const int page = lane < STEP && i < m ? __ldg(ids + i) : -1;
+      return page < p.num_pages ? page : -1;
+    };
+    int coming = fetch(warp * STEP);
+    float f[8];
+    query_sums<D>(p.q, (int64_t)b * p.hq + (int64_t)h * p.group, p.group, is_hi ? l - CH : l, is_hi,
+                  f);
+    const uint4 *box = p.bounds + (int64_t)h * LP + l;
+    for (int i0 = warp * STEP; i0 < m; i0 += WARPS * STEP) {
+      const int mine = coming;
+      uint4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int page = __shfl_sync(0xffffffffu, mine, u * PPW + sub);
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (page >= 0) x[u] = __ldg(box + (int64_t)page * p.hkv * LP);
+      }
+      coming = fetch(i0 + WARPS * STEP);
+      const float score = eight_scores<D>(f, [&](int u) { return x[u]; });
+      const int j = (lane & 7) * PPW + sub;
+      const int page = __shfl_sync(0xffffffffu, mine, j);
+      if (l < 8 && i0 + j < m) keys[i0 + j] = page < 0 ? 0u : score_key(score);
+    }
+    __syncthreads();
+    lost = select_top<kFusedThreads>(sp, n, keys, out, s_cnt, s_scan);
+  }
+  lost = __syncthreads_or(lost);
+  if (threadIdx.x == 0) {
+    sp.err[blockIdx.x] = lost;
+    if (blockIdx.x == 0) set_status_in_units(p.hdr, sp.err, gridDim.x);
   }
 }
 
-size_t select_pages_workspace(int hkv, int64_t n_indices) {
-  return 256 + ((sizeof(uint32_t) * (size_t)hkv * (size_t)n_indices + 255) & ~(size_t)255);
+static size_t select_keys_offset(int batch, int hkv) {
+  return 256 + ((sizeof(int32_t) * (size_t)batch * (size_t)hkv + 255) & ~(size_t)255);
+}
+size_t select_pages_workspace(int batch, int hkv, int64_t n_indices) {
+  return select_keys_offset(batch, hkv) +
+         ((sizeof(uint32_t) * (size_t)hkv * (size_t)n_indices + 255) & ~(size_t)255);
 }
 
 int launch_select_pages(const SelectArgs &a) {
@@ -448,7 +549,8 @@ int launch_select_pages(const SelectArgs &a) {
   const int nsm = num_sms_current_device();
   if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   WsHeader *hdr = static_cast<WsHeader *>(a.workspace);
-  uint32_t *keys = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.workspace) + 256);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.workspace) +
+                                                select_keys_offset(a.batch, a.hkv));
   ScoreParams p;
   p.q = static_cast<const uint16_t *>(a.q);
   p.bounds = static_cast<const uint4 *>(a.bounds);
@@ -463,6 +565,33 @@ int launch_select_pages(const SelectArgs &a) {
   p.top_k = a.top_k;
   p.keys = keys;
   p.hdr = hdr;
+  SelectParams s;
+  s.kv_indptr = a.kv_indptr;
+  s.n_indices = a.n_indices;
+  s.batch = a.batch;
+  s.hkv = a.hkv;
+  s.top_k = a.top_k;
+  s.first_pages = a.first_pages;
+  s.last_pages = a.last_pages;
+  s.keys = keys;
+  s.selected = a.selected;
+  s.hdr = hdr;
+  s.err = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(a.workspace) + 256);
+  if ((int64_t)a.batch * a.hkv >= (1ll << 31))
+    return set_error(PKX_EUNSUPPORTED, "select_pages: batch too large");
+  const dim3 pairs((unsigned)(a.batch * a.hkv));
+  // One kernel where the (sequence, KV head) pairs fill the GPU, or where there is
+  // too little to spread: 5 sequences of up to 49 pages, 3 KV heads, 11 us for
+  // the two kernels.  Else scores by runs of pages, then the selection.
+  const int64_t mean = a.n_indices / a.batch;
+  if ((int64_t)a.batch * a.hkv >= nsm || mean <= 256) {
+    cudaError_t e = launch_pdl(
+        a.d == 128 ? page_score_select_kernel<128> : page_score_select_kernel<64>, pairs,
+        dim3(kFusedThreads), 0, a.stream, p, s);
+    if (e != cudaSuccess)
+      return set_error(PKX_ECUDA, "page_score_select launch: %s", cudaGetErrorString(e));
+    return PKX_OK;
+  }
   // a warp's run: 32 entries, or fewer where that leaves less than 16 warps an
   // SM (a run reads the group's query rows once)
   int64_t run = a.n_indices * a.hkv / ((int64_t)nsm * 16);
@@ -471,7 +600,7 @@ int launch_select_pages(const SelectArgs &a) {
   p.runs = (a.n_indices + run - 1) / run;
   int64_t grid = (p.runs * a.hkv + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
   if (grid < 1) grid = 1;  // (the status word)
-  if (grid >= (1ll << 31) || (int64_t)a.batch * a.hkv >= (1ll << 31))
+  if (grid >= (1ll << 31))
     return set_error(PKX_EUNSUPPORTED, "select_pages: too many pages in one call");
   auto score = a.d == 128 ? page_score_kernel<128> : page_score_kernel<64>;
   const size_t smem = (size_t)(kScoreThreads / 32) * kScoreRun * a.d * 4;  // 64 KB at most
@@ -486,21 +615,8 @@ int launch_select_pages(const SelectArgs &a) {
     e = launch_pdl(score, dim3((unsigned)grid), dim3(kScoreThreads), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "page_score launch: %s", cudaGetErrorString(e));
-  SelectParams s;
-  s.kv_indptr = a.kv_indptr;
-  s.n_indices = a.n_indices;
-  s.batch = a.batch;
-  s.hkv = a.hkv;
-  s.top_k = a.top_k;
-  s.first_pages = a.first_pages;
-  s.last_pages = a.last_pages;
-  s.keys = keys;
-  s.selected = a.selected;
-  s.hdr = hdr;
   // By the batch's average: a warp holds 512 keys and needs no barrier, 256
   // threads hold 4096, 1024 hold 16384.
-  const dim3 pairs((unsigned)(a.batch * a.hkv));
-  const int64_t mean = a.n_indices / a.batch;
   if (mean <= 512)
     e = launch_pdl(page_select_kernel<32>, pairs, dim3(32), 0, a.stream, s);
   else if (mean <= 4096)

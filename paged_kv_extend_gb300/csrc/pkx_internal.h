@@ -92,6 +92,21 @@ struct WsHeader {
   int32_t pad[59];
 };
 
+// A status word of this value says that the call's warps or CTAs left theirs (0 or
+// not) in an array of the workspace, which pkx_workspace_status reads: a call of
+// one kernel has no earlier one to clear the word that all of them would set.
+// The header's padding holds the array's entries and its place.
+constexpr int kStatusInUnits = 1000;
+enum { kUnitsCount = 3, kUnitsPlace = 4 };  // the place in 256 bytes from the header
+#ifdef __CUDACC__
+__device__ __forceinline__ void set_status_in_units(WsHeader *hdr, const int32_t *err, int n) {
+  hdr->status = kStatusInUnits;
+  hdr->pad[kUnitsCount] = n;
+  hdr->pad[kUnitsPlace] = (int32_t)((reinterpret_cast<const uint8_t *>(err) -
+                                     reinterpret_cast<const uint8_t *>(hdr)) / 256);
+}
+#endif
+
 // Byte offsets of the workspace regions for one problem.
 struct WsLayout {
   size_t seq_off;      // int32 [8][batch + 1] per-sequence scratch (five used)
@@ -282,7 +297,7 @@ struct SelectArgs {
   size_t workspace_bytes;
   cudaStream_t stream;
 };
-size_t select_pages_workspace(int hkv, int64_t n_indices);
+size_t select_pages_workspace(int batch, int hkv, int64_t n_indices);
 int launch_select_pages(const SelectArgs &a);
 
 // Decode attention whose work is listed by schedulers of its own

@@ -111,7 +111,7 @@ _SIGS = {
         _i64, _i64, _i, _f, _f, _p]),
     "pkx_update_page_bounds": (_i, [
         _p, _i64, _i64, _i, _i, _i64, _i, _i, _p, _p, _i64, _p, _p]),
-    "pkx_select_pages_workspace_size": (_sz, [_i, _i64]),
+    "pkx_select_pages_workspace_size": (_sz, [_i, _i, _i64]),
     "pkx_select_pages": (_i, [
         _p, _p, _i64, _p, _p, _i64, _i, _i, _i, _i, _i, _i, _i, _p, _p, _sz, _p]),
     "pkx_decode_pages_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
@@ -1131,8 +1131,8 @@ def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
     return bounds
 
 
-def select_pages_workspace_size(hkv, n_indices) -> int:
-    return int(load_library().pkx_select_pages_workspace_size(hkv, n_indices))
+def select_pages_workspace_size(batch, hkv, n_indices) -> int:
+    return int(load_library().pkx_select_pages_workspace_size(batch, hkv, n_indices))
 
 
 def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pages=1,
@@ -1151,7 +1151,7 @@ def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pa
     if selected is None:
         selected = torch.empty((b, hkv, max(top_k, 0)), dtype=_I32, device=q.device)
     n = kv_indices.numel()
-    ws, ws_at, ws_bytes = _workspace_at(workspace, index, select_pages_workspace_size, b, hkv, n)
+    ws, ws_at, ws_bytes = _workspace_at(workspace, index, select_pages_workspace_size, b, b, hkv, n)
     _call(index, lib.pkx_select_pages, _dense_at(q, _BF16, q_shape, index, "q"),
           _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds"), pages,
           _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"),
