@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         if (!ring_ok) abort_cta(abort_flag, p.status, PKX_ETIMEOUT);
         break;
       }
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       // decode: warpgroup wg takes the unit's tiles wg, wg + 2, ... of the
       // one query tile (two key streams, merged by the combine)
       // Two key streams (decode units; split units of one query tile):
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
         const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
         if (u < 0) break;
-        const WorkUnit w = p.units[p.uorder[u]];
+        const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
         const int nt = w.n_tiles;
         if (nt == 0) continue;
         if constexpr (F4) {  // tile_keys()'s count of tiles before k_split
@@ -975,7 +975,11 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
           const int pos = p.part_first[blockIdx.x] + (int)uc;
           u = pos < p.part_first[blockIdx.x + 1] ? pos : -1;
         } else {
-          const int pos = atomicAdd(p.next_unit, 1);
+          // (listed units are claimed from the grid's size on: the first is the
+          // CTA's own)
+          const int pos = MODE != kListed ? atomicAdd(p.next_unit, 1)
+                          : uc == 0       ? (int)blockIdx.x
+                                          : (int)gridDim.x + atomicAdd(p.next_unit, 1);
           u = pos < n_units ? pos : -1;
         }
       }
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
         }
       }
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
       const bool q1 = w.n_tok > TOK;
@@ -1140,7 +1144,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
       // the unit's query rows (tokens x G heads of query tile 0) to f16 in
@@ -1194,7 +1198,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
       const uint8_t *kp8 =
@@ -1318,7 +1322,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int nt = w.n_tiles;
       auto from_ext = [&](int j) {
         int kb, ke;
@@ -1465,7 +1469,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
       for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
         const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
         if (u < 0) break;
-        const WorkUnit w = p.units[p.uorder[u]];
+        const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
         const int nt = w.n_tiles;
         if (nt == 0) continue;
         const bf16 *kp = p.k_pool + (int64_t)w.kvh * p.kb_sh + ch * 8;
@@ -1574,7 +1578,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int nt = w.n_tiles;
       if (nt == 0) continue;
       const uint8_t *kp8 =
@@ -1720,7 +1724,7 @@ __global__ void __launch_bounds__(Cfg<HD>::THREADS, 1)
     for (uint32_t uc = 0; ok && !*abort_flag; ++uc) {
       const int u = ring_unit(&bars[B_U_FULL], &bars[B_U_EMPTY], s_unit, uc, abort_flag, true, ok, p.wait_ns);
       if (u < 0) break;
-      const WorkUnit w = p.units[p.uorder[u]];
+      const WorkUnit w = p.units[MODE == kListed ? u : p.uorder[u]];
       const int t0 = max(w.k_begin, w.qpos0) - w.qpos0;
       const int t1 = min(w.k_end, w.qpos0 + w.n_tok) - w.qpos0;
       const int n = (t1 - t0) * (CK + CV);

@@ -56,7 +56,7 @@ struct __align__(16) ListedRow {
 };
 
 struct ListedLayout {
-  size_t seq_off, grp_off, units_off, order_off, rows_off, idx_off, ptr_off, err_off, plse_off,
+  size_t seq_off, grp_off, units_off, rows_off, idx_off, ptr_off, err_off, plse_off,
       po_off, total;
   int unit_max;
   int64_t gran_max;
@@ -249,8 +249,9 @@ struct RowsParams {
   int batch, hq, hkv, group;
   float scale_log2, cap_pre, cap_log2, v_scale;
   int use_cap;
-  // own keys: first key, and first piece of each sequence [batch + 1]
-  const int32_t *own_begin, *own_first;
+  // own keys [batch + 1]: first key, and first piece of each sequence; its keys
+  // below alias_len are listed by sequence alias_of
+  const int32_t *own_begin, *own_first, *alias_len, *alias_of;
   // selected pages
   const int32_t *selected, *last_page_len;
   int64_t n_indices;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
   // sequence's slots, on different SMs); then own keys are claimed (ragged), and
   // pages, of equal sizes, taken in turn
   for (int u = warp * gridDim.x + blockIdx.x; u < count;) {
-    int b, kvh, k_begin, k_end, at, n_pages = 0, last_len = 0;
+    int b, kvh, k_begin, k_end, at, n_pages = 0, last_len = 0, alias = 0, alias_at = 0;
     bool bad = false;
     const int32_t *sel = nullptr;
     if constexpr (PAGES) {
@@ -350,6 +351,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
       at = __ldg(p.kv_indptr + b);
       const int begin = __ldg(p.own_begin + b), keys = __ldg(p.kv_indptr + b + 1) - at - begin;
       const int runs = keys / kRowRun + (keys % kRowRun != 0);
+      alias = __ldg(p.alias_len + b);
+      if (alias > 0) alias_at = __ldg(p.kv_indptr + __ldg(p.alias_of + b));
       k_begin = begin + piece_at(x - first, runs, S, kRowRun, keys);
       k_end = begin + piece_at(x - first + 1, runs, S, kRowRun, keys);
     }
@@ -372,7 +375,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) rows_kernel(const RowsPara
         // (a page is inside the pool as a whole or not at all)
         return page < 0 || slot - off + p.page_size > p.num_slots ? kOutside : (int)slot;
       } else {
-        const int s = __ldg(p.kv_indices + at + k_begin + i);
+        const int j = k_begin + i;
+        const int s = __ldg(p.kv_indices + (j < alias ? alias_at : at) + j);
         return (uint32_t)s < (uint64_t)p.num_slots ? s : kOutside;
       }
     };
@@ -608,11 +612,12 @@ struct SharedParams {
   int unit_max;
   int64_t gran_max;
   int32_t *seq;     // [kSeqArrays][batch + 1]
-  int32_t *own_begin, *own_first;  // [batch + 1] first own key; first piece
+  // [batch + 1] first own key; first piece; keys that sequence alias_of lists
+  int32_t *own_begin, *own_first, *alias_len, *alias_of;
+  int key_elements;  // of a key's K and V rows, all KV heads
   int32_t *grp;     // [kGroupArrays][num_groups + 1]
   int in_smem;      // those arrays in dynamic shared memory instead
   WorkUnit *units;
-  int32_t *order;
   ListedRow *rows_out;
   WsHeader *hdr;
 };
@@ -664,12 +669,19 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 // no 64-bit division (a candidate in 64 bits took 2400 clocks); what a group
 // or a sequence needs later stays in shared memory.
 constexpr int kUnitTiles = 3;
+// Elements of K and V that sharing has to save for the tile kernel to run, whose
+// units take 20 us however short: rows_kernel reads a prefix again for every
+// sequence, mostly from L2, at 5.8 elements a picosecond from a bf16 pool (64
+// sequences, 8192 shared keys, 8 KV heads: 233 us a call against 70 shared) and
+// 4.0 from an fp8 one (8 groups of 8, 2000 keys, 4 KV heads: 55 against 47).
+constexpr unsigned long long kShareElements = 88ull << 20;
 constexpr int kSeqArrays = 3, kGroupArrays = 7;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {
   extern __shared__ int32_t s_dyn[];
   __shared__ Two sh[32];
   __shared__ uint2 s_best[32];
   __shared__ int s_longest;
+  __shared__ unsigned long long s_saved;  // keys, over the sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.batch, NG = p.num_groups, B1 = B + 1, G1 = NG + 1;
   int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + kSeqArrays * B1 : p.grp;
@@ -679,7 +691,10 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   int32_t *gS = grp, *gB = grp + G1, *gK = grp + 2 * G1, *gR = grp + 3 * G1, *gP = grp + 4 * G1;
   int32_t *gU = grp + 5 * G1, *gG = grp + 6 * G1;
   const int blk = 2 * p.tok;  // tokens of a prefix unit
-  if (tid == 0) s_longest = 0;
+  if (tid == 0) {
+    s_longest = 0;
+    s_saved = 0;
+  }
   grid_dep_wait();
   grid_dep_launch();
   // groups are consecutive runs of sequences, else nothing is shared
@@ -697,6 +712,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     bad |= !ok;
     sT[b] = ok ? T : 0;
     sS[b] = 0;
+    p.alias_len[b] = 0;
   }
   if (tid == 0) {
     p.hdr->status = 0;
@@ -718,7 +734,11 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       for (int b = lo + lane; b < hi; b += 32) least = min(least, sT[b]);
       least = __reduce_min_sync(0xffffffffu, least);
       if (hi - lo >= 2 && least >= kBlockN) S = least;
-      for (int b = lo + lane; b < hi; b += 32) sS[b] = S;
+      for (int b = lo + lane; b < hi; b += 32) {
+        sS[b] = S;
+        p.alias_len[b] = S;
+        p.alias_of[b] = lo;
+      }
     }
     __syncwarp();
     if (lane == 0) {
@@ -726,10 +746,20 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       gS[g] = S;
       gK[g] = nb;
       gR[g] = nb > 0 ? (nb - 1) * blk + (last <= p.tok ? 2 * last : last) : 0;
-      if (S > 0) atomicMax(&s_longest, tiles(S));
+      if (S > 0) {
+        atomicMax(&s_longest, tiles(S));
+        atomicAdd(&s_saved, (unsigned long long)(hi - lo - 1) * S);
+      }
     }
   }
   __syncthreads();
+  if (p.rows && s_saved * p.key_elements < kShareElements) {  // every sequence reads its prefix
+    __syncthreads();
+    for (int b = tid; b < B; b += 1024) sS[b] = 0;
+    for (int g = tid; g < NG; g += 1024) gS[g] = gK[g] = gR[g] = 0;
+    if (tid == 0) s_longest = 0;
+    __syncthreads();
+  }
   // totals: tiles of the prefixes, runs of own keys
   auto runs = [&](int b) {
     const int n = sT[b] - sS[b];
@@ -862,7 +892,6 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.slot = gG[g] + (sp * p.hkv + kvh) * gR[g] + k * blk;
     w.dq = w.claim = 0;
     p.units[u] = w;
-    p.order[u] = u;
   }
   __syncthreads();  // (own_first, for the units below)
   if (p.rows) return;  // (rows_kernel finds its units itself)
@@ -889,7 +918,6 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     w.slot = pre_gran + p.own_gran * i;
     w.dq = w.claim = 0;
     p.units[pre_units + i] = w;
-    p.order[pre_units + i] = pre_units + i;
   }
 }
 
@@ -920,13 +948,11 @@ static ListedLayout shared_layout(int batch, int num_groups, int hkv, int group,
   L.gran_max = 4ll * n * blk + 2ll * hkv * batch + own.gran * (own.target + (int64_t)hkv * batch);
   size_t off = up256(sizeof(WsHeader));
   L.seq_off = off;
-  off = up256(off + sizeof(int32_t) * (kSeqArrays + 2) * (size_t)(batch + 1));
+  off = up256(off + sizeof(int32_t) * (kSeqArrays + 4) * (size_t)(batch + 1));
   L.grp_off = off;
   off = up256(off + sizeof(int32_t) * kGroupArrays * (size_t)(num_groups + 1));
   L.units_off = off;
   off = up256(off + sizeof(WorkUnit) * (size_t)L.unit_max);
-  L.order_off = off;
-  off = up256(off + sizeof(int32_t) * (size_t)L.unit_max);
   L.rows_off = off;
   off = up256(off + sizeof(ListedRow) * (size_t)batch);
   L.plse_off = off;
@@ -954,7 +980,6 @@ struct PagesParams {
   int32_t *ptr;    // [batch * hkv] first key of each list
   int32_t *err;    // [batch * hkv]
   WorkUnit *units;
-  int32_t *order;
   ListedRow *rows_out;
   WsHeader *hdr;
 };
@@ -1049,7 +1074,6 @@ __global__ void __launch_bounds__(256) list_pages_kernel(const PagesParams p) {
     w.slot = p.gran * u;
     w.dq = w.claim = 0;
     p.units[u] = w;
-    p.order[u] = u;
   }
   // the slots, a warp an entry; a page outside the pool is listed as -1, which
   // the attention kernel reads as a zero row and reports
@@ -1084,8 +1108,6 @@ static ListedLayout pages_layout(int batch, int hkv, int group, int d, int page_
   if (!rows) {
     L.units_off = off;
     off = up256(off + sizeof(WorkUnit) * (size_t)units);
-    L.order_off = off;
-    off = up256(off + sizeof(int32_t) * (size_t)units);
     L.rows_off = off;
     off = up256(off + sizeof(ListedRow) * (size_t)batch);
     L.ptr_off = off;
@@ -1187,6 +1209,8 @@ static int launch_rows(const ListedArgs &a, const KParams &kp, const ListedLayou
   }
   p.own_begin = reinterpret_cast<int32_t *>(ws + L.seq_off) + kSeqArrays * (size_t)(a.batch + 1);
   p.own_first = p.own_begin + (a.batch + 1);
+  p.alias_len = p.own_first + (a.batch + 1);
+  p.alias_of = p.alias_len + (a.batch + 1);
   if (a.kv_fmt == kKvFp8E4M3) return launch_rows_as<D, 1, false>(p, nsm, a.stream);
   if (a.kv_fmt == kKvFp8E5M2) return launch_rows_as<D, 2, false>(p, nsm, a.stream);
   return launch_rows_as<D, 0, false>(p, nsm, a.stream);
@@ -1261,7 +1285,6 @@ static int run_listed(const ListedArgs &a, const ListedMaps *tm, const ListedLay
   kp.v_scale = a.v_scale;
   kp.inv_v_scale = 1.0f / a.v_scale;
   kp.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
-  kp.uorder = reinterpret_cast<int32_t *>(ws + L.order_off);
   kp.next_unit = &hdr->next_unit;
   kp.hdr = hdr;
   kp.status = &hdr->status;
@@ -1324,13 +1347,15 @@ int launch_decode_shared(const ListedArgs &a) {
   p.seq = reinterpret_cast<int32_t *>(ws + L.seq_off);
   p.own_begin = p.seq + kSeqArrays * (size_t)(a.batch + 1);
   p.own_first = p.own_begin + (a.batch + 1);
+  p.alias_len = p.own_first + (a.batch + 1);
+  p.alias_of = p.alias_len + (a.batch + 1);
+  p.key_elements = 2 * a.d * a.hkv;
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
   size_t smem = sizeof(int32_t) * (kSeqArrays * (size_t)(a.batch + 1) +
                                    kGroupArrays * (size_t)(a.num_groups + 1));
   p.in_smem = smem <= 40 * 1024;
   if (!p.in_smem) smem = 0;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
-  p.order = reinterpret_cast<int32_t *>(ws + L.order_off);
   p.rows_out = reinterpret_cast<ListedRow *>(ws + L.rows_off);
   p.hdr = reinterpret_cast<WsHeader *>(ws);
   cudaError_t e = launch_pdl(shared_sched_kernel, dim3(1), dim3(1024), smem, a.stream, p);
@@ -1342,13 +1367,13 @@ int launch_decode_shared(const ListedArgs &a) {
 }
 
 int launch_decode_pages(const ListedArgs &a) {
-  const int nsm = num_sms_current_device();
-  if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   const int group = a.hq / a.hkv;
   const int64_t pairs = (int64_t)a.batch * a.hkv;
   if (pairs * a.top_k * a.page_size >= INT_MAX)  // (units and granules are fewer)
     return set_error(PKX_EUNSUPPORTED,
                      "decode_pages: batch * hkv * top_k * page_size must be below 2^31");
+  const int nsm = num_sms_current_device();
+  if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   const ListedLayout L = pages_layout(a.batch, a.hkv, group, a.d, a.page_size, a.top_k, nsm);
   int rc = check_workspace(a, L);
   if (rc != PKX_OK) return rc;
@@ -1380,7 +1405,6 @@ int launch_decode_pages(const ListedArgs &a) {
   p.ptr = reinterpret_cast<int32_t *>(ws + L.ptr_off);
   p.err = err;
   p.units = reinterpret_cast<WorkUnit *>(ws + L.units_off);
-  p.order = reinterpret_cast<int32_t *>(ws + L.order_off);
   p.rows_out = reinterpret_cast<ListedRow *>(ws + L.rows_off);
   p.hdr = reinterpret_cast<WsHeader *>(ws);
   const size_t smem = sizeof(int) * (2 * (size_t)a.top_k + 1);

@@ -64,6 +64,11 @@ SELECT = [  # pages of each sequence, hq, hkv, d, top, first, last
     ([6000], 4, 1, 64, 500, 1, 1),  # past the keys held in registers (256 threads)
     ([20000], 2, 1, 64, 4000, 5, 6),  # and with 1024
     ([33] * 70, 128, 1, 64, 4, 0, 1),
+    ([900, 3], 8, 2, 64, 40, 1, 1),  # a warp each, past the keys that it holds
+    ([3000, 100], 8, 2, 128, 200, 2, 0),
+    ([7000, 10, 10], 4, 1, 64, 300, 0, 1),
+    ([5000] + [20] * 79, 2, 2, 128, 16, 1, 1),  # one kernel, keys in the workspace
+    ([600, 31, 0, 64] * 20, 6, 2, 64, 33, 1, 2),
 ]
 
 
@@ -145,6 +150,9 @@ ATTEND = [  # keys of each sequence, page, hq, hkv, d, top, kv, cap
     dict(keys=[900, 5, 64], page=32, hq=28, hkv=4, d=128, top=11, kv=torch.float8_e4m3fn, cap=0.0),
     dict(keys=[900, 5, 64], page=32, hq=8, hkv=1, d=64, top=11, kv=torch.float8_e5m2, cap=0.0),
     dict(keys=[5000], page=200, hq=128, hkv=1, d=64, top=25, kv=torch.bfloat16, cap=0.0),
+    dict(keys=[4000, 0, 90], page=64, hq=34, hkv=2, d=128, top=60, kv=torch.float8_e4m3fn, cap=0.0),
+    dict(keys=[4000, 31], page=16, hq=16, hkv=1, d=128, top=240, kv=torch.bfloat16, cap=2.0),
+    dict(keys=[3000, 9], page=24, hq=9, hkv=1, d=64, top=100, kv=torch.float8_e4m3fn, cap=0.0),
     dict(keys=[40] * 150, page=8, hq=4, hkv=2, d=128, top=3, kv=torch.bfloat16, cap=0.0),
 ]
 

@@ -85,12 +85,45 @@ def test_against_64_bits(case):
     R.check_attention(o, lse, _reference(args, **kw), cap)
 
 
-def test_the_first_sequence_lists_the_prefix():
-    """The others' entries below the shared length are not read."""
-    q, k, v, indptr, idx, gptr, shared = args = _case([(200, [9, 30])], [], [], 4, 2, 128, BF, 2)
+# Sharing runs where it saves more than 88 << 20 elements of K and V, of groups of
+# at most 16 query heads; all of these but the third do (it saves 82 << 20).
+# Groups of more heads always share.
+LARGE = [  # groups, alone, before, hq, hkv, d, kv, cap
+    ([(1000, [9, 0, 130, 300, 1] * 13)], [0, 700], [], 32, 8, 128, BF, 0.0),   # blocks of 64 and 1 sequence
+    ([(3001, [5] * 18 + [0] * 19)], [], [33, 0], 28, 4, 128, BF, 3.0),         # 18 sequences a tile, 37
+    ([(2500, [4, 300, 0]), (129, [7, 7]), (2000, [1] * 9), (20, [3, 4])], [70], [5], 16, 16, 128, BF, 0.0),
+    ([(2500, [4, 300, 0]), (129, [7, 7]), (4000, [1] * 9), (20, [3, 4])], [70], [5], 16, 16, 128, BF, 0.0),
+    ([(2222, [64] * 12), (1999, [2] * 8)], [0, 900], [], 8, 8, 128, E4, 0.0),
+    ([(6100, [3] * 120)], [], [], 9, 1, 64, E5, 0.0),                          # 14 sequences a tile
+    ([(5000, [40] * 8)], [6], [], 64, 4, 128, BF, 0.0),                        # 16 heads
+    ([(700, [40, 0, 3, 900])], [6, 0], [2], 34, 2, 128, BF, 0.0),              # 17 heads
+    ([(900, [40, 0, 3])], [6, 0, 1500], [], 80, 2, 64, E4, 0.0),               # 40 heads
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: f"{[(s, len(o)) for s, o in c[0]][:3]}-{c[3]}/{c[4]}x{c[5]}")
+def test_large_groups_against_64_bits(case):
+    groups, alone, before, hq, hkv, d, kv, cap = case
+    args = _case(groups, alone, before, hq, hkv, d, kv, 12)
+    kw = dict(cap=cap) if kv == BF else dict(cap=cap, ks=0.37, vs=1.9)
+    o, lse, ws = _run(args, **kw)
+    assert pkx.workspace_status(ws) == pkx.PKX_OK
+    saved = sum((len(o) - 1) * s for s, o in groups if s >= 128) * 2 * d * hkv
+    shares = saved >= 88 << 20 or hq // hkv > 16
+    assert (int(ws.view(torch.int32)[1]) > 0) == shares  # units of prefixes
+    R.check_attention(o, lse, _reference(args, **kw), cap)
+
+
+@pytest.mark.parametrize("keys,members", [(200, 2), (3000, 17)])
+def test_the_first_sequence_lists_the_prefix(keys, members):
+    """The others' entries below the shared length are not read, whether the
+    prefix is shared or (few members) read by each."""
+    args = _case([(keys, [9, 30] + [1] * (members - 2))], [], [], 32, 8, 128, BF, 2)
+    q, k, v, indptr, idx, gptr, shared = args
     want = _run(args)[:2]
     idx = idx.clone()
-    idx[int(indptr[1]):int(indptr[1]) + 200] = -1
+    for b in range(1, members):
+        idx[int(indptr[b]):int(indptr[b]) + keys] = -1
     o, lse, ws = _run((q, k, v, indptr, idx, gptr, shared))
     assert pkx.workspace_status(ws) == pkx.PKX_OK
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
@@ -131,21 +164,22 @@ def test_bad_groups_share_nothing_and_are_reported():
     assert pkx.workspace_status(ws) == pkx.PKX_EDEVICE and o.isfinite().all()
 
 
-def test_nan_rows_stay_their_own():
+@pytest.mark.parametrize("keys,members,hkv", [(256, 3, 2), (9000, 20, 4)])
+def test_nan_rows_stay_their_own(keys, members, hkv):
     """A NaN query is its own row's; a NaN key or value of the prefix reaches
     the whole group of its KV head and nobody else."""
-    args = _case([(256, [4, 5, 6])], [40], [], 8, 2, 64, BF, 9)
+    args = _case([(keys, [4, 5, 6] + [1] * (members - 3))], [40], [], 4 * hkv, hkv, 64, BF, 9)
     q, k, v, indptr, idx, gptr, shared = args
     q[1, 2, 3] = float("nan")
     o, lse, _ = _run(args)
-    bad = torch.zeros(4, 8, dtype=torch.bool)
+    bad = torch.zeros(members + 1, 4 * hkv, dtype=torch.bool)
     bad[1, 2] = True
     assert torch.equal(o.isnan().any(-1).cpu(), bad) and torch.equal(lse.isnan().cpu(), bad)
     q[1, 2, 3] = 0.0
     k[int(idx[100]), 1, 0] = float("nan")
     o, lse, _ = _run(args)
     bad[:] = False
-    bad[:3, 4:] = True
+    bad[:members, 4:8] = True
     assert torch.equal(o.isnan().all(-1).cpu(), bad) and torch.equal(lse.isnan().cpu(), bad)
 
 
