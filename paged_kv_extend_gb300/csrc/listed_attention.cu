@@ -615,6 +615,7 @@ struct SharedParams {
   // [batch + 1] first own key; first piece; keys that sequence alias_of lists
   int32_t *own_begin, *own_first, *alias_len, *alias_of;
   int key_elements;  // of a key's K and V rows, all KV heads
+  int row_elements;  // of a token's outputs: hq * d
   int32_t *grp;     // [kGroupArrays][num_groups + 1]
   int in_smem;      // those arrays in dynamic shared memory instead
   WorkUnit *units;
@@ -661,9 +662,11 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 // sequences) keys, nothing if that is less than a tile of keys or if it has one
 // sequence.  A prefix is cut into equal pieces of at most C tiles.  The units
 // are few and long, so C is the one of up to 64 candidates (the longest prefix
-// in 1, 2, ... pieces) whose rounds over the SMs take least, a unit counting
-// C + kUnitTiles tiles (its query load, pipeline fill and partials).  Own keys
-// are cut for a given number of units.
+// in 1, 2, ... pieces) that takes least: its rounds over the SMs, a unit counting
+// C + kUnitTiles tiles (its query load, pipeline fill and partials), and for
+// each piece a partial of every row that goes out and comes back (256 sequences
+// and 32768 shared keys in 4 pieces instead of 9: combine 15 -> 11.5 us, the tile
+// kernel 112 -> 116.5, half the partials' traffic).  Own keys are cut for a given number of units.
 //
 // The whole call waits for this one CTA, so it is a chain of few barriers with
 // no 64-bit division (a candidate in 64 bits took 2400 clocks); what a group
@@ -682,6 +685,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   __shared__ uint2 s_best[32];
   __shared__ int s_longest;
   __shared__ unsigned long long s_saved;  // keys, over the sequences
+  __shared__ uint32_t s_members;          // sequences in groups that share
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.batch, NG = p.num_groups, B1 = B + 1, G1 = NG + 1;
   int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + kSeqArrays * B1 : p.grp;
@@ -694,6 +698,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   if (tid == 0) {
     s_longest = 0;
     s_saved = 0;
+    s_members = 0;
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -749,6 +754,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       if (S > 0) {
         atomicMax(&s_longest, tiles(S));
         atomicAdd(&s_saved, (unsigned long long)(hi - lo - 1) * S);
+        atomicAdd(&s_members, (uint32_t)(hi - lo));
       }
     }
   }
@@ -785,7 +791,9 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     // at most four units an SM and one more a block
     const float each = (float)all.x * (float)p.hkv / (4.0f * p.sms) * 1.000001f;
     const int least = max((int)ceilf(min(each, 1e9f)), kMinSplitTiles);
-    uint2 best = make_uint2(0xFFFFFFFFu, 0u);  // (tiles of all rounds, C)
+    // a piece's partials, in 1/64 of the 1.7 us that a tile takes (4 TB/s)
+    const uint32_t piece_cost = mul_held(s_members, p.row_elements) / 13000u;
+    uint2 best = make_uint2(0xFFFFFFFFu, 0u);  // (1/64 tiles, C)
     for (int j = warp + 1; j <= 64; j += 32) {
       const uint32_t c = max((s_longest + j - 1) / j, least);
       uint32_t n = 0;
@@ -793,7 +801,8 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
         n = add_held(n, mul_held(gK[g], ((uint32_t)tiles(gS[g]) + c - 1) / c));
       n = __reduce_add_sync(0xffffffffu, min(n, kMany / 32));
       const uint32_t rounds = (mul_held(n, p.hkv) + p.sms - 1) / (uint32_t)p.sms;
-      const uint32_t t = mul_held(rounds, c + kUnitTiles);
+      const uint32_t t = add_held(mul_held(rounds, 64 * (c + kUnitTiles)),
+                                  mul_held((s_longest + c - 1) / c, piece_cost));
       if (t < best.x) best = make_uint2(t, c);
     }
     if (lane == 0) s_best[warp] = best;
@@ -1350,6 +1359,7 @@ int launch_decode_shared(const ListedArgs &a) {
   p.alias_len = p.own_first + (a.batch + 1);
   p.alias_of = p.alias_len + (a.batch + 1);
   p.key_elements = 2 * a.d * a.hkv;
+  p.row_elements = a.d * a.hq;
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
   size_t smem = sizeof(int32_t) * (kSeqArrays * (size_t)(a.batch + 1) +
                                    kGroupArrays * (size_t)(a.num_groups + 1));

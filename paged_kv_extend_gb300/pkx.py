@@ -1068,8 +1068,14 @@ def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_w
     q_at, k_at = _rows_at(q, q_shape, index, "q"), _rows_at(k, k_shape, index, "k")
     if q_out is None:
         q_out = torch.empty(q_shape, dtype=_BF16, device=q.device)
+        qo = q_out.data_ptr(), hq * d, d
+    else:
+        qo = _rows_at(q_out, q_shape, index, "q_out")
     if k_out is None:
-        k_out = torch.empty(k_shape, dtype=_BF16, device=k.device)
+        k_out = torch.empty(k_shape, dtype=_BF16, device=q.device)
+        ko = k_out.data_ptr(), hkv * d, d
+    else:
+        ko = _rows_at(k_out, k_shape, index, "k_out")
     pos_at = axis_at = table_at = None
     axes, rotary, rows = 1, 0, 0
     if cos_sin is not None:
@@ -1107,8 +1113,7 @@ def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_w
         raise ValueError("the KV write needs cache_loc")
     _call(index, lib.pkx_qk_norm_rope, *q_at, *k_at, *v_at, n, hq, hkv, d, pos_at, axes, axis_at,
           table_at, rows, rotary, 1 if interleaved else 0, qw_at, kw_at, eps, weight_offset,
-          *_rows_at(q_out, q_shape, index, "q_out"), *_rows_at(k_out, k_shape, index, "k_out"),
-          loc_at, *kb, *vb, slots, fmt, k_scale, v_scale)
+          *qo, *ko, loc_at, *kb, *vb, slots, fmt, k_scale, v_scale)
     return q_out, k_out
 
 
