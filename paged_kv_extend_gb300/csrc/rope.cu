@@ -16,13 +16,15 @@
 // in the smallest power of two of lanes that holds it 8 elements a lane, so a
 // warp holds two rows of 128 dims.  Of half-split pairs a lane takes four pairs,
 // as two runs of four elements (8 bytes) half the rotated dims apart, so that a
-// pair never crosses lanes; only the sum of squares goes through shuffles.  (One
-// run of eight elements a lane, with the partners' elements shuffled and eight
-// cosines and sines held, took 171 us on 16384 tokens of 32 + 8 + 8 heads of
-// 128.)  A warp belongs to one token and walks its rows, kRows steps loaded
-// before the first is used: the lane's cosines and sines are fetched once for all
-// heads.  A token's rows are shared by as many warps as fill the GPU (a
-// decode step has few tokens), by one warp when there are many tokens.
+// pair never crosses lanes; only the sum of squares goes through shuffles.  A
+// warp belongs to one token and walks its rows, kRows steps at a time and the
+// next ones on their way: the cosines and sines, with the weights multiplied
+// in, are made once for all heads.  A token's rows are shared by as many warps as
+// fill the GPU (a decode step has few tokens), by one warp when there are many.
+// Measured on 16384 tokens of 32 + 8 + 8 heads of 128 (436 MB): 171 us with one
+// run of eight elements a lane and the partners shuffled, 107 without the
+// shuffles, 85 with the weights folded in, 78.5 with the next rows loaded early
+// (5.6 TB/s, 0.82 of the copy bandwidth; 45 % of the issue slots).
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
@@ -134,17 +136,22 @@ __global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const Rop
     const int k_part = (part + p.parts - p.q_steps % p.parts) % p.parts;
     const int v_part = (k_part + p.parts - p.k_steps % p.parts) % p.parts;
     const int stride = p.parts * ROWS;  // rows between a warp's steps
-    uint4 val[kRows];
-    auto load = [&](const uint16_t *x, int64_t hs, int heads, int h0) {
+    uint4 val[kRows], next[kRows];
+    auto load = [&](uint4 (&to)[kRows], const uint16_t *x, int64_t hs, int heads, int h0) {
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const int h = h0 + u * stride + sub;
-        val[u] = make_uint4(0, 0, 0, 0);
-        if (in_row && h < heads) val[u] = load_row<LEAVED>(x + h * hs, second);
+        to[u] = make_uint4(0, 0, 0, 0);
+        if (in_row && h < heads) to[u] = load_row<LEAVED>(x + h * hs, second);
       }
     };
-    const uint16_t *qp = a.q + tok * a.q_ts + at;
-    load(qp, a.q_hs, a.hq, part * ROWS);
+    auto advance = [&] {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) val[u] = next[u];
+    };
+    const uint16_t *qp = a.q + tok * a.q_ts + at, *kp = a.k + tok * a.k_ts + at;
+    const uint16_t *vp = a.v + tok * a.v_ts + at;
+    load(val, qp, a.q_hs, a.hq, part * ROWS);
     int64_t slot = -1;
     if (a.cache_loc) {
       slot = __ldg(a.cache_loc + tok);
@@ -217,8 +224,11 @@ __global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const Rop
       const bool norm = a.q_weight != nullptr;
       const Turn T = make_turn<LEAVED>(wq, norm, a.weight_offset, turned, cs, sn);
       uint16_t *out = a.q_out + tok * a.qo_ts + at;
-      for (int h0 = part * ROWS; h0 < a.hq; h0 += kRows * stride) {
-        if (h0 != part * ROWS) load(qp, a.q_hs, a.hq, h0);
+      for (int h0 = part * ROWS;; h0 += kRows * stride) {
+        // the rows after these: of q, or the first of k
+        const int h1 = h0 + kRows * stride;
+        if (h1 < a.hq) load(next, qp, a.q_hs, a.hq, h1);
+        else load(next, kp, a.k_hs, a.hkv, k_part * ROWS);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           if (h0 + u * stride >= a.hq) break;  // (the same for the whole warp)
@@ -226,15 +236,18 @@ __global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const Rop
           const uint4 r = turn_row(val[u], norm, T);
           if (in_row && h < a.hq) store_row<LEAVED>(out + h * a.qo_hs, second, r);
         }
+        advance();
+        if (h1 >= a.hq) break;
       }
     }
     {
       const bool norm = a.k_weight != nullptr;
       const Turn T = make_turn<LEAVED>(wk, norm, a.weight_offset, turned, cs, sn);
-      const uint16_t *kp = a.k + tok * a.k_ts + at;
       uint16_t *out = a.k_out + tok * a.ko_ts + at;
-      for (int h0 = k_part * ROWS; h0 < a.hkv; h0 += kRows * stride) {
-        load(kp, a.k_hs, a.hkv, h0);
+      for (int h0 = k_part * ROWS;; h0 += kRows * stride) {
+        const int h1 = h0 + kRows * stride;
+        if (h1 < a.hkv) load(next, kp, a.k_hs, a.hkv, h1);
+        else if (a.v && slot >= 0) load(next, vp, a.v_hs, a.hkv, v_part * ROWS);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           if (h0 + u * stride >= a.hkv) break;
@@ -244,12 +257,13 @@ __global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const Rop
           store_row<LEAVED>(out + h * a.ko_hs, second, r);
           if (slot >= 0) store_pool(a.k_buffer, slot * a.kb_ss + h * a.kb_hs, r, a.k_scale);
         }
+        advance();
+        if (h1 >= a.hkv) break;
       }
     }
     if (a.v && slot >= 0) {
-      const uint16_t *vp = a.v + tok * a.v_ts + at;
       for (int h0 = v_part * ROWS; h0 < a.hkv; h0 += kRows * stride) {
-        load(vp, a.v_hs, a.hkv, h0);
+        if (h0 != v_part * ROWS) load(val, vp, a.v_hs, a.hkv, h0);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           const int h = h0 + u * stride + sub;
