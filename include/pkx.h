@@ -731,7 +731,7 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
  *              256-byte aligned; pkx_workspace_status reports a candidate page
  *              outside [0, num_pages) (it ranks last) and an indptr that
  *              decreases or passes n_indices (that sequence selects nothing)
- * first_pages + last_pages <= top_k <= 4096.
+ * first_pages + last_pages <= top_k <= 4096, n_indices <= 2^30.
  */
 size_t pkx_select_pages_workspace_size(int batch, int hkv, int64_t n_indices);
 int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
@@ -771,10 +771,12 @@ int pkx_decode_attention_fwd_pages(
  * Decode attention for sequences in groups that share a prefix:
  * pkx_decode_attention_fwd (without a window) for batches in which the
  * sequences group_indptr[g] .. group_indptr[g+1] - 1 have their first
- * shared_lens[g] keys in common.  Those are read once a group, through the
- * group's first sequence's kv_indices; the other sequences' entries there are
- * not read.  A group shares at most its shortest sequence's keys.  Sequences
- * before group_indptr[0] or from group_indptr[num_groups] on stand alone.
+ * shared_lens[g] keys in common.  Those are listed by the group's first
+ * sequence's kv_indices (the other sequences' entries there are not read) and
+ * are read once for up to 256 / (hq / hkv) sequences, or, where that would
+ * save too little, by each.  A group shares at most its shortest sequence's
+ * keys.  Sequences before group_indptr[0] or from group_indptr[num_groups] on
+ * stand alone.
  * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools.
  *   group_indptr  int32 [num_groups + 1], non-decreasing within [0, batch]
  *   shared_lens   int32 [num_groups], >= 0

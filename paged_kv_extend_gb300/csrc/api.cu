@@ -1027,8 +1027,8 @@ int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
     return set_error(PKX_EINVAL, "select_pages: first_pages + last_pages must be in [0, top_k]");
   if (num_pages < 0 || n_indices < 0)
     return set_error(PKX_EINVAL, "select_pages: negative count of pages");
-  if (n_indices >= (1ll << 31))
-    return set_error(PKX_EUNSUPPORTED, "select_pages: 2^31 or more pages in one call");
+  if (n_indices > (1ll << 30))
+    return set_error(PKX_EUNSUPPORTED, "select_pages: more than 2^30 pages in one call");
   if (batch == 0) return PKX_OK;
   if ((rc = check_rows("q", q, 8, 8))) return rc;
   if (num_pages > 0 && (!bounds || !aligned(bounds, 16)))

@@ -658,9 +658,11 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 }
 
 // One CTA of 1024 threads: the units of every group's prefix and the pieces of
-// every sequence's own keys.  A group shares min(shared_lens, the shortest of its
-// sequences) keys, nothing if that is less than a tile of keys or if it has one
-// sequence.  A prefix is cut into equal pieces of at most C tiles.  The units
+// every sequence's own keys.  A group has min(shared_lens, the shortest of its
+// sequences) keys in common, which its first sequence lists for all.  They are
+// shared unless each sequence reads them as own keys: less than a tile of them, a
+// group of one, or (kShareElements) too little to save.  A prefix is cut into equal
+// pieces of at most C tiles.  The units
 // are few and long, so C is the one of up to 64 candidates (the longest prefix
 // in 1, 2, ... pieces) that takes least: its rounds over the SMs, a unit counting
 // C + kUnitTiles tiles (its query load, pipeline fill and partials), and for
@@ -738,10 +740,11 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       int least = gS[g];
       for (int b = lo + lane; b < hi; b += 32) least = min(least, sT[b]);
       least = __reduce_min_sync(0xffffffffu, least);
-      if (hi - lo >= 2 && least >= kBlockN) S = least;
+      if (hi - lo < 2) least = 0;
+      if (least >= kBlockN || !p.rows) S = least;
       for (int b = lo + lane; b < hi; b += 32) {
         sS[b] = S;
-        p.alias_len[b] = S;
+        p.alias_len[b] = least;
         p.alias_of[b] = lo;
       }
     }

@@ -470,17 +470,21 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
   if (lost) atomicCAS(&p.hdr->status, 0, PKX_EDEVICE);
 }
 
-// Scores and selection in one: a CTA for each (sequence, KV head), whose eight
-// warps take eight copies of bounds at a time and leave the keys in shared memory
-// (in the workspace past kFusedKeys pages).  The queries are summed once a CTA
-// and the keys make no round trip; it needs CTAs enough to fill the GPU.
-constexpr int kFusedThreads = 256, kFusedKeys = 4096;
+// Scores and selection in one: a CTA for each (sequence, KV head), whose warps
+// take eight copies of bounds at a time and leave the keys in shared memory (in
+// the workspace past kFusedKeys pages).  The queries are summed once a CTA and the
+// keys make no round trip; it needs CTAs enough to fill the GPU.  A warp keeps the
+// next eight copies on their way (cp.async, each lane its own 16 bytes).  64
+// sequences of 512 pages, 8 KV heads of 128 (134 MB): 45 us by two kernels, 31 in
+// one with eight loads at a time.
+constexpr int kFusedThreads = 128, kFusedKeys = 2048;
 template <int D>
-__global__ void __launch_bounds__(kFusedThreads, 4) page_score_select_kernel(const ScoreParams p,
+__global__ void __launch_bounds__(kFusedThreads, 5) page_score_select_kernel(const ScoreParams p,
                                                                              const SelectParams sp) {
   constexpr int LP = D / 4, PPW = 32 / LP, CH = D / 8, WARPS = kFusedThreads / 32;
   constexpr int STEP = 8 * PPW;  // pages of a warp's step
   __shared__ uint32_t s_keys[kFusedKeys];
+  __shared__ __align__(16) uint8_t s_box[WARPS][2][8 * 512];
   __shared__ int s_cnt[2][32][3];
   __shared__ int s_scan[2][32];
   grid_dep_wait();
@@ -506,26 +510,36 @@ __global__ void __launch_bounds__(kFusedThreads, 4) page_score_select_kernel(con
       const int page = lane < STEP && i < m ? __ldg(ids + i) : -1;
       return page < p.num_pages ? page : -1;
     };
-    int coming = fetch(warp * STEP);
+    const uint4 *box = p.bounds + (int64_t)h * LP + l;
+    const uint32_t mine = smem_u32(&s_box[warp][0][lane * 16]);
+    auto issue = [&](int stage, int pages) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int page = __shfl_sync(0xffffffffu, pages, u * PPW + sub);
+        if (page >= 0)
+          cp_async_16(mine + stage * 4096 + u * 512, box + (int64_t)page * p.hkv * LP, 16u);
+      }
+      cp_async_commit();
+    };
+    int here = fetch(warp * STEP), next = fetch((warp + WARPS) * STEP);
+    issue(0, here);
     float f[8];
     query_sums<D>(p.q, (int64_t)b * p.hq + (int64_t)h * p.group, p.group, is_hi ? l - CH : l, is_hi,
                   f);
-    const uint4 *box = p.bounds + (int64_t)h * LP + l;
-    for (int i0 = warp * STEP; i0 < m; i0 += WARPS * STEP) {
-      const int mine = coming;
-      uint4 x[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int page = __shfl_sync(0xffffffffu, mine, u * PPW + sub);
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (page >= 0) x[u] = __ldg(box + (int64_t)page * p.hkv * LP);
-      }
-      coming = fetch(i0 + WARPS * STEP);
-      const float score = eight_scores<D>(f, [&](int u) { return x[u]; });
+    int stage = 0;
+    for (int i0 = warp * STEP; i0 < m; i0 += WARPS * STEP, stage ^= 1) {
+      issue(stage ^ 1, next);
+      const int after = fetch(i0 + 2 * WARPS * STEP);
+      cp_async_wait_group<1>();
+      const float score = eight_scores<D>(
+          f, [&](int u) { return ld_shared_u4(mine + stage * 4096 + u * 512); });
       const int j = (lane & 7) * PPW + sub;
-      const int page = __shfl_sync(0xffffffffu, mine, j);
+      const int page = __shfl_sync(0xffffffffu, here, j);
       if (l < 8 && i0 + j < m) keys[i0 + j] = page < 0 ? 0u : score_key(score);
+      here = next;
+      next = after;
     }
+    cp_async_wait_all();
     __syncthreads();
     lost = select_top<kFusedThreads>(sp, n, keys, out, s_cnt, s_scan);
   }

@@ -114,11 +114,11 @@ def test_large_groups_against_64_bits(case):
     R.check_attention(o, lse, _reference(args, **kw), cap)
 
 
-@pytest.mark.parametrize("keys,members", [(200, 2), (3000, 17)])
-def test_the_first_sequence_lists_the_prefix(keys, members):
+@pytest.mark.parametrize("keys,members,hq,hkv", [(200, 2, 32, 8), (3000, 17, 32, 8), (50, 3, 8, 2), (50, 3, 34, 2)])
+def test_the_first_sequence_lists_the_prefix(keys, members, hq, hkv):
     """The others' entries below the shared length are not read, whether the
     prefix is shared or (few members) read by each."""
-    args = _case([(keys, [9, 30] + [1] * (members - 2))], [], [], 32, 8, 128, BF, 2)
+    args = _case([(keys, [9, 30] + [1] * (members - 2))], [], [], hq, hkv, 128, BF, 2)
     q, k, v, indptr, idx, gptr, shared = args
     want = _run(args)[:2]
     idx = idx.clone()
