@@ -604,7 +604,8 @@ struct SharedParams {
   int batch, num_groups, hkv;
   int tok;          // tokens of a query tile
   int sms;
-  int own_run;      // keys that own keys are cut at
+  int own_run;      // keys that own keys are cut at: 1 << own_shift
+  int own_shift;
   int own_least;    // fewest such runs of a unit
   int own_target;   // units of own keys wanted
   int own_gran;     // granules of one
@@ -679,15 +680,15 @@ constexpr int kUnitTiles = 3;
 // sequence, mostly from L2, at 5.8 elements a picosecond from a bf16 pool (64
 // sequences, 8192 shared keys, 8 KV heads: 233 us a call against 70 shared) and
 // 4.0 from an fp8 one (8 groups of 8, 2000 keys, 4 KV heads: 55 against 47).
-constexpr unsigned long long kShareElements = 88ull << 20;
+constexpr float kShareElements = 88 << 20;
 constexpr int kSeqArrays = 3, kGroupArrays = 7;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {
   extern __shared__ int32_t s_dyn[];
   __shared__ Two sh[32];
-  __shared__ uint2 s_best[32];
+  __shared__ float2 s_best[32];
   __shared__ int s_longest;
-  __shared__ unsigned long long s_saved;  // keys, over the sequences
-  __shared__ uint32_t s_members;          // sequences in groups that share
+  __shared__ uint32_t s_saved;    // tiles of keys, over the sequences
+  __shared__ uint32_t s_members;  // sequences in groups that share
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = p.batch, NG = p.num_groups, B1 = B + 1, G1 = NG + 1;
   int32_t *seq = p.in_smem ? s_dyn : p.seq, *grp = p.in_smem ? s_dyn + kSeqArrays * B1 : p.grp;
@@ -756,13 +757,13 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
       gR[g] = nb > 0 ? (nb - 1) * blk + (last <= p.tok ? 2 * last : last) : 0;
       if (S > 0) {
         atomicMax(&s_longest, tiles(S));
-        atomicAdd(&s_saved, (unsigned long long)(hi - lo - 1) * S);
+        atomicAdd(&s_saved, (uint32_t)(hi - lo - 1) * (uint32_t)tiles(S));
         atomicAdd(&s_members, (uint32_t)(hi - lo));
       }
     }
   }
   __syncthreads();
-  if (p.rows && s_saved * p.key_elements < kShareElements) {  // every sequence reads its prefix
+  if (p.rows && (float)s_saved * kBlockN * p.key_elements < kShareElements) {  // every sequence reads its prefix
     __syncthreads();
     for (int b = tid; b < B; b += 1024) sS[b] = 0;
     for (int g = tid; g < NG; g += 1024) gS[g] = gK[g] = gR[g] = 0;
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   // totals: tiles of the prefixes, runs of own keys
   auto runs = [&](int b) {
     const int n = sT[b] - sS[b];
-    return n / p.own_run + (n % p.own_run != 0);
+    return (n >> p.own_shift) + ((n & (p.own_run - 1)) != 0);
   };
   const int bc = (B + 1023) / 1024, b0 = min(B, tid * bc), b1 = min(B, b0 + bc);
   Two sum = {0, 0}, all;
@@ -794,25 +795,29 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     // at most four units an SM and one more a block
     const float each = (float)all.x * (float)p.hkv / (4.0f * p.sms) * 1.000001f;
     const int least = max((int)ceilf(min(each, 1e9f)), kMinSplitTiles);
-    // a piece's partials, in 1/64 of the 1.7 us that a tile takes (4 TB/s)
-    const uint32_t piece_cost = mul_held(s_members, p.row_elements) / 13000u;
-    uint2 best = make_uint2(0xFFFFFFFFu, 0u);  // (1/64 tiles, C)
+    // (estimates, in fp32: any C of at least `least` does; a piece's partials in
+    // the 1.7 us that a tile takes, at 4 TB/s)
+    const float piece_cost = (float)s_members * (float)p.row_elements * (1.0f / 832000.0f);
+    const float per_sm = (float)p.hkv / (float)p.sms;
+    float2 best = make_float2(INFINITY, 0.f);  // (tiles, C)
     for (int j = warp + 1; j <= 64; j += 32) {
-      const uint32_t c = max((s_longest + j - 1) / j, least);
-      uint32_t n = 0;
-      for (int g = lane; g < NG; g += 32)
-        n = add_held(n, mul_held(gK[g], ((uint32_t)tiles(gS[g]) + c - 1) / c));
-      n = __reduce_add_sync(0xffffffffu, min(n, kMany / 32));
-      const uint32_t rounds = (mul_held(n, p.hkv) + p.sms - 1) / (uint32_t)p.sms;
-      const uint32_t t = add_held(mul_held(rounds, 64 * (c + kUnitTiles)),
-                                  mul_held((s_longest + c - 1) / c, piece_cost));
-      if (t < best.x) best = make_uint2(t, c);
+      const float c = fmaxf(ceilf((float)s_longest / (float)j), (float)least), inv = 1.0f / c;
+      float n = 0.f;
+      for (int g = lane; g < NG; g += 32) n += (float)gK[g] * ceilf((float)tiles(gS[g]) * inv);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      const float t = ceilf(n * per_sm) * (c + kUnitTiles) + ceilf((float)s_longest * inv) * piece_cost;
+      if (t < best.x) best = make_float2(t, c);
     }
     if (lane == 0) s_best[warp] = best;
     __syncthreads();
     best = s_best[lane];
-    const uint32_t t = __reduce_min_sync(0xffffffffu, best.x);
-    const int C = (int)__reduce_min_sync(0xffffffffu, best.x == t ? best.y : 0xFFFFFFFFu);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 x = {__shfl_xor_sync(0xffffffffu, best.x, o), __shfl_xor_sync(0xffffffffu, best.y, o)};
+      if (x.x < best.x || (x.x == best.x && x.y < best.y)) best = x;
+    }
+    const int C = max((int)best.y, least);
     // first unit and granule of each group
     const int gc = (NG + 1023) / 1024, g0 = min(NG, tid * gc), g1 = min(NG, g0 + gc);
     auto size = [&](int g) {  // units and granules
@@ -1350,6 +1355,8 @@ int launch_decode_shared(const ListedArgs &a) {
   p.sms = nsm;
   const OwnUnits own = own_units(group, nsm);
   p.own_run = own.run;
+  p.own_shift = own.run == kRowRun ? 6 : 7;
+  static_assert(kRowRun == 64 && kBlockN == 128, "own_shift");
   p.own_least = own.least;
   p.own_target = own.target;
   p.own_gran = own.gran;
