@@ -663,7 +663,8 @@ int pkx_decode_attention_fwd_streaming(
  * Elements from rotary_dim on are not rotated.  Computed in fp32 and rounded
  * once to bf16.  With cache_loc the k_out row is also stored at that slot of
  * k_buffer and v's row at that slot of v_buffer, as pkx_set_kv_buffer (or
- * pkx_set_kv_buffer_fp8 for an fp8 pool) stores rows.
+ * pkx_set_kv_buffer_fp8 for an fp8 pool) stores rows (two tokens with the same
+ * slot leave that slot's rows undefined).
  *   q, k       bf16 [n_tokens, hq / hkv, d], strides (ts, hs)
  *   v          bf16 [n_tokens, hkv, d], or NULL (only keys are written);
  *              needs cache_loc

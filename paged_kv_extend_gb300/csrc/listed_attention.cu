@@ -10,16 +10,18 @@
 //    of the prefix are read once for 256 query rows instead of once for each
 //    sequence, and the tensor core works on full tiles instead of on
 //    Hq / Hkv rows of 128.
-//  * selected pages: each (sequence, KV head) attends to pages of its own; a
-//    first kernel writes its list of pool slots, and the units follow from the
-//    batch alone (equal shares of the longest list), so no scan is needed.
+//  * selected pages: each (sequence, KV head) attends to pages of its own; the
+//    units follow from the batch alone (equal shares of top_k pages), so no scan
+//    is needed.
 //
 // One-token units (own keys, selected pages) of groups of at most 16 query
 // heads run in rows_kernel, a warp a unit: 128 rows of the tensor core would be
 // padding for them, and a unit's way through the pipeline of the tile kernel
 // (claim, query load, two tiles in flight, epilogue) takes 3 us of an SM however
 // short it is (256 sequences of 32 own keys behind a shared prefix: 2048 units,
-// 40 us).  Larger groups and the prefixes run in the tile kernel.
+// 40 us).  Larger groups and the prefixes run in the tile kernel; for selected
+// pages of larger groups a first kernel writes each list of pool slots, where
+// rows_kernel's warps look their pages up themselves.
 //
 // Partials are fp32 (o normalised, lse in natural logs) and merged as
 //   lse = log sum_i exp(lse_i),  o = sum_i exp(lse_i - lse) o_i.
@@ -676,10 +678,10 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 // or a sequence needs later stays in shared memory.
 constexpr int kUnitTiles = 3;
 // Elements of K and V that sharing has to save for the tile kernel to run, whose
-// units take 20 us however short: rows_kernel reads a prefix again for every
-// sequence, mostly from L2, at 5.8 elements a picosecond from a bf16 pool (64
-// sequences, 8192 shared keys, 8 KV heads: 233 us a call against 70 shared) and
-// 4.0 from an fp8 one (8 groups of 8, 2000 keys, 4 KV heads: 55 against 47).
+// units take 20 us however short.  rows_kernel reads a prefix again for every
+// sequence, mostly from L2: 64 sequences, 8192 shared keys, 8 KV heads, bf16 (1057
+// million elements saved): 233 us a call against 70 shared; 8 groups of 8, about
+// 2000 keys, 4 KV heads, fp8 (115 million): 55 against 47.
 constexpr float kShareElements = 88 << 20;
 constexpr int kSeqArrays = 3, kGroupArrays = 7;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {

@@ -17,14 +17,14 @@
 // depend on how the work is split: a lane adds its 8 dims as a tree, and a
 // butterfly over the lanes goes on with it.
 //
-// What bounds it: the bounds are read once, 4 d bytes a page and KV head
-// (1/32 of K and V at pages of 64 bf16 keys); 4 operations an element stay
-// below a third of the issue slots.  The scores go to the workspace as
-// ordered 32-bit keys and a second kernel, one CTA for each (sequence, KV
-// head), finds the threshold of the top k by halving the key range two bits a
-// round with counts over the CTA (a histogram by shared atomics would
-// serialise: the scores share their exponents) and writes the pages in order,
-// so equal scores go to the lower page and no atomic decides.
+// What bounds it: the bounds are read once, 4 d bytes a page and KV head (1/64
+// of K and V at pages of 64 bf16 keys).  The scores are ordered 32-bit keys; the
+// threshold of the top k is found by halving the key range two bits a round with
+// counts over the CTA (a histogram by shared atomics would serialise: the scores
+// share their exponents), and the pages are written in order, so equal scores go
+// to the lower page and no atomic decides.  Where the (sequence, KV head) pairs
+// fill the GPU one kernel does all of it for a pair; a few long sequences are
+// scored by runs of pages first.
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"

@@ -1221,10 +1221,10 @@ def decode_attention_fwd_shared(q, o, k_buffer, v_buffer, kv_indptr, kv_indices,
                                 shared_lens, sm_scale=None, logit_cap=0.0, lse=None,
                                 workspace=None, k_scale=1.0, v_scale=1.0):
     """Decode attention for sequences in groups that share a prefix, whose keys
-    are read once a group (pkx_decode_attention_fwd_shared): the sequences
-    group_indptr[g] .. group_indptr[g + 1] - 1 have their first shared_lens[g]
-    keys in common; both int32.  Other arguments as decode_attention_fwd.
-    Returns the workspace."""
+    are read once for many sequences (pkx_decode_attention_fwd_shared): the
+    sequences group_indptr[g] .. group_indptr[g + 1] - 1 have their first
+    shared_lens[g] keys in common, listed by the first of them; both int32.
+    Other arguments as decode_attention_fwd.  Returns the workspace."""
     lib = _lib or load_library()
     index = _gpu(q, "q")
     dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(

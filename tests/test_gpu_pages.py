@@ -152,6 +152,8 @@ ATTEND = [  # keys of each sequence, page, hq, hkv, d, top, kv, cap
     dict(keys=[5000], page=200, hq=128, hkv=1, d=64, top=25, kv=torch.bfloat16, cap=0.0),
     dict(keys=[4000, 0, 90], page=64, hq=34, hkv=2, d=128, top=60, kv=torch.float8_e4m3fn, cap=0.0),
     dict(keys=[4000, 31], page=16, hq=16, hkv=1, d=128, top=240, kv=torch.bfloat16, cap=2.0),
+    dict(keys=[90, 3, 0, 41], page=16, hq=12, hkv=2, d=128, top=6, kv=torch.float8_e4m3fn, cap=0.0),  # one unit a head
+    dict(keys=[90, 3, 0, 41], page=16, hq=26, hkv=2, d=64, top=5, kv=torch.float8_e5m2, cap=2.0),
     dict(keys=[3000, 9], page=24, hq=9, hkv=1, d=64, top=100, kv=torch.float8_e4m3fn, cap=0.0),
     dict(keys=[40] * 150, page=8, hq=4, hkv=2, d=128, top=3, kv=torch.bfloat16, cap=0.0),
 ]

@@ -129,6 +129,16 @@ def test_the_first_sequence_lists_the_prefix(keys, members, hq, hkv):
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("hq", [1, 17])
+def test_many_sequences_and_groups(hq):
+    """5000 sequences in 1500 groups: more than the scheduler's threads, and
+    than its shared memory holds."""
+    args = _case([(130 + i % 3, [i % 5, 2, 0]) for i in range(1500)], [i % 7 for i in range(500)], [], hq, 1, 64, BF, 3)
+    o, lse, ws = _run(args)
+    assert pkx.workspace_status(ws) == pkx.PKX_OK
+    R.check_attention(o, lse, _reference(args))
+
+
 def test_shared_lengths_past_a_sequence():
     """A group shares at most its shortest sequence's keys."""
     q, k, v, indptr, idx, gptr, _ = args = _case([(300, [9, 0, 100])], [20], [], 8, 2, 64, BF, 4)
