@@ -779,6 +779,8 @@ int pkx_decode_attention_fwd_pages(
  * keys.  Sequences before group_indptr[0] or from group_indptr[num_groups] on
  * stand alone.
  * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools.
+ *   n_indices     entries of kv_indices (an indptr that passes it, or
+ *                 decreases, is reported and that sequence has no keys)
  *   group_indptr  int32 [num_groups + 1], non-decreasing within [0, batch]
  *   shared_lens   int32 [num_groups], >= 0
  *                 (both NULL when num_groups is 0; if either is out of range,
@@ -790,8 +792,8 @@ size_t pkx_decode_shared_workspace_size(int batch, int num_groups, int hq, int h
                                         int lv);
 int pkx_decode_attention_fwd_shared(
     const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
-    const int32_t *kv_indices, const int32_t *group_indptr, const int32_t *shared_lens,
-    int num_groups, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
+    const int32_t *kv_indices, int64_t n_indices, const int32_t *group_indptr,
+    const int32_t *shared_lens, int num_groups, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
     int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
     float k_scale, float v_scale, float *lse_out, void *workspace, size_t workspace_bytes,
     void *stream);

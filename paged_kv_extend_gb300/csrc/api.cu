@@ -1108,20 +1108,22 @@ size_t pkx_decode_shared_workspace_size(int batch, int num_groups, int hq, int h
 
 int pkx_decode_attention_fwd_shared(
     const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
-    const int32_t *kv_indices, const int32_t *group_indptr, const int32_t *shared_lens,
-    int num_groups, int batch, int hq, int hkv, int lq, int lv, int64_t kb_ss, int64_t kb_sh,
-    int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
+    const int32_t *kv_indices, int64_t n_indices, const int32_t *group_indptr,
+    const int32_t *shared_lens, int num_groups, int batch, int hq, int hkv, int lq, int lv,
+    int64_t kb_ss, int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
     float k_scale, float v_scale, float *lse_out, void *workspace, size_t workspace_bytes,
     void *stream) {
   int rc;
   if ((rc = check_equal_heads("decode with shared prefixes", hq, hkv, lq, lv))) return rc;
-  if (num_groups < 0) return set_error(PKX_EINVAL, "negative num_groups");
+  if (num_groups < 0 || n_indices < 0)
+    return set_error(PKX_EINVAL, "negative num_groups or n_indices");
   AttnArgs a{};
   bool done;
   rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,
                    kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, -1, kv_dtype,
                    k_scale, v_scale, lse_out, &done);
   if (rc != PKX_OK || done) return rc;
+  if (n_indices > 0 && !kv_indices) return set_error(PKX_EINVAL, "kv_indices is null");
   if (num_groups > 0 && (!group_indptr || !shared_lens || !aligned(group_indptr, 4) ||
                          !aligned(shared_lens, 4)))
     return set_error(PKX_EINVAL, "group_indptr or shared_lens null or misaligned");
@@ -1130,6 +1132,7 @@ int pkx_decode_attention_fwd_shared(
   l.group_indptr = group_indptr;
   l.shared_lens = shared_lens;
   l.num_groups = num_groups;
+  l.n_indices = n_indices;
   return launch_decode_shared(l);
 }
 

@@ -612,6 +612,8 @@ struct SharedParams {
   int own_target;   // units of own keys wanted
   int own_gran;     // granules of one
   int rows;         // own keys go to rows_kernel
+  int tile_kernel;  // the tile kernel runs
+  int64_t n_indices;
   int unit_max;
   int64_t gran_max;
   int32_t *seq;     // [kSeqArrays][batch + 1]
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
   }
   for (int b = tid; b < B; b += 1024) {
     const int k0 = p.kv_indptr[b], T = p.kv_indptr[b + 1] - k0;
-    const bool ok = k0 >= 0 && T >= 0;
+    const bool ok = k0 >= 0 && T >= 0 && (int64_t)k0 + T <= p.n_indices;
     bad |= !ok;
     sT[b] = ok ? T : 0;
     sS[b] = 0;
@@ -765,7 +767,8 @@ __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParam
     }
   }
   __syncthreads();
-  if (p.rows && (float)s_saved * kBlockN * p.key_elements < kShareElements) {  // every sequence reads its prefix
+  if (p.rows &&
+      (!p.tile_kernel || (float)s_saved * kBlockN * p.key_elements < kShareElements)) {  // every sequence reads its prefix
     __syncthreads();
     for (int b = tid; b < B; b += 1024) sS[b] = 0;
     for (int g = tid; g < NG; g += 1024) gS[g] = gK[g] = gR[g] = 0;
@@ -1343,8 +1346,6 @@ int launch_decode_shared(const ListedArgs &a) {
   if (rc != PKX_OK) return rc;
   if (L.unit_max >= INT_MAX / 4 || L.gran_max >= INT_MAX)
     return set_error(PKX_EUNSUPPORTED, "decode_shared: batch too large");
-  ListedMaps tm;
-  if ((rc = make_maps(tm, a)) != PKX_OK) return rc;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   SharedParams p;
   p.kv_indptr = a.kv_indptr;
@@ -1363,6 +1364,11 @@ int launch_decode_shared(const ListedArgs &a) {
   p.own_target = own.target;
   p.own_gran = own.gran;
   p.rows = group <= kRowsGroup;
+  // (the lists hold every prefix once a sequence: no more than all of them can be
+  // saved)
+  p.tile_kernel = !p.rows || (a.num_groups > 0 && (float)a.n_indices * 2 * a.d * a.hkv >=
+                                                      kShareElements);
+  p.n_indices = a.n_indices;
   p.unit_max = L.unit_max;
   p.gran_max = L.gran_max;
   p.seq = reinterpret_cast<int32_t *>(ws + L.seq_off);
@@ -1373,6 +1379,8 @@ int launch_decode_shared(const ListedArgs &a) {
   p.key_elements = 2 * a.d * a.hkv;
   p.row_elements = a.d * a.hq;
   p.grp = reinterpret_cast<int32_t *>(ws + L.grp_off);
+  ListedMaps tm;
+  if (p.tile_kernel && (rc = make_maps(tm, a)) != PKX_OK) return rc;
   size_t smem = sizeof(int32_t) * (kSeqArrays * (size_t)(a.batch + 1) +
                                    kGroupArrays * (size_t)(a.num_groups + 1));
   p.in_smem = smem <= 40 * 1024;
@@ -1383,8 +1391,7 @@ int launch_decode_shared(const ListedArgs &a) {
   cudaError_t e = launch_pdl(shared_sched_kernel, dim3(1), dim3(1024), smem, a.stream, p);
   if (e != cudaSuccess)
     return set_error(PKX_ECUDA, "shared_sched launch: %s", cudaGetErrorString(e));
-  return run_listed(a, a.num_groups > 0 || !p.rows ? &tm : nullptr, L, nsm, a.kv_indptr,
-                    a.kv_indices, 0,
+  return run_listed(a, p.tile_kernel ? &tm : nullptr, L, nsm, a.kv_indptr, a.kv_indices, 0,
                     OwnPartials{p.rows_out, own.gran, own.gran * a.hkv, 0, nullptr, 0});
 }
 

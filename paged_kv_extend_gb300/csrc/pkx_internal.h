@@ -320,7 +320,8 @@ struct ListedArgs {
   // selected pages
   const int32_t *last_page_len = nullptr, *selected = nullptr;
   int page_size = 0, top_k = 0;
-  int64_t n_indices = 0;  // entries of kv_indices
+  // entries of kv_indices
+  int64_t n_indices = 0;
   void *workspace;
   size_t workspace_bytes;
   cudaStream_t stream;

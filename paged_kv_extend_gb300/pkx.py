@@ -120,7 +120,7 @@ _SIGS = {
         _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _f, _f, _p, _p, _sz, _p]),
     "pkx_decode_shared_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "pkx_decode_attention_fwd_shared": (_i, [
-        _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i,
+        _p, _p, _p, _p, _p, _p, _i64, _p, _p, _i, _i, _i, _i, _i, _i,
         _i64, _i64, _i64, _i64, _i64, _f, _f, _i, _f, _f, _p, _p, _sz, _p]),
 }
 
@@ -1229,11 +1229,11 @@ def decode_attention_fwd_shared(q, o, k_buffer, v_buffer, kv_indptr, kv_indices,
     index = _gpu(q, "q")
     dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
         q, o, lse, k_buffer, v_buffer, kv_indptr, index)
-    b, groups = dims[0], shared_lens.numel()
+    b, groups, n = dims[0], shared_lens.numel(), kv_indices.numel()
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_shared_workspace_size, b, b,
                                         groups, *dims[1:])
     _call(index, lib.pkx_decode_attention_fwd_shared, q_at, o_at, kb[0], vb[0], ptr_at,
-          _flat_at(kv_indices, _I32, kv_indices.numel(), index, "kv_indices"),
+          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n,
           _flat_at(group_indptr, _I32, groups + 1, index, "group_indptr"),
           _flat_at(shared_lens, _I32, groups, index, "shared_lens"), groups, *dims, kb[1], kb[2],
           vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale, v_scale, lse_at,

@@ -168,6 +168,13 @@ def test_bad_groups_share_nothing_and_are_reported():
     o, lse, ws = _run(args, ws=ws)
     assert pkx.workspace_status(ws) == pkx.PKX_OK
     R.check_attention(o, lse, ref)
+    # an indptr that decreases, or that passes the list: no keys, reported
+    for at, value in ((2, int(indptr[1]) - 1), (4, int(indptr[4]) + 1), (1, -5)):
+        broken = indptr.clone()
+        broken[at] = value
+        o, lse, ws = _run((q, k, v, broken, idx, gptr, shared), ws=ws)
+        assert pkx.workspace_status(ws) == pkx.PKX_EDEVICE
+        assert not o[at - 1].any() and (lse[at - 1] == float("-inf")).all() and o.isfinite().all()
     idx = idx.clone()
     idx[5] = k.shape[0]
     o, lse, ws = _run((q, k, v, indptr, idx, gptr, shared), ws=ws)

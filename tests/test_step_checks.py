@@ -146,11 +146,11 @@ def _pages(lib, **over):
 
 
 def _shared(lib, **over):
-    a = dict(q=P, o=P, k=P, v=P, ptr=P, idx=P, gptr=P, lens=P, groups=1, batch=2, hq=8, hkv=2, lq=128, lv=128,
+    a = dict(q=P, o=P, k=P, v=P, ptr=P, idx=P, n=640, gptr=P, lens=P, groups=1, batch=2, hq=8, hkv=2, lq=128, lv=128,
              st=(256, 128, 256, 128), slots=640, scale=0.0, cap=0.0, fmt=0, s=1.0, t=1.0, lse=None, ws=P, wsb=1 << 40)
     a.update(over)
     return lib.pkx_decode_attention_fwd_shared(
-        a["q"], a["o"], a["k"], a["v"], a["ptr"], a["idx"], a["gptr"], a["lens"], a["groups"], a["batch"], a["hq"],
+        a["q"], a["o"], a["k"], a["v"], a["ptr"], a["idx"], a["n"], a["gptr"], a["lens"], a["groups"], a["batch"], a["hq"],
         a["hkv"], a["lq"], a["lv"], *a["st"], a["slots"], a["scale"], a["cap"], a["fmt"], a["s"], a["t"], a["lse"],
         a["ws"], a["wsb"], None)
 
@@ -175,7 +175,7 @@ def test_pages_refuse(lib, over, code):
 
 
 @pytest.mark.parametrize("over,code", BOTH + [
-    (dict(groups=-1), INVALID), (dict(gptr=None), INVALID), (dict(lens=P + 2), INVALID),
+    (dict(groups=-1), INVALID), (dict(n=-1), INVALID), (dict(idx=None), INVALID), (dict(gptr=None), INVALID), (dict(lens=P + 2), INVALID),
 ], ids=str)
 def test_shared_refuse(lib, over, code):
     assert _shared(lib, **over) == code and lib.pkx_last_error_string()
