@@ -477,14 +477,15 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
 // next eight copies on their way (cp.async, each lane its own 16 bytes).  64
 // sequences of 512 pages, 8 KV heads of 128 (134 MB): 45 us by two kernels, 31 in
 // one with eight loads at a time.
-constexpr int kFusedThreads = 128, kFusedKeys = 2048;
-template <int D>
-__global__ void __launch_bounds__(kFusedThreads, 5) page_score_select_kernel(const ScoreParams p,
-                                                                             const SelectParams sp) {
-  constexpr int LP = D / 4, PPW = 32 / LP, CH = D / 8, WARPS = kFusedThreads / 32;
+constexpr int kFusedKeys = 2048;
+constexpr int kFusedRing = 2 * 8 * 512;  // bytes of a warp
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, 640 / THREADS) page_score_select_kernel(
+    const ScoreParams p, const SelectParams sp) {
+  constexpr int LP = D / 4, PPW = 32 / LP, CH = D / 8, WARPS = THREADS / 32;
   constexpr int STEP = 8 * PPW;  // pages of a warp's step
   __shared__ uint32_t s_keys[kFusedKeys];
-  __shared__ __align__(16) uint8_t s_box[WARPS][2][8 * 512];
+  extern __shared__ __align__(16) uint8_t smem[];  // [WARPS][2][8 copies]
   __shared__ int s_cnt[2][32][3];
   __shared__ int s_scan[2][32];
   grid_dep_wait();
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kFusedThreads, 5) page_score_select_kernel(con
   bool lost = bad;
   const int n = bad ? 0 : (int)n64;
   if (n <= p.top_k) {  // every page
-    for (int i = threadIdx.x; i < p.top_k; i += kFusedThreads) out[i] = i < n ? i : -1;
+    for (int i = threadIdx.x; i < p.top_k; i += THREADS) out[i] = i < n ? i : -1;
   } else {
     const int sub = lane / LP, l = lane - sub * LP;
     const bool is_hi = l >= CH;
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kFusedThreads, 5) page_score_select_kernel(con
       return page < p.num_pages ? page : -1;
     };
     const uint4 *box = p.bounds + (int64_t)h * LP + l;
-    const uint32_t mine = smem_u32(&s_box[warp][0][lane * 16]);
+    const uint32_t mine = smem_u32(smem) + warp * kFusedRing + lane * 16;
     auto issue = [&](int stage, int pages) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kFusedThreads, 5) page_score_select_kernel(con
     }
     cp_async_wait_all();
     __syncthreads();
-    lost = select_top<kFusedThreads>(sp, n, keys, out, s_cnt, s_scan);
+    lost = select_top<THREADS>(sp, n, keys, out, s_cnt, s_scan);
   }
   lost = __syncthreads_or(lost);
   if (threadIdx.x == 0) {
@@ -556,6 +557,25 @@ static size_t select_keys_offset(int batch, int hkv) {
 size_t select_pages_workspace(int batch, int hkv, int64_t n_indices) {
   return select_keys_offset(batch, hkv) +
          ((sizeof(uint32_t) * (size_t)hkv * (size_t)n_indices + 255) & ~(size_t)255);
+}
+
+template <int D, int THREADS>
+static int launch_score_select(const ScoreParams &p, const SelectParams &s, dim3 pairs,
+                               cudaStream_t st) {
+  constexpr int smem = THREADS / 32 * kFusedRing;
+  static PerDevice configured;
+  std::atomic<int> *done = configured.here();
+  cudaError_t e = cudaSuccess;
+  if (!done || done->load(std::memory_order_acquire) == 0) {
+    e = cudaFuncSetAttribute(page_score_select_kernel<D, THREADS>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && done) done->store(1, std::memory_order_release);
+  }
+  if (e == cudaSuccess)
+    e = launch_pdl(page_score_select_kernel<D, THREADS>, pairs, dim3(THREADS), smem, st, p, s);
+  if (e != cudaSuccess)
+    return set_error(PKX_ECUDA, "page_score_select launch: %s", cudaGetErrorString(e));
+  return PKX_OK;
 }
 
 int launch_select_pages(const SelectArgs &a) {
@@ -594,17 +614,19 @@ int launch_select_pages(const SelectArgs &a) {
   if ((int64_t)a.batch * a.hkv >= (1ll << 31))
     return set_error(PKX_EUNSUPPORTED, "select_pages: batch too large");
   const dim3 pairs((unsigned)(a.batch * a.hkv));
-  // One kernel where the (sequence, KV head) pairs fill the GPU, or where there is
-  // too little to spread: 5 sequences of up to 49 pages, 3 KV heads, 11 us for
-  // the two kernels.  Else scores by runs of pages, then the selection.
+  // One kernel where the (sequence, KV head) pairs fill the GPU (64 sequences of
+  // 512 pages, 8 KV heads: 31 us against 43 by two kernels) or where there is
+  // too little to spread (5 sequences of up to 49 pages, 3 KV heads: 8 against
+  // 10).  Else scores by runs of pages, then the selection.
   const int64_t mean = a.n_indices / a.batch;
   if ((int64_t)a.batch * a.hkv >= nsm || mean <= 256) {
-    cudaError_t e = launch_pdl(
-        a.d == 128 ? page_score_select_kernel<128> : page_score_select_kernel<64>, pairs,
-        dim3(kFusedThreads), 0, a.stream, p, s);
-    if (e != cudaSuccess)
-      return set_error(PKX_ECUDA, "page_score_select launch: %s", cudaGetErrorString(e));
-    return PKX_OK;
+    // eight warps a pair while three such CTAs an SM hold all pairs, else four
+    // (24 sequences of 512 pages, 8 KV heads: 23 us and 27; 64: 41.5 by four)
+    if (pairs.x <= 3u * nsm)
+      return a.d == 128 ? launch_score_select<128, 256>(p, s, pairs, a.stream)
+                        : launch_score_select<64, 256>(p, s, pairs, a.stream);
+    return a.d == 128 ? launch_score_select<128, 128>(p, s, pairs, a.stream)
+                      : launch_score_select<64, 128>(p, s, pairs, a.stream);
   }
   // a warp's run: 32 entries, or fewer where that leaves less than 16 warps an
   // SM (a run reads the group's query rows once)
