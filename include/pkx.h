@@ -748,7 +748,8 @@ int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
  * the last one (the paged format of pkx_expand_paged_kv_indices).  Entries
  * below 0 are ignored; entries may come in any order, one listed twice counts
  * twice.  A row without keys gets o = 0 and lse = -inf.  For (lq, lv) =
- * (64, 64) and (128, 128), bf16 and fp8 pools.
+ * (64, 64) and (128, 128), bf16 and fp8 pools (whose strides are multiples of
+ * 16 bytes).
  *   n_indices  entries of kv_indices
  *   selected   int32 [batch, hkv, top_k], top_k <= 4096
  *   workspace  >= pkx_decode_pages_workspace_size(...) bytes, 256-byte aligned
@@ -778,7 +779,8 @@ int pkx_decode_attention_fwd_pages(
  * save too little, by each.  A group shares at most its shortest sequence's
  * keys.  Sequences before group_indptr[0] or from group_indptr[num_groups] on
  * stand alone.
- * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools.
+ * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools (whose strides are
+ * multiples of 16 bytes).
  *   n_indices     entries of kv_indices (an indptr that passes it, or
  *                 decreases, is reported and that sequence has no keys)
  *   group_indptr  int32 [num_groups + 1], non-decreasing within [0, batch]

@@ -139,7 +139,8 @@ int pkx_workspace_status(const void *workspace, void *stream) {
   int32_t st = hdr.status;
   if (e == cudaSuccess && st == kStatusInUnits) {  // the units' own words
     st = PKX_OK;
-    const uint8_t *at = static_cast<const uint8_t *>(workspace) + 256 * (size_t)hdr.pad[kUnitsPlace];
+    const uint8_t *at =
+        static_cast<const uint8_t *>(workspace) + 256 * (size_t)hdr.pad[kUnitsPlace];
     int32_t part[1024];
     for (int64_t i = 0; i < hdr.pad[kUnitsCount] && st == PKX_OK && e == cudaSuccess; i += 1024) {
       const int64_t n = std::min<int64_t>(1024, hdr.pad[kUnitsCount] - i);
@@ -888,6 +889,14 @@ static int check_equal_heads(const char *what, int hq, int hkv, int lq, int lv) 
   return PKX_OK;
 }
 
+// Rows of an fp8 pool that are copied 16 bytes at a time.
+static int check_fp8_strides(int kv_dtype, int64_t kb_ss, int64_t kb_sh, int64_t vb_ss,
+                             int64_t vb_sh) {
+  if (kv_dtype != kKvBf16 && ((kb_ss | kb_sh | vb_ss | vb_sh) & 15))
+    return set_error(PKX_EINVAL, "the strides of an fp8 pool must be multiples of 16 bytes");
+  return PKX_OK;
+}
+
 // Pages of one call: a selection fits the listing kernel's shared memory.
 constexpr int kMaxTopK = 4096;
 static int check_top_k(int top_k) {
@@ -1083,6 +1092,7 @@ int pkx_decode_attention_fwd_pages(
                    kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, -1, kv_dtype,
                    k_scale, v_scale, lse_out, &done);
   if (rc != PKX_OK || done) return rc;
+  if ((rc = check_fp8_strides(kv_dtype, kb_ss, kb_sh, vb_ss, vb_sh))) return rc;
   if (n_indices > 0 && !kv_indices) return set_error(PKX_EINVAL, "kv_indices is null");
   if (!kv_last_page_len || !aligned(kv_last_page_len, 4))
     return set_error(PKX_EINVAL, "kv_last_page_len null or misaligned");
@@ -1110,9 +1120,9 @@ int pkx_decode_attention_fwd_shared(
     const void *q, void *o, const void *k_buffer, const void *v_buffer, const int32_t *kv_indptr,
     const int32_t *kv_indices, int64_t n_indices, const int32_t *group_indptr,
     const int32_t *shared_lens, int num_groups, int batch, int hq, int hkv, int lq, int lv,
-    int64_t kb_ss, int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale, float logit_cap, int kv_dtype,
-    float k_scale, float v_scale, float *lse_out, void *workspace, size_t workspace_bytes,
-    void *stream) {
+    int64_t kb_ss, int64_t kb_sh, int64_t vb_ss, int64_t vb_sh, int64_t num_slots, float sm_scale,
+    float logit_cap, int kv_dtype, float k_scale, float v_scale, float *lse_out, void *workspace,
+    size_t workspace_bytes, void *stream) {
   int rc;
   if ((rc = check_equal_heads("decode with shared prefixes", hq, hkv, lq, lv))) return rc;
   if (num_groups < 0 || n_indices < 0)
@@ -1123,6 +1133,7 @@ int pkx_decode_attention_fwd_shared(
                    kb_ss, kb_sh, vb_ss, vb_sh, num_slots, sm_scale, logit_cap, -1, kv_dtype,
                    k_scale, v_scale, lse_out, &done);
   if (rc != PKX_OK || done) return rc;
+  if ((rc = check_fp8_strides(kv_dtype, kb_ss, kb_sh, vb_ss, vb_sh))) return rc;
   if (n_indices > 0 && !kv_indices) return set_error(PKX_EINVAL, "kv_indices is null");
   if (num_groups > 0 && (!group_indptr || !shared_lens || !aligned(group_indptr, 4) ||
                          !aligned(shared_lens, 4)))

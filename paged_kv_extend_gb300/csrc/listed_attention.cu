@@ -627,6 +627,7 @@ struct SharedParams {
   ListedRow *rows_out;
   WsHeader *hdr;
 };
+
 // Exclusive sums over a block of 1024 threads of two values in [0, kMany] each,
 // and the totals; sums are held at kMany, far above any count that the
 // workspace takes (an indptr that decreases can make them larger than 32 bits).
@@ -666,14 +667,14 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 // every sequence's own keys.  A group has min(shared_lens, the shortest of its
 // sequences) keys in common, which its first sequence lists for all.  They are
 // shared unless each sequence reads them as own keys: less than a tile of them, a
-// group of one, or (kShareElements) too little to save.  A prefix is cut into equal
-// pieces of at most C tiles.  The units
-// are few and long, so C is the one of up to 64 candidates (the longest prefix
-// in 1, 2, ... pieces) that takes least: its rounds over the SMs, a unit counting
-// C + kUnitTiles tiles (its query load, pipeline fill and partials), and for
-// each piece a partial of every row that goes out and comes back (256 sequences
-// and 32768 shared keys in 4 pieces instead of 9: combine 15 -> 11.5 us, the tile
-// kernel 112 -> 116.5, half the partials' traffic).  Own keys are cut for a given number of units.
+// group of one, or (kShareElements) too little to save.  A prefix is cut into
+// equal pieces of at most C tiles.  The units are few and long, so C is the one of
+// up to 64 candidates (the longest prefix in 1, 2, ... pieces) that takes least:
+// its rounds over the SMs, a unit counting C + kUnitTiles tiles (its query load,
+// pipeline fill and partials), and for each piece a partial of every row that
+// goes out and comes back (256 sequences and 32768 shared keys in 4 pieces
+// instead of 9: combine 15 -> 11.5 us, the tile kernel 112 -> 116.5, half the
+// partials' traffic).  Own keys are cut for a given number of units.
 //
 // The whole call waits for this one CTA, so it is a chain of few barriers with
 // no 64-bit division (a candidate in 64 bits took 2400 clocks); what a group
@@ -965,9 +966,12 @@ static ListedLayout shared_layout(int batch, int num_groups, int hkv, int group,
   const int64_t blocks = batch / blk + std::min(num_groups, batch / 2);
   const int64_t units = 4ll * n + own.target + (int64_t)hkv * (blocks + batch);
   L.unit_max = (int)std::min<int64_t>(units, INT_MAX / 4);
-  // four prefix units an SM of blk granules and, a block's first piece, twice
-  // its tokens; the units of own keys
-  L.gran_max = 4ll * n * blk + 2ll * hkv * batch + own.gran * (own.target + (int64_t)hkv * batch);
+  // four prefix units an SM of blk granules, or twice the batch's tokens, and,
+  // a block's first piece, twice its tokens; the units of own keys
+  const int64_t prefix = num_groups > 0 ? 4ll * n * std::min<int64_t>(blk, 2ll * batch) +
+                                              2ll * hkv * batch
+                                        : 0;
+  L.gran_max = prefix + own.gran * (own.target + (int64_t)hkv * batch);
   size_t off = up256(sizeof(WsHeader));
   L.seq_off = off;
   off = up256(off + sizeof(int32_t) * (kSeqArrays + 4) * (size_t)(batch + 1));

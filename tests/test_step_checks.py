@@ -162,6 +162,7 @@ BOTH = [
     (dict(o=P + 8), INVALID), (dict(k=None), INVALID), (dict(v=P + 4), INVALID), (dict(st=(256, 100, 256, 128)), INVALID),
     (dict(st=(256, 128, -8, 128)), INVALID), (dict(ptr=None), INVALID), (dict(idx=P + 1), INVALID),
     (dict(lse=P + 2), INVALID), (dict(slots=0), INVALID), (dict(slots=1 << 31), UNSUPPORTED),
+    (dict(fmt=1, st=(264, 128, 256, 128)), INVALID), (dict(fmt=2, st=(256, 128, 256, 136)), INVALID),
 ]
 
 
