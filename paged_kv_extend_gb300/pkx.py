@@ -1006,6 +1006,14 @@ def _flat_at(t, dtype, n, index, name):
     return t.data_ptr()
 
 
+def _list_at(t, index, name):
+    """Address and entries of a contiguous int32 list."""
+    if t.dtype is not _I32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), t.numel()
+
+
 def _dense_at(t, dtype, shape, index, name):
     """Address of a contiguous tensor of ``shape``."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or \
@@ -1016,11 +1024,14 @@ def _dense_at(t, dtype, shape, index, name):
 
 
 def _rows_at(t, shape, index, name):
-    """Address, row stride and head stride of bf16 rows [n, heads, dim]."""
+    """Address, row stride and head stride of bf16 rows [n, heads, dim]; ``shape``
+    None: already looked at."""
     st = t.stride()
-    if t.dtype is not _BF16 or t.shape != shape or st[2] != 1 or t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor {tuple(shape)} on cuda:{index} with a "
-                         f"contiguous last dim, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not _BF16 or st[2] != 1 or t.get_device() != index or \
+            (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a CUDA bf16 tensor {tuple(shape or t.shape)} on "
+                         f"cuda:{index} with a contiguous last dim, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr(), st[0], st[1]
 
 
@@ -1065,14 +1076,15 @@ def qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_w
     hkv = k_shape[1]
     if k_shape[0] != n or k_shape[2] != d:
         raise ValueError(f"k {tuple(k_shape)} does not fit q {tuple(q_shape)}")
-    q_at, k_at = _rows_at(q, q_shape, index, "q"), _rows_at(k, k_shape, index, "k")
+    q_at, k_at = _rows_at(q, None, index, "q"), _rows_at(k, None, index, "k")
+    # (sizes one by one: torch takes a shape object 2 us slower)
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=_BF16, device=q.device)
+        q_out = torch.empty(n, hq, d, dtype=_BF16, device=q.device)
         qo = q_out.data_ptr(), hq * d, d
     else:
         qo = _rows_at(q_out, q_shape, index, "q_out")
     if k_out is None:
-        k_out = torch.empty(k_shape, dtype=_BF16, device=q.device)
+        k_out = torch.empty(n, hkv, d, dtype=_BF16, device=q.device)
         ko = k_out.data_ptr(), hkv * d, d
     else:
         ko = _rows_at(k_out, k_shape, index, "k_out")
@@ -1126,13 +1138,14 @@ def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
     lib = _lib or load_library()
     index = _gpu(k_buffer, "k_buffer")
     *kb, (slots, hkv, d), fmt = _pool_at(k_buffer, index, "k_buffer")
-    pages, page_size, n = bounds.shape[0], int(page_size), page_ids.numel()
+    pages, page_size = bounds.shape[0], int(page_size)
+    ids_at, n = _list_at(page_ids, index, "page_ids")
     bounds_at = _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds")
     if page_size < 1 or pages * page_size > slots:
         raise ValueError(f"{pages} pages of {page_size} slots do not fit a pool of {slots} slots")
     lens_at = None if page_lens is None else _flat_at(page_lens, _I32, n, index, "page_lens")
-    _call(index, lib.pkx_update_page_bounds, *kb, fmt, page_size, pages, hkv, d,
-          _flat_at(page_ids, _I32, n, index, "page_ids"), lens_at, n, bounds_at)
+    _call(index, lib.pkx_update_page_bounds, *kb, fmt, page_size, pages, hkv, d, ids_at, lens_at, n,
+          bounds_at)
     return bounds
 
 
@@ -1154,15 +1167,16 @@ def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pa
     b, hq, d = q_shape
     pages, hkv = b_shape[0], b_shape[1]
     if selected is None:
-        selected = torch.empty((b, hkv, max(top_k, 0)), dtype=_I32, device=q.device)
-    n = kv_indices.numel()
+        selected = torch.empty(b, hkv, max(top_k, 0), dtype=_I32, device=q.device)
+        selected_at = selected.data_ptr()
+    else:
+        selected_at = _dense_at(selected, _I32, (b, hkv, max(top_k, 0)), index, "selected")
+    idx_at, n = _list_at(kv_indices, index, "kv_indices")
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, select_pages_workspace_size, b, b, hkv, n)
-    _call(index, lib.pkx_select_pages, _dense_at(q, _BF16, q_shape, index, "q"),
+    _call(index, lib.pkx_select_pages, _flat_at(q, _BF16, b * hq * d, index, "q"),
           _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds"), pages,
-          _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"),
-          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n, b, hq, hkv, d, top_k,
-          int(first_pages), int(last_pages),
-          _dense_at(selected, _I32, (b, hkv, max(top_k, 0)), index, "selected"), ws_at, ws_bytes)
+          _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"), idx_at, n, b, hq, hkv, d, top_k,
+          int(first_pages), int(last_pages), selected_at, ws_at, ws_bytes)
     return selected, ws
 
 
@@ -1179,7 +1193,7 @@ def _listed_at(q, o, lse, k_buffer, v_buffer, kv_indptr, index):
         raise ValueError(f"q must be [batch, heads, {lq}] as k_buffer's rows, got {tuple(q_shape)}")
     b, hq, _ = q_shape
     lse_at = None if lse is None else _dense_at(lse, _F32, (b, hq), index, "lse")
-    return ((b, hq, hkv, lq, lv), _dense_at(q, _BF16, q_shape, index, "q"),
+    return ((b, hq, hkv, lq, lv), _flat_at(q, _BF16, b * hq * lq, index, "q"),
             _dense_at(o, _BF16, (b, hq, lv), index, "o"), lse_at,
             _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"), kb, vb, slots, fmt)
 
@@ -1201,11 +1215,11 @@ def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, 
     index = _gpu(q, "q")
     dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
         q, o, lse, k_buffer, v_buffer, kv_indptr, index)
-    b, n, top_k, page_size = dims[0], kv_indices.numel(), selected.shape[-1], int(page_size)
+    b, top_k, page_size = dims[0], selected.shape[-1], int(page_size)
+    idx_at, n = _list_at(kv_indices, index, "kv_indices")
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_pages_workspace_size, b, *dims,
                                         page_size, top_k)
-    _call(index, lib.pkx_decode_attention_fwd_pages, q_at, o_at, kb[0], vb[0], ptr_at,
-          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n,
+    _call(index, lib.pkx_decode_attention_fwd_pages, q_at, o_at, kb[0], vb[0], ptr_at, idx_at, n,
           _flat_at(kv_last_page_len, _I32, b, index, "kv_last_page_len"), page_size,
           _dense_at(selected, _I32, (b, dims[2], top_k), index, "selected"), top_k, *dims, kb[1],
           kb[2], vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale, v_scale,
@@ -1229,13 +1243,13 @@ def decode_attention_fwd_shared(q, o, k_buffer, v_buffer, kv_indptr, kv_indices,
     index = _gpu(q, "q")
     dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
         q, o, lse, k_buffer, v_buffer, kv_indptr, index)
-    b, groups, n = dims[0], shared_lens.numel(), kv_indices.numel()
+    b = dims[0]
+    lens_at, groups = _list_at(shared_lens, index, "shared_lens")
+    idx_at, n = _list_at(kv_indices, index, "kv_indices")
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_shared_workspace_size, b, b,
                                         groups, *dims[1:])
-    _call(index, lib.pkx_decode_attention_fwd_shared, q_at, o_at, kb[0], vb[0], ptr_at,
-          _flat_at(kv_indices, _I32, n, index, "kv_indices"), n,
-          _flat_at(group_indptr, _I32, groups + 1, index, "group_indptr"),
-          _flat_at(shared_lens, _I32, groups, index, "shared_lens"), groups, *dims, kb[1], kb[2],
-          vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale, v_scale, lse_at,
-          ws_at, ws_bytes)
+    _call(index, lib.pkx_decode_attention_fwd_shared, q_at, o_at, kb[0], vb[0], ptr_at, idx_at, n,
+          _flat_at(group_indptr, _I32, groups + 1, index, "group_indptr"), lens_at, groups, *dims,
+          kb[1], kb[2], vb[1], vb[2], slots, sm_scale or 0.0, logit_cap or 0.0, fmt, k_scale,
+          v_scale, lse_at, ws_at, ws_bytes)
     return ws
