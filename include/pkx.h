@@ -725,8 +725,8 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
  * with the largest scores (of equal scores the lower page; NaN above all).
  *   q          bf16 [batch, hq, d] contiguous
  *   kv_indptr  int32 [batch + 1] over kv_indices; kv_indices int32
- *              [n_indices] page ids (entries past kv_indptr[batch] are not
- *              read for any sequence)
+ *              [n_indices] page ids (entries before kv_indptr[0], which may be
+ *              positive, or past kv_indptr[batch] are no sequence's)
  *   selected   int32 [batch, hkv, top_k] (written)
  *   workspace  >= pkx_select_pages_workspace_size(...) bytes,
  *              256-byte aligned; pkx_workspace_status reports a candidate page

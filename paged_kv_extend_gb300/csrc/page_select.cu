@@ -287,7 +287,11 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScorePa
       span = min(step, span - last * step);
     }
     const int64_t first = __ldg(p.kv_indptr + b), end = __ldg(p.kv_indptr + b + 1);
-    if (first > e || end <= e) break;  // behind the last sequence
+    if (first > e) {  // in front of the first sequence
+      i = (int)min(first - e0, (int64_t)n);
+      continue;
+    }
+    if (end <= e) break;  // behind the last one
     const int seg = (int)min(end - e0, (int64_t)n);
     if (end - first <= p.top_k) {  // all of its pages are taken
       i = seg;
