@@ -731,7 +731,8 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
  *   workspace  >= pkx_select_pages_workspace_size(...) bytes,
  *              256-byte aligned; pkx_workspace_status reports a candidate page
  *              outside [0, num_pages) (it ranks last) and an indptr that
- *              decreases or passes n_indices (that sequence selects nothing)
+ *              decreases or passes n_indices (that sequence selects nothing;
+ *              where it decreases, others may select nothing too)
  * first_pages + last_pages <= top_k <= 4096, n_indices <= 2^30.
  */
 size_t pkx_select_pages_workspace_size(int batch, int hkv, int64_t n_indices);

@@ -433,8 +433,7 @@ __device__ __forceinline__ bool select_top(const SelectParams &p, int n, const u
     const unsigned below = (1u << lane) - 1u;
     const int my_gt = gt + (before & 0xFFFF) + __popc(g & below);
     const int my_eq = eq + (before >> 16) + __popc(q & below);
-    // (my_gt + my_eq < want always, but for keys that another CTA changes: an
-    // indptr that decreases can give two sequences the same ones)
+    // (pos < want always, but where two calls use one workspace at once)
     const int pos = my_gt + min(my_eq, ties);
     if (i < m && (k > T || (k == T && my_eq < ties)) && pos < want) out[lo + pos] = lo + i;
     gt += all & 0xFFFF;
@@ -450,6 +449,16 @@ __device__ __forceinline__ bool select_top(const SelectParams &p, int n, const u
   return lost;
 }
 
+// Whether kv_indptr decreases anywhere (a CTA asks together).  Sequences may then
+// overlap, and of the keys in the workspace, one an entry of kv_indices and KV head,
+// some be another sequence's.
+template <int THREADS>
+__device__ __forceinline__ bool decreases(const int32_t *indptr, int batch) {
+  bool any = false;
+  for (int i = threadIdx.x; i < batch; i += THREADS) any |= __ldg(indptr + i + 1) < __ldg(indptr + i);
+  return __syncthreads_or(any);
+}
+
 // One CTA for each (sequence, KV head): its pages' numbers from the keys in the
 // workspace.
 template <int THREADS>
@@ -462,7 +471,8 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
   const int64_t at = __ldg(p.kv_indptr + b);
   const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
   int32_t *out = p.selected + (int64_t)blockIdx.x * p.top_k;
-  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
+  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices ||
+                   (n64 > p.top_k && decreases<THREADS>(p.kv_indptr, p.batch));
   bool lost = bad;
   const int n = bad ? 0 : (int)n64;
   if (n <= p.top_k) {  // every page
@@ -499,7 +509,9 @@ __global__ void __launch_bounds__(THREADS, 640 / THREADS) page_score_select_kern
   const int64_t at = __ldg(p.kv_indptr + b);
   const int64_t n64 = (int64_t)__ldg(p.kv_indptr + b + 1) - at;
   int32_t *out = sp.selected + (int64_t)blockIdx.x * p.top_k;
-  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices;
+  const bool bad = at < 0 || n64 < 0 || at + n64 > p.n_indices ||
+                   (n64 - sp.first_pages - sp.last_pages > kFusedKeys &&
+                    decreases<THREADS>(p.kv_indptr, p.batch));
   bool lost = bad;
   const int n = bad ? 0 : (int)n64;
   if (n <= p.top_k) {  // every page

@@ -43,3 +43,25 @@ def test_a_slice_of_a_page_table(indptr, n, fill):
     sel, status = _select(q, box, indptr, ids, 17, fill)
     assert torch.equal(sel, R.select(q, box, indptr, ids, 17, 1, 1))
     assert status == pkx.PKX_OK
+
+
+@pytest.mark.parametrize("indptr,hkv", [
+    ((0, 600, 300, 900), 2),                         # two kernels
+    ((0, 5000, 2000, 2100, 7000), 1),
+    ((0, 3000, 100) + (3100,) * 158, 1),             # one kernel, scores in the workspace
+    ((0, 500, 100, 700) + (700,) * 157, 1),          # and in shared memory
+], ids=["600", "5000", "160 of 3000", "160 of 600"])
+def test_an_indptr_that_decreases(indptr, hkv):
+    """Reported; the sequence that it ends before it begins selects nothing, and
+    those that it makes overlap select their own pages or nothing."""
+    ptr = torch.tensor(indptr, dtype=torch.int32)
+    n = max(indptr)
+    q, box, ids = _inputs(len(ptr) - 1, n, 2 * hkv, hkv, 128, n)
+    sel, status = _select(q, box, ptr, ids, 33, 0)
+    assert status == pkx.PKX_EDEVICE
+    for b in range(len(ptr) - 1):
+        if ptr[b + 1] < ptr[b]:
+            assert (sel[b] == -1).all()
+            continue
+        want = R.select(q[b:b + 1], box, ptr[b:b + 2], ids, 33, 1, 1)[0]
+        assert torch.equal(sel[b], want) or (sel[b] == -1).all()
