@@ -714,7 +714,8 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
 /*
  * Selection of the pages that a decode step reads, for d = 64 or 128.  With
  * qp[j] = the sum over a KV head's query heads, in order, of max(q[j], 0) and qn[j]
- * that of min(q[j], 0), each sum rounded to fp32, a page's score is
+ * that of min(q[j], 0) (NaN where q[j] is), each sum rounded to fp32, a page's
+ * score is
  *   tree(qn[j] * bounds[page, h, 0, j]) + tree(qp[j] * bounds[page, h, 1, j]),
  * where tree() adds neighbours pairwise over the dims (0 + 1, 2 + 3, ..., then
  * the sums likewise) and every product and sum is rounded to fp32: the sum

@@ -189,7 +189,8 @@ __device__ __forceinline__ void query_sums(const uint16_t *q, int64_t first_row,
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float qv = __uint_as_float(k & 1 ? wd[k / 2] & 0xFFFF0000u : wd[k / 2] << 16);
-      f[k] = __fadd_rn(f[k], is_hi ? (qv > 0.f ? qv : 0.f) : (qv < 0.f ? qv : 0.f));
+      // (a NaN stays one)
+      f[k] = __fadd_rn(f[k], is_hi ? (qv <= 0.f ? 0.f : qv) : (qv >= 0.f ? 0.f : qv));
     }
   }
 }
