@@ -704,7 +704,7 @@ int pkx_qk_norm_rope(const void *q, int64_t q_ts, int64_t q_hs, const void *k, i
  * listed twice must have the same length both times.
  *   page_ids, page_lens  int32 [n_pages]
  *   bounds     bf16 [num_pages, hkv, 2, d] contiguous, 16-byte aligned
- * d is a multiple of 8.
+ * d is a multiple of 8, page_size at most 2^30.
  */
 int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, int kv_dtype,
                            int page_size, int64_t num_pages, int hkv, int d,
@@ -755,7 +755,7 @@ int pkx_select_pages(const void *q, const void *bounds, int64_t num_pages,
  *   n_indices  entries of kv_indices
  *   selected   int32 [batch, hkv, top_k], top_k <= 4096
  *   workspace  >= pkx_decode_pages_workspace_size(...) bytes, 256-byte aligned
- * batch * hkv * top_k * page_size < 2^31.  pkx_workspace_status reports a
+ * batch * hkv * top_k * page_size < 2^31 - 4096.  pkx_workspace_status reports a
  * page outside the pool (its keys read as zero rows), a selected number past
  * the sequence's pages (ignored), a last page length outside [0, page_size]
  * (held at its limit), and an indptr that decreases or passes n_indices (that
@@ -783,8 +783,9 @@ int pkx_decode_attention_fwd_pages(
  * stand alone.
  * For (lq, lv) = (64, 64) and (128, 128), bf16 and fp8 pools (whose strides are
  * multiples of 16 bytes).
- *   n_indices     entries of kv_indices (an indptr that passes it, or
- *                 decreases, is reported and that sequence has no keys)
+ *   n_indices     entries of kv_indices, below 2^31 - 4096 (an indptr that
+ *                 passes it, or decreases, is reported and that sequence has no
+ *                 keys)
  *   group_indptr  int32 [num_groups + 1], non-decreasing within [0, batch]
  *   shared_lens   int32 [num_groups], >= 0
  *                 (both NULL when num_groups is 0; if either is out of range,

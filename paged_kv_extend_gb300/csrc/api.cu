@@ -1008,6 +1008,8 @@ int pkx_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_sh, i
     return set_error(PKX_EINVAL, "update_page_bounds: hkv > 0, d a multiple of 8");
   if (hkv > (1 << 20) || d > (1 << 10))
     return set_error(PKX_EUNSUPPORTED, "update_page_bounds: more than 2^20 heads or d > 1024");
+  if (page_size > (1 << 30))
+    return set_error(PKX_EUNSUPPORTED, "update_page_bounds: more than 2^30 slots a page");
   if (n_pages == 0) return PKX_OK;
   if ((rc = check_rows("k_buffer", k_buffer, kb_ss, kb_sh))) return rc;
   if (!bounds || !aligned(bounds, 16))
@@ -1069,7 +1071,7 @@ size_t pkx_decode_pages_workspace_size(int batch, int hq, int hkv, int lq, int l
                                        int top_k) {
   if (batch < 0 || hkv <= 0 || hq <= 0 || hq % hkv || hq / hkv > kBlockM || lq != lv ||
       (lq != 64 && lq != 128) || page_size <= 0 || top_k <= 0 || top_k > kMaxTopK ||
-      (int64_t)top_k * page_size >= (1ll << 31))
+      (int64_t)top_k * page_size > kMaxListedKeys)
     return 0;
   return pages_decode_workspace(batch, hq, hkv, lq, page_size, top_k, num_sms_current_device());
 }
@@ -1127,6 +1129,8 @@ int pkx_decode_attention_fwd_shared(
   if ((rc = check_equal_heads("decode with shared prefixes", hq, hkv, lq, lv))) return rc;
   if (num_groups < 0 || n_indices < 0)
     return set_error(PKX_EINVAL, "negative num_groups or n_indices");
+  if (n_indices > kMaxListedKeys)
+    return set_error(PKX_EUNSUPPORTED, "more than 2^31 - 4097 entries of kv_indices");
   AttnArgs a{};
   bool done;
   rc = decode_args(a, q, o, k_buffer, v_buffer, kv_indptr, kv_indices, batch, hq, hkv, lq, lv,

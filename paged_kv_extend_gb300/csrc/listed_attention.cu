@@ -1402,9 +1402,9 @@ int launch_decode_shared(const ListedArgs &a) {
 int launch_decode_pages(const ListedArgs &a) {
   const int group = a.hq / a.hkv;
   const int64_t pairs = (int64_t)a.batch * a.hkv;
-  if (pairs * a.top_k * a.page_size >= INT_MAX)  // (units and granules are fewer)
+  if (pairs * a.top_k * a.page_size > kMaxListedKeys)  // (units and granules are fewer)
     return set_error(PKX_EUNSUPPORTED,
-                     "decode_pages: batch * hkv * top_k * page_size must be below 2^31");
+                     "decode_pages: batch * hkv * top_k * page_size must be below 2^31 - 4096");
   const int nsm = num_sms_current_device();
   if (nsm <= 0) return set_error(PKX_ECUDA, "cannot query the current device");
   const ListedLayout L = pages_layout(a.batch, a.hkv, group, a.d, a.page_size, a.top_k, nsm);

@@ -303,6 +303,9 @@ int launch_select_pages(const SelectArgs &a);
 // Decode attention whose work is listed by schedulers of its own
 // (listed_attention.cu): sequences in groups that share a prefix, or selected
 // pages of each KV head.  Lq = Lv = d.
+// Most keys of one of its lists: what runs past the end of a list (a tile, a run, a
+// warp's block of slots) has to stay below 2^31.
+constexpr int kMaxListedKeys = INT32_MAX - 4096;
 struct ListedArgs {
   const void *q;
   void *o;
