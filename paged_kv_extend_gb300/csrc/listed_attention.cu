@@ -39,9 +39,10 @@
 
 namespace pkx {
 
-// Position of every listed unit's queries: past every key, so that no causal
-// mask applies.
-constexpr int kPastAll = 1 << 30;
+// Position of the first of a listed unit's at most 256 query tokens: past every
+// key, so that no causal mask applies.
+constexpr int kPastAll = kMaxListedKeys;
+static_assert(kPastAll <= INT_MAX - 256, "positions of a unit's tokens");
 
 // Groups of at most this many query heads take one-token units to rows_kernel.
 constexpr int kRowsGroup = 16;
