@@ -661,7 +661,8 @@ int pkx_decode_attention_fwd_streaming(
  *   c = cos_sin[p, i],  s = cos_sin[p, rotary_dim / 2 + i],
  *   p = positions[pair_axis[i], t]   (axis 0 without pair_axis).
  * Elements from rotary_dim on are not rotated.  Computed in fp32 and rounded
- * once to bf16.  With cache_loc the k_out row is also stored at that slot of
+ * once to bf16; rows whose squares leave fp32's range are scaled by a power of
+ * two before them.  With cache_loc the k_out row is also stored at that slot of
  * k_buffer and v's row at that slot of v_buffer, as pkx_set_kv_buffer (or
  * pkx_set_kv_buffer_fp8 for an fp8 pool) stores rows (two tokens with the same
  * slot leave that slot's rows undefined).
