@@ -1027,8 +1027,8 @@ def _rows_at(t, shape, index, name):
     """Address, row stride and head stride of bf16 rows [n, heads, dim]; ``shape``
     None: already looked at."""
     st = t.stride()
-    if t.dtype is not _BF16 or st[2] != 1 or t.get_device() != index or \
-            (shape is not None and t.shape != shape):
+    if t.dtype is not _BF16 or (shape is not None and t.shape != shape) or st[2] != 1 or \
+            t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA bf16 tensor {tuple(shape or t.shape)} on "
                          f"cuda:{index} with a contiguous last dim, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -1138,6 +1138,8 @@ def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
     lib = _lib or load_library()
     index = _gpu(k_buffer, "k_buffer")
     *kb, (slots, hkv, d), fmt = _pool_at(k_buffer, index, "k_buffer")
+    if bounds.dim() != 4:
+        raise ValueError(f"bounds must be [pages, heads, 2, dim], got {tuple(bounds.shape)}")
     pages, page_size = bounds.shape[0], int(page_size)
     ids_at, n = _list_at(page_ids, index, "page_ids")
     bounds_at = _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds")
@@ -1215,7 +1217,9 @@ def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, 
     index = _gpu(q, "q")
     dims, q_at, o_at, lse_at, ptr_at, kb, vb, slots, fmt = _listed_at(
         q, o, lse, k_buffer, v_buffer, kv_indptr, index)
-    b, top_k, page_size = dims[0], selected.shape[-1], int(page_size)
+    if selected.dim() != 3:
+        raise ValueError(f"selected must be [batch, heads, top_k], got {tuple(selected.shape)}")
+    b, top_k, page_size = dims[0], selected.shape[2], int(page_size)
     idx_at, n = _list_at(kv_indices, index, "kv_indices")
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_pages_workspace_size, b, *dims,
                                         page_size, top_k)

@@ -1,6 +1,7 @@
 """CPU tests of the sizes at which a decode step's operators stop, and of what the
 binding does with numbers and shapes that do not fit (nothing reaches a GPU)."""
 import pytest
+import torch
 
 from paged_kv_extend_gb300 import build as pkx_build
 from paged_kv_extend_gb300 import pkx
@@ -39,3 +40,10 @@ def test_lists_of_shared_prefixes_end_below_the_int_range(lib, n, hq):
 def test_pages_of_bounds_end_below_the_int_range(lib):
     bounds = lambda page: lib.pkx_update_page_bounds(P, 64, 64, 0, page, 1, 1, 64, P, None, 1, P, None)
     assert bounds(2 ** 30 + 1) == pkx.PKX_EUNSUPPORTED and bounds(2 ** 31 - 1) == pkx.PKX_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (64,), (), (3, 2, 32), (3, 2, 64, 1)])
+def test_rows_of_another_shape_are_refused(shape):
+    with pytest.raises(ValueError, match="v must be a CUDA bf16 tensor"):
+        pkx._rows_at(torch.zeros(shape, dtype=torch.bfloat16), (3, 2, 64), -1, "v")
+    assert pkx._rows_at(x := torch.zeros(3, 2, 64, dtype=torch.bfloat16), (3, 2, 64), -1, "v") == (x.data_ptr(), 128, 64)
