@@ -1140,7 +1140,7 @@ def update_page_bounds(k_buffer, bounds, page_ids, page_size, page_lens=None):
     *kb, (slots, hkv, d), fmt = _pool_at(k_buffer, index, "k_buffer")
     if bounds.dim() != 4:
         raise ValueError(f"bounds must be [pages, heads, 2, dim], got {tuple(bounds.shape)}")
-    pages, page_size = bounds.shape[0], int(page_size)
+    pages, page_size = bounds.shape[0], _c_int(page_size)
     ids_at, n = _list_at(page_ids, index, "page_ids")
     bounds_at = _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds")
     if page_size < 1 or pages * page_size > slots:
@@ -1163,13 +1163,13 @@ def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pa
     [B, hkv, top_k], workspace)."""
     lib = _lib or load_library()
     index = _gpu(q, "q")
-    q_shape, b_shape, top_k = q.shape, bounds.shape, int(top_k)
+    q_shape, b_shape, top_k = q.shape, bounds.shape, _c_int(top_k)
     if len(q_shape) != 3 or len(b_shape) != 4:
         raise ValueError("q must be [batch, heads, dim] and bounds [pages, heads, 2, dim]")
     b, hq, d = q_shape
     pages, hkv = b_shape[0], b_shape[1]
-    if selected is None:
-        selected = torch.empty(b, hkv, max(top_k, 0), dtype=_I32, device=q.device)
+    if selected is None:  # (the library takes no larger one)
+        selected = torch.empty(b, hkv, min(max(top_k, 0), 4096), dtype=_I32, device=q.device)
         selected_at = selected.data_ptr()
     else:
         selected_at = _dense_at(selected, _I32, (b, hkv, max(top_k, 0)), index, "selected")
@@ -1178,7 +1178,7 @@ def select_pages(q, bounds, kv_indptr, kv_indices, top_k, first_pages=1, last_pa
     _call(index, lib.pkx_select_pages, _flat_at(q, _BF16, b * hq * d, index, "q"),
           _dense_at(bounds, _BF16, (pages, hkv, 2, d), index, "bounds"), pages,
           _flat_at(kv_indptr, _I32, b + 1, index, "kv_indptr"), idx_at, n, b, hq, hkv, d, top_k,
-          int(first_pages), int(last_pages), selected_at, ws_at, ws_bytes)
+          _c_int(first_pages), _c_int(last_pages), selected_at, ws_at, ws_bytes)
     return selected, ws
 
 
@@ -1201,8 +1201,8 @@ def _listed_at(q, o, lse, k_buffer, v_buffer, kv_indptr, index):
 
 
 def decode_pages_workspace_size(batch, hq, hkv, lq, lv, page_size, top_k) -> int:
-    return int(load_library().pkx_decode_pages_workspace_size(batch, hq, hkv, lq, lv, page_size,
-                                                              top_k))
+    return int(load_library().pkx_decode_pages_workspace_size(batch, hq, hkv, lq, lv,
+                                                              _c_int(page_size), _c_int(top_k)))
 
 
 def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, kv_last_page_len,
@@ -1219,7 +1219,7 @@ def decode_attention_fwd_pages(q, o, k_buffer, v_buffer, kv_indptr, kv_indices, 
         q, o, lse, k_buffer, v_buffer, kv_indptr, index)
     if selected.dim() != 3:
         raise ValueError(f"selected must be [batch, heads, top_k], got {tuple(selected.shape)}")
-    b, top_k, page_size = dims[0], selected.shape[2], int(page_size)
+    b, top_k, page_size = dims[0], selected.shape[2], _c_int(page_size)
     idx_at, n = _list_at(kv_indices, index, "kv_indices")
     ws, ws_at, ws_bytes = _workspace_at(workspace, index, decode_pages_workspace_size, b, *dims,
                                         page_size, top_k)

@@ -47,3 +47,9 @@ def test_rows_of_another_shape_are_refused(shape):
     with pytest.raises(ValueError, match="v must be a CUDA bf16 tensor"):
         pkx._rows_at(torch.zeros(shape, dtype=torch.bfloat16), (3, 2, 64), -1, "v")
     assert pkx._rows_at(x := torch.zeros(3, 2, 64, dtype=torch.bfloat16), (3, 2, 64), -1, "v") == (x.data_ptr(), 128, 64)
+
+
+def test_workspace_sizes_past_the_c_int_range():
+    assert pkx.decode_pages_workspace_size(2, 8, 2, 64, 64, 16, 4) > 0
+    assert pkx.decode_pages_workspace_size(2, 8, 2, 64, 64, 2 ** 32 + 16, 4) == 0
+    assert pkx.decode_pages_workspace_size(2, 8, 2, 64, 64, 16, 2 ** 32 + 4) == 0
