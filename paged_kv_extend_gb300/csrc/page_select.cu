@@ -41,7 +41,7 @@ struct BoundParams {
   const uint8_t *k;
   int64_t kb_ss, kb_hs;  // bytes
   const int32_t *page_ids, *page_lens;
-  int64_t n_pages, num_pages;
+  int64_t num_pages;
   int page_size, hkv, d;
   int slices;  // runs of 32 chunks of a slot's row (all heads)
   uint4 *bounds;  // [num_pages][hkv][2][d / 8]
@@ -130,7 +130,6 @@ int launch_update_page_bounds(const void *k_buffer, int64_t kb_ss, int64_t kb_hs
   p.kb_hs = kb_hs * size;
   p.page_ids = page_ids;
   p.page_lens = page_lens;
-  p.n_pages = n_pages;
   p.num_pages = num_pages;
   p.page_size = page_size;
   p.hkv = hkv;

@@ -65,3 +65,33 @@ def test_an_indptr_that_decreases(indptr, hkv):
             continue
         want = R.select(q[b:b + 1], box, ptr[b:b + 2], ids, 33, 1, 1)[0]
         assert torch.equal(sel[b], want) or (sel[b] == -1).all()
+
+
+@pytest.mark.parametrize("hq", [8, 34])
+def test_decode_over_slices_of_larger_lists(hq):
+    """Decode over selected pages and with a shared prefix, whose first sequence's entries
+    begin past entry 0: the same bits as with the lists cut to size."""
+    g = torch.Generator().manual_seed(hq)
+    hkv, d, page = 2, 64, 16
+    k, v = (torch.randn(60 * page, hkv, d, generator=g).bfloat16().to(DEV) for _ in range(2))
+    q = torch.randn(3, hq, d, generator=g).bfloat16().to(DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    ids = torch.randperm(60, generator=g)[:57].to(torch.int32).to(DEV)
+    slots = torch.randperm(60 * page, generator=g)[:900].to(torch.int32).to(DEV)
+
+    def run(cut):
+        at = 7 * (not cut)
+        o, o2 = torch.empty_like(q), torch.empty_like(q)
+        lse, lse2 = torch.empty(3, hq, device=DEV), torch.empty(3, hq, device=DEV)
+        sel, ws = pkx.select_pages(q, box, i32(at, at + 20, at + 20, at + 45), ids[7:].contiguous() if cut else ids, 9)
+        ws2 = pkx.decode_attention_fwd_pages(q, o, k, v, i32(at, at + 20, at + 20, at + 45),
+                                             ids[7:].contiguous() if cut else ids, i32(5, 0, 16), page, sel, lse=lse)
+        ws3 = pkx.decode_attention_fwd_shared(q, o2, k, v, i32(at, at + 300, at + 610, at + 880),
+                                              slots[7:].contiguous() if cut else slots, i32(0, 2), i32(290), lse=lse2)
+        assert all(pkx.workspace_status(w) == pkx.PKX_OK for w in (ws, ws2, ws3))
+        return sel, o, lse, o2, lse2
+
+    box = torch.zeros(60, hkv, 2, d, dtype=torch.bfloat16, device=DEV)
+    pkx.update_page_bounds(k, box, torch.arange(60, dtype=torch.int32, device=DEV), page)
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
