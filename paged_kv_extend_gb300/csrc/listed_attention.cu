@@ -17,9 +17,10 @@
 // One-token units (own keys, selected pages) of groups of at most 16 query
 // heads run in rows_kernel, a warp a unit: 128 rows of the tensor core would be
 // padding for them, and a unit's way through the pipeline of the tile kernel
-// (claim, query load, two tiles in flight, epilogue) takes 3 us of an SM however
-// short it is (256 sequences of 32 own keys behind a shared prefix: 2048 units,
-// 40 us).  Larger groups and the prefixes run in the tile kernel; for selected
+// (claim, query load, two tiles in flight, epilogue) takes an SM some us however
+// short it is: 3 with 4 heads (256 sequences of 32 own keys behind a shared prefix:
+// 2048 units, 40 us), 5.8 with 17 heads and one key (1672 units, 71 us; 152 units, one
+// an SM: 13 us).  Larger groups and the prefixes run in the tile kernel; for selected
 // pages of larger groups a first kernel writes each list of pool slots, where
 // rows_kernel's warps look their pages up themselves.
 //
@@ -28,6 +29,16 @@
 // A unit's partial rows lie in granules of Hq / Hkv rows (one token's heads of
 // one KV head): n_tok granules a key stream, so that a one-token unit takes one
 // (rows_kernel) or two (the tile kernel's two streams) and not two whole tiles.
+//
+// Roundings.  Both kernels round the softmax weights P to bf16 for the product
+// with V, as decode_attention_fwd does: the tensor core's bf16 form takes both
+// factors in it, and V of a bf16 pool has no other 16-bit form that holds it (an
+// fp8 pool's codes would fit f16, and P three more bits with them; not built).  Sums of
+// P are of the fp32 values before that rounding; logits, maxima, sums, O and the
+// partials are fp32.  Independent roundings of the weights (2^-9 each at most) move
+// o by 0.0017 of its norm, as much as o's own rounding to bf16 does; measured
+// against 64 bits (o, lse) are off by 0.0017 to 0.0022, a plain fp32 form rounded once
+// by 0.0017.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -681,11 +692,22 @@ __device__ __forceinline__ Two block_sum_before(Two v, Two *sh, Two &total) {
 // no 64-bit division (a candidate in 64 bits took 2400 clocks); what a group
 // or a sequence needs later stays in shared memory.
 constexpr int kUnitTiles = 3;
-// Elements of K and V that sharing has to save for the tile kernel to run, whose
-// units take 20 us however short.  rows_kernel reads a prefix again for every
-// sequence, mostly from L2: 64 sequences, 8192 shared keys, 8 KV heads, bf16 (1057
-// million elements saved): 233 us a call against 70 shared; 8 groups of 8, about
-// 2000 keys, 4 KV heads, fp8 (115 million): 55 against 47.
+// Elements of K and V that sharing has to save for the tile kernel to run, which
+// takes 13 us with one short unit an SM and more than 20 with a few.  rows_kernel
+// reads a prefix again for every sequence, from L2 where it fits.  A captured call
+// from a cold cache, shared / read by each, us, one group of sequences with 64 keys
+// of their own, 32 heads over 8 KV heads of 128 (16 over 16: the same within 7 us),
+// by saved elements >> 20:
+//                        44         66         88        110        176        352
+//   bf16, 8 sequences   37 / 33    39 / 37    39 / 44    41 / 52    46 / 64    56 / 105
+//   bf16, 64            43 / 29    48 / 36    43 / 39    46 / 41    48 / 56    48 / 82
+//   e4m3, 8             46 / 37    48 / 39    48 / 46    48 / 56    52 / 68    64 / 111
+//   e4m3, 64            51 / 31    56 / 37    52 / 44    52 / 46    54 / 64    54 / 95
+//   bf16, 2             58 / 60    66 / 78    72 / 93    80 / 107  101 / 150  156 / 254
+//   e4m3, 2             60 / 52    74 / 64    84 / 80    95 / 86   125 / 120  209 / 192
+// The rule counts elements alone: for two sequences it is late in a bf16 pool, and
+// in an fp8 pool, whose tiles are converted before the products, sharing between two
+// never pays.
 constexpr float kShareElements = 88 << 20;
 constexpr int kSeqArrays = 3, kGroupArrays = 7;
 __global__ void __launch_bounds__(1024, 1) shared_sched_kernel(const SharedParams p) {

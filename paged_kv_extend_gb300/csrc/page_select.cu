@@ -239,8 +239,8 @@ __device__ __forceinline__ float eight_scores(const float (&f)[8], F &&copy) {
 // the run's bounds are on their way (cp.async, each lane its own 16 bytes, so
 // nothing is shared) before the warp looks for its sequence and sums up its
 // queries: with loads into registers, 8 pages at a time, that preparation stood
-// between the loads (64 sequences of 512 pages, 8 KV heads of 128: 45 us for
-// 134 MB).
+// between the loads (64 sequences of 512 pages, 8 KV heads of 128, 134 MB: this
+// kernel took 65 us and takes 35).
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreParams p) {
   constexpr int LP = D / 4;        // lanes of a page
@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(THREADS) page_select_kernel(const SelectParams
 // the workspace past kFusedKeys pages).  The queries are summed once a CTA and the
 // keys make no round trip; it needs CTAs enough to fill the GPU.  A warp keeps the
 // next eight copies on their way (cp.async, each lane its own 16 bytes).  64
-// sequences of 512 pages, 8 KV heads of 128 (134 MB): 45 us by two kernels, 31 in
-// one with eight loads at a time.
+// sequences of 512 pages, 8 KV heads of 128 (134 MB): 31 us back to back in a
+// captured graph and 41 from a cold cache, by two kernels 48 and 58.
 constexpr int kFusedKeys = 2048;
 constexpr int kFusedRing = 2 * 8 * 512;  // bytes of a warp
 template <int D, int THREADS>
@@ -630,14 +630,19 @@ int launch_select_pages(const SelectArgs &a) {
   if ((int64_t)a.batch * a.hkv >= (1ll << 31))
     return set_error(PKX_EUNSUPPORTED, "select_pages: batch too large");
   const dim3 pairs((unsigned)(a.batch * a.hkv));
-  // One kernel where the (sequence, KV head) pairs fill the GPU (64 sequences of
-  // 512 pages, 8 KV heads: 31 us against 43 by two kernels) or where there is
-  // too little to spread (5 sequences of up to 49 pages, 3 KV heads: 8 against
-  // 10).  Else scores by runs of pages, then the selection.
+  // One kernel where the (sequence, KV head) pairs fill the GPU or where there is
+  // too little to spread, else scores by runs of pages, then the selection.  Back
+  // to back in a captured graph, 8 KV heads of 128, one kernel / two: 64 sequences of
+  // 512 pages 31 / 48 us, 24 of them 16.5 / 23; 5 sequences of up to 49 pages, 3 KV
+  // heads 8.3 / 10.3.  The rules below go by the number of pairs and the batch's
+  // average, which the host knows, not by each sequence: one sequence of 8192 pages
+  // and 23 of 20 take 90 us (two kernels: 109), one of 6000 and 15 of 20, whose long
+  // rows a warp selects from, 82.
   const int64_t mean = a.n_indices / a.batch;
   if ((int64_t)a.batch * a.hkv >= nsm || mean <= 256) {
-    // eight warps a pair while three such CTAs an SM hold all pairs, else four
-    // (24 sequences of 512 pages, 8 KV heads: 23 us and 27; 64: 41.5 by four)
+    // eight warps a pair for up to three pairs an SM, else four (512 pages each, 8 KV
+    // heads, from a cold cache, eight / four: 24 sequences 25 / 28 us, 57: 37 / 37, 64:
+    // 48 / 41, 96: 58 / 64)
     if (pairs.x <= 3u * nsm)
       return a.d == 128 ? launch_score_select<128, 256>(p, s, pairs, a.stream)
                         : launch_score_select<64, 256>(p, s, pairs, a.stream);
